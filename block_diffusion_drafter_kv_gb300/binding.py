@@ -21,6 +21,8 @@ DEV_TIMEOUT, DEV_CAPACITY, DEV_TOKEN = 1, 2, 4
 OPT_WAIT_LIMIT_NS, OPT_CHAIN_MAX, OPT_GEMV_VARIANT, OPT_ATTN_SPLIT, OPT_ATTN_KEY_GROUPS = 1, 2, 3, 4, 5
 OPT_INJECT_PASS_ROWS = 6
 OPT_ATTN_MODE = 7
+F32, F16, BF16 = 0, 1, 2
+PAGE_POSITIONS = 64
 
 
 class DflashConfig(ctypes.Structure):
@@ -37,6 +39,18 @@ class DflashLayerWeights(ctypes.Structure):
 class DflashWeights(ctypes.Structure):
     _fields_ = [("w_fc", c_void_p), ("g_ctx", c_void_p), ("embed", c_void_p), ("mask_emb", c_void_p),
                 ("g_final", c_void_p), ("lm_head", c_void_p), ("layers", POINTER(DflashLayerWeights))]
+
+
+class DflashPagePool(ctypes.Structure):
+    _fields_ = [("n_pages", c_int32), ("pages_per_seq", c_int32), ("max_batch", c_int32), ("reserved", c_int32),
+                ("page_table", c_void_p), ("held", c_void_p), ("free_list", c_void_p), ("state", c_void_p)]
+
+
+class DflashCacheConfig(ctypes.Structure):
+    _fields_ = [("n_layers", c_int32), ("n_heads", c_int32), ("n_kv_heads", c_int32), ("head_dim", c_int32),
+                ("dtype", c_int32), ("n_pages", c_int32), ("pages_per_seq", c_int32), ("max_batch", c_int32),
+                ("max_block", c_int32), ("rope_dim", c_int32), ("rope_interleaved", c_int32),
+                ("rope_positions", c_int32), ("scale", c_float)]
 
 
 # name -> (restype, argtypes); mirrors include/dflash.h
@@ -56,6 +70,22 @@ SIGNATURES = {
                                          c_void_p, c_void_p]),
     "dflash_verify_greedy_hidden": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32,
                                               c_void_p, c_void_p, c_void_p]),
+    "dflash_logprobs": (c_int32, [c_void_p, c_void_p, c_int32, ctypes.c_int64, c_void_p, c_int32, c_float, c_int32,
+                                  c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "dflash_pages_init": (c_int32, [POINTER(DflashPagePool), c_void_p]),
+    "dflash_pages_reserve": (c_int32, [POINTER(DflashPagePool), c_void_p, c_void_p, c_int32, c_int32, c_void_p,
+                                       c_void_p]),
+    "dflash_pages_release": (c_int32, [POINTER(DflashPagePool), c_void_p, c_int32, c_void_p]),
+    "dflash_cache_config_check": (c_int32, [POINTER(DflashCacheConfig)]),
+    "dflash_cache_workspace_size": (c_size_t, [POINTER(DflashCacheConfig)]),
+    "dflash_cache_create": (c_int32, [POINTER(DflashCacheConfig), POINTER(c_void_p)]),
+    "dflash_cache_destroy": (c_int32, [c_void_p]),
+    "dflash_cache_bind": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                    c_size_t]),
+    "dflash_cache_append": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_int32, ctypes.c_int64,
+                                      ctypes.c_int64, ctypes.c_int64, c_void_p, c_int32, c_int32, c_void_p, c_void_p]),
+    "dflash_cache_attend": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_void_p]),
+    "dflash_cache_read_error": (c_int32, [c_void_p, POINTER(c_int32), c_int32, c_void_p]),
     "dflash_linear_bf16": (c_int32, [c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_int32, c_void_p,
                                      c_void_p]),
     "dflash_read_device_error": (c_int32, [c_void_p, POINTER(c_int32), c_int32, c_void_p]),
@@ -128,12 +158,18 @@ class Drafter:
     `weights` has the attributes of the input generator's `Weights` (bf16 CUDA tensors)."""
 
     def __init__(self, shape, weights, max_block: int, max_batch: int, kv_capacity: int, n_pages: int = 0,
-                 page_table=None):
+                 page_table=None, pages: "Optional[PagePool]" = None):
         """n_pages > 0 binds a paged KV cache: a pool of n_pages pages of 64 positions
         (k_cache / v_cache [L][n_pages * 64][nkv][d]) and `page_table`, an int32 CUDA tensor
         [max_batch][pages_per_seq] of page ids that the caller fills (and may change between
-        calls)."""
+        calls). `pages` binds one whose table a PagePool keeps instead: reserve room for
+        [len, len + B) before a draft and for the new positions before an injection."""
         import torch
+        if pages is not None:
+            if n_pages or page_table is not None or pages.max_batch < max_batch:
+                raise DFlashError(DFLASH_E_INVAL, "pages: a pool of at least max_batch sequences, without n_pages or page_table")
+            n_pages, page_table = pages.n_pages, pages.page_table
+        self.pages = pages
         self.L = lib()
         self.shape = shape
         self.cfg = make_config(shape, max_block, max_batch, kv_capacity)
@@ -229,6 +265,29 @@ class Drafter:
                                                  accept_len.data_ptr(), committed.data_ptr(), _stream(stream)),
               "dflash_verify_greedy_hidden")
 
+    def logprobs(self, logits, tokens, logprob, entropy, top_ids=None, top_logprobs=None, temperature: float = 1.0,
+                 stream=None):
+        """Log probabilities of `tokens` (int32 [rows]; -1: a row without one, left out; None
+        with logprob None) under softmax(logits / temperature), the rows' entropies and, with
+        top_ids (int32 [rows][n]) and top_logprobs (fp32 [rows][n]), the n most likely tokens.
+        logits: fp32, fp16 or bf16 [rows][vocab], rows a stride apart."""
+        import torch
+        rows, vocab = logits.shape if logits.dim() == 2 else (0, 0)
+        dtype = _DTYPES.get(str(logits.dtype), -1)
+        if dtype < 0 or vocab != self.cfg.vocab or logits.stride(1) != 1 or logits.device != self.last_token.device:
+            raise DFlashError(DFLASH_E_INVAL, "logits must be fp32, fp16 or bf16 [rows][vocab] on the drafter's device")
+        n = 0 if top_ids is None else top_ids.numel() // max(rows, 1)
+        for t, dt, size, name in ((tokens, torch.int32, rows, "tokens"), (logprob, torch.float32, rows, "logprob"),
+                                  (entropy, torch.float32, rows, "entropy"), (top_ids, torch.int32, rows * n, "top_ids"),
+                                  (top_logprobs, torch.float32, rows * n, "top_logprobs")):
+            _require_on(t, dt, size, name, logits.device)
+        if entropy is None or (n > 0) != (top_logprobs is not None and top_logprobs.numel() > 0):
+            raise DFlashError(DFLASH_E_INVAL, "entropy, and top_ids with top_logprobs, are needed")
+        check(self.L.dflash_logprobs(self.h, logits.data_ptr(), dtype, logits.stride(0) if rows > 1 else vocab,
+                                     _ptr(tokens), rows, float(temperature), n, _ptr(logprob), entropy.data_ptr(),
+                                     _ptr(top_ids) if n else None, _ptr(top_logprobs) if n else None,
+                                     _stream_on(stream, logits.device)), "dflash_logprobs")
+
     # -- helpers -------------------------------------------------------------------------
     def linear(self, W, X, Y, stream=None):
         import torch
@@ -297,6 +356,207 @@ def _require(t, dtype, name):
 def _require_opt(t, dtype, name):
     if t is not None:
         _require(t, dtype, name)
+
+
+def _require_on(t, dtype, numel, name, device):
+    if t is not None and (t.dtype != dtype or t.device != device or not t.is_contiguous() or t.numel() != numel):
+        raise DFlashError(DFLASH_E_INVAL, f"{name} must be a contiguous {dtype} tensor of {numel} values on {device} "
+                                          f"(got {t.dtype}, {t.numel()} values on {t.device}, contiguous={t.is_contiguous()})")
+
+
+def _stream_on(stream, device) -> int:
+    import torch
+    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+
+
+_DTYPES = {"torch.float32": F32, "torch.float16": F16, "torch.bfloat16": BF16}
+
+
+class PagePool:
+    """Cache pages handed out on the GPU from sequence lengths: the page table of a paged
+    cache, the pages each sequence holds and the free list, all int32 CUDA tensors."""
+
+    def __init__(self, n_pages: int, pages_per_seq: int, max_batch: int, device="cuda"):
+        import torch
+        self.L = lib()
+        self.n_pages, self.pages_per_seq, self.max_batch = n_pages, pages_per_seq, max_batch
+        if min(n_pages, pages_per_seq, max_batch) < 1:
+            raise DFlashError(DFLASH_E_INVAL, "PagePool")
+        with torch.cuda.device(device):
+            self.page_table = torch.empty(max_batch, pages_per_seq, dtype=torch.int32, device="cuda")
+            self.held = torch.empty(max_batch, dtype=torch.int32, device="cuda")
+            self.free_list = torch.empty(n_pages, dtype=torch.int32, device="cuda")
+            self.state = torch.empty(4, dtype=torch.int32, device="cuda")
+            self.device = self.state.device
+            self._pool = DflashPagePool(n_pages, pages_per_seq, max_batch, 0, self.page_table.data_ptr(),
+                                        self.held.data_ptr(), self.free_list.data_ptr(), self.state.data_ptr())
+            self._ref = ctypes.byref(self._pool)
+            check(self.L.dflash_pages_init(self._ref, _stream_on(None, self.device)), "dflash_pages_init")
+        self.n_free = self.state[:1]
+
+    def reserve(self, length, n_new, rows_per_seq: int, batch: int, slots=None, stream=None):
+        """Pages for positions [length[s], length[s] + n_new[s]) of every sequence; `slots` (int32
+        [batch * rows_per_seq]) gets their cache rows, -1 for rows past n_new[s] and for
+        sequences that the pool has no pages for."""
+        import torch
+        _require_min(length, torch.int32, batch, "length", self.device)
+        _require_min(n_new, torch.int32, batch, "n_new", self.device)
+        if slots is not None:
+            _require_on(slots, torch.int32, batch * rows_per_seq, "slots", self.device)
+        self._call(self.L.dflash_pages_reserve, "dflash_pages_reserve", stream, length.data_ptr(), n_new.data_ptr(), batch,
+                   rows_per_seq, _ptr(slots))
+
+    def release(self, length, batch: int, stream=None):
+        """Gives back every page past the first length[s] positions of each sequence (0: all)."""
+        import torch
+        _require_min(length, torch.int32, batch, "length", self.device)
+        self._call(self.L.dflash_pages_release, "dflash_pages_release", stream, length.data_ptr(), batch)
+
+    def device_error(self, clear: bool = True) -> int:
+        """The device error flags of the calls so far (waits for the current stream)."""
+        v = int(self.state[2])
+        if clear and v:
+            self.state[2:3].zero_()
+        return v
+
+    def _call(self, f, what, stream, *args):
+        import torch
+        if torch.cuda.current_device() == self.device.index:
+            check(f(self._ref, *args, _stream_on(stream, self.device)), what)
+        else:
+            with torch.cuda.device(self.device):
+                check(f(self._ref, *args, _stream_on(stream, self.device)), what)
+
+
+class PagedCache:
+    """The paged K/V cache of a causal target model: rotary append and attention of new rows.
+
+    `pages` keeps the page table; `length` (int32 CUDA [max_batch]) holds every sequence's
+    positions before the new rows and stays the caller's to advance. k_pool / v_pool:
+    [n_layers][n_pages * 64][n_kv_heads][head_dim] of `dtype` (fp16 or bf16), allocated here
+    unless given. rope_cos / rope_sin: fp32 [positions][rope_dim / 2] (see rope_tables)."""
+
+    def __init__(self, n_layers: int, n_heads: int, n_kv_heads: int, head_dim: int, pages: PagePool, length, dtype=None,
+                 max_block: int = 0, rope_cos=None, rope_sin=None, rope_interleaved: bool = False, scale: float = 0.0,
+                 k_pool=None, v_pool=None):
+        import torch
+        self.L = lib()
+        dtype = torch.float16 if dtype is None else dtype
+        self.dtype, self.device, self.pages, self.length = dtype, pages.device, pages, length
+        batch = min(length.numel(), pages.max_batch)
+        _require_min(length, torch.int32, 1, "length", self.device)
+        positions, rope_dim = (0, 0) if rope_cos is None else (rope_cos.shape[0], 2 * rope_cos.shape[1])
+        for t, n in ((rope_cos, "rope_cos"), (rope_sin, "rope_sin")):
+            if (t is None) != (rope_cos is None):
+                raise DFlashError(DFLASH_E_INVAL, "rope_cos and rope_sin go together")
+            _require_on(t, torch.float32, positions * rope_dim // 2, n, self.device)
+        if not max_block:  # as many rows as a call can take
+            max_block = max(1, min(16, 128 // max(1, n_heads // max(1, n_kv_heads))))
+        self.cfg = DflashCacheConfig(n_layers, n_heads, n_kv_heads, head_dim, _DTYPES.get(str(dtype), -1), pages.n_pages,
+                                     pages.pages_per_seq, batch, max_block, rope_dim, int(rope_interleaved), positions,
+                                     float(scale))
+        check(self.L.dflash_cache_config_check(ctypes.byref(self.cfg)), "dflash_cache_config_check")
+        shape = (n_layers, pages.n_pages * PAGE_POSITIONS, n_kv_heads, head_dim)
+        numel = shape[0] * shape[1] * shape[2] * shape[3]
+        _require_on(k_pool, dtype, numel, "k_pool", self.device)
+        _require_on(v_pool, dtype, numel, "v_pool", self.device)
+        self.k_pool = torch.zeros(shape, dtype=dtype, device=self.device) if k_pool is None else k_pool
+        self.v_pool = torch.zeros(shape, dtype=dtype, device=self.device) if v_pool is None else v_pool
+        self.rope_cos, self.rope_sin = rope_cos, rope_sin
+        nbytes = self.L.dflash_cache_workspace_size(ctypes.byref(self.cfg))
+        with torch.cuda.device(self.device):
+            self.workspace = torch.empty(nbytes + 256, dtype=torch.uint8, device="cuda")
+            h = c_void_p()
+            check(self.L.dflash_cache_create(ctypes.byref(self.cfg), ctypes.byref(h)), "dflash_cache_create")
+            self.c = h
+            check(self.L.dflash_cache_bind(h, self.k_pool.data_ptr(), self.v_pool.data_ptr(), pages.page_table.data_ptr(),
+                                           length.data_ptr(), _ptr(rope_cos), _ptr(rope_sin),
+                                           (self.workspace.data_ptr() + 255) // 256 * 256, nbytes), "dflash_cache_bind")
+        self._q_row, self._kv_row = n_heads * head_dim, n_kv_heads * head_dim
+
+    def append(self, layer: int, q, k, v, slots, batch: int, rows_per_seq: int, q_out, stream=None):
+        """Rotary positions on q and k, k and v into the cache at `slots` (from
+        PagePool.reserve), the rotated q to q_out. q, k, v: fp16 or bf16 [batch * rows_per_seq]
+        rows of heads x dims, rows a stride apart (slices of one fused projection are fine);
+        q and q_out may be None."""
+        import torch
+        rows = batch * rows_per_seq
+        dt = k.dtype
+        for t, n, name in ((q, self._q_row, "q"), (k, self._kv_row, "k"), (v, self._kv_row, "v")):
+            if t is not None and (t.dtype != dt or t.device != self.device or t.shape[0] != rows or t.numel() != rows * n
+                                  or not _rows_dense(t)):
+                raise DFlashError(DFLASH_E_INVAL, f"{name} must be {rows} dense rows of {n} values of one type on {self.device}")
+        _require_on(slots, torch.int32, rows, "slots", self.device)
+        _require_on(q_out, self.dtype, rows * self._q_row, "q_out", self.device)
+        check(self.L.dflash_cache_append(self.c, layer, _ptr(q), k.data_ptr(), v.data_ptr(), _DTYPES.get(str(dt), -1),
+                                         0 if q is None else _row_stride(q, self._q_row), _row_stride(k, self._kv_row),
+                                         _row_stride(v, self._kv_row), slots.data_ptr(), batch, rows_per_seq, _ptr(q_out),
+                                         _stream_on(stream, self.device)), "dflash_cache_append")
+
+    def attend(self, layer: int, q, n_new, batch: int, rows_per_seq: int, out, stream=None):
+        """Causal attention of row r of every sequence (position length[s] + r, r < n_new[s]) over
+        the cache; q and out: contiguous [batch * rows_per_seq][n_heads][head_dim] of the
+        cache's dtype. Rows past n_new[s] of out are left as they were."""
+        import torch
+        numel = batch * rows_per_seq * self._q_row
+        _require_on(q, self.dtype, numel, "q", self.device)
+        _require_on(out, self.dtype, numel, "out", self.device)
+        _require_min(n_new, torch.int32, batch, "n_new", self.device)
+        check(self.L.dflash_cache_attend(self.c, layer, q.data_ptr(), n_new.data_ptr(), batch, rows_per_seq, out.data_ptr(),
+                                         _stream_on(stream, self.device)), "dflash_cache_attend")
+
+    def device_error(self, clear: bool = True, stream=None) -> int:
+        """The device error flags once the work queued on `stream` has finished."""
+        f = c_int32(0)
+        check(self.L.dflash_cache_read_error(self.c, ctypes.byref(f), 1 if clear else 0, _stream_on(stream, self.device)),
+              "dflash_cache_read_error")
+        return f.value
+
+    def close(self):
+        if getattr(self, "c", None):
+            self.L.dflash_cache_destroy(self.c)
+            self.c = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _require_min(t, dtype, numel, name, device):
+    if t.dtype != dtype or t.device != device or not t.is_contiguous() or t.numel() < numel:
+        raise DFlashError(DFLASH_E_INVAL, f"{name} must be a contiguous {dtype} tensor of at least {numel} values on {device}")
+
+
+def _row_stride(t, row: int) -> int:
+    """Elements from one row to the next (a single row's stride means nothing)."""
+    return t.stride(0) if t.shape[0] > 1 else max(row, t.stride(0) // 8 * 8)
+
+
+def _rows_dense(t) -> bool:
+    """Whether each row t[i] is contiguous."""
+    return t.stride(-1) == 1 and (t.dim() == 2 or (t.dim() == 3 and (t.shape[1] == 1 or t.stride(1) == t.shape[2])))
+
+
+def rope_tables(n_positions: int, rope_dim: int, theta: float, linear: float = 1.0, bands=None, attention_factor: float = 1.0,
+                device="cuda"):
+    """cos and sin (fp32 [n_positions][rope_dim / 2], angles in float64) of rotary positions for
+    PagedCache. Pair j turns by position * theta^(-2j / rope_dim). For contexts past the trained
+    length: `linear` divides every angle; `bands` = (factor, low, high, trained) divides by `factor`
+    the pairs that make fewer than `low` turns within `trained` positions, keeps those that make
+    more than `high`, and goes linearly (in the number of turns) from one to the other between them.
+    attention_factor scales cos and sin."""
+    import math
+    import torch
+    inv = theta ** (-torch.arange(0, rope_dim, 2, dtype=torch.float64) / max(1, rope_dim)) / linear
+    if bands is not None:
+        factor, low, high, trained = bands
+        turns = trained * inv / (2 * math.pi)
+        keep = ((turns - low) / (high - low)).clamp(0, 1)
+        inv = inv / factor * (1 - keep) + inv * keep
+    angle = torch.arange(n_positions, dtype=torch.float64)[:, None] * inv
+    return [(attention_factor * f(angle)).float().contiguous().to(device) for f in (torch.cos, torch.sin)]
 
 
 def verify_greedy_noalloc(target_logits, drafted, batch: int, block: int, accept_len, committed, last_token,

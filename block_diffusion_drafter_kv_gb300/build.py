@@ -19,7 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libdflash.so")
-SOURCES = ["gemv.cu", "attention.cu", "attn_tc.cu", "small.cu", "capi.cu", "verify_noalloc.cu"]
+SOURCES = ["gemv.cu", "attention.cu", "attn_tc.cu", "small.cu", "capi.cu", "verify_noalloc.cu", "pages.cu", "append.cu",
+           "paged_attn.cu", "logprobs.cu", "cache.cu"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

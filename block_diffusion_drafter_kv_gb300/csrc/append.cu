@@ -1,0 +1,137 @@
+// Rotary positions on a step's new q and k rows, and k and v into the paged cache, in one
+// pass: every value is read once and written once, so the bound is memory bandwidth
+// (2 bytes in, 2 bytes out per value; the rotary tables come from L2).
+//
+// A thread owns 16 dims of a head that are closed under the rotation: [8i, 8i + 8) and its
+// partners rope_dim / 2 further on (half layout), or the eight pairs of [16i, 16i + 16)
+// (interleaved), or 16 plain dims past rope_dim. Its eight angles are the same for every
+// head of the row, so it keeps their cos and sin in registers and walks the row's heads.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "ptx.cuh"
+#include "target.h"
+
+namespace dfl {
+
+namespace {
+
+template <typename T>
+DEV float to_f32(T v);
+template <>
+DEV float to_f32<__half>(__half v) {
+  return __half2float(v);
+}
+template <>
+DEV float to_f32<__nv_bfloat16>(__nv_bfloat16 v) {
+  return __bfloat162float(v);
+}
+template <typename T>
+DEV T from_f32(float v);
+template <>
+DEV __half from_f32<__half>(float v) {
+  return __float2half_rn(v);
+}
+template <>
+DEV __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+
+constexpr int kThreads = 128;
+
+// One CTA per row. blockDim covers d / 16 items of kThreads / (d / 16) heads at a time.
+template <typename X, typename Y>
+__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams P) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const long long row = blockIdx.x;
+  const int slot = __ldcg(P.slots + row);
+  const int s = static_cast<int>(row / P.rows_per_seq);
+  const long long pos = static_cast<long long>(__ldcg(P.len + s)) + (row - static_cast<long long>(s) * P.rows_per_seq);
+  if (slot == -1) return;
+  if (slot < 0 || slot >= P.pool_rows || (P.rope_dim > 0 && (pos < 0 || pos >= P.positions))) {
+    if (threadIdx.x == 0) raise_flag(P.err, kDevCapacity);
+    return;
+  }
+  const int items = P.d / 16;  // 4 or 8
+  const int item = threadIdx.x % items, h0 = threadIdx.x / items, step = kThreads / items;
+  const bool turn = item * 16 < P.rope_dim;
+  const int half = P.rope_dim / 2;
+  // the two runs of eight dims
+  const int d0 = turn && !P.interleaved ? 8 * item : 16 * item;
+  const int d1 = turn && !P.interleaved ? d0 + half : d0 + 8;
+  float cs[8], sn[8];
+  if (turn) {
+    const float4* c4 = reinterpret_cast<const float4*>(P.cos + pos * half + 8 * item);
+    const float4* s4 = reinterpret_cast<const float4*>(P.sin + pos * half + 8 * item);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 c = __ldg(c4 + i), t = __ldg(s4 + i);
+      cs[4 * i] = c.x, cs[4 * i + 1] = c.y, cs[4 * i + 2] = c.z, cs[4 * i + 3] = c.w;
+      sn[4 * i] = t.x, sn[4 * i + 1] = t.y, sn[4 * i + 2] = t.z, sn[4 * i + 3] = t.w;
+    }
+  }
+  const int nq = P.q ? P.nq : 0, heads = nq + 2 * P.nkv;
+  for (int h = h0; h < heads; h += step) {
+    const X* src;
+    Y* dst;
+    bool rot = turn;
+    if (h < nq) {
+      src = static_cast<const X*>(P.q) + row * P.q_stride + static_cast<size_t>(h) * P.d;
+      dst = static_cast<Y*>(P.q_out) + (static_cast<size_t>(row) * P.nq + h) * P.d;
+    } else if (h < nq + P.nkv) {
+      src = static_cast<const X*>(P.k) + row * P.k_stride + static_cast<size_t>(h - nq) * P.d;
+      dst = static_cast<Y*>(P.k_pool) + (static_cast<size_t>(slot) * P.nkv + (h - nq)) * P.d;
+    } else {
+      src = static_cast<const X*>(P.v) + row * P.v_stride + static_cast<size_t>(h - nq - P.nkv) * P.d;
+      dst = static_cast<Y*>(P.v_pool) + (static_cast<size_t>(slot) * P.nkv + (h - nq - P.nkv)) * P.d;
+      rot = false;
+    }
+    uint4 in[2] = {__ldcs(reinterpret_cast<const uint4*>(src + d0)), __ldcs(reinterpret_cast<const uint4*>(src + d1))};
+    const X* x = reinterpret_cast<const X*>(in);
+    uint4 out[2];
+    Y* y = reinterpret_cast<Y*>(out);
+    if (rot) {
+      auto pair = [&](int i0, int i1, int e) {
+        const float a = to_f32(x[i0]), b = to_f32(x[i1]);
+        y[i0] = from_f32<Y>(a * cs[e] - b * sn[e]);
+        y[i1] = from_f32<Y>(b * cs[e] + a * sn[e]);
+      };
+      if (P.interleaved) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) pair(2 * e, 2 * e + 1, e);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) pair(e, e + 8, e);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) y[e] = from_f32<Y>(to_f32(x[e]));
+    }
+    *reinterpret_cast<uint4*>(dst + d0) = out[0];
+    *reinterpret_cast<uint4*>(dst + d1) = out[1];
+  }
+}
+
+}  // namespace
+
+int launch_append(const AppendParams& p, int x_dtype, int pool_dtype, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.rows));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const bool xh = x_dtype == DFLASH_F16, yh = pool_dtype == DFLASH_F16;
+  cudaError_t e;
+  if (xh && yh) e = cudaLaunchKernelEx(&cfg, append_kernel<__half, __half>, p);
+  else if (xh) e = cudaLaunchKernelEx(&cfg, append_kernel<__half, __nv_bfloat16>, p);
+  else if (yh) e = cudaLaunchKernelEx(&cfg, append_kernel<__nv_bfloat16, __half>, p);
+  else e = cudaLaunchKernelEx(&cfg, append_kernel<__nv_bfloat16, __nv_bfloat16>, p);
+  return static_cast<int>(e);
+}
+
+}  // namespace dfl

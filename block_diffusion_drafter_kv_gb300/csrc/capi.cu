@@ -14,6 +14,7 @@
 
 #include "dflash.h"
 #include "internal.h"
+#include "target.h"
 
 using namespace dfl;
 
@@ -31,6 +32,7 @@ struct WsLayout {
   size_t ss_fc, ss_x, ss_emb, cfeat, x, xg, q, o, act, vpart_v, vpart_i, chain_bar;
   size_t tgt_xg, tgt_ss, tgt_g;  // fused target-side verification
   size_t attn_part, attn_cnt;    // flat key-split attention: partial slots, per-pair counters
+  size_t lp_part, lp_cnt;        // log probabilities: parts of rows that are cut, per-row counters
   size_t total;
   int R;          // draft rows allocated (multiple of 16)
   int max_tiles;  // tile counters
@@ -86,6 +88,8 @@ WsLayout layout_of(const dflash_config& c) {
   // flat attention slots: a head's 16 slots x its query heads, or two KV heads' (tensor-core kernel)
   L.attn_part = take(static_cast<size_t>(2) * kMaxCtas * 2 * (nq / c.n_kv_heads) * 16 * (d + 4) * 4);
   L.attn_cnt = take(static_cast<size_t>(c.max_batch) * c.n_kv_heads * 4);
+  L.lp_part = take(static_cast<size_t>(kLpSlots) * kLpSlotWords * 4);
+  L.lp_cnt = take(static_cast<size_t>(kLpSlots) * 4);
   L.total = off;
   return L;
 }
@@ -919,6 +923,46 @@ int dflash_verify_greedy_hidden(dflash_handle* h, const void* target_hidden, con
   return DFLASH_OK;
 }
 
+int dflash_logprobs(dflash_handle* h, const void* logits, int32_t dtype, int64_t row_stride, const int32_t* tokens,
+                    int32_t rows, float temperature, int32_t n_top, float* logprob, float* entropy, int32_t* top_ids,
+                    float* top_logprobs, void* stream) {
+  if (!h) return DFLASH_E_INVAL;
+  if (!h->bound) return DFLASH_E_STATE;
+  const int V = h->cfg.vocab;
+  if (!logits || !entropy || rows < 1 || n_top < 0 || n_top > kLpMaxTop || n_top > V || row_stride < V ||
+      !(temperature > 0.f) || !std::isfinite(temperature) || !tokens != !logprob || (n_top > 0 && (!top_ids || !top_logprobs)))
+    return DFLASH_E_INVAL;
+  if (dtype != DFLASH_F32 && dtype != DFLASH_F16 && dtype != DFLASH_BF16) return DFLASH_E_INVAL;
+  const int elem = dtype == DFLASH_F32 ? 4 : 2;
+  if ((reinterpret_cast<uintptr_t>(logits) & (elem - 1)) || !aligned4(tokens) || !aligned4(logprob) || !aligned4(entropy) ||
+      !aligned4(top_ids) || !aligned4(top_logprobs))
+    return DFLASH_E_INVAL;
+  const DeviceGuard on(h->device);
+  if (!on.ok()) return DFLASH_E_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  call_begin(h, st);
+  LogprobParams P{};
+  P.logits = logits;
+  P.row_stride = row_stride;
+  P.tokens = tokens;
+  P.scale = static_cast<float>(1.4426950408889634 / temperature);
+  P.inv_temp = static_cast<float>(1.0 / temperature);
+  P.V = V;
+  P.rows = rows;
+  P.n_top = n_top;
+  P.chunks = logprob_chunks(rows, V, elem, h->n_sms);
+  P.logprob = logprob;
+  P.entropy = entropy;
+  P.top_ids = top_ids;
+  P.top_logprobs = top_logprobs;
+  P.part = h->at<float>(h->L.lp_part);
+  P.row_cnt = h->at<int>(h->L.lp_cnt);
+  P.err = h->at<int>(h->L.err);
+  if (launch_logprobs(P, dtype, st) != 0) return DFLASH_E_CUDA;
+  note_launch(h, st);
+  return DFLASH_OK;
+}
+
 int dflash_linear_bf16(dflash_handle* h, const void* W, int32_t n_out, int32_t K, const void* X, int32_t rows,
                        float* Y, void* stream) {
   if (!h) return DFLASH_E_INVAL;
@@ -973,7 +1017,8 @@ int dflash_read_device_error(dflash_handle* h, int32_t* flags, int32_t clear, vo
                                {L.cta_cnt, 4},
                                {L.seq_cnt, static_cast<size_t>(h->cfg.max_batch) * 4},
                                {L.chain_bar, static_cast<size_t>(kChainSlots) * (kMaxPhases + 4) * 4},
-                               {L.attn_cnt, static_cast<size_t>(h->cfg.max_batch) * h->cfg.n_kv_heads * 4}};
+                               {L.attn_cnt, static_cast<size_t>(h->cfg.max_batch) * h->cfg.n_kv_heads * 4},
+                               {L.lp_cnt, static_cast<size_t>(kLpSlots) * 4}};
     for (const auto& sp : spans)
       if (cudaMemsetAsync(h->ws + sp[0], 0, sp[1], st) != cudaSuccess) return DFLASH_E_CUDA;
     if (cudaStreamSynchronize(st) != cudaSuccess) return DFLASH_E_CUDA;

@@ -1,0 +1,817 @@
+// Causal attention of a few new rows per sequence over a paged K/V cache: one new token
+// (decoding) or a block of up to 16 (verification).
+//
+//   out[s][r][h] = sum_j p_j V_j / sum_j p_j,  p_j = exp(scale q.K_j - m),  j = 0 .. len[s] + r
+//
+// The query heads that share a KV head and the sequence's new rows are the M rows of one
+// problem (row r * group + head in group), so every K and V byte is read once for all of
+// them. Bound: the K/V bytes, 4 d per key and KV head.
+//
+// Split. The 64-key tiles (pages) of all (sequence, KV head) pairs form one list, cut evenly
+// over the CTAs (one per SM), which balances ragged lengths and splits a long cache when
+// there are few sequences. A pair inside one range is finished there; of a pair that a cut
+// divides each CTA leaves its unnormalised output with the rows' (max, sum), and a second
+// small kernel joins those in CTA order: the result does not depend on timing, and no
+// counter has to be kept between calls.
+//
+// CTA. One producer warp walks the range: page ids a warp-load at a time, K/V tiles by TMA
+// into a ring of shared-memory stages, each segment's q rows by bulk copies. The compute
+// warps are RG row groups of 16 * MT rows times KG key groups; a warp takes 16-key slices of
+// every tile (slice number mod KG is its group) with a softmax state of its own, so
+// that warps meet only where a segment ends. S = q K^T and O += P V are mma.sync m16n8k16
+// with fp32 accumulation: the rows are few (4 in ordinary grouped decoding), so a
+// 128-row tcgen05 tile would be mostly padding, while the loads bound the kernel.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "ptx.cuh"
+#include "target.h"
+
+namespace dfl {
+
+namespace {
+
+constexpr int kKeys = kPagePos;  // keys per tile
+constexpr int kSlice = 16;       // keys per warp step
+
+DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool TRANS>
+DEV void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  if (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+template <bool BF16>
+DEV void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two values as the cache's 16-bit type, the first in the low half.
+template <bool BF16>
+DEV uint32_t pack2(float lo, float hi) {
+  if (BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <bool BF16>
+DEV float2 unpack2(uint32_t u) {
+  if (BF16) return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+// Whether one of the two 16-bit values is infinite or NaN.
+template <bool BF16>
+DEV bool non_finite2(uint32_t u) {
+  constexpr uint32_t kExp = BF16 ? 0x7f80u : 0x7c00u;
+  return (u & kExp) == kExp || ((u >> 16) & kExp) == kExp;
+}
+
+// Byte address of element (key, dim) in a staged tile: d / 64 boxes of 64 keys x 128 bytes,
+// written by TMA with the 128-byte swizzle (16-byte chunk c of row r lands at c ^ (r & 7)).
+DEV uint32_t tile_addr(uint32_t base, int key, int dim) {
+  return base + (dim >> 6) * (kKeys * 128) + key * 128 + ((((dim & 63) >> 3) ^ (key & 7)) << 4) + (dim & 7) * 2;
+}
+
+DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// First tile of CTA c's range, and the CTA whose range holds tile u (G <= T: none is empty).
+DEV long long range_begin(long long c, long long T, int G) { return c * T / G; }
+DEV int cta_of(long long u, long long T, int G) { return static_cast<int>(((u + 1) * G - 1) / T); }
+
+template <int D, int MT, int RG, int KG, int STAGES>
+struct Layout {
+  static constexpr int kWarps = RG * KG;
+  static constexpr int kThreads = 32 * (kWarps + 1);
+  static constexpr int kRows = 16 * MT * RG;
+  static constexpr int kTileBytes = kKeys * D * 2;          // one operand
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kQStride = D * 2 + 16;               // bytes; the pad keeps ldmatrix free of conflicts
+  static constexpr int kQBufs = kRows <= 64 ? 2 : 1;
+  static constexpr bool kAllAtOnce = kRows == 16;           // every key group's output exchanged at once
+  static constexpr int kCopies = kAllAtOnce ? KG : KG > 1 ? 1 : 0;
+  static constexpr int kQOff = STAGES * kStageBytes;
+  static constexpr int kXOff = kQOff + kQBufs * kRows * kQStride;
+  static constexpr int kMlOff = kXOff + kCopies * kRows * D * 4;
+  static constexpr int kBarOff = kMlOff + KG * kRows * 8;   // full, empty [STAGES]; q full, q empty [kQBufs]
+  static constexpr int kMetaOff = kBarOff + (2 * STAGES + 2 * kQBufs) * 8;
+  static constexpr int kPreOff = kMetaOff + (STAGES + 4) * 4;  // stage valid flags, abort flag, scan scratch
+  static constexpr int smem(int batch) { return 1024 + kPreOff + 64 + (batch + 1) * 4; }
+};
+
+// Sequence s's rows of this call: 0 where its lengths are out of range.
+DEV int rows_of(const PagedAttnParams& P, int s, int& len, bool& bad) {
+  len = __ldcg(P.len + s);
+  const int n = __ldcg(P.n_new + s);
+  bad = len < 0 || n < 0 || n > P.rows_per_seq ||
+        static_cast<long long>(len) + n > static_cast<long long>(P.pages_per_seq) * kPagePos;
+  return bad ? 0 : n;
+}
+
+template <int D, bool BF16, int MT, int RG, int KG, int STAGES>
+__global__ void __launch_bounds__(Layout<D, MT, RG, KG, STAGES>::kThreads, 1)
+    paged_attn_kernel(const __grid_constant__ PagedAttnParams P) {
+  using L = Layout<D, MT, RG, KG, STAGES>;
+  constexpr int NT = D / 8;  // 8-dim column tiles of the output
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float4* s_x = reinterpret_cast<float4*>(smem + L::kXOff);
+  float2* s_ml = reinterpret_cast<float2*>(smem + L::kMlOff);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  uint64_t* empty = full + STAGES;
+  uint64_t* qfull = empty + STAGES;
+  uint64_t* qempty = qfull + L::kQBufs;
+  volatile int* s_valid = reinterpret_cast<volatile int*>(smem + L::kMetaOff);
+  volatile int* s_abort = s_valid + STAGES;
+  int* s_warp = reinterpret_cast<int*>(smem + L::kPreOff);
+  int* s_pre = s_warp + 16;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], L::kWarps);
+    }
+    for (int i = 0; i < L::kQBufs; ++i) {
+      mbar_init(&qfull[i], 1);
+      mbar_init(&qempty[i], L::kWarps);
+    }
+    *s_abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&P.kmap);
+    tma_prefetch_desc(&P.vmap);
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // tiles per head before each sequence: each thread a run of sequences, then a scan
+  {
+    const int per = (P.batch + L::kThreads - 1) / L::kThreads;
+    const int s0 = min(tid * per, P.batch), s1 = min(s0 + per, P.batch);
+    int mine = 0;
+    for (int s = s0; s < s1; ++s) {
+      int len;
+      bool bad;
+      const int n = rows_of(P, s, len, bad);
+      if (bad && blockIdx.x == 0) raise_flag(P.err, kDevCapacity);
+      s_pre[s + 1] = n > 0 ? (len + n + kKeys - 1) / kKeys : 0;
+      mine += s_pre[s + 1];
+    }
+    int v = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    if (lane == 31) s_warp[warp] = v;
+    __syncthreads();
+    int before = v - mine;
+    for (int w = 0; w < warp; ++w) before += s_warp[w];
+    for (int s = s0; s < s1; ++s) {
+      before += s_pre[s + 1];
+      s_pre[s + 1] = before;
+    }
+    if (tid == 0) s_pre[0] = 0;
+    __syncthreads();
+  }
+  if (blockIdx.x == 0)
+    for (int s = tid; s <= P.batch; s += L::kThreads) P.prefix[s] = s_pre[s];
+  const int batch = P.batch, nkv = P.nkv, grp = P.nq / nkv;
+  const long long T = static_cast<long long>(nkv) * s_pre[batch];
+  const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), T));
+  const int cta = blockIdx.x;
+  if (cta >= G) return;
+  const long long T0 = range_begin(cta, T, G), T1 = range_begin(cta + 1, T, G);
+  // list position u -> sequence s, KV head g, tile t of the pair's nt
+  auto locate = [&](long long u, int& s, int& g, int& t, int& nt) {
+    int lo = 0, hi = batch - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (static_cast<long long>(nkv) * s_pre[mid] <= u) lo = mid;
+      else hi = mid - 1;
+    }
+    s = lo;
+    nt = s_pre[s + 1] - s_pre[s];
+    const long long rest = u - static_cast<long long>(nkv) * s_pre[s];
+    g = static_cast<int>(rest / nt);
+    t = static_cast<int>(rest - static_cast<long long>(g) * nt);
+  };
+  // Every wait is bounded: past the limit the flag is set, later waits pass at once and the
+  // CTA walks to its end without results.
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (*s_abort) return;
+    if (!mbar_wait(bar, parity, P.wait_ns)) {
+      *s_abort = 1;
+      raise_flag(P.err, kDevTimeout);
+    }
+  };
+
+  if (warp == L::kWarps) {
+    // ------------------------------------------------------------ producer warp
+    // K/V are read once per call: streamed through L2
+    const uint64_t pol = policy_evict_first();
+    int i = 0, seg_no = 0;
+    int q_issued = 0, kv_issued = 0;  // of the segments and tiles walked so far
+    for (long long u = T0; u < T1; ++seg_no) {
+      int s, g, t0, nt;
+      locate(u, s, g, t0, nt);
+      const int seg = static_cast<int>(min(T1 - u, static_cast<long long>(nt - t0)));
+      int len;
+      bool bad;
+      const int n = rows_of(P, s, len, bad);
+      const int qb = seg_no % L::kQBufs;
+      if (seg_no >= L::kQBufs) wait(&qempty[qb], (seg_no / L::kQBufs - 1) & 1);
+      if (__all_sync(0xffffffffu, !*s_abort)) {
+        q_issued = seg_no + 1;
+        if (lane == 0) mbar_arrive_expect_tx(&qfull[qb], n * grp * D * 2);
+        __syncwarp();
+        const uint32_t qdst = smem_u32(smem + L::kQOff + qb * L::kRows * L::kQStride);
+        const uint16_t* q = static_cast<const uint16_t*>(P.q);
+        for (int m = lane; m < n * grp; m += 32) {
+          const int r = m / grp, hh = m - r * grp;
+          bulk_load(qdst + m * L::kQStride,
+                    q + ((static_cast<size_t>(s) * P.rows_per_seq + r) * P.nq + static_cast<size_t>(g) * grp + hh) * D,
+                    D * 2, &qfull[qb]);
+        }
+      }
+      for (int b0 = 0; b0 < seg; b0 += 32) {
+        int page = -1;
+        if (b0 + lane < seg) {
+          page = __ldcg(P.page_table + static_cast<size_t>(s) * P.pages_per_seq + t0 + b0 + lane);
+          if (page < 0 || page >= P.n_pages) {
+            raise_flag(P.err, kDevCapacity);
+            page = -1;
+          }
+        }
+        const int cnt = min(32, seg - b0);
+        for (int k = 0; k < cnt; ++k, ++i) {
+          const int pg = __shfl_sync(0xffffffffu, page, k);
+          const int st = i % STAGES;
+          if (lane == 0) {
+            if (i >= STAGES) wait(&empty[st], (i / STAGES - 1) & 1);
+            if (!*s_abort) {
+              kv_issued = i + 1;
+              s_valid[st] = pg >= 0;
+              if (pg >= 0) {
+                uint8_t* kd = smem + st * L::kStageBytes;
+                mbar_arrive_expect_tx(&full[st], L::kStageBytes);
+#pragma unroll
+                for (int b = 0; b < D / 64; ++b)
+                  tma_load_3d(kd + b * kKeys * 128, &P.kmap, &full[st], b * 64, g, pg * kKeys, pol);
+#pragma unroll
+                for (int b = 0; b < D / 64; ++b)
+                  tma_load_3d(kd + L::kTileBytes + b * kKeys * 128, &P.vmap, &full[st], b * 64, g, pg * kKeys, pol);
+              } else {
+                mbar_arrive(&full[st]);
+              }
+            }
+          }
+          __syncwarp();
+        }
+      }
+      u += seg;
+    }
+    // after an abandoned wait: the copies still in flight land before the CTA leaves
+    if (lane == 0 && *s_abort) {
+      for (int k = max(0, kv_issued - STAGES); k < kv_issued; ++k) mbar_wait(&full[k % STAGES], (k / STAGES) & 1, P.wait_ns);
+      for (int k = max(0, q_issued - L::kQBufs); k < q_issued; ++k)
+        mbar_wait(&qfull[k % L::kQBufs], (k / L::kQBufs) & 1, P.wait_ns);
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- compute warps
+  const int rg = warp / KG, kg = warp % KG;
+  const int r0 = lane >> 2, kq = (lane & 3) * 2;
+  const int mrow0 = rg * 16 * MT;  // first of the warp's rows
+  int i = 0, seg_no = 0;
+  for (long long u = T0; u < T1; ++seg_no) {
+    int s, g, t0, nt;
+    locate(u, s, g, t0, nt);
+    const int seg = static_cast<int>(min(T1 - u, static_cast<long long>(nt - t0)));
+    int len;
+    bool bad;
+    const int n_new = rows_of(P, s, len, bad);
+    const int nk = len + n_new;
+    int lim[MT][2];  // last key each of the thread's rows may see
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) lim[mt][h] = len + (mrow0 + mt * 16 + h * 8 + r0) / grp;
+    const int qb = seg_no % L::kQBufs;
+    wait(&qfull[qb], (seg_no / L::kQBufs) & 1);
+    __syncwarp();
+    const uint32_t qbase = smem_u32(smem + L::kQOff + qb * L::kRows * L::kQStride) +
+                           (mrow0 + (lane & 15)) * L::kQStride + (lane >> 4) * 16;
+    uint32_t qa[MT == 1 ? D / 16 : 1][4];  // one row tile's q stays in registers; two are re-read per slice
+    if (MT == 1) {
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) ldsm4<false>(qbase + kk * 32, qa[kk]);
+    }
+    float o[MT][NT][4], m_[MT][2], l_[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      m_[mt][0] = m_[mt][1] = -INFINITY;
+      l_[mt][0] = l_[mt][1] = 0.f;
+#pragma unroll
+      for (int nt2 = 0; nt2 < NT; ++nt2) o[mt][nt2][0] = o[mt][nt2][1] = o[mt][nt2][2] = o[mt][nt2][3] = 0.f;
+    }
+    for (int j = 0; j < seg; ++j, ++i) {
+      const int st = i % STAGES;
+      wait(&full[st], (i / STAGES) & 1);
+      const uint32_t kb = smem_u32(smem + st * L::kStageBytes), vb = kb + L::kTileBytes;
+      // the whole warp takes the tile or skips it: the steps below are collective
+      if (__all_sync(0xffffffffu, s_valid[st] != 0 && !*s_abort)) {
+#pragma unroll 1
+        for (int sl = kg; sl < kKeys / kSlice; sl += KG) {
+          const int key0 = (t0 + j) * kKeys + sl * kSlice;  // position of the slice's first key
+          if (key0 >= nk) break;
+          const bool edge = key0 + kSlice - 1 > len;  // some row may not see some key
+          float sc[MT][2][4];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) sc[mt][0][c] = sc[mt][1][c] = 0.f;
+          const int mi = lane >> 3;
+          // matrices 0..3: keys 0-7 dims lo, keys 0-7 dims hi, keys 8-15 dims lo, keys 8-15 dims hi
+          const int kkey = sl * kSlice + (mi >> 1) * 8 + (lane & 7);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t b[4];
+            ldsm4<false>(tile_addr(kb, kkey, kk * 16 + (mi & 1) * 8), b);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              if (MT == 1) {
+                mma16816<BF16>(sc[mt][0], qa[kk], b[0], b[1]);
+                mma16816<BF16>(sc[mt][1], qa[kk], b[2], b[3]);
+              } else {
+                uint32_t a[4];
+                ldsm4<false>(qbase + mt * 16 * L::kQStride + kk * 32, a);
+                mma16816<BF16>(sc[mt][0], a, b[0], b[1]);
+                mma16816<BF16>(sc[mt][1], a, b[2], b[3]);
+              }
+            }
+          }
+          // online softmax in log2 units
+          uint32_t pa[MT][4];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int nt2 = 0; nt2 < 2; ++nt2)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                float v = sc[mt][nt2][c] * P.scale_log2;
+                if (edge && key0 + nt2 * 8 + kq + (c & 1) > lim[mt][c >> 1]) v = -INFINITY;
+                sc[mt][nt2][c] = v;
+                mx[c >> 1] = fmaxf(mx[c >> 1], v);
+              }
+            float corr[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+              mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+              const float mnew = fmaxf(m_[mt][h], mx[h]);
+              const float base = mnew == -INFINITY ? 0.f : mnew;
+              corr[h] = ex2(m_[mt][h] - base);
+              m_[mt][h] = mnew;
+              mx[h] = base;
+            }
+            float ls[2] = {0.f, 0.f};
+#pragma unroll
+            for (int nt2 = 0; nt2 < 2; ++nt2)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const float p = ex2(sc[mt][nt2][c] - mx[c >> 1]);
+                sc[mt][nt2][c] = p;
+                ls[c >> 1] += p;
+              }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) l_[mt][h] = l_[mt][h] * corr[h] + ls[h];
+#pragma unroll
+            for (int nt2 = 0; nt2 < NT; ++nt2) {
+              o[mt][nt2][0] *= corr[0];
+              o[mt][nt2][1] *= corr[0];
+              o[mt][nt2][2] *= corr[1];
+              o[mt][nt2][3] *= corr[1];
+            }
+            // the probabilities in the cache's type for the tensor cores, at most half a step
+            // of it from their fp32 values; their sum keeps fp32
+            pa[mt][0] = pack2<BF16>(sc[mt][0][0], sc[mt][0][1]);
+            pa[mt][1] = pack2<BF16>(sc[mt][0][2], sc[mt][0][3]);
+            pa[mt][2] = pack2<BF16>(sc[mt][1][0], sc[mt][1][1]);
+            pa[mt][3] = pack2<BF16>(sc[mt][1][2], sc[mt][1][3]);
+          }
+          // O += P V. Matrices 0..3: keys 0-7 dims lo, keys 8-15 dims lo, keys 0-7 dims hi, keys 8-15 dims hi
+          const int vkey = sl * kSlice + (mi & 1) * 8 + (lane & 7);
+          if (!edge) {
+#pragma unroll
+            for (int dp = 0; dp < D / 16; ++dp) {
+              uint32_t b[4];
+              ldsm4<true>(tile_addr(vb, vkey, dp * 16 + (mi >> 1) * 8), b);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                mma16816<BF16>(o[mt][2 * dp], pa[mt], b[0], b[1]);
+                mma16816<BF16>(o[mt][2 * dp + 1], pa[mt], b[2], b[3]);
+              }
+            }
+          } else {
+            // What lies behind the last key may be anything (0 * NaN is NaN): cleared. A key
+            // that is in the cache but hidden from some row may be infinite or NaN: then the
+            // slice's products are taken one key at a time, for the rows that see it.
+            uint32_t keep[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int key = key0 + h * 8 + kq;
+              keep[h] = (key < nk ? 0xffffu : 0u) | (key + 1 < nk ? 0xffff0000u : 0u);
+            }
+            bool odd = false;
+            if (n_new > 1) {
+#pragma unroll
+              for (int dp = 0; dp < D / 16; ++dp) {
+                uint32_t b[4];
+                ldsm4<true>(tile_addr(vb, vkey, dp * 16 + (mi >> 1) * 8), b);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) odd |= non_finite2<BF16>(b[x] & keep[x & 1]);
+              }
+              odd = __any_sync(0xffffffffu, odd);
+            }
+            if (!odd) {
+#pragma unroll
+              for (int dp = 0; dp < D / 16; ++dp) {
+                uint32_t b[4];
+                ldsm4<true>(tile_addr(vb, vkey, dp * 16 + (mi >> 1) * 8), b);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) b[x] &= keep[x & 1];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                  mma16816<BF16>(o[mt][2 * dp], pa[mt], b[0], b[1]);
+                  mma16816<BF16>(o[mt][2 * dp + 1], pa[mt], b[2], b[3]);
+                }
+              }
+            } else {
+#pragma unroll
+              for (int x = 0; x < kSlice; ++x) {
+                const int key = key0 + x;
+                if (key < nk) {
+#pragma unroll
+                  for (int mt = 0; mt < MT; ++mt) {
+                    const int from = (lane & ~3) + ((x & 7) >> 1);
+                    const float pr0 = __shfl_sync(0xffffffffu, sc[mt][x >> 3][x & 1], from);
+                    const float pr1 = __shfl_sync(0xffffffffu, sc[mt][x >> 3][2 + (x & 1)], from);
+#pragma unroll
+                    for (int nt2 = 0; nt2 < NT; ++nt2) {
+                      uint32_t raw;
+                      asm volatile("ld.shared.b32 %0, [%1];"
+                                   : "=r"(raw)
+                                   : "r"(tile_addr(vb, sl * kSlice + x, nt2 * 8 + kq))
+                                   : "memory");
+                      const float2 v = unpack2<BF16>(raw);
+                      if (key <= lim[mt][0]) {
+                        o[mt][nt2][0] += pr0 * v.x;
+                        o[mt][nt2][1] += pr0 * v.y;
+                      }
+                      if (key <= lim[mt][1]) {
+                        o[mt][nt2][2] += pr1 * v.x;
+                        o[mt][nt2][3] += pr1 * v.y;
+                      }
+                    }
+                  }
+                }
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&qempty[qb]);
+    // row sums over the four lanes of a row
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        l_[mt][h] += __shfl_xor_sync(0xffffffffu, l_[mt][h], 1);
+        l_[mt][h] += __shfl_xor_sync(0xffffffffu, l_[mt][h], 2);
+      }
+    // ---- the key groups' states into one: o = sum_k 2^(m_k - M) o_k, l alike
+    // (max, sum) of every row and group first, then the outputs, in fragment order
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if ((lane & 3) == 0) s_ml[kg * L::kRows + mrow0 + mt * 16 + h * 8 + r0] = make_float2(m_[mt][h], l_[mt][h]);
+    if (L::kAllAtOnce) {
+#pragma unroll
+      for (int nt2 = 0; nt2 < NT; ++nt2)
+        s_x[(kg * NT + nt2) * 32 + lane] = make_float4(o[0][nt2][0], o[0][nt2][1], o[0][nt2][2], o[0][nt2][3]);
+    }
+    named_bar_sync(1, 32 * L::kWarps);
+    float M[MT][2], den[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = mrow0 + mt * 16 + h * 8 + r0;
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < KG; ++k) top = fmaxf(top, s_ml[k * L::kRows + row].x);
+#pragma unroll
+        for (int k = 0; k < KG; ++k) {
+          const float2 ml = s_ml[k * L::kRows + row];
+          sum += ml.x == -INFINITY ? 0.f : ml.y * ex2(ml.x - top);
+        }
+        M[mt][h] = top;
+        den[mt][h] = sum;
+      }
+    const bool whole = t0 == 0 && seg == nt;
+    // finished rows to the output, a cut pair's to this CTA's slot
+    float* slot = P.part + (2 * static_cast<size_t>(cta) + (seg_no == 0 ? 0 : 1)) * static_cast<size_t>(L::kRows) * (D + 2);
+    auto put = [&](int mt, int nt2, const float (&v)[4]) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = mrow0 + mt * 16 + h * 8 + r0;
+        if (row >= n_new * grp) continue;
+        if (whole) {
+          const float inv = den[mt][h] > 0.f ? 1.f / den[mt][h] : (den[mt][h] == 0.f ? 0.f : den[mt][h]);
+          const int r = row / grp, hh = row - r * grp;
+          uint16_t* dst = static_cast<uint16_t*>(P.out) +
+                          ((static_cast<size_t>(s) * P.rows_per_seq + r) * P.nq + static_cast<size_t>(g) * grp + hh) * D;
+          *reinterpret_cast<uint32_t*>(dst + nt2 * 8 + kq) = pack2<BF16>(v[2 * h] * inv, v[2 * h + 1] * inv);
+        } else {
+          __stcg(reinterpret_cast<float2*>(slot + static_cast<size_t>(row) * D + nt2 * 8 + kq),
+                 make_float2(v[2 * h], v[2 * h + 1]));
+        }
+      }
+    };
+    auto put_ml = [&](int mt) {
+      if (!whole && (lane & 3) == 0)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          __stcg(reinterpret_cast<float2*>(slot + static_cast<size_t>(L::kRows) * D) + mrow0 + mt * 16 + h * 8 + r0,
+                 make_float2(M[mt][h], den[mt][h]));
+    };
+    if (L::kAllAtOnce) {
+      // each key group finishes its share of the columns
+      float w[KG][2];
+#pragma unroll
+      for (int k = 0; k < KG; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float mk = s_ml[k * L::kRows + h * 8 + r0].x;
+          w[k][h] = mk == -INFINITY ? 0.f : ex2(mk - M[0][h]);
+        }
+#pragma unroll
+      for (int n4 = 0; n4 < NT / KG; ++n4) {
+        const int nt2 = kg * (NT / KG) + n4;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < KG; ++k) {
+          const float4 x = s_x[(k * NT + nt2) * 32 + lane];
+          v[0] += w[k][0] * x.x;
+          v[1] += w[k][0] * x.y;
+          v[2] += w[k][1] * x.z;
+          v[3] += w[k][1] * x.w;
+        }
+        put(0, nt2, v);
+      }
+      if (kg == 0) put_ml(0);
+    } else {
+      // one group after another through one buffer per row group, into group 0
+      float4* xb = s_x + static_cast<size_t>(rg) * MT * NT * 32;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        float w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) w[h] = m_[mt][h] == -INFINITY ? 0.f : ex2(m_[mt][h] - M[mt][h]);
+#pragma unroll
+        for (int nt2 = 0; nt2 < NT; ++nt2) {
+          o[mt][nt2][0] *= w[0];
+          o[mt][nt2][1] *= w[0];
+          o[mt][nt2][2] *= w[1];
+          o[mt][nt2][3] *= w[1];
+        }
+      }
+#pragma unroll
+      for (int k = 1; k < KG; ++k) {
+        if (kg == k) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int nt2 = 0; nt2 < NT; ++nt2)
+              xb[(mt * NT + nt2) * 32 + lane] = make_float4(o[mt][nt2][0], o[mt][nt2][1], o[mt][nt2][2], o[mt][nt2][3]);
+        }
+        named_bar_sync(1, 32 * L::kWarps);
+        if (kg == 0) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int nt2 = 0; nt2 < NT; ++nt2) {
+              const float4 x = xb[(mt * NT + nt2) * 32 + lane];
+              o[mt][nt2][0] += x.x;
+              o[mt][nt2][1] += x.y;
+              o[mt][nt2][2] += x.z;
+              o[mt][nt2][3] += x.w;
+            }
+        }
+        named_bar_sync(1, 32 * L::kWarps);
+      }
+      if (kg == 0) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+          for (int nt2 = 0; nt2 < NT; ++nt2) put(mt, nt2, o[mt][nt2]);
+          put_ml(mt);
+        }
+      }
+    }
+    named_bar_sync(1, 32 * L::kWarps);  // the exchange buffers are the next segment's
+    u += seg;
+  }
+}
+
+// ---------------------------------------------------------------- the join of cut pairs
+// One warp per (pair, row): weights 2^(m_c - M) / sum_c 2^(m_c - M) l_c over the CTAs whose
+// ranges the pair lies in, in CTA order.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) paged_attn_join_kernel(const __grid_constant__ PagedAttnParams P, int n_ctas, int slot_rows) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int pair = blockIdx.x, s = pair / P.nkv, g = pair - s * P.nkv;
+  const int lane = threadIdx.x & 31;
+  const int grp = P.nq / P.nkv;
+  const int row = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int p0 = __ldcg(P.prefix + s), p1 = __ldcg(P.prefix + s + 1);
+  const long long T = static_cast<long long>(P.nkv) * __ldcg(P.prefix + P.batch);
+  const int nt = p1 - p0;
+  if (nt == 0 || row >= __ldcg(P.n_new + s) * grp) return;
+  const int G = static_cast<int>(min(static_cast<long long>(n_ctas), T));
+  const long long base = static_cast<long long>(P.nkv) * p0 + static_cast<long long>(g) * nt;
+  const int c0 = cta_of(base, T, G), c1 = cta_of(base + nt - 1, T, G);
+  if (c0 == c1) return;
+  const size_t slot_floats = static_cast<size_t>(slot_rows) * (D + 2);
+  // a CTA whose range starts inside the pair or with it has it as its first segment
+  auto slot_of = [&](int c) { return P.part + (2 * static_cast<size_t>(c) + (range_begin(c, T, G) >= base ? 0 : 1)) * slot_floats; };
+  float M = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32)
+    M = fmaxf(M, __ldcg(reinterpret_cast<const float2*>(slot_of(c) + static_cast<size_t>(slot_rows) * D) + row).x);
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  constexpr int E = D / 32;  // columns of a lane
+  float acc[E] = {};
+  float den = 0.f;
+  for (int b = c0; b <= c1; b += 32) {
+    float w = 0.f, wl = 0.f;
+    if (b + lane <= c1) {
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(slot_of(b + lane) + static_cast<size_t>(slot_rows) * D) + row);
+      w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+      wl = w * ml.y;
+    }
+    const int cnt = min(32, c1 - b + 1);
+#pragma unroll 4
+    for (int k = 0; k < cnt; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      den += __shfl_sync(0xffffffffu, wl, k);
+      const float* src = slot_of(b + k) + static_cast<size_t>(row) * D + lane * E;
+      float v[E];
+      if (E == 4) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+        v[0] = x.x, v[1] = x.y, v[E - 2] = x.z, v[E - 1] = x.w;
+      } else {
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+        v[0] = x.x, v[1] = x.y;
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += wk * v[e];
+    }
+  }
+  const float inv = den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den);
+  const int r = row / grp, hh = row - r * grp;
+  uint16_t* dst = static_cast<uint16_t*>(P.out) +
+                  ((static_cast<size_t>(s) * P.rows_per_seq + r) * P.nq + static_cast<size_t>(g) * grp + hh) * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t*>(dst + e) = pack2<BF16>(acc[e] * inv, acc[e + 1] * inv);
+}
+
+template <int D>
+struct Stages {
+  static constexpr int few = D == 128 ? 5 : 10, mid = D == 128 ? 4 : 8, many = D == 128 ? 5 : 10;
+};
+
+// Variants by rows of a problem: up to 16 and 32 as one row group and four key groups, 64 as
+// four row groups of 16 and two key groups, 128 as eight row groups.
+template <typename F>
+int with_variant(int rows, F&& f) {
+  if (rows <= 16) return f(std::integral_constant<int, 0>());
+  if (rows <= 32) return f(std::integral_constant<int, 1>());
+  if (rows <= 64) return f(std::integral_constant<int, 2>());
+  return f(std::integral_constant<int, 3>());
+}
+
+template <int D, int V>
+struct Variant;
+template <int D>
+struct Variant<D, 0> {
+  static constexpr int MT = 1, RG = 1, KG = 4, ST = Stages<D>::few;
+};
+template <int D>
+struct Variant<D, 1> {
+  static constexpr int MT = 2, RG = 1, KG = 4, ST = Stages<D>::few;
+};
+template <int D>
+struct Variant<D, 2> {
+  static constexpr int MT = 1, RG = 4, KG = 2, ST = Stages<D>::mid;
+};
+template <int D>
+struct Variant<D, 3> {
+  static constexpr int MT = 1, RG = 8, KG = 1, ST = Stages<D>::many;
+};
+
+template <int D, bool BF16, int V>
+int set_attr() {
+  using W = Variant<D, V>;
+  using L = Layout<D, W::MT, W::RG, W::KG, W::ST>;
+  static_assert(L::smem(kCacheMaxBatch) <= 232448, "shared memory of a CTA");
+  return static_cast<int>(cudaFuncSetAttribute(paged_attn_kernel<D, BF16, W::MT, W::RG, W::KG, W::ST>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, L::smem(kCacheMaxBatch)));
+}
+
+template <int D, bool BF16, int V>
+int launch(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
+  using W = Variant<D, V>;
+  using L = Layout<D, W::MT, W::RG, W::KG, W::ST>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(n_ctas);
+  cfg.blockDim = dim3(L::kThreads);
+  cfg.dynamicSmemBytes = L::smem(p.batch);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<D, BF16, W::MT, W::RG, W::KG, W::ST>, p);
+  if (e != cudaSuccess) return static_cast<int>(e);
+  cfg.gridDim = dim3(p.batch * p.nkv, (p.rows + 7) / 8);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<D, BF16>, p, n_ctas, static_cast<int>(L::kRows)));
+}
+
+}  // namespace
+
+int paged_attn_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+
+int paged_attn_set_attributes() {
+  const int e[] = {set_attr<64, false, 0>(),  set_attr<64, false, 1>(),  set_attr<64, false, 2>(),  set_attr<64, false, 3>(),
+                   set_attr<64, true, 0>(),   set_attr<64, true, 1>(),   set_attr<64, true, 2>(),   set_attr<64, true, 3>(),
+                   set_attr<128, false, 0>(), set_attr<128, false, 1>(), set_attr<128, false, 2>(), set_attr<128, false, 3>(),
+                   set_attr<128, true, 0>(),  set_attr<128, true, 1>(),  set_attr<128, true, 2>(),  set_attr<128, true, 3>()};
+  for (int x : e)
+    if (x != 0) return x;
+  return 0;
+}
+
+int launch_paged_attn(const PagedAttnParams& p, bool bf16, int n_ctas, cudaStream_t stream) {
+  if (p.batch < 1 || p.batch > kCacheMaxBatch || n_ctas < 1 || n_ctas > kPagedMaxCtas || p.rows > 128)
+    return static_cast<int>(cudaErrorInvalidValue);
+  return with_variant(p.rows, [&](auto v) {
+    constexpr int V = decltype(v)::value;
+    if (p.d == 128) return bf16 ? launch<128, true, V>(p, n_ctas, stream) : launch<128, false, V>(p, n_ctas, stream);
+    return bf16 ? launch<64, true, V>(p, n_ctas, stream) : launch<64, false, V>(p, n_ctas, stream);
+  });
+}
+
+}  // namespace dfl

@@ -233,6 +233,37 @@ int dflash_verify_greedy_hidden(dflash_handle* h, const void* target_hidden, con
                                 const void* target_lm_head, const int32_t* drafted, int32_t batch, int32_t block,
                                 int32_t* accept_len, int32_t* committed, void* stream);
 
+/* ---- log probabilities of given tokens --------------------------------------------
+ * For each row z of logits, with p = softmax(z / temperature):
+ *   logprob  = log p(token)
+ *   entropy  = -sum p log p (nats)
+ *   top_ids, top_logprobs: the n_top most likely tokens, most likely first (ties: lowest
+ *              index first, NaN before everything else) and their log probabilities
+ * in one pass over the logits. The step's use: the committed tokens of a verified block
+ * (row i of target_logits with committed[i]; the -1 behind the accepted prefix skips the
+ * rows it stands for).
+ *   logits        [rows][vocab of the config] of `dtype`, row_stride elements from one row
+ *                 to the next (>= vocab; the start aligned to its element, nothing more);
+ *                 -inf where a token is masked
+ *   dtype         DFLASH_F32, DFLASH_F16 or DFLASH_BF16
+ *   tokens        int32 [rows], or NULL (then logprob is NULL too). -1: a row without a
+ *                 token, which is not read: logprob and entropy 0, top_ids -1, top_logprobs
+ *                 0. Other values outside [0, vocab) do the same and set DFLASH_DEV_TOKEN.
+ *   rows          >= 1; any number (not bound by max_batch and max_block)
+ *   temperature   > 0
+ *   n_top         0..32, at most vocab
+ *   logprob, entropy   fp32 [rows] out
+ *   top_ids            int32 [rows][n_top] out, or NULL with n_top 0
+ *   top_logprobs       fp32 [rows][n_top] out, or NULL with n_top 0
+ * Sums run in fp32. A row that is -inf everywhere has logprob and top_logprobs -inf and
+ * entropy 0; a row with a NaN or +inf has NaN there. */
+#define DFLASH_F32 0
+#define DFLASH_F16 1
+#define DFLASH_BF16 2
+int dflash_logprobs(dflash_handle* h, const void* logits, int32_t dtype, int64_t row_stride,
+                    const int32_t* tokens, int32_t rows, float temperature, int32_t n_top, float* logprob,
+                    float* entropy, int32_t* top_ids, float* top_logprobs, void* stream);
+
 /* Weight-streaming bf16 GEMM of the draft path, exposed for testing the engine alone:
  * Y[r][m] = sum_k X[r][k] * W[m][k] in fp32 accumulation.
  *   W  bf16 [n_out][K] (K multiple of 64), X bf16 [rows][K] (any rows; passes of 256),
@@ -362,6 +393,133 @@ const char* dflash_status_string(int status);
 int dflash_verify_greedy_noalloc(const float* target_logits, const int32_t* drafted, int32_t batch,
                                  int32_t block, int32_t vocab, int32_t* accept_len, int32_t* committed,
                                  int32_t* last_token, void* stream);
+
+/* ---- page pool: cache pages handed out on the GPU ----------------------------------
+ * Keeps the page table of a paged cache (dflash_bind_state_paged, dflash_cache_bind) from
+ * the sequences' lengths alone: a list of free pages, the pages each sequence holds, and
+ * the table. Pages hold 64 positions. All arrays are the caller's, on the device; the calls
+ * need no host synchronisation and can be captured. Calls on one pool are ordered on one
+ * stream (two at once would hand out the same pages). Pages are not shared.
+ *   page_table  int32 [max_batch][pages_per_seq]; -1 behind the pages a sequence holds
+ *   held        int32 [max_batch] pages held by each sequence
+ *   free_list   int32 [n_pages] the free pages are its first state[0] entries, the next
+ *               one handed out last
+ *   state       int32 [4]: free pages; a counter of the kernels (0 between calls); device
+ *               error flags (DFLASH_DEV_*: read and cleared by the caller); unused */
+typedef struct dflash_page_pool {
+  int32_t n_pages;       /* >= 1, n_pages * 64 < 2^31 */
+  int32_t pages_per_seq; /* >= 1 */
+  int32_t max_batch;     /* 1..4096 */
+  int32_t reserved;      /* 0 */
+  int32_t* page_table;
+  int32_t* held;
+  int32_t* free_list;
+  int32_t* state;
+} dflash_page_pool;
+
+/* All pages free (page 0 is handed out first), no sequence holds any. */
+int dflash_pages_init(const dflash_page_pool* p, void* stream);
+
+/* Room for n_new[s] positions behind the len[s] that sequence s < batch has: takes pages
+ * until ceil((len + n_new) / 64) are held and writes the new positions' cache rows.
+ *   len, n_new    int32 [batch] on the device; 0 <= n_new[s] <= rows_per_seq
+ *   rows_per_seq  rows per sequence in `slots` (>= 1)
+ *   slots         int32 [batch * rows_per_seq] out, or NULL: the cache row of position
+ *                 len[s] + r at s * rows_per_seq + r (page * 64 + place in the page); -1 for
+ *                 r >= n_new[s]
+ * Sequences are served in order while the pages last: one whose pages, with those of all
+ * sequences before it, exceed the free ones gets none and -1 in all its slots, as does one
+ * with lengths out of range or past pages_per_seq; both set DFLASH_DEV_CAPACITY. A
+ * sequence that needs no new page is always served. */
+int dflash_pages_reserve(const dflash_page_pool* p, const int32_t* len, const int32_t* n_new, int32_t batch,
+                         int32_t rows_per_seq, int32_t* slots, void* stream);
+
+/* The pages of sequence s < batch past its first len[s] positions (0: all of them) go back
+ * to the free list: rejected drafts, finished sequences. Releasing what the last reserve
+ * took leaves list and table as they were. A negative len[s] sets DFLASH_DEV_CAPACITY and
+ * releases nothing. */
+int dflash_pages_release(const dflash_page_pool* p, const int32_t* len, int32_t batch, void* stream);
+
+/* ---- the target's paged cache ------------------------------------------------------
+ * K/V of a causal target model whose attention runs in this library: rotary positions
+ * and append of a step's new rows, and their attention. One handle serves all layers.
+ * A step: dflash_pages_reserve, then for every layer dflash_cache_append and
+ * dflash_cache_attend, verification, len[s] += the accepted rows (by the caller), and
+ * dflash_pages_release. Rows that verification rejects need no undoing: the next step
+ * writes over them. */
+typedef struct dflash_cache_config {
+  int32_t n_layers;         /* 1..1024 */
+  int32_t n_heads;          /* nq: query heads */
+  int32_t n_kv_heads;       /* nkv; nq % nkv == 0, (nq / nkv) * max_block <= 128 */
+  int32_t head_dim;         /* d: 64 or 128 */
+  int32_t dtype;            /* DFLASH_F16 or DFLASH_BF16: the pools, and q of the attention */
+  int32_t n_pages;          /* pages of 64 positions per layer, n_pages * 64 < 2^31 */
+  int32_t pages_per_seq;    /* columns of the page table */
+  int32_t max_batch;        /* 1..1024 */
+  int32_t max_block;        /* new rows per sequence that one attention call takes, 1..16 */
+  int32_t rope_dim;         /* dims of each head that are rotated: 0..d, a multiple of 16 */
+  int32_t rope_interleaved; /* pairs (2j, 2j + 1) instead of (j, j + rope_dim / 2) */
+  int32_t rope_positions;   /* rows of the rotary tables */
+  float scale;              /* of the scores; 0: 1 / sqrt(d) */
+} dflash_cache_config;
+
+typedef struct dflash_cache dflash_cache;
+
+/* Validate a shape without touching the GPU. Returns DFLASH_OK or DFLASH_E_CONFIG. */
+int dflash_cache_config_check(const dflash_cache_config* cfg);
+
+/* Workspace bytes dflash_cache_bind needs (0 if the shape is invalid). */
+size_t dflash_cache_workspace_size(const dflash_cache_config* cfg);
+
+int dflash_cache_create(const dflash_cache_config* cfg, dflash_cache** out);
+int dflash_cache_destroy(dflash_cache* c);
+
+/* Bind caller-owned state. Pools and rotary tables 16-byte aligned, the workspace 256-byte.
+ *   k_pool, v_pool      [L][n_pages * 64][nkv][d] of the config's dtype
+ *   page_table          int32 [max_batch][pages_per_seq], read at every call
+ *   len                 int32 [max_batch] positions of each sequence before the new rows,
+ *                       read at every call
+ *   rope_cos, rope_sin  fp32 [rope_positions][rope_dim / 2] (NULL with rope_dim 0): cos and
+ *                       sin of every position's angles, with any frequency scaling or
+ *                       attention factor of the model in them
+ *   workspace           dflash_cache_workspace_size(cfg) bytes; cleared here (synchronous).
+ *                       Calls on one handle are ordered on one stream. */
+int dflash_cache_bind(dflash_cache* c, void* k_pool, void* v_pool, const int32_t* page_table, int32_t* len,
+                      const float* rope_cos, const float* rope_sin, void* workspace, size_t workspace_bytes);
+
+/* Rotary positions on q and k, and k and v into the cache, for one layer's new rows (any
+ * number: a token, a block, a prompt). Row s * rows_per_seq + r is position len[s] + r.
+ * u = x cos - y sin, v = y cos + x sin for each pair (x, y) of the head's first rope_dim
+ * dims; fp32 arithmetic, rounded once.
+ *   q, k, v     [batch * rows_per_seq] rows of nq * d (q) and nkv * d (k, v) values of
+ *               x_dtype (DFLASH_F16 or DFLASH_BF16), *_stride elements apart (multiples of 8);
+ *               16-byte aligned. q and q_out may both be NULL.
+ *   slots       int32 [batch * rows_per_seq] cache rows as from dflash_pages_reserve. A row
+ *               with slot -1 is not read and leaves everything as it was; other values
+ *               outside the pool, and positions past the rotary tables, do the same and
+ *               set DFLASH_DEV_CAPACITY. Slots are distinct.
+ *   q_out       [batch * rows_per_seq][nq][d] of the cache's dtype out; not overlapping q */
+int dflash_cache_append(dflash_cache* c, int32_t layer, const void* q, const void* k, const void* v,
+                        int32_t x_dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                        const int32_t* slots, int32_t batch, int32_t rows_per_seq, void* q_out, void* stream);
+
+/* Causal attention of the new rows over the cache, one layer:
+ *   out[s][r][h] = sum_j softmax_j(scale * q[s][r][h] . K_j) V_j,  j = 0 .. len[s] + r
+ * for r < n_new[s] (head h reads KV head h / (nq / nkv)); one row a sequence is ordinary
+ * decoding, a block of rows is verification.
+ *   q        [batch * rows_per_seq][nq][d] of the cache's dtype
+ *   n_new    int32 [batch] on the device, 0 <= n_new[s] <= rows_per_seq <= max_block
+ *   out      [batch * rows_per_seq][nq][d] of the cache's dtype. Rows past n_new[s] are left
+ *            as they were.
+ * The positions of the new rows are in the cache already. What lies in the cache behind
+ * them is never used, whatever its value. A sequence whose lengths are out of range or pass
+ * pages_per_seq * 64 is left out, and a page id outside [0, n_pages) drops that page's
+ * positions (a row with none left is 0); both set DFLASH_DEV_CAPACITY. */
+int dflash_cache_attend(dflash_cache* c, int32_t layer, const void* q, const int32_t* n_new, int32_t batch,
+                        int32_t rows_per_seq, void* out, void* stream);
+
+/* As dflash_read_device_error, for a cache handle. */
+int dflash_cache_read_error(dflash_cache* c, int32_t* flags, int32_t clear, void* stream);
 
 /* ---- synthetic target (benchmark harness, not part of DFlash) ---------------------
  * Stand-in for a target model inside a timed, graph-captured step: planting raises the
