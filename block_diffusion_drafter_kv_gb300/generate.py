@@ -27,7 +27,7 @@ The target is any object with three methods:
 from __future__ import annotations
 
 from dataclasses import dataclass, field
-from typing import List, Optional, Sequence
+from typing import List, Optional, Sequence, Tuple
 
 import torch
 
@@ -36,6 +36,10 @@ import torch
 class GenerationStats:
     steps: int = 0                       # draft-and-verify steps
     accept_lens: List[int] = field(default_factory=list)
+    # with logprobs=n, one entry per new token, under the target's distribution at temperature 1:
+    token_logprobs: List[float] = field(default_factory=list)
+    token_entropies: List[float] = field(default_factory=list)
+    top_logprobs: List[List[Tuple[int, float]]] = field(default_factory=list)  # n (token, log probability), best first
 
     @property
     def mean_tau(self) -> float:
@@ -44,12 +48,14 @@ class GenerationStats:
 
 def spec_generate(drafter, target, input_ids, max_new_tokens: int, temperature: float = 0.0,
                   stop_token_ids: Sequence[int] = (), block: Optional[int] = None,
-                  generator: Optional[torch.Generator] = None, stream=None):
+                  generator: Optional[torch.Generator] = None, stream=None, logprobs: Optional[int] = None):
     """Generate up to max_new_tokens tokens after input_ids (a 1-D token sequence) with the
     drafter (a binding.Drafter bound with max_batch >= 1; sequence slot 0 is used and reset)
     and the caller's target. Generation stops after the first token in stop_token_ids.
     temperature > 0 verifies by speculative sampling with uniforms drawn from `generator`.
-    Returns (new tokens as a list of ints, GenerationStats)."""
+    logprobs=n (0..32) also collects every new token's log probability, the entropy of its
+    distribution and the n most likely tokens at its place in the stats. A drafter bound with
+    `pages` gets its pages as the sequence grows. Returns (new tokens as a list of ints, GenerationStats)."""
     dev = drafter.last_token.device
     B = block or drafter.cfg.max_block
     V = drafter.shape.vocab
@@ -66,27 +72,50 @@ def spec_generate(drafter, target, input_ids, max_new_tokens: int, temperature: 
             return int(min(int(torch.searchsorted(torch.cumsum(p, 0), u, right=True)), V - 1))
         return int(torch.argmax(logits_row))
 
-    def emit(tokens) -> bool:
-        for t in tokens:
+    def score(rows, tokens):
+        """(log probability, entropy, alternatives) of each token >= 0 from its row of logits."""
+        n = rows.shape[0]
+        lp, ent, tv = (torch.empty(k, dtype=torch.float32, device=dev) for k in (n, n, n * logprobs))
+        ti = torch.empty(n * logprobs, dtype=torch.int32, device=dev)
+        drafter.logprobs(rows, tokens, lp, ent, ti if logprobs else None, tv if logprobs else None, stream=stream)
+        alts = [list(zip(i, v)) for i, v in zip(ti.reshape(n, logprobs).tolist(), tv.reshape(n, logprobs).tolist())]
+        return list(zip(lp.tolist(), ent.tolist(), alts))
+
+    def emit(tokens, scores) -> bool:
+        for k, t in enumerate(tokens):
             out.append(int(t))
+            if scores is not None:
+                for to, x in zip((stats.token_logprobs, stats.token_entropies, stats.top_logprobs), scores[k]):
+                    to.append(x)
             if int(t) in stops or len(out) >= max_new_tokens:
                 return True
         return False
 
+    pages = getattr(drafter, "pages", None)
+    room = None if pages is None else torch.full((1,), B, dtype=torch.int32, device=dev)
     ids = torch.as_tensor(input_ids, dtype=torch.int64, device=dev).reshape(-1)
     tapped, logits = target.prefill(ids)
     P = ids.numel()
     drafter.len.zero_()
-    drafter.inject(tapped.contiguous(), P, torch.tensor([P], dtype=torch.int32, device=dev), 1, stream)
+    n_prompt = torch.tensor([P], dtype=torch.int32, device=dev)
+    if pages is not None:
+        pages.release(drafter.len, 1, stream)   # what an earlier sequence in the slot still holds
+        pages.reserve(drafter.len, n_prompt, P, 1, stream=stream)
+    drafter.inject(tapped.contiguous(), P, n_prompt, 1, stream)
     first = pick(logits.reshape(-1))
     drafter.last_token[0] = first
-    if emit([first]):
+    scores = None
+    if logprobs is not None:
+        scores = score(logits.to(torch.float32).reshape(1, V), drafter.last_token[:1])
+    if emit([first], scores):
         return out, stats
     drafted = torch.zeros(1, max(B - 1, 1), dtype=torch.int32, device=dev)
     acc = torch.zeros(1, dtype=torch.int32, device=dev)
     com = torch.zeros(1, B, dtype=torch.int32, device=dev)
     n_cached = P
     while True:
+        if pages is not None:
+            pages.reserve(drafter.len, room, B, 1, stream=stream)
         drafter.draft(1, B, drafted, stream=stream)
         block_tokens = torch.cat([drafter.last_token[:1].to(torch.int64), drafted[0, : B - 1].to(torch.int64)])
         tapped, logits = target.forward_block(block_tokens)
@@ -104,5 +133,7 @@ def spec_generate(drafter, target, input_ids, max_new_tokens: int, temperature: 
         rows[:, :tau] = tapped[:, :tau]
         drafter.inject(rows, B, acc, 1, stream)
         n_cached += tau
-        if emit(com[0, :tau].tolist()):
+        if logprobs is not None:
+            scores = score(logits[0], com[0])
+        if emit(com[0, :tau].tolist(), scores):
             return out, stats
