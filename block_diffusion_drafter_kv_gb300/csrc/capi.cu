@@ -88,8 +88,8 @@ WsLayout layout_of(const dflash_config& c) {
   // flat attention slots: a head's 16 slots x its query heads, or two KV heads' (tensor-core kernel)
   L.attn_part = take(static_cast<size_t>(2) * kMaxCtas * 2 * (nq / c.n_kv_heads) * 16 * (d + 4) * 4);
   L.attn_cnt = take(static_cast<size_t>(c.max_batch) * c.n_kv_heads * 4);
-  L.lp_part = take(static_cast<size_t>(kLpSlots) * kLpSlotWords * 4);
-  L.lp_cnt = take(static_cast<size_t>(kLpSlots) * 4);
+  L.lp_part = take(static_cast<size_t>(2) * kLpMaxCtas * kLpSlotWords * 4);
+  L.lp_cnt = take(static_cast<size_t>(kLpMaxCtas) * 4);
   L.total = off;
   return L;
 }
@@ -326,7 +326,8 @@ int dflash_create(const dflash_config* cfg, const dflash_weights* w, dflash_hand
   h->inject_pass_rows = 16 * nb_for_rows(std::min(cfg->max_batch * cfg->max_block, kMaxPassRows));
   if (cudaGetDevice(&h->device) != cudaSuccess ||
       cudaDeviceGetAttribute(&h->n_sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess ||
-      gemv_set_attributes() != 0 || attn_set_attributes() != 0 || attn_tc_set_attributes() != 0) {
+      gemv_set_attributes() != 0 || attn_set_attributes() != 0 || attn_tc_set_attributes() != 0 ||
+      logprob_set_attributes() != 0) {
     delete h;
     return DFLASH_E_CUDA;
   }
@@ -950,7 +951,6 @@ int dflash_logprobs(dflash_handle* h, const void* logits, int32_t dtype, int64_t
   P.V = V;
   P.rows = rows;
   P.n_top = n_top;
-  P.chunks = logprob_chunks(rows, V, elem, h->n_sms);
   P.logprob = logprob;
   P.entropy = entropy;
   P.top_ids = top_ids;
@@ -958,7 +958,8 @@ int dflash_logprobs(dflash_handle* h, const void* logits, int32_t dtype, int64_t
   P.part = h->at<float>(h->L.lp_part);
   P.row_cnt = h->at<int>(h->L.lp_cnt);
   P.err = h->at<int>(h->L.err);
-  if (launch_logprobs(P, dtype, st) != 0) return DFLASH_E_CUDA;
+  P.wait_ns = h->wait_ns;
+  if (launch_logprobs(P, dtype, h->n_sms, st) != 0) return DFLASH_E_CUDA;
   note_launch(h, st);
   return DFLASH_OK;
 }
@@ -1018,7 +1019,7 @@ int dflash_read_device_error(dflash_handle* h, int32_t* flags, int32_t clear, vo
                                {L.seq_cnt, static_cast<size_t>(h->cfg.max_batch) * 4},
                                {L.chain_bar, static_cast<size_t>(kChainSlots) * (kMaxPhases + 4) * 4},
                                {L.attn_cnt, static_cast<size_t>(h->cfg.max_batch) * h->cfg.n_kv_heads * 4},
-                               {L.lp_cnt, static_cast<size_t>(kLpSlots) * 4}};
+                               {L.lp_cnt, static_cast<size_t>(kLpMaxCtas) * 4}};
     for (const auto& sp : spans)
       if (cudaMemsetAsync(h->ws + sp[0], 0, sp[1], st) != cudaSuccess) return DFLASH_E_CUDA;
     if (cudaStreamSynchronize(st) != cudaSuccess) return DFLASH_E_CUDA;

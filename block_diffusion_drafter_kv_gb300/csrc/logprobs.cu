@@ -1,26 +1,38 @@
 // Log probabilities of given tokens, the entropy of their distributions and the most likely
 // alternatives, in one pass over the logits.
 //
-// With c = log2(e) / T, M = max z, d = c (z - M), S = sum 2^d, W = sum 2^d d:
-//   log p(token) = (z_token - M) / T - ln 2 log2 S,  H = ln 2 (log2 S - W / S)
-// (M, S, W) of two parts join by rescaling the smaller max's: W' = 2^e (W + e S), e = c (M - M').
-// The difference z - M is taken before the scaling: a row of nothing but the type's lowest
-// value stays a uniform one.
-// The bound is reading the logits. A row is cut into chunks where there are few rows; the
-// CTA that arrives last at a row joins its parts in chunk order (no waiting, no dependence
-// on timing).
+// With c = log2(e) / T, a base B near c max z, d = c z - B, S = sum 2^d, W = sum 2^d d:
+//   log p(token) = (z_token - max z) / T - ln 2 (log2 S - (c max z - B)),  H = ln 2 (log2 S - W / S)
+// hold for any B. B is c max z rounded, and d one fused multiply-add, so that only 2^d rounds;
+// sums of two bases join by 2^(B - B'): W' = 2^e (W + e S), e = B - B'. Where c max z is past 2^30
+// (masks of the type's lowest value, tiny temperatures) d is c (z - max z), which cannot
+// overflow, and every base involved stands for its exact c max z.
+//
+// Bound: reading the logits, once, at 2 or 4 bytes each.
+// Split. The rows that have a token, in units of 4 KB of logits, form one list that is cut
+// evenly over three persistent CTAs per SM: rows without a token cost nothing, no wave is left
+// half full, few rows are split over all SMs, and a CTA has at most two rows that it shares with
+// others. Those join in CTA order in the CTA that arrives last at the row, which does not depend
+// on who that is; a row inside one range never leaves its CTA. (Chunks of 64 KB taken from a
+// counter, each joined through global memory, took 129 us for 293 rows of 151936 fp32 against 46:
+// fence, counter and parts are microseconds of latency, too many for 1.4 us of copying.)
+// In a CTA a producer warp keeps a ring of 16 KB stages full by bulk copies across rows, and
+// eight consumer warps share each stage.
 //
 // The n_top largest: every warp keeps the best of what it has read as a sorted list of 64-bit
 // keys, one per lane, (order-preserving bits of the logit, ~index): ties go to the lowest
 // index and all keys differ. What keeps this off the streaming path is a threshold that the
 // warps share: each publishes the ceil(n_top / 8)-th largest value it has seen, and the least
-// of the eight bounds the n_top-th largest of the CTA from below. It starts from one sort of
-// the lane maxima of the first batch, so that a few dozen values of a chunk of thousands
+// of the eight bounds the n_top-th largest of the item from below. It starts from one sort of
+// the lane maxima of the first stage, so that a few dozen values of a chunk of thousands
 // reach a list. Values come one at a time by insertion, or many at once (sorted inputs, long
 // runs of equal values) by sorting and merging 32, so that no order of the logits costs
 // more than a small multiple of another.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <algorithm>
+#include <type_traits>
 
 #include "ptx.cuh"
 #include "target.h"
@@ -29,8 +41,15 @@ namespace dfl {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarps = 8;                    // consumer warps
+constexpr int kConsumers = 32 * kWarps;
+constexpr int kThreads = kConsumers + 32;
+constexpr int kUnitWords = kConsumers;       // 16-byte words of a unit: one per consumer thread
+constexpr int kStageUnits = 4;
+constexpr int kStageWords = kStageUnits * kUnitWords;
+constexpr int kStages = 4;
+constexpr int kCtasPerSm = 3;
+constexpr int kListed = 1024;                // rows of a call whose tokens are looked through before the list is cut
 constexpr unsigned kAll = 0xffffffffu;
 using Key = unsigned long long;
 
@@ -38,6 +57,33 @@ DEV float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// NaN if one of them is.
+DEV float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+DEV float warp_max_nan(float x) {
+  float y;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two fp32 operations in one instruction.
+DEV float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(*reinterpret_cast<unsigned long long*>(&d))
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
+        "l"(*reinterpret_cast<unsigned long long*>(&c)));
+  return d;
+}
+DEV float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(*reinterpret_cast<unsigned long long*>(&d))
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+  return d;
 }
 
 // Order-preserving bits of a logit: NaN above all, -0 as +0.
@@ -59,7 +105,8 @@ DEV V exchange(V v, int mask, bool up) {
   const bool lower = (threadIdx.x & mask) == 0;
   return (lower != up) == (v > w) ? v : w;
 }
-// The lanes' values in descending order.
+// The lanes' values in descending order. This and the functions below that are not inlined run a
+// few times per chunk: inlined at each use they made the loop's code miss the instruction cache.
 template <typename V>
 DEV V sort_desc(V v) {
   const int lane = threadIdx.x & 31;
@@ -77,285 +124,646 @@ DEV Key merge_desc(Key a, Key b) {
   for (int step = 16; step >= 1; step >>= 1) v = exchange(v, step, false);
   return v;
 }
+__device__ __noinline__ Key merge_lists(Key a, Key b) { return merge_desc(a, b); }
+// Eight lists in shared memory into one.
+__device__ __noinline__ Key merge_eight(const Key (*lists)[32]) {
+  const int lane = threadIdx.x & 31;
+  Key l[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) l[i] = lists[i][lane];
+#pragma unroll
+  for (int h = 4; h >= 1; h >>= 1)
+#pragma unroll
+    for (int i = 0; i < h; ++i) l[i] = merge_desc(l[i], l[i + h]);
+  return l[0];
+}
+DEV float widen1(float v) { return v; }
+DEV float widen1(__half v) { return __half2float(v); }
+DEV float widen1(__nv_bfloat16 v) { return __bfloat162float(v); }
+// A warp's best values: a sorted list, one key per lane, and keys that wait for it until there
+// are enough of them to sort.
+constexpr int kWaiting = 96;
+__device__ __noinline__ Key sort_into(Key list, const Key* waiting, int count) {  // count <= 32
+  const int lane = threadIdx.x & 31;
+  return merge_desc(list, sort_desc(lane < count ? waiting[lane] : 0));
+}
+// Candidates of a warp, the values not below `floor` of the lanes in `votes`: their NW words of a
+// lane are read again by the whole warp, an element each. Lane 0's words start at `vals` and lie
+// `stride` apart there and in the row, from `index` on; elements from `limit` on do not count.
+// Returns the new count of waiting keys. (A chain of latencies on the streaming path: the lanes'
+// numbers go through shared memory, and two rounds of loads and votes are in flight together.)
+template <typename T, int NW>
+__device__ __noinline__ int note_candidates(Key& list, Key* waiting, uint8_t* lanes, int count, unsigned votes, float floor,
+                                            const T* vals, int stride, int index, int limit) {
+  constexpr int VE = 16 / sizeof(T), N = NW * VE;  // elements of a lane: 32 or 16
+  const int lane = threadIdx.x & 31, sub = lane % N;
+  const unsigned below = (1u << lane) - 1;
+  if (votes >> lane & 1) lanes[__popc(votes & below)] = static_cast<uint8_t>(lane);
+  __syncwarp();
+  const int total = __popc(votes);
+  for (int done = 0; done < total; done += 2 * (32 / N)) {
+    float x[2];
+    int at[2];
+    unsigned in[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int who = done + i * (32 / N) + lane / N;
+      const int off = (who < total ? lanes[who] : 0) * VE + sub / VE * stride + sub % VE;
+      at[i] = who < total && index + off < limit ? index + off : -1;
+      x[i] = widen1(vals[off]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) in[i] = __ballot_sync(kAll, at[i] >= 0 && !(x[i] < floor));
+    int n = count;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (in[i] >> lane & 1) waiting[n + __popc(in[i] & below)] = make_key(order_bits(x[i]), at[i]);
+      n += __popc(in[i]);
+    }
+    count = n;
+    __syncwarp();
+    while (count >= 32) {  // (at most 31 + 64)
+      count -= 32;
+      list = sort_into(list, waiting + count, 32);
+      __syncwarp();
+    }
+  }
+  return count;
+}
 
+// Sums relative to the maximum M.
 struct Part {
   float M, S, W;
 };
-DEV Part join(const Part& a, const Part& b, float c) {
-  Part r;
-  r.M = fmaxf(a.M, b.M);
-  const float base = r.M == -INFINITY ? 0.f : r.M;
-  // a part without mass has M = -inf, S = W = 0; its shift must not become 0 * inf
-  const float da = a.M == -INFINITY ? 0.f : (a.M - base) * c, db = b.M == -INFINITY ? 0.f : (b.M - base) * c;
-  const float ea = ex2(da), eb = ex2(db);
-  r.S = ea * a.S + eb * b.S;
-  r.W = ea * (a.W + fmaxf(da, -200.f) * a.S) + eb * (b.W + fmaxf(db, -200.f) * b.S);
-  return r;
-}
-DEV Part shfl_xor(const Part& p, int mask) {
-  return {__shfl_xor_sync(kAll, p.M, mask), __shfl_xor_sync(kAll, p.S, mask), __shfl_xor_sync(kAll, p.W, mask)};
-}
-
-template <typename T>
-DEV float widen(T v);
-template <>
-DEV float widen<float>(float v) {
-  return v;
-}
-template <>
-DEV float widen<__half>(__half v) {
-  return __half2float(v);
-}
-template <>
-DEV float widen<__nv_bfloat16>(__nv_bfloat16 v) {
-  return __bfloat162float(v);
-}
-
-// Lists of the CTA's warps into warp 0's, the chunk's or row's best.
-DEV Key merge_warps(Key list, Key (*s_list)[32]) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-  for (int half = kWarps / 2; half >= 1; half >>= 1) {
-    if (warp >= half && warp < 2 * half) s_list[warp][lane] = list;
-    __syncthreads();
-    if (warp < half) list = merge_desc(list, s_list[warp + half][lane]);
+struct Scale {
+  float c;
+  float floor;  // kFloor / 16 of the logits' type
+  // whether sums on the base of M can be taken by fused multiply-adds over raised logits
+  DEV bool fast(float M) const { return fabsf(M * c) < 1073741824.f && M > floor && c < 1e8f; }
+  // log2 of the factor between sums on base `from` and sums on base `to` >= from
+  DEV float shift(float from, float to) const {
+    return fast(from) && fast(to) ? __fmul_rn(from, c) - __fmul_rn(to, c) : (from - to) * c;
   }
-  return list;
-}
-DEV Part merge_parts(Part p, Part* s_part, float c) {  // every thread's part into every thread of warp 0
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) p = join(p, shfl_xor(p, o), c);
-  if (lane == 0) s_part[warp] = p;
-  __syncthreads();
-  p = s_part[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) p = join(p, s_part[w], c);
-  return p;
-}
+  // c z - B, the base B of M
+  DEV float residual(float M) const { return fast(M) ? fmaf(M, c, -__fmul_rn(M, c)) : 0.f; }
+  DEV Part join(const Part& a, const Part& b) const {
+    Part r;
+    r.M = fmaxf(a.M, b.M);
+    // a part without mass has M = -inf and S = W = 0: its shift must not become 0 * inf
+    const float da = a.M == -INFINITY ? 0.f : shift(a.M, r.M), db = b.M == -INFINITY ? 0.f : shift(b.M, r.M);
+    const float ea = ex2(da), eb = ex2(db);
+    r.S = ea * a.S + eb * b.S;
+    r.W = ea * (a.W + fmaxf(da, -200.f) * a.S) + eb * (b.W + fmaxf(db, -200.f) * b.S);
+    return r;
+  }
+};
 
+// A 16-byte word of logits: their maximum (NaN if one is), and their values as fp32 with what
+// lies below kFloor raised to it: d of a masked logit is then finite, and 2^d d is 0.
 template <typename T>
-DEV void write_row(const LogprobParams& P, int row, const T* z, int token, const Part& p, Key list) {
-  constexpr float kLn2 = 0.6931471805599453f;
-  const int lane = threadIdx.x & 31;
-  const bool empty = p.S == 0.f;  // no finite logit
-  const float base = p.M == -INFINITY ? 0.f : p.M, ls = log2f(p.S);
-  if (lane == 0) {
-    if (P.logprob) {
-      P.logprob[row] = empty ? -INFINITY : (widen(z[token]) - base) * P.inv_temp - kLn2 * ls;
+struct Word;
+template <>
+struct Word<float> {
+  static constexpr int N = 4;
+  static constexpr uint32_t kMinusInf = 0xff800000u;
+  static constexpr float kFloor = -1e30f;
+  DEV static void widen(const uint4& q, float* x) {
+    x[0] = __uint_as_float(q.x), x[1] = __uint_as_float(q.y), x[2] = __uint_as_float(q.z), x[3] = __uint_as_float(q.w);
+  }
+  DEV static float top(const uint4& q) {
+    return max_nan(max_nan(__uint_as_float(q.x), __uint_as_float(q.y)), max_nan(__uint_as_float(q.z), __uint_as_float(q.w)));
+  }
+  DEV static uint4 raised(uint4 q) {
+    q.x = __float_as_uint(fmaxf(__uint_as_float(q.x), kFloor)), q.y = __float_as_uint(fmaxf(__uint_as_float(q.y), kFloor));
+    q.z = __float_as_uint(fmaxf(__uint_as_float(q.z), kFloor)), q.w = __float_as_uint(fmaxf(__uint_as_float(q.w), kFloor));
+    return q;
+  }
+};
+template <typename H2>
+struct Word16 {
+  DEV static H2 as2(uint32_t u) { return *reinterpret_cast<const H2*>(&u); }
+  DEV static uint32_t bits(H2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+  DEV static H2 top2(const uint4& q) { return __hmax2_nan(__hmax2_nan(as2(q.x), as2(q.y)), __hmax2_nan(as2(q.z), as2(q.w))); }
+  DEV static uint4 raised(const uint4& q, H2 floor) {
+    return {bits(__hmax2(as2(q.x), floor)), bits(__hmax2(as2(q.y), floor)), bits(__hmax2(as2(q.z), floor)), bits(__hmax2(as2(q.w), floor))};
+  }
+};
+template <>
+struct Word<__nv_bfloat16> : Word16<__nv_bfloat162> {
+  static constexpr int N = 8;
+  static constexpr uint32_t kMinusInf = 0xff80ff80u;
+  static constexpr float kFloor = -1e30f;
+  DEV static void widen(const uint4& q, float* x) {
+    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(u[i] << 16), x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+  DEV static float top(const uint4& q) {
+    const float2 f = __bfloat1622float2(top2(q));
+    return max_nan(f.x, f.y);
+  }
+  DEV static uint4 raised(const uint4& q) { return Word16::raised(q, __float2bfloat162_rn(kFloor)); }
+};
+template <>
+struct Word<__half> : Word16<__half2> {
+  static constexpr int N = 8;
+  static constexpr uint32_t kMinusInf = 0xfc00fc00u;
+  static constexpr float kFloor = -65504.f;
+  DEV static void widen(const uint4& q, float* x) {
+    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+      x[2 * i] = f.x, x[2 * i + 1] = f.y;
     }
-    P.entropy[row] = empty ? 0.f : kLn2 * (ls - p.W / p.S);
   }
-  if (lane < P.n_top) {
-    const size_t at = static_cast<size_t>(row) * P.n_top + lane;
-    const float x = from_order_bits(static_cast<uint32_t>(list >> 32));
-    P.top_ids[at] = static_cast<int>(0xffffffffu - static_cast<uint32_t>(list));
-    P.top_logprobs[at] = empty ? -INFINITY : (x - base) * P.inv_temp - kLn2 * ls;
+  DEV static float top(const uint4& q) {
+    const float2 f = __half22float2(top2(q));
+    return max_nan(f.x, f.y);
+  }
+  DEV static uint4 raised(const uint4& q) { return Word16::raised(q, __float2half2_rn(kFloor)); }
+};
+
+// A row's words of 16 bytes: `lead` logits before the first whole aligned word, `words` whole
+// ones, the rest behind them.
+template <typename T>
+struct RowWords {
+  const T* z;
+  int lead, words;
+  DEV RowWords(const LogprobParams& P, int row) {
+    constexpr int N = Word<T>::N;
+    z = static_cast<const T*>(P.logits) + row * P.row_stride;
+    lead = min(P.V, static_cast<int>((N - (reinterpret_cast<uintptr_t>(z) & 15) / sizeof(T)) % N));
+    words = (P.V - lead) / N;
+  }
+};
+
+// First unit of CTA c's range, and the CTA whose range holds unit u (G <= U: none is empty).
+DEV long long range_begin(long long c, long long U, int G) { return c * U / G; }
+DEV int cta_of(long long u, long long U, int G) { return static_cast<int>(((u + 1) * G - 1) / U); }
+
+struct Shared {
+  uint4 ring[kStages][kStageWords];
+  Key waiting[kWarps][kWaiting];
+  uint8_t lanes[kWarps][32];
+  Key list[kWarps][32];         // the warps' results of a segment
+  Part part[kWarps];
+  uint64_t full[kStages], empty[kStages], ready, taken;
+  volatile uint32_t thr[kWarps];
+  volatile int abort;
+  volatile int last[2];         // whether this CTA arrived last at the row it begins with, at the row it ends with
+  int warp_rows[kWarps + 1];
+  uint16_t rows[2];             // [min(rows, kListed)] the rows that have a token
+};
+
+__device__ __noinline__ void wait_long(uint64_t* bar, uint32_t parity, volatile int* abort, int* err, unsigned long long limit_ns) {
+  if (*abort) return;
+  if (!mbar_wait(bar, parity, limit_ns)) {
+    *abort = 1;
+    raise_flag(err, kDevTimeout);
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams P) {
-  constexpr int VE = 16 / sizeof(T);      // logits per 16-byte load
-  constexpr int U = sizeof(T) == 4 ? 4 : 2;  // loads per thread and batch
-  constexpr int NV = VE * U;              // 16 logits per thread and batch
-  __shared__ Key s_list[kWarps][32];
-  __shared__ Part s_part[kWarps];
-  __shared__ volatile uint32_t s_thr[kWarps];
-  __shared__ int s_last;
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const LogprobParams P) {
+  constexpr int VE = Word<T>::N;
+  constexpr float kLn2 = 0.6931471805599453f;
+  extern __shared__ uint8_t smem_raw[];
+  Shared& sh = *reinterpret_cast<Shared*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int V = P.V, k = TOP ? P.n_top : 0;
+  const bool listed = P.rows <= kListed;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], kWarps);
+    }
+    mbar_init(&sh.ready, kWarps);
+    mbar_init(&sh.taken, 1);
+    sh.abort = sh.last[0] = sh.last[1] = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int row = blockIdx.x / P.chunks, chunk = blockIdx.x - row * P.chunks;
-  const int V = P.V, k = P.n_top;
-  const int token = P.tokens ? __ldcg(P.tokens + row) : 0;
-  if (token < 0 || token >= V) {  // a row without a token
-    if (chunk == 0) {
-      if (tid == 0) {
-        if (token != -1) raise_flag(P.err, kDevToken);
-        if (P.logprob) P.logprob[row] = 0.f;
-        P.entropy[row] = 0.f;
-      }
-      if (tid < k) {
-        P.top_ids[static_cast<size_t>(row) * k + tid] = -1;
-        P.top_logprobs[static_cast<size_t>(row) * k + tid] = 0.f;
-      }
-    }
-    return;
-  }
-  const T* z = static_cast<const T*>(P.logits) + row * P.row_stride;
-  // 16-byte words from the one that holds the row's first logit: word w holds logits
-  // w * VE - skew .. + VE, of which those in [0, V) are the row's
-  const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(T));
-  const uint4* words = reinterpret_cast<const uint4*>(z - skew);
-  const int n_words = (V + skew + VE - 1) / VE;
-  const int per = (n_words + P.chunks - 1) / P.chunks;
-  const int w0 = min(chunk * per, n_words), w1 = min(w0 + per, n_words);
-  const float c = P.scale;
-  const int m = (k + kWarps - 1) / kWarps;  // a warp's share of the n_top largest
-  Part p = {-INFINITY, 0.f, 0.f};
-  Key list = 0;
-  if (k > 0 && lane == 0) s_thr[warp] = 0;
-  __syncthreads();
-
-  auto load = [&](int base, uint4 (&q)[U]) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int w = base + u * kThreads + tid;
-      if (w > 0 && w < w1 && w + 1 < n_words) {
-        q[u] = __ldcs(words + w);
-      } else {
-        // the row's first and last word by single logits, what is not the row's as -inf
-        T e[VE];
-#pragma unroll
-        for (int x = 0; x < VE; ++x) {
-          const int at = w * VE - skew + x;
-          e[x] = w < w1 && at >= 0 && at < V ? __ldcs(z + at) : static_cast<T>(-INFINITY);
-        }
-        q[u] = *reinterpret_cast<const uint4*>(e);
-      }
+  // Every wait is bounded: past the limit the flag is set and every role leaves its loop.
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!mbar_try_wait(bar, parity)) wait_long(bar, parity, &sh.abort, P.err, P.wait_ns);
+  };
+  // The rows to read. Rows without a token get their values from CTA 0, or in calls of more rows
+  // than are looked through from the CTA that walks past them.
+  auto no_token = [&](int row, int token) {  // one thread
+    if (token != -1) raise_flag(P.err, kDevToken);
+    if (P.logprob) P.logprob[row] = 0.f;
+    P.entropy[row] = 0.f;
+    for (int i = 0; i < k; ++i) {
+      P.top_ids[static_cast<size_t>(row) * k + i] = -1;
+      P.top_logprobs[static_cast<size_t>(row) * k + i] = 0.f;
     }
   };
-  bool first = true;
-  uint4 next[U];
-  if (w0 < w1) load(w0, next);
-  for (int base = w0; base < w1; base += U * kThreads) {
-    float x[NV];
+  auto has_token = [&](int token) { return token >= 0 && token < V; };
+  int n_rows = P.rows;
+  if (listed && P.tokens) {
+    // each thread a run of rows, all its loads in flight, then a scan over the threads
+    constexpr int kRun = (kListed + kThreads - 1) / kThreads;
+    const int run = (P.rows + kThreads - 1) / kThreads;
+    int token[kRun];
+    uint32_t in = 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const T* e = reinterpret_cast<const T*>(&next[u]);
-#pragma unroll
-      for (int y = 0; y < VE; ++y) x[u * VE + y] = widen(e[y]);
+    for (int i = 0; i < kRun; ++i) {
+      const int row = tid * run + i;
+      token[i] = i < run && row < P.rows ? __ldcg(P.tokens + row) : -1;
     }
-    if (base + U * kThreads < w1) load(base + U * kThreads, next);
-    float top = x[0];
 #pragma unroll
-    for (int y = 1; y < NV; ++y) top = fmaxf(top, x[y]);
-    if (top > p.M) p = join(p, Part{top, 0.f, 0.f}, c);
-    const float b = p.M == -INFINITY ? 0.f : p.M;
-    float ps = 0.f, pw = 0.f;
-#pragma unroll
-    for (int y = 0; y < NV; ++y) {
-      const float d = (x[y] - b) * c, e = ex2(d);
-      ps += e;
-      pw = fmaf(e, fmaxf(d, -200.f), pw);  // a masked logit: 0 * -200
+    for (int i = 0; i < kRun; ++i) {
+      const int row = tid * run + i;
+      if (has_token(token[i])) in |= 1u << i;
+      else if (blockIdx.x == 0 && i < run && row < P.rows) no_token(row, token[i]);
     }
-    p.S += ps;
-    p.W += pw;
-    if (k > 0) {
-      // the logit's index of x[u * VE + y] is (base + u * kThreads + tid) * VE - skew + y
-      uint32_t best = 0;
+    int upto = __popc(in);
 #pragma unroll
-      for (int y = 0; y < NV; ++y) best = max(best, order_bits(x[y]));
-      uint32_t thr;
-      if (first) {
-        const uint32_t sorted = sort_desc(best);
-        if (lane == m - 1) s_thr[warp] = sorted;
-        __syncthreads();
-        first = false;
-      }
-      thr = __reduce_min_sync(kAll, s_thr[lane & (kWarps - 1)]);
-      if (__any_sync(kAll, best >= thr)) {
-        Key kth = __shfl_sync(kAll, list, k - 1);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kAll, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) sh.warp_rows[warp] = upto;
+    __syncthreads();
+    int at = upto - __popc(in);
+    n_rows = 0;
 #pragma unroll
-        for (int y = 0; y < NV; ++y) {
-          const int at = (base + (y / VE) * kThreads + tid) * VE - skew + y % VE;
-          const uint32_t ord = order_bits(x[y]);
-          const Key key = make_key(ord, at);
-          const bool cand = ord >= thr && key > kth && at >= 0 && at < V && at < w1 * VE - skew;
-          unsigned votes = __ballot_sync(kAll, cand);
-          if (votes == 0) continue;
-          if (__popc(votes) <= 6) {
-            while (votes) {
-              const int from = __ffs(votes) - 1;
-              votes &= votes - 1;
-              const Key in = __shfl_sync(kAll, key, from);
-              const Key above = __shfl_up_sync(kAll, list, 1);
-              const bool keep = list > in;
-              const bool above_keep = lane == 0 || above > in;
-              list = keep ? list : above_keep ? in : above;
-            }
-          } else {
-            list = merge_desc(list, sort_desc(cand ? key : 0));
-          }
-          kth = __shfl_sync(kAll, list, k - 1);
+    for (int w = 0; w <= kWarps; ++w) {
+      if (w < warp) at += sh.warp_rows[w];
+      n_rows += sh.warp_rows[w];
+    }
+#pragma unroll
+    for (int i = 0; i < kRun; ++i)
+      if (in >> i & 1) sh.rows[at++] = static_cast<uint16_t>(tid * run + i);
+    __syncthreads();
+  }
+  const int per_row = P.units;  // units of a row
+  const long long U = static_cast<long long>(n_rows) * per_row;
+  // two stages a CTA at least; where every row goes to eight or more CTAs, the same number for each
+  int G = static_cast<int>(min(static_cast<long long>(gridDim.x), (U + 2 * kStageUnits - 1) / (2 * kStageUnits)));
+  if (G >= 8 * n_rows && n_rows > 0) G -= G % n_rows;
+  const int cta = blockIdx.x;
+  if (cta >= G) return;
+  const long long U0 = range_begin(cta, U, G), U1 = range_begin(cta + 1, U, G);
+  // The walk of both roles: the rows of this range from rank r0 on (the first from its unit u00),
+  // with their first and last unit in the range. No division past the first: a 64-bit one is
+  // a hundred instructions, for every warp and row.
+  const int r0 = static_cast<int>(U0 / per_row), u00 = static_cast<int>(U0 - static_cast<long long>(r0) * per_row);
+  auto row_of = [&](int rank) { return listed && P.tokens ? static_cast<int>(sh.rows[rank]) : rank; };
+  auto token_of = [&](int row) { return P.tokens ? __ldcg(P.tokens + row) : 0; };
+
+  if (warp == kWarps) {
+    // ------------------------------------------------------------ producer warp
+    if (lane != 0) return;
+    const uint64_t pol = policy_evict_first();
+    int n = 0;  // stages issued
+    int rank = r0, u0 = u00;
+    for (long long left = U1 - U0; left > 0 && !sh.abort; ++rank, u0 = 0) {
+      const int u1 = static_cast<int>(min(static_cast<long long>(per_row), u0 + left)), row = row_of(rank);
+      left -= u1 - u0;
+      if (!listed && P.tokens) {
+        const int token = token_of(row);
+        if (!has_token(token)) {
+          if (u0 == 0) no_token(row, token);
+          continue;
         }
-        const uint32_t mine = static_cast<uint32_t>(list >> 32);
-        if (lane == m - 1 && mine > s_thr[warp]) s_thr[warp] = mine;
+      }
+      const RowWords<T> rw(P, row);
+      const int end = min(u1 * kUnitWords, rw.words);
+      for (int w = u0 * kUnitWords; w < end && !sh.abort; w += kStageWords) {
+        const int st = n % kStages, words = min(kStageWords, end - w);
+        if (n >= kStages) wait(&sh.empty[st], (n / kStages - 1) & 1);
+        if (sh.abort) break;
+        mbar_arrive_expect_tx(&sh.full[st], words * 16);
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+                smem_u32(sh.ring[st])),
+            "l"(reinterpret_cast<uint64_t>(rw.z + rw.lead + static_cast<size_t>(w) * VE)), "r"(words * 16),
+            "r"(smem_u32(&sh.full[st])), "l"(pol)
+            : "memory");
+        ++n;
+      }
+    }
+    if (sh.abort)  // the copies still in flight land before the CTA leaves
+      for (int i = max(0, n - kStages); i < n; ++i) mbar_wait(&sh.full[i % kStages], (i / kStages) & 1, P.wait_ns);
+    return;
+  }
+
+  // -------------------------------------------------------------- consumer warps
+  const Scale sc = {P.scale, Word<T>::kFloor / 16};
+  const int m = (k + kWarps - 1) / kWarps;  // a warp's share of the n_top largest
+  float M = -INFINITY;                       // the warp's, the same in every lane
+  float2 S2 = {0.f, 0.f}, W2 = {0.f, 0.f};   // the thread's
+  Key list = 0;
+  int waiting = 0;                           // keys that are not in the list yet
+  uint32_t best = 0;                         // the lane's largest value in the segment
+  bool fresh = true;
+
+  auto rebase = [&](float wtop) {  // onto a larger maximum
+    if (wtop <= M) return;
+    if (wtop == wtop) {
+      const float e = M == -INFINITY ? 0.f : sc.shift(M, wtop);
+      const float f = ex2(e), ec = fmaxf(e, -200.f);
+      W2 = {f * (W2.x + ec * S2.x), f * (W2.y + ec * S2.y)};
+      S2 = {f * S2.x, f * S2.y};
+      M = wtop;
+    } else {
+      S2.x = W2.x = wtop;  // a NaN spoils the row's sums
+    }
+  };
+  // NW words of each thread. The warp's words start at `vals` and lie a unit apart there and in the
+  // row, from `index` on; elements from `limit` on are filled up with -inf and do not count.
+  auto take = [&](auto& q, auto nw_const, const T* vals, int index, int limit) {
+    constexpr int NW = decltype(nw_const)::value;
+    float top = Word<T>::top(q[0]);
+#pragma unroll
+    for (int w = 1; w < NW; ++w) top = max_nan(top, Word<T>::top(q[w]));
+    const float wtop = warp_max_nan(top);
+    rebase(wtop);
+    if (sc.fast(M)) {
+      const float B = __fmul_rn(M, sc.c);
+      const float2 c2 = {sc.c, sc.c}, b2 = {-B, -B};
+      float2 s2 = {0.f, 0.f}, w2 = {0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        float x[VE];
+        Word<T>::widen(Word<T>::raised(q[w]), x);
+#pragma unroll
+        for (int y = 0; y < VE; y += 2) {
+          const float2 d = fma2(float2{x[y], x[y + 1]}, c2, b2);
+          const float2 e = {ex2(d.x), ex2(d.y)};
+          s2 = add2(s2, e);
+          w2 = fma2(e, d, w2);
+        }
+      }
+      S2 = add2(S2, s2);
+      W2 = add2(W2, w2);
+    } else if (M > -INFINITY) {  // (nothing but -inf so far: nothing to add)
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        float x[VE];
+        Word<T>::widen(q[w], x);
+#pragma unroll
+        for (int y = 0; y < VE; ++y) {
+          const float d = (x[y] - M) * sc.c, e = ex2(d);
+          S2.x += e;
+          W2.x = fmaf(e, fmaxf(d, -200.f), W2.x);  // a masked logit: 0 * -200
+        }
+      }
+    }
+    if (TOP) {
+      best = max(best, order_bits(top));
+      // what the warp knows of the threshold: the m-th largest of its lanes' maxima
+      auto publish = [&]() {
+        uint32_t rest = best, found = 0;
+        int left = m;
+#pragma unroll
+        for (int i = 0; i < kLpMaxTop / kWarps; ++i) {
+          const uint32_t top_rest = __reduce_max_sync(kAll, rest);
+          if (left > 0) found = top_rest;
+          left -= __popc(__ballot_sync(kAll, rest == top_rest));
+          if (rest == top_rest) rest = 0;
+        }
+        if (lane == 0) sh.thr[warp] = found;
+      };
+      if (fresh) {
+        publish();
+        named_bar_sync(1, kConsumers);
+        fresh = false;
+      }
+      const uint32_t thr = __reduce_min_sync(kAll, sh.thr[lane & (kWarps - 1)]);
+      const float thr_f = from_order_bits(thr);  // NaN bits where there is none yet
+      if (!(wtop < thr_f)) {
+        waiting = note_candidates<T, NW>(list, sh.waiting[warp], sh.lanes[warp], waiting, __ballot_sync(kAll, !(top < thr_f)), thr_f, vals,
+                                         kUnitWords * VE, index, limit);
+        publish();
         __syncwarp();
       }
     }
-  }
-  if (k > 0) list = merge_warps(list, s_list);
-  p = merge_parts(p, s_part, c);
-  if (P.chunks == 1) {
-    if (warp == 0) write_row(P, row, z, token, p, list);
-    return;
-  }
-  float* slot = P.part + static_cast<size_t>(blockIdx.x) * kLpSlotWords;
-  if (warp == 0) {
-    if (lane == 0) __stcg(reinterpret_cast<float4*>(slot), make_float4(p.M, p.S, p.W, 0.f));
-    if (lane < k) __stcg(reinterpret_cast<Key*>(slot + 4) + lane, list);
-    __threadfence();
-    __syncwarp();
+  };
+  // The parts of the first `lanes` lanes (a power of two) into one, in all lanes.
+  auto join_lanes = [&](Part p, int lanes) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+      if (o >= lanes) continue;
+      p = sc.join(p, Part{__shfl_xor_sync(kAll, p.M, o), __shfl_xor_sync(kAll, p.S, o), __shfl_xor_sync(kAll, p.W, o)});
+    }
+    return p;
+  };
+  auto write_row = [&](int row, const T* z, const Part& p) {  // one warp; its list is the row's
+    const bool empty = p.S == 0.f;  // every logit -inf
+    const float top = p.M == -INFINITY ? 0.f : p.M;
+    const float ls = kLn2 * (log2f(p.S) - (p.M == -INFINITY ? 0.f : sc.residual(p.M)));
     if (lane == 0) {
-      const int before = atomicAdd(P.row_cnt + row, 1);
-      s_last = before == P.chunks - 1;
-      if (s_last) P.row_cnt[row] = 0;
+      if (P.logprob) P.logprob[row] = empty ? -INFINITY : (widen1(z[token_of(row)]) - top) * P.inv_temp - ls;
+      P.entropy[row] = empty ? 0.f : kLn2 * (log2f(p.S) - p.W / p.S);
     }
-  }
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  // the row's chunks in order: (max, sums) by threads, lists by warps
-  const float* parts = P.part + static_cast<size_t>(row) * P.chunks * kLpSlotWords;
-  p = {-INFINITY, 0.f, 0.f};
-  for (int i = tid; i < P.chunks; i += kThreads) {
-    const float4 q = __ldcg(reinterpret_cast<const float4*>(parts + static_cast<size_t>(i) * kLpSlotWords));
-    p = join(p, Part{q.x, q.y, q.z}, c);
-  }
-  if (k > 0) {
+    if (lane < k) {
+      const size_t to = static_cast<size_t>(row) * k + lane;
+      P.top_ids[to] = static_cast<int>(0xffffffffu - static_cast<uint32_t>(list));
+      P.top_logprobs[to] = empty ? -INFINITY : (from_order_bits(static_cast<uint32_t>(list >> 32)) - top) * P.inv_temp - ls;
+    }
+  };
+  // a CTA's part of the row that it begins with, or of the row that it ends with; a row's counter is
+  // that of the first CTA that has a part of it
+  auto slot_of = [&](int c, long long base) {
+    return P.part + (2 * static_cast<size_t>(c) + (range_begin(c, U, G) >= base ? 0 : 1)) * kLpSlotWords;
+  };
+
+  int n = 0, seg_no = 0;
+  int rank = r0, u0 = u00;
+  for (long long left = U1 - U0; left > 0; ++rank, u0 = 0) {
+    const int u1 = static_cast<int>(min(static_cast<long long>(per_row), u0 + left)), row = row_of(rank);
+    left -= u1 - u0;
+    if (!listed && P.tokens && !has_token(token_of(row))) continue;
+    const RowWords<T> rw(P, row);
+    // the logits outside whole words, before and behind them, one to a lane of warp 0: loaded now,
+    // taken at the segment's end
+    int edge = -1;
+    if (warp == 0 && lane < VE) edge = u0 == 0 && lane < rw.lead ? lane : -1;
+    else if (warp == 0 && lane < 2 * VE) edge = rw.lead + rw.words * VE + lane - VE;
+    if (edge >= V || (lane >= VE && u1 < per_row)) edge = -1;
+    const float edge_x = edge >= 0 ? widen1(rw.z[edge]) : -INFINITY;
+    const int end = min(u1 * kUnitWords, rw.words);
+    for (int w0 = u0 * kUnitWords; w0 < end; w0 += kStageWords, ++n) {
+      const int st = n % kStages, words = min(kStageWords, end - w0);
+      wait(&sh.full[st], (n / kStages) & 1);
+      __syncwarp();
+      constexpr int L = kStageUnits;  // words of a thread at a time
+      uint4* ring = sh.ring[st] + tid;
+      if (words < kStageWords) {  // the thread's words that the stage lacks
+        constexpr uint32_t f = Word<T>::kMinusInf;
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+          if (i * kUnitWords + tid >= words) ring[i * kUnitWords] = uint4{f, f, f, f};
+        fence_async_shared();  // the next copy into them comes after
+      }
+      uint4 q[L];
+#pragma unroll
+      for (int i = 0; i < L; ++i) q[i] = ring[i * kUnitWords];
+      take(q, std::integral_constant<int, L>(), reinterpret_cast<const T*>(sh.ring[st] + warp * 32),
+           rw.lead + (w0 + warp * 32) * VE, rw.lead + end * VE);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.empty[st]);
+    }
+    // ---- the segment's end
+    if (TOP && fresh) named_bar_sync(1, kConsumers);  // a segment without a whole word
+    if (__any_sync(kAll, edge >= 0)) {
+      rebase(warp_max_nan(edge_x));
+      if (M > -INFINITY) {
+        const float d = sc.fast(M) ? fmaf(fmaxf(edge_x, Word<T>::kFloor), sc.c, -__fmul_rn(M, sc.c)) : (edge_x - M) * sc.c;
+        const float e = ex2(d);
+        S2.x += e;
+        W2.x = fmaf(e, fmaxf(d, -200.f), W2.x);
+      }
+      if (TOP) {
+        const uint32_t thr = fresh ? 0 : __reduce_min_sync(kAll, sh.thr[lane & (kWarps - 1)]);
+        const bool in = edge >= 0 && order_bits(edge_x) >= thr;
+        const unsigned votes = __ballot_sync(kAll, in);
+        if (in) sh.waiting[warp][waiting + __popc(votes & ((1u << lane) - 1))] = make_key(order_bits(edge_x), edge);
+        waiting += __popc(votes);  // at most 31 + 16
+        __syncwarp();
+        if (waiting >= 32) {
+          waiting -= 32;
+          list = sort_into(list, sh.waiting[warp] + waiting, 32);
+          __syncwarp();
+        }
+      }
+    }
+    if (TOP) {
+      list = sort_into(list, sh.waiting[warp], waiting);
+      waiting = 0;
+    }
+    float S = S2.x + S2.y, W = W2.x + W2.y;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+      S += __shfl_xor_sync(kAll, S, o);
+      W += __shfl_xor_sync(kAll, W, o);
+    }
+    // The warps hand their results to one of them, another for each segment, and go on.
+    const int finisher = seg_no % kWarps;
+    if (seg_no >= 1) wait(&sh.taken, (seg_no - 1) & 1);
+    __syncwarp();
+    if (lane == 0) sh.part[warp] = {M, S, W};
+    if (TOP) sh.list[warp][lane] = list;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.ready);
+    M = -INFINITY;
+    S2 = W2 = {0.f, 0.f};
+    fresh = true;
+    best = 0;
+    const uint32_t round = seg_no++;
+    if (warp == finisher) {
+      wait(&sh.ready, round & 1);
+      __syncwarp();
+      if (TOP) list = merge_eight(sh.list);
+      const Part p = join_lanes(sh.part[lane & (kWarps - 1)], kWarps);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.taken);
+      if (u0 == 0 && u1 == per_row) {
+        write_row(row, rw.z, p);
+      } else {
+        const long long base = static_cast<long long>(rank) * per_row;
+        const int c0 = cta_of(base, U, G), c1 = cta_of(base + per_row - 1, U, G);
+        float* slot = slot_of(cta, base);
+        if (lane == 0) __stcg(reinterpret_cast<float4*>(slot), make_float4(p.M, p.S, p.W, 0.f));
+        if (lane < k) __stcg(reinterpret_cast<Key*>(slot + 4) + lane, list);
+        __threadfence();
+        __syncwarp();
+        if (lane == 0 && atomicAdd(P.row_cnt + c0, 1) == c1 - c0) {
+          P.row_cnt[c0] = 0;
+          sh.last[base > U0] = 1;
+        }
+      }
+    }
     list = 0;
-    for (int i = warp; i < P.chunks; i += kWarps) {
-      const Key* other = reinterpret_cast<const Key*>(parts + static_cast<size_t>(i) * kLpSlotWords + 4);
-      list = merge_desc(list, lane < k ? __ldcg(other + lane) : 0);
-    }
-    list = merge_warps(list, s_list);
   }
-  __syncthreads();  // s_part of the first use has been read
-  p = merge_parts(p, s_part, c);
-  if (warp == 0) write_row(P, row, z, token, p, list);
+  // ---- the rows that this CTA shares with others and was the last to arrive at, by all warps
+  named_bar_sync(1, kConsumers);
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    if (!sh.last[which]) continue;
+    __threadfence();
+    const int rank = which == 0 ? r0 : static_cast<int>((U1 - 1) / per_row), row = row_of(rank);
+    const long long base = static_cast<long long>(rank) * per_row;
+    const int c0 = cta_of(base, U, G), c1 = cta_of(base + per_row - 1, U, G);
+    if (TOP) {
+      list = 0;
+#pragma unroll 1
+      for (int c = c0 + warp; c <= c1; c += 4 * kWarps) {
+        Key other[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int from = c + i * kWarps;
+          other[i] = from <= c1 && lane < k ? __ldcg(reinterpret_cast<const Key*>(slot_of(from, base) + 4) + lane) : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) list = merge_lists(list, other[i]);
+      }
+      sh.list[warp][lane] = list;
+      named_bar_sync(1, kConsumers);
+    }
+    if (warp == 0) {
+      if (TOP) list = merge_eight(sh.list);
+      Part p = {-INFINITY, 0.f, 0.f};
+      for (int c = c0 + lane; c <= c1; c += 32) {
+        const float4 q = __ldcg(reinterpret_cast<const float4*>(slot_of(c, base)));
+        p = sc.join(p, Part{q.x, q.y, q.z});
+      }
+      p = join_lanes(p, 32);
+      write_row(row, RowWords<T>(P, row).z, p);
+    }
+    if (TOP) named_bar_sync(1, kConsumers);  // the lists' buffer is the other row's
+  }
 }
 
-}  // namespace
+int smem_bytes(int rows) { return static_cast<int>(sizeof(Shared)) + 128 + 2 * rows; }
+static_assert(sizeof(Shared) + 128 + 2 * kListed + 1024 <= 233472 / kCtasPerSm, "shared memory of an SM");
 
-// Chunks per row: enough CTAs to fill the GPU eight times over (so that the last wave's
-// remainder is small), chunks of 16 KB of logits at least, and no more parts than the
-// workspace holds; rows that need no cutting are not cut.
-int logprob_chunks(int rows, int vocab, int elem_bytes, int n_sms) {
-  const long long bytes = static_cast<long long>(vocab) * elem_bytes;
-  long long chunks = (8LL * n_sms + rows - 1) / rows;
-  chunks = chunks < bytes / 16384 ? chunks : bytes / 16384;
-  if (chunks < 1) chunks = 1;
-  if (chunks > 256) chunks = 256;
-  if (chunks > 1 && rows * chunks > kLpSlots) chunks = kLpSlots / rows;
-  return chunks < 1 ? 1 : static_cast<int>(chunks);
-}
-
-int launch_logprobs(const LogprobParams& p, int dtype, cudaStream_t stream) {
+template <typename T, bool TOP>
+cudaError_t launch(const LogprobParams& p, int n_ctas, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.rows) * p.chunks);
+  cfg.gridDim = dim3(n_ctas);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes(p.rows <= kListed ? p.rows : 0);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, TOP>, p);
+}
+
+template <typename T, bool TOP>
+cudaError_t set_attr() {
+  return cudaFuncSetAttribute(logprobs_kernel<T, TOP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(kListed));
+}
+
+}  // namespace
+
+int logprob_set_attributes() {
+  const cudaError_t e[] = {set_attr<float, false>(),  set_attr<float, true>(),         set_attr<__half, false>(),
+                           set_attr<__half, true>(),  set_attr<__nv_bfloat16, false>(), set_attr<__nv_bfloat16, true>()};
+  for (cudaError_t x : e)
+    if (x != cudaSuccess) return static_cast<int>(x);
+  return 0;
+}
+
+int launch_logprobs(LogprobParams p, int dtype, int n_sms, cudaStream_t stream) {
+  const long long bytes = static_cast<long long>(p.V) * (dtype == DFLASH_F32 ? 4 : 2);
+  p.units = static_cast<int>((bytes + 16 * kUnitWords - 1) / (16 * kUnitWords));
+  const long long stages = (static_cast<long long>(p.rows) * p.units + kStageUnits - 1) / kStageUnits;
+  const int most = std::min(kCtasPerSm * n_sms, kLpMaxCtas);
+  const int ctas = static_cast<int>(std::min<long long>(stages, most));
+  const bool top = p.n_top > 0;
   cudaError_t e;
-  if (dtype == DFLASH_F32) e = cudaLaunchKernelEx(&cfg, logprobs_kernel<float>, p);
-  else if (dtype == DFLASH_F16) e = cudaLaunchKernelEx(&cfg, logprobs_kernel<__half>, p);
-  else e = cudaLaunchKernelEx(&cfg, logprobs_kernel<__nv_bfloat16>, p);
+  if (dtype == DFLASH_F32) e = top ? launch<float, true>(p, ctas, stream) : launch<float, false>(p, ctas, stream);
+  else if (dtype == DFLASH_F16) e = top ? launch<__half, true>(p, ctas, stream) : launch<__half, false>(p, ctas, stream);
+  else e = top ? launch<__nv_bfloat16, true>(p, ctas, stream) : launch<__nv_bfloat16, false>(p, ctas, stream);
   return static_cast<int>(e);
 }
 

@@ -75,7 +75,7 @@ int launch_paged_attn(const PagedAttnParams& p, bool bf16, int n_ctas, cudaStrea
 
 // ---------------------------------------------------------------- log probabilities
 constexpr int kLpMaxTop = 32;
-constexpr int kLpSlots = 4096;     // partial slots: rows x chunks of a call that cuts its rows
+constexpr int kLpMaxCtas = 512;
 constexpr int kLpSlotWords = 68;   // (max, sum, weighted sum, pad) then 32 keys of 64 bits
 struct LogprobParams {
   const void* logits;
@@ -84,16 +84,17 @@ struct LogprobParams {
   float scale;        // log2(e) / temperature
   float inv_temp;     // 1 / temperature
   int V, rows, n_top;
-  int chunks;         // CTAs per row
+  int units;          // 4 KB units of a row (set by the launcher)
   float* logprob;
   float* entropy;
   int* top_ids;
   float* top_logprobs;
-  float* part;        // [rows * chunks][kLpSlotWords]
-  int* row_cnt;       // [rows] arrival counters, zero between launches
+  float* part;        // [2 * kLpMaxCtas][kLpSlotWords]: each CTA's part of its first and of its last row
+  int* row_cnt;       // [kLpMaxCtas] arrivals at the row that a CTA ends with, zero between launches
   int* err;
+  unsigned long long wait_ns;  // limit of every wait in the kernel
 };
-int logprob_chunks(int rows, int vocab, int elem_bytes, int n_sms);
-int launch_logprobs(const LogprobParams& p, int dtype, cudaStream_t stream);
+int logprob_set_attributes();
+int launch_logprobs(LogprobParams p, int dtype, int n_sms, cudaStream_t stream);
 
 }  // namespace dfl
