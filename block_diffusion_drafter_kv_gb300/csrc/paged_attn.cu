@@ -16,8 +16,8 @@
 //
 // CTA. One producer warp walks the range: page ids a warp-load at a time, K/V tiles by TMA
 // into a ring of shared-memory stages, each segment's q rows by bulk copies. The compute
-// warps are RG row groups of 16 * MT rows times KG key groups; a warp takes 16-key slices of
-// every tile (slice number mod KG is its group) with a softmax state of its own, so
+// warps are RG row groups of 16 rows times KG key groups; a warp takes 32-key halves of tiles (of
+// every tile, or with four key groups of every second one) with a softmax state of its own, so
 // that warps meet only where a segment ends. S = q K^T and O += P V are mma.sync m16n8k16
 // with fp32 accumulation: the rows are few (4 in ordinary grouped decoding), so a
 // 128-row tcgen05 tile would be mostly padding, while the loads bound the kernel.
@@ -34,7 +34,7 @@ namespace dfl {
 namespace {
 
 constexpr int kKeys = kPagePos;  // keys per tile
-constexpr int kSlice = 16;       // keys per warp step
+constexpr int kStep = 32;        // keys per warp step
 
 DEV float ex2(float x) {
   float y;
@@ -108,11 +108,12 @@ DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar)
 DEV long long range_begin(long long c, long long T, int G) { return c * T / G; }
 DEV int cta_of(long long u, long long T, int G) { return static_cast<int>(((u + 1) * G - 1) / T); }
 
-template <int D, int MT, int RG, int KG, int STAGES>
+template <int D, int RG, int KG, int STAGES>
 struct Layout {
   static constexpr int kWarps = RG * KG;
   static constexpr int kThreads = 32 * (kWarps + 1);
-  static constexpr int kRows = 16 * MT * RG;
+  static constexpr int kRows = 16 * RG;
+  static constexpr int kTileWarps = RG * (KG < 2 ? KG : 2);  // warps that use one tile
   static constexpr int kTileBytes = kKeys * D * 2;          // one operand
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kQStride = D * 2 + 16;               // bytes; the pad keeps ldmatrix free of conflicts
@@ -137,10 +138,20 @@ DEV int rows_of(const PagedAttnParams& P, int s, int& len, bool& bad) {
   return bad ? 0 : n;
 }
 
-template <int D, bool BF16, int MT, int RG, int KG, int STAGES>
-__global__ void __launch_bounds__(Layout<D, MT, RG, KG, STAGES>::kThreads, 1)
-    paged_attn_kernel(const __grid_constant__ PagedAttnParams P) {
-  using L = Layout<D, MT, RG, KG, STAGES>;
+__device__ __noinline__ void wait_long(uint64_t* bar, uint32_t parity, volatile int* abort, int* err, unsigned long long limit_ns) {
+  if (*abort) return;
+  if (!mbar_wait(bar, parity, limit_ns)) {
+    *abort = 1;
+    raise_flag(err, kDevTimeout);
+  }
+}
+
+template <int D, bool BF16, int RG, int KG, int STAGES>
+__global__ void __launch_bounds__(Layout<D, RG, KG, STAGES>::kThreads, 1) paged_attn_kernel(const __grid_constant__ PagedAttnParams P) {
+  using L = Layout<D, RG, KG, STAGES>;
+  // With four key groups a stage has to serve the same two of them every time: a group that
+  // skipped a phase of a stage's barrier could take the phase before it for its own.
+  static_assert(KG != 4 || STAGES % 2 == 0, "stages of alternating tiles");
   constexpr int NT = D / 8;  // 8-dim column tiles of the output
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -159,7 +170,7 @@ __global__ void __launch_bounds__(Layout<D, MT, RG, KG, STAGES>::kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], L::kWarps);
+      mbar_init(&empty[i], L::kTileWarps);
     }
     for (int i = 0; i < L::kQBufs; ++i) {
       mbar_init(&qfull[i], 1);
@@ -228,17 +239,14 @@ __global__ void __launch_bounds__(Layout<D, MT, RG, KG, STAGES>::kThreads, 1)
   // Every wait is bounded: past the limit the flag is set, later waits pass at once and the
   // CTA walks to its end without results.
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (*s_abort) return;
-    if (!mbar_wait(bar, parity, P.wait_ns)) {
-      *s_abort = 1;
-      raise_flag(P.err, kDevTimeout);
-    }
+    if (!mbar_try_wait(bar, parity)) wait_long(bar, parity, s_abort, P.err, P.wait_ns);
   };
 
   if (warp == L::kWarps) {
     // ------------------------------------------------------------ producer warp
-    // K/V are read once per call: streamed through L2
-    const uint64_t pol = policy_evict_first();
+    // K/V are read once per call: streamed through L2, unless all of it (16 MB, one eighth of L2)
+    // can stay there until it is read again
+    const uint64_t pol = T * L::kStageBytes > (16ll << 20) ? policy_evict_first() : policy_evict_last();
     int i = 0, seg_no = 0;
     int q_issued = 0, kv_issued = 0;  // of the segments and tiles walked so far
     for (long long u = T0; u < T1; ++seg_no) {
@@ -311,8 +319,8 @@ __global__ void __launch_bounds__(Layout<D, MT, RG, KG, STAGES>::kThreads, 1)
 
   // -------------------------------------------------------------- compute warps
   const int rg = warp / KG, kg = warp % KG;
-  const int r0 = lane >> 2, kq = (lane & 3) * 2;
-  const int mrow0 = rg * 16 * MT;  // first of the warp's rows
+  const int r0 = lane >> 2, kq = (lane & 3) * 2, mi = lane >> 3;
+  const int mrow0 = rg * 16;  // first of the warp's rows
   int i = 0, seg_no = 0;
   for (long long u = T0; u < T1; ++seg_no) {
     int s, g, t0, nt;
@@ -322,190 +330,176 @@ __global__ void __launch_bounds__(Layout<D, MT, RG, KG, STAGES>::kThreads, 1)
     bool bad;
     const int n_new = rows_of(P, s, len, bad);
     const int nk = len + n_new;
-    int lim[MT][2];  // last key each of the thread's rows may see
+    int lim[2];  // last key each of the thread's rows may see
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) lim[mt][h] = len + (mrow0 + mt * 16 + h * 8 + r0) / grp;
+    for (int h = 0; h < 2; ++h) lim[h] = len + (mrow0 + h * 8 + r0) / grp;
     const int qb = seg_no % L::kQBufs;
     wait(&qfull[qb], (seg_no / L::kQBufs) & 1);
     __syncwarp();
-    const uint32_t qbase = smem_u32(smem + L::kQOff + qb * L::kRows * L::kQStride) +
-                           (mrow0 + (lane & 15)) * L::kQStride + (lane >> 4) * 16;
-    uint32_t qa[MT == 1 ? D / 16 : 1][4];  // one row tile's q stays in registers; two are re-read per slice
-    if (MT == 1) {
+    uint32_t qa[D / 16][4];
+    {
+      const uint32_t qbase = smem_u32(smem + L::kQOff + qb * L::kRows * L::kQStride) + (mrow0 + (lane & 15)) * L::kQStride + (lane >> 4) * 16;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) ldsm4<false>(qbase + kk * 32, qa[kk]);
     }
-    float o[MT][NT][4], m_[MT][2], l_[MT][2];
+    float o[NT][4], m_[2] = {-INFINITY, -INFINITY}, l_[2] = {0.f, 0.f};
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      m_[mt][0] = m_[mt][1] = -INFINITY;
-      l_[mt][0] = l_[mt][1] = 0.f;
-#pragma unroll
-      for (int nt2 = 0; nt2 < NT; ++nt2) o[mt][nt2][0] = o[mt][nt2][1] = o[mt][nt2][2] = o[mt][nt2][3] = 0.f;
-    }
+    for (int nt2 = 0; nt2 < NT; ++nt2) o[nt2][0] = o[nt2][1] = o[nt2][2] = o[nt2][3] = 0.f;
     for (int j = 0; j < seg; ++j, ++i) {
+      if (KG == 4 && (i & 1) != kg >> 1) continue;  // the other two key groups' tile
       const int st = i % STAGES;
       wait(&full[st], (i / STAGES) & 1);
       const uint32_t kb = smem_u32(smem + st * L::kStageBytes), vb = kb + L::kTileBytes;
       // the whole warp takes the tile or skips it: the steps below are collective
       if (__all_sync(0xffffffffu, s_valid[st] != 0 && !*s_abort)) {
 #pragma unroll 1
-        for (int sl = kg; sl < kKeys / kSlice; sl += KG) {
-          const int key0 = (t0 + j) * kKeys + sl * kSlice;  // position of the slice's first key
+        for (int half = KG == 1 ? 0 : kg & 1; half < 2; half += KG == 1 ? 1 : 2) {
+          const int key0 = (t0 + j) * kKeys + half * kStep;  // position of the step's first key
           if (key0 >= nk) break;
-          const bool edge = key0 + kSlice - 1 > len;  // some row may not see some key
-          float sc[MT][2][4];
+          const bool edge = key0 + kStep - 1 > len;  // some row may not see some key
+          float sc[4][4];
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) sc[mt][0][c] = sc[mt][1][c] = 0.f;
-          const int mi = lane >> 3;
+          for (int n8 = 0; n8 < 4; ++n8) sc[n8][0] = sc[n8][1] = sc[n8][2] = sc[n8][3] = 0.f;
           // matrices 0..3: keys 0-7 dims lo, keys 0-7 dims hi, keys 8-15 dims lo, keys 8-15 dims hi
-          const int kkey = sl * kSlice + (mi >> 1) * 8 + (lane & 7);
+          const int kkey = half * kStep + (mi >> 1) * 8 + (lane & 7);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            uint32_t b[4];
-            ldsm4<false>(tile_addr(kb, kkey, kk * 16 + (mi & 1) * 8), b);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              if (MT == 1) {
-                mma16816<BF16>(sc[mt][0], qa[kk], b[0], b[1]);
-                mma16816<BF16>(sc[mt][1], qa[kk], b[2], b[3]);
-              } else {
-                uint32_t a[4];
-                ldsm4<false>(qbase + mt * 16 * L::kQStride + kk * 32, a);
-                mma16816<BF16>(sc[mt][0], a, b[0], b[1]);
-                mma16816<BF16>(sc[mt][1], a, b[2], b[3]);
-              }
+            for (int n16 = 0; n16 < 2; ++n16) {
+              uint32_t b[4];
+              ldsm4<false>(tile_addr(kb, kkey + n16 * 16, kk * 16 + (mi & 1) * 8), b);
+              mma16816<BF16>(sc[2 * n16], qa[kk], b[0], b[1]);
+              mma16816<BF16>(sc[2 * n16 + 1], qa[kk], b[2], b[3]);
             }
           }
-          // online softmax in log2 units
-          uint32_t pa[MT][4];
+          // Online softmax in log2 units. The reference of a row moves only where a score passes
+          // it by more than 8 (a weight is then at most 256, as exact in 16 bits as near 1), so that
+          // the outputs are rarely rescaled.
+          float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            float mx[2] = {-INFINITY, -INFINITY};
+          for (int n8 = 0; n8 < 4; ++n8)
 #pragma unroll
-            for (int nt2 = 0; nt2 < 2; ++nt2)
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                float v = sc[mt][nt2][c] * P.scale_log2;
-                if (edge && key0 + nt2 * 8 + kq + (c & 1) > lim[mt][c >> 1]) v = -INFINITY;
-                sc[mt][nt2][c] = v;
-                mx[c >> 1] = fmaxf(mx[c >> 1], v);
-              }
+            for (int c = 0; c < 4; ++c) {
+              float v = sc[n8][c] * P.scale_log2;
+              if (edge && key0 + n8 * 8 + kq + (c & 1) > lim[c >> 1]) v = -INFINITY;
+              sc[n8][c] = v;
+              mx[c >> 1] = fmaxf(mx[c >> 1], v);
+            }
+          if (__any_sync(0xffffffffu, mx[0] > m_[0] + 8.f || mx[1] > m_[1] + 8.f)) {
             float corr[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
               mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-              const float mnew = fmaxf(m_[mt][h], mx[h]);
-              const float base = mnew == -INFINITY ? 0.f : mnew;
-              corr[h] = ex2(m_[mt][h] - base);
-              m_[mt][h] = mnew;
-              mx[h] = base;
+              const float mnew = fmaxf(m_[h], mx[h]);
+              corr[h] = ex2(m_[h] - (mnew == -INFINITY ? 0.f : mnew));
+              m_[h] = mnew;
+              l_[h] *= corr[h];
             }
-            float ls[2] = {0.f, 0.f};
-#pragma unroll
-            for (int nt2 = 0; nt2 < 2; ++nt2)
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const float p = ex2(sc[mt][nt2][c] - mx[c >> 1]);
-                sc[mt][nt2][c] = p;
-                ls[c >> 1] += p;
-              }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) l_[mt][h] = l_[mt][h] * corr[h] + ls[h];
 #pragma unroll
             for (int nt2 = 0; nt2 < NT; ++nt2) {
-              o[mt][nt2][0] *= corr[0];
-              o[mt][nt2][1] *= corr[0];
-              o[mt][nt2][2] *= corr[1];
-              o[mt][nt2][3] *= corr[1];
+              o[nt2][0] *= corr[0];
+              o[nt2][1] *= corr[0];
+              o[nt2][2] *= corr[1];
+              o[nt2][3] *= corr[1];
             }
-            // the probabilities in the cache's type for the tensor cores, at most half a step
-            // of it from their fp32 values; their sum keeps fp32
-            pa[mt][0] = pack2<BF16>(sc[mt][0][0], sc[mt][0][1]);
-            pa[mt][1] = pack2<BF16>(sc[mt][0][2], sc[mt][0][3]);
-            pa[mt][2] = pack2<BF16>(sc[mt][1][0], sc[mt][1][1]);
-            pa[mt][3] = pack2<BF16>(sc[mt][1][2], sc[mt][1][3]);
+          }
+          const float base[2] = {m_[0] == -INFINITY ? 0.f : m_[0], m_[1] == -INFINITY ? 0.f : m_[1]};
+          float ls[2] = {0.f, 0.f};
+#pragma unroll
+          for (int n8 = 0; n8 < 4; ++n8)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const float p = ex2(sc[n8][c] - base[c >> 1]);
+              sc[n8][c] = p;
+              ls[c >> 1] += p;
+            }
+          l_[0] += ls[0];
+          l_[1] += ls[1];
+          // the probabilities in the cache's type for the tensor cores, at most half a step of it
+          // from their fp32 values; their sum keeps fp32
+          uint32_t pa[2][4];
+#pragma unroll
+          for (int k16 = 0; k16 < 2; ++k16) {
+            pa[k16][0] = pack2<BF16>(sc[2 * k16][0], sc[2 * k16][1]);
+            pa[k16][1] = pack2<BF16>(sc[2 * k16][2], sc[2 * k16][3]);
+            pa[k16][2] = pack2<BF16>(sc[2 * k16 + 1][0], sc[2 * k16 + 1][1]);
+            pa[k16][3] = pack2<BF16>(sc[2 * k16 + 1][2], sc[2 * k16 + 1][3]);
           }
           // O += P V. Matrices 0..3: keys 0-7 dims lo, keys 8-15 dims lo, keys 0-7 dims hi, keys 8-15 dims hi
-          const int vkey = sl * kSlice + (mi & 1) * 8 + (lane & 7);
+          const int vkey = half * kStep + (mi & 1) * 8 + (lane & 7);
           if (!edge) {
 #pragma unroll
-            for (int dp = 0; dp < D / 16; ++dp) {
-              uint32_t b[4];
-              ldsm4<true>(tile_addr(vb, vkey, dp * 16 + (mi >> 1) * 8), b);
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                mma16816<BF16>(o[mt][2 * dp], pa[mt], b[0], b[1]);
-                mma16816<BF16>(o[mt][2 * dp + 1], pa[mt], b[2], b[3]);
-              }
-            }
-          } else {
-            // What lies behind the last key may be anything (0 * NaN is NaN): cleared. A key
-            // that is in the cache but hidden from some row may be infinite or NaN: then the
-            // slice's products are taken one key at a time, for the rows that see it.
-            uint32_t keep[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int key = key0 + h * 8 + kq;
-              keep[h] = (key < nk ? 0xffffu : 0u) | (key + 1 < nk ? 0xffff0000u : 0u);
-            }
-            bool odd = false;
-            if (n_new > 1) {
+            for (int k16 = 0; k16 < 2; ++k16)
 #pragma unroll
               for (int dp = 0; dp < D / 16; ++dp) {
                 uint32_t b[4];
-                ldsm4<true>(tile_addr(vb, vkey, dp * 16 + (mi >> 1) * 8), b);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) odd |= non_finite2<BF16>(b[x] & keep[x & 1]);
+                ldsm4<true>(tile_addr(vb, vkey + k16 * 16, dp * 16 + (mi >> 1) * 8), b);
+                mma16816<BF16>(o[2 * dp], pa[k16], b[0], b[1]);
+                mma16816<BF16>(o[2 * dp + 1], pa[k16], b[2], b[3]);
               }
+          } else {
+            // What lies behind the last key may be anything (0 * NaN is NaN): cleared. A key
+            // that is in the cache but hidden from some row may be infinite or NaN: then the
+            // step's products are taken one key at a time, for the rows that see it.
+            uint32_t keep[2][2];
+#pragma unroll
+            for (int k16 = 0; k16 < 2; ++k16)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int key = key0 + k16 * 16 + h * 8 + kq;
+                keep[k16][h] = (key < nk ? 0xffffu : 0u) | (key + 1 < nk ? 0xffff0000u : 0u);
+              }
+            bool odd = false;
+            if (n_new > 1) {
+#pragma unroll
+              for (int k16 = 0; k16 < 2; ++k16)
+#pragma unroll 1
+                for (int dp = 0; dp < D / 16; ++dp) {
+                  uint32_t b[4];
+                  ldsm4<true>(tile_addr(vb, vkey + k16 * 16, dp * 16 + (mi >> 1) * 8), b);
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) odd |= non_finite2<BF16>(b[x] & keep[k16][x & 1]);
+                }
               odd = __any_sync(0xffffffffu, odd);
             }
             if (!odd) {
 #pragma unroll
-              for (int dp = 0; dp < D / 16; ++dp) {
-                uint32_t b[4];
-                ldsm4<true>(tile_addr(vb, vkey, dp * 16 + (mi >> 1) * 8), b);
+              for (int k16 = 0; k16 < 2; ++k16)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) b[x] &= keep[x & 1];
+                for (int dp = 0; dp < D / 16; ++dp) {
+                  uint32_t b[4];
+                  ldsm4<true>(tile_addr(vb, vkey + k16 * 16, dp * 16 + (mi >> 1) * 8), b);
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                  mma16816<BF16>(o[mt][2 * dp], pa[mt], b[0], b[1]);
-                  mma16816<BF16>(o[mt][2 * dp + 1], pa[mt], b[2], b[3]);
+                  for (int x = 0; x < 4; ++x) b[x] &= keep[k16][x & 1];
+                  mma16816<BF16>(o[2 * dp], pa[k16], b[0], b[1]);
+                  mma16816<BF16>(o[2 * dp + 1], pa[k16], b[2], b[3]);
                 }
-              }
             } else {
+#pragma unroll 1
+              for (int x = 0; x < kStep && key0 + x < nk; ++x) {
+                float mine[2];  // the weights that this lane may hold of key x, by row
 #pragma unroll
-              for (int x = 0; x < kSlice; ++x) {
-                const int key = key0 + x;
-                if (key < nk) {
+                for (int h = 0; h < 2; ++h) {
+                  float v = 0.f;
 #pragma unroll
-                  for (int mt = 0; mt < MT; ++mt) {
-                    const int from = (lane & ~3) + ((x & 7) >> 1);
-                    const float pr0 = __shfl_sync(0xffffffffu, sc[mt][x >> 3][x & 1], from);
-                    const float pr1 = __shfl_sync(0xffffffffu, sc[mt][x >> 3][2 + (x & 1)], from);
+                  for (int n8 = 0; n8 < 4; ++n8)
+                    if (x >> 3 == n8) v = x & 1 ? sc[n8][2 * h + 1] : sc[n8][2 * h];
+                  mine[h] = v;
+                }
+                const int from = (lane & ~3) + ((x & 7) >> 1);
+                const float p0 = __shfl_sync(0xffffffffu, mine[0], from), p1 = __shfl_sync(0xffffffffu, mine[1], from);
+                const bool see0 = key0 + x <= lim[0], see1 = key0 + x <= lim[1];
 #pragma unroll
-                    for (int nt2 = 0; nt2 < NT; ++nt2) {
-                      uint32_t raw;
-                      asm volatile("ld.shared.b32 %0, [%1];"
-                                   : "=r"(raw)
-                                   : "r"(tile_addr(vb, sl * kSlice + x, nt2 * 8 + kq))
-                                   : "memory");
-                      const float2 v = unpack2<BF16>(raw);
-                      if (key <= lim[mt][0]) {
-                        o[mt][nt2][0] += pr0 * v.x;
-                        o[mt][nt2][1] += pr0 * v.y;
-                      }
-                      if (key <= lim[mt][1]) {
-                        o[mt][nt2][2] += pr1 * v.x;
-                        o[mt][nt2][3] += pr1 * v.y;
-                      }
-                    }
-                  }
+                for (int nt2 = 0; nt2 < NT; ++nt2) {
+                  uint32_t raw;
+                  asm volatile("ld.shared.b32 %0, [%1];"
+                               : "=r"(raw)
+                               : "r"(tile_addr(vb, half * kStep + x, nt2 * 8 + kq))
+                               : "memory");
+                  const float2 v = unpack2<BF16>(raw);
+                  if (see0) o[nt2][0] += p0 * v.x, o[nt2][1] += p0 * v.y;
+                  if (see1) o[nt2][2] += p1 * v.x, o[nt2][3] += p1 * v.y;
                 }
               }
             }
@@ -519,79 +513,63 @@ __global__ void __launch_bounds__(Layout<D, MT, RG, KG, STAGES>::kThreads, 1)
     if (lane == 0) mbar_arrive(&qempty[qb]);
     // row sums over the four lanes of a row
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        l_[mt][h] += __shfl_xor_sync(0xffffffffu, l_[mt][h], 1);
-        l_[mt][h] += __shfl_xor_sync(0xffffffffu, l_[mt][h], 2);
-      }
+    for (int h = 0; h < 2; ++h) {
+      l_[h] += __shfl_xor_sync(0xffffffffu, l_[h], 1);
+      l_[h] += __shfl_xor_sync(0xffffffffu, l_[h], 2);
+    }
     // ---- the key groups' states into one: o = sum_k 2^(m_k - M) o_k, l alike
     // (max, sum) of every row and group first, then the outputs, in fragment order
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if ((lane & 3) == 0) s_ml[kg * L::kRows + mrow0 + mt * 16 + h * 8 + r0] = make_float2(m_[mt][h], l_[mt][h]);
+    for (int h = 0; h < 2; ++h)
+      if ((lane & 3) == 0) s_ml[kg * L::kRows + mrow0 + h * 8 + r0] = make_float2(m_[h], l_[h]);
     if (L::kAllAtOnce) {
 #pragma unroll
       for (int nt2 = 0; nt2 < NT; ++nt2)
-        s_x[(kg * NT + nt2) * 32 + lane] = make_float4(o[0][nt2][0], o[0][nt2][1], o[0][nt2][2], o[0][nt2][3]);
+        s_x[(kg * NT + nt2) * 32 + lane] = make_float4(o[nt2][0], o[nt2][1], o[nt2][2], o[nt2][3]);
     }
     named_bar_sync(1, 32 * L::kWarps);
-    float M[MT][2], den[MT][2];
+    float M[2], den[2], w[KG][2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int h = 0; h < 2; ++h) {
+      const int row = mrow0 + h * 8 + r0;
+      float top = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = mrow0 + mt * 16 + h * 8 + r0;
-        float top = -INFINITY, sum = 0.f;
+      for (int k = 0; k < KG; ++k) top = fmaxf(top, s_ml[k * L::kRows + row].x);
 #pragma unroll
-        for (int k = 0; k < KG; ++k) top = fmaxf(top, s_ml[k * L::kRows + row].x);
-#pragma unroll
-        for (int k = 0; k < KG; ++k) {
-          const float2 ml = s_ml[k * L::kRows + row];
-          sum += ml.x == -INFINITY ? 0.f : ml.y * ex2(ml.x - top);
-        }
-        M[mt][h] = top;
-        den[mt][h] = sum;
+      for (int k = 0; k < KG; ++k) {
+        const float2 ml = s_ml[k * L::kRows + row];
+        w[k][h] = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+        sum += ml.x == -INFINITY ? 0.f : w[k][h] * ml.y;
       }
+      M[h] = top;
+      den[h] = sum;
+    }
     const bool whole = t0 == 0 && seg == nt;
     // finished rows to the output, a cut pair's to this CTA's slot
     float* slot = P.part + (2 * static_cast<size_t>(cta) + (seg_no == 0 ? 0 : 1)) * static_cast<size_t>(L::kRows) * (D + 2);
-    auto put = [&](int mt, int nt2, const float (&v)[4]) {
+    uint16_t* dst[2];
+    bool there[2];
+    float inv[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = mrow0 + h * 8 + r0, r = row / grp, hh = row - r * grp;
+      there[h] = row < n_new * grp;
+      inv[h] = den[h] > 0.f ? 1.f / den[h] : (den[h] == 0.f ? 0.f : den[h]);
+      dst[h] = static_cast<uint16_t*>(P.out) + ((static_cast<size_t>(s) * P.rows_per_seq + r) * P.nq + static_cast<size_t>(g) * grp + hh) * D;
+    }
+    auto put = [&](int nt2, const float (&v)[4]) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int row = mrow0 + mt * 16 + h * 8 + r0;
-        if (row >= n_new * grp) continue;
-        if (whole) {
-          const float inv = den[mt][h] > 0.f ? 1.f / den[mt][h] : (den[mt][h] == 0.f ? 0.f : den[mt][h]);
-          const int r = row / grp, hh = row - r * grp;
-          uint16_t* dst = static_cast<uint16_t*>(P.out) +
-                          ((static_cast<size_t>(s) * P.rows_per_seq + r) * P.nq + static_cast<size_t>(g) * grp + hh) * D;
-          *reinterpret_cast<uint32_t*>(dst + nt2 * 8 + kq) = pack2<BF16>(v[2 * h] * inv, v[2 * h + 1] * inv);
-        } else {
-          __stcg(reinterpret_cast<float2*>(slot + static_cast<size_t>(row) * D + nt2 * 8 + kq),
+        if (!there[h]) continue;
+        if (whole)
+          *reinterpret_cast<uint32_t*>(dst[h] + nt2 * 8 + kq) = pack2<BF16>(v[2 * h] * inv[h], v[2 * h + 1] * inv[h]);
+        else
+          __stcg(reinterpret_cast<float2*>(slot + static_cast<size_t>(mrow0 + h * 8 + r0) * D + nt2 * 8 + kq),
                  make_float2(v[2 * h], v[2 * h + 1]));
-        }
       }
-    };
-    auto put_ml = [&](int mt) {
-      if (!whole && (lane & 3) == 0)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          __stcg(reinterpret_cast<float2*>(slot + static_cast<size_t>(L::kRows) * D) + mrow0 + mt * 16 + h * 8 + r0,
-                 make_float2(M[mt][h], den[mt][h]));
     };
     if (L::kAllAtOnce) {
       // each key group finishes its share of the columns
-      float w[KG][2];
-#pragma unroll
-      for (int k = 0; k < KG; ++k)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float mk = s_ml[k * L::kRows + h * 8 + r0].x;
-          w[k][h] = mk == -INFINITY ? 0.f : ex2(mk - M[0][h]);
-        }
 #pragma unroll
       for (int n4 = 0; n4 < NT / KG; ++n4) {
         const int nt2 = kg * (NT / KG) + n4;
@@ -604,57 +582,50 @@ __global__ void __launch_bounds__(Layout<D, MT, RG, KG, STAGES>::kThreads, 1)
           v[2] += w[k][1] * x.z;
           v[3] += w[k][1] * x.w;
         }
-        put(0, nt2, v);
+        put(nt2, v);
       }
-      if (kg == 0) put_ml(0);
     } else {
       // one group after another through one buffer per row group, into group 0
-      float4* xb = s_x + static_cast<size_t>(rg) * MT * NT * 32;
+      float4* xb = s_x + static_cast<size_t>(rg) * NT * 32;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        float w[2];
+      for (int nt2 = 0; nt2 < NT; ++nt2) {
+        float w0 = w[0][0], w1 = w[0][1];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) w[h] = m_[mt][h] == -INFINITY ? 0.f : ex2(m_[mt][h] - M[mt][h]);
-#pragma unroll
-        for (int nt2 = 0; nt2 < NT; ++nt2) {
-          o[mt][nt2][0] *= w[0];
-          o[mt][nt2][1] *= w[0];
-          o[mt][nt2][2] *= w[1];
-          o[mt][nt2][3] *= w[1];
-        }
+        for (int k = 1; k < KG; ++k)
+          if (kg == k) w0 = w[k][0], w1 = w[k][1];
+        o[nt2][0] *= w0;
+        o[nt2][1] *= w0;
+        o[nt2][2] *= w1;
+        o[nt2][3] *= w1;
       }
 #pragma unroll
       for (int k = 1; k < KG; ++k) {
         if (kg == k) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int nt2 = 0; nt2 < NT; ++nt2)
-              xb[(mt * NT + nt2) * 32 + lane] = make_float4(o[mt][nt2][0], o[mt][nt2][1], o[mt][nt2][2], o[mt][nt2][3]);
+          for (int nt2 = 0; nt2 < NT; ++nt2) xb[nt2 * 32 + lane] = make_float4(o[nt2][0], o[nt2][1], o[nt2][2], o[nt2][3]);
         }
         named_bar_sync(1, 32 * L::kWarps);
         if (kg == 0) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int nt2 = 0; nt2 < NT; ++nt2) {
-              const float4 x = xb[(mt * NT + nt2) * 32 + lane];
-              o[mt][nt2][0] += x.x;
-              o[mt][nt2][1] += x.y;
-              o[mt][nt2][2] += x.z;
-              o[mt][nt2][3] += x.w;
-            }
+          for (int nt2 = 0; nt2 < NT; ++nt2) {
+            const float4 x = xb[nt2 * 32 + lane];
+            o[nt2][0] += x.x;
+            o[nt2][1] += x.y;
+            o[nt2][2] += x.z;
+            o[nt2][3] += x.w;
+          }
         }
-        named_bar_sync(1, 32 * L::kWarps);
+        if (k + 1 < KG) named_bar_sync(1, 32 * L::kWarps);
       }
       if (kg == 0) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-          for (int nt2 = 0; nt2 < NT; ++nt2) put(mt, nt2, o[mt][nt2]);
-          put_ml(mt);
-        }
+        for (int nt2 = 0; nt2 < NT; ++nt2) put(nt2, o[nt2]);
       }
+    }
+    if (kg == 0 && !whole && (lane & 3) == 0) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        __stcg(reinterpret_cast<float2*>(slot + static_cast<size_t>(L::kRows) * D) + mrow0 + h * 8 + r0, make_float2(M[h], den[h]));
     }
     named_bar_sync(1, 32 * L::kWarps);  // the exchange buffers are the next segment's
     u += seg;
@@ -727,11 +698,11 @@ __global__ void __launch_bounds__(256) paged_attn_join_kernel(const __grid_const
 
 template <int D>
 struct Stages {
-  static constexpr int few = D == 128 ? 5 : 10, mid = D == 128 ? 4 : 8, many = D == 128 ? 5 : 10;
+  static constexpr int few = D == 128 ? 4 : 8, mid = D == 128 ? 4 : 8, many = D == 128 ? 5 : 10;
 };
 
-// Variants by rows of a problem: up to 16 and 32 as one row group and four key groups, 64 as
-// four row groups of 16 and two key groups, 128 as eight row groups.
+// Variants by rows of a problem: up to 16 rows as one row group and four key groups, 32 as two
+// and four, 64 as four and two, 128 as eight row groups.
 template <typename F>
 int with_variant(int rows, F&& f) {
   if (rows <= 16) return f(std::integral_constant<int, 0>());
@@ -744,34 +715,34 @@ template <int D, int V>
 struct Variant;
 template <int D>
 struct Variant<D, 0> {
-  static constexpr int MT = 1, RG = 1, KG = 4, ST = Stages<D>::few;
+  static constexpr int RG = 1, KG = 4, ST = Stages<D>::few;
 };
 template <int D>
 struct Variant<D, 1> {
-  static constexpr int MT = 2, RG = 1, KG = 4, ST = Stages<D>::few;
+  static constexpr int RG = 2, KG = 4, ST = Stages<D>::few;
 };
 template <int D>
 struct Variant<D, 2> {
-  static constexpr int MT = 1, RG = 4, KG = 2, ST = Stages<D>::mid;
+  static constexpr int RG = 4, KG = 2, ST = Stages<D>::mid;
 };
 template <int D>
 struct Variant<D, 3> {
-  static constexpr int MT = 1, RG = 8, KG = 1, ST = Stages<D>::many;
+  static constexpr int RG = 8, KG = 1, ST = Stages<D>::many;
 };
 
 template <int D, bool BF16, int V>
 int set_attr() {
   using W = Variant<D, V>;
-  using L = Layout<D, W::MT, W::RG, W::KG, W::ST>;
+  using L = Layout<D, W::RG, W::KG, W::ST>;
   static_assert(L::smem(kCacheMaxBatch) <= 232448, "shared memory of a CTA");
-  return static_cast<int>(cudaFuncSetAttribute(paged_attn_kernel<D, BF16, W::MT, W::RG, W::KG, W::ST>,
+  return static_cast<int>(cudaFuncSetAttribute(paged_attn_kernel<D, BF16, W::RG, W::KG, W::ST>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, L::smem(kCacheMaxBatch)));
 }
 
 template <int D, bool BF16, int V>
 int launch(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
   using W = Variant<D, V>;
-  using L = Layout<D, W::MT, W::RG, W::KG, W::ST>;
+  using L = Layout<D, W::RG, W::KG, W::ST>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(n_ctas);
   cfg.blockDim = dim3(L::kThreads);
@@ -782,7 +753,7 @@ int launch(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<D, BF16, W::MT, W::RG, W::KG, W::ST>, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<D, BF16, W::RG, W::KG, W::ST>, p);
   if (e != cudaSuccess) return static_cast<int>(e);
   cfg.gridDim = dim3(p.batch * p.nkv, (p.rows + 7) / 8);
   cfg.blockDim = dim3(256);
