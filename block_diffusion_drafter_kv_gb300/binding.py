@@ -366,7 +366,9 @@ def _require_on(t, dtype, numel, name, device):
 
 def _stream_on(stream, device) -> int:
     import torch
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 _DTYPES = {"torch.float32": F32, "torch.float16": F16, "torch.bfloat16": BF16}
@@ -480,18 +482,15 @@ class PagedCache:
         rows of heads x dims, rows a stride apart (slices of one fused projection are fine);
         q and q_out may be None."""
         import torch
-        rows = batch * rows_per_seq
-        dt = k.dtype
-        for t, n, name in ((q, self._q_row, "q"), (k, self._kv_row, "k"), (v, self._kv_row, "v")):
-            if t is not None and (t.dtype != dt or t.device != self.device or t.shape[0] != rows or t.numel() != rows * n
-                                  or not _rows_dense(t)):
-                raise DFlashError(DFLASH_E_INVAL, f"{name} must be {rows} dense rows of {n} values of one type on {self.device}")
-        _require_on(slots, torch.int32, rows, "slots", self.device)
-        _require_on(q_out, self.dtype, rows * self._q_row, "q_out", self.device)
+        rows, dev, dt = batch * rows_per_seq, self.device, k.dtype
+        q_stride = 0 if q is None else _row_stride(q, dt, rows, self._q_row, "q", dev)
+        k_stride = _row_stride(k, dt, rows, self._kv_row, "k", dev)
+        v_stride = _row_stride(v, dt, rows, self._kv_row, "v", dev)
+        _require_on(slots, torch.int32, rows, "slots", dev)
+        _require_on(q_out, self.dtype, rows * self._q_row, "q_out", dev)
         check(self.L.dflash_cache_append(self.c, layer, _ptr(q), k.data_ptr(), v.data_ptr(), _DTYPES.get(str(dt), -1),
-                                         0 if q is None else _row_stride(q, self._q_row), _row_stride(k, self._kv_row),
-                                         _row_stride(v, self._kv_row), slots.data_ptr(), batch, rows_per_seq, _ptr(q_out),
-                                         _stream_on(stream, self.device)), "dflash_cache_append")
+                                         q_stride, k_stride, v_stride, slots.data_ptr(), batch, rows_per_seq, _ptr(q_out),
+                                         _stream_on(stream, dev)), "dflash_cache_append")
 
     def attend(self, layer: int, q, n_new, batch: int, rows_per_seq: int, out, stream=None):
         """Causal attention of row r of every sequence (position length[s] + r, r < n_new[s]) over
@@ -529,14 +528,17 @@ def _require_min(t, dtype, numel, name, device):
         raise DFlashError(DFLASH_E_INVAL, f"{name} must be a contiguous {dtype} tensor of at least {numel} values on {device}")
 
 
-def _row_stride(t, row: int) -> int:
-    """Elements from one row to the next (a single row's stride means nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else max(row, t.stride(0) // 8 * 8)
-
-
-def _rows_dense(t) -> bool:
-    """Whether each row t[i] is contiguous."""
-    return t.stride(-1) == 1 and (t.dim() == 2 or (t.dim() == 3 and (t.shape[1] == 1 or t.stride(1) == t.shape[2])))
+def _row_stride(t, dtype, rows: int, row: int, name, device) -> int:
+    """Elements from one row of a [rows][row] or [rows][heads][dims] tensor to the next; each row
+    has to be dense."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3:
+        dense = shape[1] * shape[2] == row and stride[2] == 1 and (shape[1] == 1 or stride[1] == shape[2])
+    else:
+        dense = len(shape) == 2 and shape[1] == row and stride[1] == 1
+    if not dense or shape[0] != rows or t.dtype != dtype or t.device != device:
+        raise DFlashError(DFLASH_E_INVAL, f"{name} must be {rows} dense rows of {row} values of one type on {device}")
+    return stride[0] if rows > 1 else max(row, stride[0] // 8 * 8)   # a single row's stride means nothing
 
 
 def rope_tables(n_positions: int, rope_dim: int, theta: float, linear: float = 1.0, bands=None, attention_factor: float = 1.0,

@@ -567,11 +567,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
       P.top_logprobs[to] = empty ? -INFINITY : (from_order_bits(static_cast<uint32_t>(list >> 32)) - top) * P.inv_temp - ls;
     }
   };
-  // a CTA's part of the row that it begins with, or of the row that it ends with; a row's counter is
-  // that of the first CTA that has a part of it
-  auto slot_of = [&](int c, long long base) {
-    return P.part + (2 * static_cast<size_t>(c) + (range_begin(c, U, G) >= base ? 0 : 1)) * kLpSlotWords;
-  };
+  // a CTA's part of the row that it begins with (0), or of the row that it ends with (1); a row's
+  // counter is that of the first CTA that has a part of it
+  auto slot_of = [&](int c, int which) { return P.part + (2 * static_cast<size_t>(c) + which) * kLpSlotWords; };
 
   int n = 0, seg_no = 0;
   int rank = r0, u0 = u00;
@@ -668,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
       } else {
         const long long base = static_cast<long long>(rank) * per_row;
         const int c0 = cta_of(base, U, G), c1 = cta_of(base + per_row - 1, U, G);
-        float* slot = slot_of(cta, base);
+        float* slot = slot_of(cta, base > U0);
         if (lane == 0) __stcg(reinterpret_cast<float4*>(slot), make_float4(p.M, p.S, p.W, 0.f));
         if (lane < k) __stcg(reinterpret_cast<Key*>(slot + 4) + lane, list);
         __threadfence();
@@ -690,6 +688,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
     const int rank = which == 0 ? r0 : static_cast<int>((U1 - 1) / per_row), row = row_of(rank);
     const long long base = static_cast<long long>(rank) * per_row;
     const int c0 = cta_of(base, U, G), c1 = cta_of(base + per_row - 1, U, G);
+    // the row is the first of every CTA that has a part of it but perhaps c0
+    const int c0_which = range_begin(c0, U, G) < base;
     if (TOP) {
       list = 0;
 #pragma unroll 1
@@ -698,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int from = c + i * kWarps;
-          other[i] = from <= c1 && lane < k ? __ldcg(reinterpret_cast<const Key*>(slot_of(from, base) + 4) + lane) : 0;
+          other[i] = from <= c1 && lane < k ? __ldcg(reinterpret_cast<const Key*>(slot_of(from, from == c0 ? c0_which : 0) + 4) + lane) : 0;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) list = merge_lists(list, other[i]);
@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
       if (TOP) list = merge_eight(sh.list);
       Part p = {-INFINITY, 0.f, 0.f};
       for (int c = c0 + lane; c <= c1; c += 32) {
-        const float4 q = __ldcg(reinterpret_cast<const float4*>(slot_of(c, base)));
+        const float4 q = __ldcg(reinterpret_cast<const float4*>(slot_of(c, c == c0 ? c0_which : 0)));
         p = sc.join(p, Part{q.x, q.y, q.z});
       }
       p = join_lanes(p, 32);

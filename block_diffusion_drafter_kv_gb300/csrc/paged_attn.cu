@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(Layout<D, RG, KG, STAGES>::kThreads, 1) paged_
     s = lo;
     nt = s_pre[s + 1] - s_pre[s];
     const long long rest = u - static_cast<long long>(nkv) * s_pre[s];
-    g = static_cast<int>(rest / nt);
+    g = static_cast<int>(rest < (1ll << 32) ? static_cast<uint32_t>(rest) / static_cast<uint32_t>(nt) : rest / nt);
     t = static_cast<int>(rest - static_cast<long long>(g) * nt);
   };
   // Every wait is bounded: past the limit the flag is set, later waits pass at once and the
@@ -652,8 +652,10 @@ __global__ void __launch_bounds__(256) paged_attn_join_kernel(const __grid_const
   const int c0 = cta_of(base, T, G), c1 = cta_of(base + nt - 1, T, G);
   if (c0 == c1) return;
   const size_t slot_floats = static_cast<size_t>(slot_rows) * (D + 2);
-  // a CTA whose range starts inside the pair or with it has it as its first segment
-  auto slot_of = [&](int c) { return P.part + (2 * static_cast<size_t>(c) + (range_begin(c, T, G) >= base ? 0 : 1)) * slot_floats; };
+  // The pair is the first segment of every CTA whose range starts with it or inside it: of all but
+  // perhaps c0. (Asking each range's start, a 64-bit division, took most of this kernel's time.)
+  const int c0_second = range_begin(c0, T, G) < base;
+  auto slot_of = [&](int c) { return P.part + (2 * static_cast<size_t>(c) + (c == c0 ? c0_second : 0)) * slot_floats; };
   float M = -INFINITY;
   for (int c = c0 + lane; c <= c1; c += 32)
     M = fmaxf(M, __ldcg(reinterpret_cast<const float2*>(slot_of(c) + static_cast<size_t>(slot_rows) * D) + row).x);

@@ -24,6 +24,7 @@ struct PageParams {
   const int* n_new;  // reserve only
   int* slots;        // reserve only; null: none wanted
   int batch, rows_per_seq;
+  int wide;          // slots is 16-byte aligned
 };
 
 // Exclusive prefix sum of `mine` over the block's threads; `total` gets the sum.
@@ -58,9 +59,8 @@ DEV int owner_of(const int* s_off, int batch, int i) {
   return lo;
 }
 
-// Pages that sequence s wants beyond those it holds; -1 where its lengths are out of range.
-DEV int pages_wanted(const PageParams& P, int s, int held) {
-  const int len = __ldcg(P.len + s), n = __ldcg(P.n_new + s);
+// Pages that a sequence wants beyond those it holds; -1 where its lengths are out of range.
+DEV int pages_wanted(const PageParams& P, int len, int n, int held) {
   if (len < 0 || n < 0 || n > P.rows_per_seq || held < 0 || held > P.p.pages_per_seq) return -1;
   const long long need = (static_cast<long long>(len) + n + kPagePos - 1) / kPagePos;
   if (need > P.p.pages_per_seq) return -1;
@@ -68,24 +68,33 @@ DEV int pages_wanted(const PageParams& P, int s, int held) {
 }
 
 __global__ void __launch_bounds__(kThreads) pages_reserve_kernel(const PageParams P) {
-  extern __shared__ int s_off[];  // [batch] number of the sequence's first new page
-  int* s_new = s_off + P.batch;   // [batch] its new pages; -1: refused
+  extern __shared__ int s_off[];    // [batch] number of the sequence's first new page
+  int* s_new = s_off + P.batch;     // [batch] its new pages; -1: refused
+  int* s_held = s_new + P.batch;    // [batch] the pages it holds
+  int* s_len = s_held + P.batch;    // [batch]
+  int* s_rows = s_len + P.batch;    // [batch] its new rows, 0 if it is refused
   __shared__ long long warp_sum[kThreads / 32];
   __shared__ int s_total, s_last;
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, batch = P.batch;
   const int n_free = min(max(__ldcg(P.p.state), 0), P.p.n_pages);
+  for (int s = tid; s < batch; s += kThreads) {
+    s_held[s] = __ldcg(P.p.held + s);
+    s_len[s] = __ldcg(P.len + s);
+    s_rows[s] = __ldcg(P.n_new + s);
+  }
+  if (tid == 0) s_total = 0;
+  __syncthreads();
   // each thread a run of neighbouring sequences
   const int per = (batch + kThreads - 1) / kThreads;
   const int s0 = min(tid * per, batch), s1 = min(s0 + per, batch);
   long long mine = 0;
   for (int s = s0; s < s1; ++s) {
-    const int w = pages_wanted(P, s, __ldcg(P.p.held + s));
+    const int w = pages_wanted(P, s_len[s], s_rows[s], s_held[s]);
     s_new[s] = w;
     mine += max(w, 0);
   }
-  if (tid == 0) s_total = 0;
   long long total;
   long long off = block_scan(mine, warp_sum, total);
   int served = 0;
@@ -99,45 +108,67 @@ __global__ void __launch_bounds__(kThreads) pages_reserve_kernel(const PageParam
       if (off > n_free) s_new[s] = -1;
       else served = static_cast<int>(off);
     }
-    refused |= s_new[s] < 0;
+    if (s_new[s] < 0) {
+      refused = true;
+      s_rows[s] = 0;
+    }
   }
   if (refused && blockIdx.x == 0) raise_flag(P.p.state + 2, kDevCapacity);
   if (served) atomicMax(&s_total, served);
   __syncthreads();
   const int N = s_total;
   // owner_of() never names a refused sequence: the first of them starts at N, the rest later.
+  const int* newest = P.p.free_list + n_free - 1;  // page number i of the call is newest[-i]
   const long long stride = static_cast<long long>(gridDim.x) * kThreads;
   const long long me = static_cast<long long>(blockIdx.x) * kThreads + tid;
   for (long long i = me; i < N; i += stride) {
     const int s = owner_of(s_off, batch, static_cast<int>(i));
-    const int j = __ldcg(P.p.held + s) + static_cast<int>(i) - s_off[s];
-    P.p.page_table[static_cast<size_t>(s) * P.p.pages_per_seq + j] = __ldcg(P.p.free_list + n_free - 1 - i);
+    const int j = s_held[s] + static_cast<int>(i) - s_off[s];
+    P.p.page_table[static_cast<size_t>(s) * P.p.pages_per_seq + j] = __ldcg(newest - i);
   }
   if (P.slots) {
-    const long long rows = static_cast<long long>(batch) * P.rows_per_seq;
-    for (long long row = me; row < rows; row += stride) {
-      const int s = static_cast<int>(row / P.rows_per_seq);
-      const int r = static_cast<int>(row - static_cast<long long>(s) * P.rows_per_seq);
-      int slot = -1;
-      if (s_new[s] >= 0 && r < __ldcg(P.n_new + s)) {
-        const int pos = __ldcg(P.len + s) + r, j = pos / kPagePos, held = __ldcg(P.p.held + s);
-        const int page = j < held ? __ldcg(P.p.page_table + static_cast<size_t>(s) * P.p.pages_per_seq + j)
-                                  : __ldcg(P.p.free_list + n_free - 1 - (s_off[s] + j - held));
-        slot = page * kPagePos + pos % kPagePos;
+    auto page_of = [&](int s, int j) {
+      return j < s_held[s] ? __ldcg(P.p.page_table + static_cast<size_t>(s) * P.p.pages_per_seq + j)
+                           : __ldcg(newest - (s_off[s] + j - s_held[s]));
+    };
+    const uint32_t rows = static_cast<uint32_t>(batch) * P.rows_per_seq;  // < 2^31
+    const uint32_t quads = (rows + 3) / 4;
+    for (uint32_t q = static_cast<uint32_t>(me); q < quads; q += static_cast<uint32_t>(stride)) {
+      int s = static_cast<int>(4 * q / P.rows_per_seq), r = static_cast<int>(4 * q - static_cast<uint32_t>(s) * P.rows_per_seq);
+      int slot[4], j = -1, page = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        slot[e] = -1;
+        if (s < batch && r < s_rows[s]) {
+          const int pos = s_len[s] + r;
+          if (pos / kPagePos != j) page = page_of(s, j = pos / kPagePos);
+          slot[e] = page * kPagePos + pos % kPagePos;
+        }
+        if (++r == P.rows_per_seq) r = 0, ++s, j = -1;
       }
-      P.slots[row] = slot;
+      if (P.wide && 4 * q + 3 < rows) {
+        *reinterpret_cast<int4*>(P.slots + 4 * static_cast<size_t>(q)) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (4 * q + e < rows) P.slots[4 * static_cast<size_t>(q) + e] = slot[e];
+      }
     }
   }
-  __syncthreads();  // every thread of this CTA has read held and the list's length
+  __syncthreads();
+  // every CTA has read the held counts and the list's length before the last one writes them
   if (tid == 0) {
-    __threadfence();
-    s_last = atomicAdd(P.p.state + 1, 1) == static_cast<int>(gridDim.x) - 1;
+    s_last = 1;
+    if (gridDim.x > 1) {
+      __threadfence();
+      s_last = atomicAdd(P.p.state + 1, 1) == static_cast<int>(gridDim.x) - 1;
+      __threadfence();
+    }
   }
   __syncthreads();
   if (!s_last) return;
-  __threadfence();
   for (int s = s0; s < s1; ++s)
-    if (s_new[s] > 0) P.p.held[s] += s_new[s];
+    if (s_new[s] > 0) P.p.held[s] = s_held[s] + s_new[s];
   if (tid == 0) {
     P.p.state[0] = n_free - N;
     P.p.state[1] = 0;
@@ -145,27 +176,29 @@ __global__ void __launch_bounds__(kThreads) pages_reserve_kernel(const PageParam
 }
 
 __global__ void __launch_bounds__(kThreads) pages_release_kernel(const PageParams P) {
-  extern __shared__ int s_off[];  // [batch] number of the sequence's first released page
-  int* s_drop = s_off + P.batch;  // [batch] pages it releases
+  extern __shared__ int s_off[];   // [batch] number of the sequence's first released page
+  int* s_drop = s_off + P.batch;   // [batch] pages it releases
+  int* s_held = s_drop + P.batch;  // [batch] pages it holds
   __shared__ long long warp_sum[kThreads / 32];
   __shared__ int s_last;
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, batch = P.batch;
   const int n_free = min(max(__ldcg(P.p.state), 0), P.p.n_pages);
+  bool bad = false;
+  for (int s = tid; s < batch; s += kThreads) {
+    const int len = __ldcg(P.len + s), held = __ldcg(P.p.held + s);
+    const int keep = len / kPagePos + (len % kPagePos != 0);
+    const bool ok = len >= 0 && held >= 0 && held <= P.p.pages_per_seq;
+    bad |= !ok;
+    s_drop[s] = ok && held > keep ? held - keep : 0;
+    s_held[s] = held;
+  }
+  __syncthreads();
   const int per = (batch + kThreads - 1) / kThreads;
   const int s0 = min(tid * per, batch), s1 = min(s0 + per, batch);
   long long mine = 0;
-  bool bad = false;
-  for (int s = s0; s < s1; ++s) {
-    const int len = __ldcg(P.len + s), held = __ldcg(P.p.held + s);
-    const int keep = len / kPagePos + (len % kPagePos != 0);
-    int drop = 0;
-    if (len < 0 || held < 0 || held > P.p.pages_per_seq) bad = true;
-    else if (held > keep) drop = held - keep;
-    s_drop[s] = drop;
-    mine += drop;
-  }
+  for (int s = s0; s < s1; ++s) mine += s_drop[s];
   long long total;
   long long off = block_scan(mine, warp_sum, total);
   // held counts and a list that do not add up to the pool: nothing is released
@@ -180,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) pages_release_kernel(const PageParam
   const int stride = gridDim.x * kThreads;
   for (int i = blockIdx.x * kThreads + tid; i < R; i += stride) {
     const int s = owner_of(s_off, batch, i);
-    const int j = __ldcg(P.p.held + s) - s_drop[s] + i - s_off[s];
+    const int j = s_held[s] - s_drop[s] + i - s_off[s];
     int* entry = P.p.page_table + static_cast<size_t>(s) * P.p.pages_per_seq + j;
     const int page = __ldcg(entry);
     *entry = -1;
@@ -188,14 +221,17 @@ __global__ void __launch_bounds__(kThreads) pages_release_kernel(const PageParam
   }
   __syncthreads();
   if (tid == 0) {
-    __threadfence();
-    s_last = atomicAdd(P.p.state + 1, 1) == static_cast<int>(gridDim.x) - 1;
+    s_last = 1;
+    if (gridDim.x > 1) {
+      __threadfence();
+      s_last = atomicAdd(P.p.state + 1, 1) == static_cast<int>(gridDim.x) - 1;
+      __threadfence();
+    }
   }
   __syncthreads();
   if (!s_last) return;
-  __threadfence();
   for (int s = s0; s < s1 && !broken; ++s)
-    if (s_drop[s] > 0) P.p.held[s] -= s_drop[s];
+    if (s_drop[s] > 0) P.p.held[s] = s_held[s] - s_drop[s];
   if (tid == 0) {
     P.p.state[0] = n_free + R;
     P.p.state[1] = 0;
@@ -224,9 +260,12 @@ bool pool_ok(const dflash_page_pool* p) {
 template <typename K, typename A>
 int launch(K kernel, long long items, size_t smem, const A& arg, void* stream) {
   cudaLaunchConfig_t cfg = {};
-  // a thread per item up to 1024 CTAs (each repeats the prefix sum), then more items a thread
+  // a thread per item up to 512 CTAs (each repeats the prefix sum), then more items a thread
   const long long ctas = (items + kThreads - 1) / kThreads;
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas < 1 ? 1 : ctas > 1024 ? 1024 : ctas));
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas < 1 ? 1 : ctas > 512 ? 512 : ctas));
+  if (smem > 40 * 1024 &&  // with the static part past the 48 KB that need no asking
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    return DFLASH_E_CUDA;
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
@@ -263,8 +302,11 @@ extern "C" int dflash_pages_reserve(const dflash_page_pool* p, const int32_t* le
   P.slots = slots;
   P.batch = batch;
   P.rows_per_seq = rows_per_seq;
+  P.wide = (reinterpret_cast<uintptr_t>(slots) & 15) == 0;
+  // four slots a thread; without slots, a thread for about every page
   const long long rows = static_cast<long long>(batch) * rows_per_seq;
-  return dfl::launch(dfl::pages_reserve_kernel, slots ? rows : rows / dfl::kPagePos + batch, 8 * batch, P, stream);
+  return dfl::launch(dfl::pages_reserve_kernel, slots ? (rows + 3) / 4 : rows / dfl::kPagePos + batch,
+                     5 * sizeof(int) * batch, P, stream);
 }
 
 extern "C" int dflash_pages_release(const dflash_page_pool* p, const int32_t* len, int32_t batch, void* stream) {
@@ -276,5 +318,6 @@ extern "C" int dflash_pages_release(const dflash_page_pool* p, const int32_t* le
   P.batch = batch;
   // at most the pool's pages come back, and at most what the sequences can hold
   const long long most = static_cast<long long>(batch) * p->pages_per_seq;
-  return dfl::launch(dfl::pages_release_kernel, (most < p->n_pages ? most : p->n_pages) / 4, 8 * batch, P, stream);
+  return dfl::launch(dfl::pages_release_kernel, (most < p->n_pages ? most : p->n_pages) / 2, 3 * sizeof(int) * batch, P,
+                     stream);
 }
