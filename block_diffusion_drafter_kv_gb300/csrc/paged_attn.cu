@@ -104,9 +104,20 @@ DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar)
                : "memory");
 }
 
+// What a state (max, sum) weighs against the maximum of all of them: nothing where it has seen no
+// key, and NaN as it is where all it has seen were NaN.
+DEV float weight_of(float2 ml, float top) {
+  if (ml.x == -INFINITY) return ml.y == 0.f ? 0.f : 1.f;
+  return ex2(ml.x - top);
+}
+
 // First tile of CTA c's range, and the CTA whose range holds tile u (G <= T: none is empty).
-DEV long long range_begin(long long c, long long T, int G) { return c * T / G; }
-DEV int cta_of(long long u, long long T, int G) { return static_cast<int>(((u + 1) * G - 1) / T); }
+// (A 64-bit division is a hundred instructions in a chain: products that fit take the 32-bit one.)
+DEV long long quotient(long long a, long long b) {
+  return static_cast<unsigned long long>(a | b) < (1ull << 32) ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
+DEV long long range_begin(long long c, long long T, int G) { return quotient(c * T, G); }
+DEV int cta_of(long long u, long long T, int G) { return static_cast<int>(quotient((u + 1) * G - 1, T)); }
 
 template <int D, int RG, int KG, int STAGES>
 struct Layout {
@@ -126,7 +137,7 @@ struct Layout {
   static constexpr int kBarOff = kMlOff + KG * kRows * 8;   // full, empty [STAGES]; q full, q empty [kQBufs]
   static constexpr int kMetaOff = kBarOff + (2 * STAGES + 2 * kQBufs) * 8;
   static constexpr int kPreOff = kMetaOff + (STAGES + 4) * 4;  // stage valid flags, abort flag, scan scratch
-  static constexpr int smem(int batch) { return 1024 + kPreOff + 64 + (batch + 1) * 4; }
+  static constexpr int smem(int batch) { return 1024 + kPreOff + 64 + (3 * batch + 1) * 4; }
 };
 
 // Sequence s's rows of this call: 0 where its lengths are out of range.
@@ -164,7 +175,9 @@ __global__ void __launch_bounds__(Layout<D, RG, KG, STAGES>::kThreads, 1) paged_
   volatile int* s_valid = reinterpret_cast<volatile int*>(smem + L::kMetaOff);
   volatile int* s_abort = s_valid + STAGES;
   int* s_warp = reinterpret_cast<int*>(smem + L::kPreOff);
-  int* s_pre = s_warp + 16;
+  int* s_pre = s_warp + 16;        // [batch + 1]
+  int* s_len = s_pre + P.batch + 1;  // [batch]
+  int* s_new = s_len + P.batch;      // [batch] rows of this call
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -194,6 +207,8 @@ __global__ void __launch_bounds__(Layout<D, RG, KG, STAGES>::kThreads, 1) paged_
       bool bad;
       const int n = rows_of(P, s, len, bad);
       if (bad && blockIdx.x == 0) raise_flag(P.err, kDevCapacity);
+      s_len[s] = len;
+      s_new[s] = n;
       s_pre[s + 1] = n > 0 ? (len + n + kKeys - 1) / kKeys : 0;
       mine += s_pre[s + 1];
     }
@@ -233,7 +248,7 @@ __global__ void __launch_bounds__(Layout<D, RG, KG, STAGES>::kThreads, 1) paged_
     s = lo;
     nt = s_pre[s + 1] - s_pre[s];
     const long long rest = u - static_cast<long long>(nkv) * s_pre[s];
-    g = static_cast<int>(rest < (1ll << 32) ? static_cast<uint32_t>(rest) / static_cast<uint32_t>(nt) : rest / nt);
+    g = static_cast<int>(quotient(rest, nt));
     t = static_cast<int>(rest - static_cast<long long>(g) * nt);
   };
   // Every wait is bounded: past the limit the flag is set, later waits pass at once and the
@@ -253,9 +268,7 @@ __global__ void __launch_bounds__(Layout<D, RG, KG, STAGES>::kThreads, 1) paged_
       int s, g, t0, nt;
       locate(u, s, g, t0, nt);
       const int seg = static_cast<int>(min(T1 - u, static_cast<long long>(nt - t0)));
-      int len;
-      bool bad;
-      const int n = rows_of(P, s, len, bad);
+      const int n = s_new[s];
       const int qb = seg_no % L::kQBufs;
       if (seg_no >= L::kQBufs) wait(&qempty[qb], (seg_no / L::kQBufs - 1) & 1);
       if (__all_sync(0xffffffffu, !*s_abort)) {
@@ -326,9 +339,7 @@ __global__ void __launch_bounds__(Layout<D, RG, KG, STAGES>::kThreads, 1) paged_
     int s, g, t0, nt;
     locate(u, s, g, t0, nt);
     const int seg = static_cast<int>(min(T1 - u, static_cast<long long>(nt - t0)));
-    int len;
-    bool bad;
-    const int n_new = rows_of(P, s, len, bad);
+    const int len = s_len[s], n_new = s_new[s];
     const int nk = len + n_new;
     int lim[2];  // last key each of the thread's rows may see
 #pragma unroll
@@ -538,8 +549,8 @@ __global__ void __launch_bounds__(Layout<D, RG, KG, STAGES>::kThreads, 1) paged_
 #pragma unroll
       for (int k = 0; k < KG; ++k) {
         const float2 ml = s_ml[k * L::kRows + row];
-        w[k][h] = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-        sum += ml.x == -INFINITY ? 0.f : w[k][h] * ml.y;
+        w[k][h] = weight_of(ml, top);
+        sum += w[k][h] == 0.f ? 0.f : w[k][h] * ml.y;
       }
       M[h] = top;
       den[h] = sum;
@@ -656,37 +667,50 @@ __global__ void __launch_bounds__(256) paged_attn_join_kernel(const __grid_const
   // perhaps c0. (Asking each range's start, a 64-bit division, took most of this kernel's time.)
   const int c0_second = range_begin(c0, T, G) < base;
   auto slot_of = [&](int c) { return P.part + (2 * static_cast<size_t>(c) + (c == c0 ? c0_second : 0)) * slot_floats; };
-  float M = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32)
-    M = fmaxf(M, __ldcg(reinterpret_cast<const float2*>(slot_of(c) + static_cast<size_t>(slot_rows) * D) + row).x);
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   constexpr int E = D / 32;  // columns of a lane
+  constexpr int kAhead = 8;  // parts whose loads are in flight together
   float acc[E] = {};
-  float den = 0.f;
+  float M = -INFINITY, den = 0.f;
   for (int b = c0; b <= c1; b += 32) {
-    float w = 0.f, wl = 0.f;
-    if (b + lane <= c1) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(slot_of(b + lane) + static_cast<size_t>(slot_rows) * D) + row);
-      w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-      wl = w * ml.y;
-    }
     const int cnt = min(32, c1 - b + 1);
-#pragma unroll 4
-    for (int k = 0; k < cnt; ++k) {
-      const float wk = __shfl_sync(0xffffffffu, w, k);
-      den += __shfl_sync(0xffffffffu, wl, k);
-      const float* src = slot_of(b + k) + static_cast<size_t>(row) * D + lane * E;
-      float v[E];
-      if (E == 4) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
-        v[0] = x.x, v[1] = x.y, v[E - 2] = x.z, v[E - 1] = x.w;
-      } else {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
-        v[0] = x.x, v[1] = x.y;
-      }
+    float v[kAhead][E];
+    auto load = [&](int k0) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += wk * v[e];
+      for (int k = 0; k < kAhead; ++k) {
+        if (k0 + k >= cnt) break;
+        const float* src = slot_of(b + k0 + k) + static_cast<size_t>(row) * D + lane * E;
+        if (E == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+          v[k][0] = x.x, v[k][1] = x.y, v[k][E - 2] = x.z, v[k][E - 1] = x.w;
+        } else {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+          v[k][0] = x.x, v[k][1] = x.y;
+        }
+      }
+    };
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < cnt) ml = __ldcg(reinterpret_cast<const float2*>(slot_of(b + lane) + static_cast<size_t>(slot_rows) * D) + row);
+    load(0);
+    float top = ml.x;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    top = fmaxf(top, M);
+    const float before = M == -INFINITY ? 0.f : ex2(M - top);  // what the parts so far weigh now
+    M = top;
+    den *= before;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= before;
+    const float w = weight_of(ml, M), wl = w == 0.f ? 0.f : w * ml.y;
+    for (int k0 = 0; k0 < cnt; k0 += kAhead) {
+      if (k0 > 0) load(k0);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (k0 + k >= cnt) break;
+        const float wk = __shfl_sync(0xffffffffu, w, k0 + k);
+        den += __shfl_sync(0xffffffffu, wl, k0 + k);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += wk * v[k][e];
+      }
     }
   }
   const float inv = den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den);

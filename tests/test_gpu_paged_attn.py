@@ -155,6 +155,16 @@ def test_keys_hidden_from_a_row_may_be_anything(B, dtype, nq, rows):
             assert bool(torch.isfinite(rest[..., :7]).all()) and bool(torch.isfinite(rest[..., 8:]).all())
 
 
+def test_nothing_but_nan_is_nan(B):
+    """A sequence whose every key is NaN, in one CTA and split over several."""
+    c = Case(B, 4, 2, 128, torch.float16, [0, 3000, 5], [1, 1, 1], 1)
+    c.cache.k_pool[0, c.at(0)] = NAN
+    c.cache.k_pool[0, c.at(1)] = NAN
+    c.attend()
+    assert bool(c.out[:2].isnan().all())
+    c.check(seqs=[2])
+
+
 def test_large_and_equal_scores(B):
     """Scores of hundreds (one key takes all), and all-zero queries (the mean of the values)."""
     c = Case(B, 8, 2, 128, torch.bfloat16, [700, 3], [3, 3], 3, spread=100.0)
