@@ -21,26 +21,15 @@
 // that warps meet only where a segment ends. S = q K^T and O += P V are mma.sync m16n8k16
 // with fp32 accumulation: the rows are few (4 in ordinary grouped decoding), so a
 // 128-row tcgen05 tile would be mostly padding, while the loads bound the kernel.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include <type_traits>
 
-#include "ptx.cuh"
-#include "target.h"
+#include "paged_attn.cuh"
 
 namespace dfl {
 
 namespace {
 
-constexpr int kKeys = kPagePos;  // keys per tile
-constexpr int kStep = 32;        // keys per warp step
-
-DEV float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
+constexpr int kStep = 32;  // keys per warp step
 
 template <bool TRANS>
 DEV void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -70,28 +59,6 @@ DEV void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two values as the cache's 16-bit type, the first in the low half.
-template <bool BF16>
-DEV uint32_t pack2(float lo, float hi) {
-  if (BF16) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-template <bool BF16>
-DEV float2 unpack2(uint32_t u) {
-  if (BF16) return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
-  return __half22float2(*reinterpret_cast<const __half2*>(&u));
-}
-// Whether one of the two 16-bit values is infinite or NaN.
-template <bool BF16>
-DEV bool non_finite2(uint32_t u) {
-  constexpr uint32_t kExp = BF16 ? 0x7f80u : 0x7c00u;
-  return (u & kExp) == kExp || ((u >> 16) & kExp) == kExp;
-}
-
 // Byte address of element (key, dim) in a staged tile: d / 64 boxes of 64 keys x 128 bytes,
 // written by TMA with the 128-byte swizzle (16-byte chunk c of row r lands at c ^ (r & 7)).
 DEV uint32_t tile_addr(uint32_t base, int key, int dim) {
@@ -103,21 +70,6 @@ DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar)
                "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
-
-// What a state (max, sum) weighs against the maximum of all of them: nothing where it has seen no
-// key, and NaN as it is where all it has seen were NaN.
-DEV float weight_of(float2 ml, float top) {
-  if (ml.x == -INFINITY) return ml.y == 0.f ? 0.f : 1.f;
-  return ex2(ml.x - top);
-}
-
-// First tile of CTA c's range, and the CTA whose range holds tile u (G <= T: none is empty).
-// (A 64-bit division is a hundred instructions in a chain: products that fit take the 32-bit one.)
-DEV long long quotient(long long a, long long b) {
-  return static_cast<unsigned long long>(a | b) < (1ull << 32) ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
-}
-DEV long long range_begin(long long c, long long T, int G) { return quotient(c * T, G); }
-DEV int cta_of(long long u, long long T, int G) { return static_cast<int>(quotient((u + 1) * G - 1, T)); }
 
 template <int D, int RG, int KG, int STAGES>
 struct Layout {
@@ -139,23 +91,6 @@ struct Layout {
   static constexpr int kPreOff = kMetaOff + (STAGES + 4) * 4;  // stage valid flags, abort flag, scan scratch
   static constexpr int smem(int batch) { return 1024 + kPreOff + 64 + (3 * batch + 1) * 4; }
 };
-
-// Sequence s's rows of this call: 0 where its lengths are out of range.
-DEV int rows_of(const PagedAttnParams& P, int s, int& len, bool& bad) {
-  len = __ldcg(P.len + s);
-  const int n = __ldcg(P.n_new + s);
-  bad = len < 0 || n < 0 || n > P.rows_per_seq ||
-        static_cast<long long>(len) + n > static_cast<long long>(P.pages_per_seq) * kPagePos;
-  return bad ? 0 : n;
-}
-
-__device__ __noinline__ void wait_long(uint64_t* bar, uint32_t parity, volatile int* abort, int* err, unsigned long long limit_ns) {
-  if (*abort) return;
-  if (!mbar_wait(bar, parity, limit_ns)) {
-    *abort = 1;
-    raise_flag(err, kDevTimeout);
-  }
-}
 
 template <int D, bool BF16, int RG, int KG, int STAGES>
 __global__ void __launch_bounds__(Layout<D, RG, KG, STAGES>::kThreads, 1) paged_attn_kernel(const __grid_constant__ PagedAttnParams P) {
@@ -197,60 +132,13 @@ __global__ void __launch_bounds__(Layout<D, RG, KG, STAGES>::kThreads, 1) paged_
   pdl_wait();
   pdl_launch_dependents();
 
-  // tiles per head before each sequence: each thread a run of sequences, then a scan
-  {
-    const int per = (P.batch + L::kThreads - 1) / L::kThreads;
-    const int s0 = min(tid * per, P.batch), s1 = min(s0 + per, P.batch);
-    int mine = 0;
-    for (int s = s0; s < s1; ++s) {
-      int len;
-      bool bad;
-      const int n = rows_of(P, s, len, bad);
-      if (bad && blockIdx.x == 0) raise_flag(P.err, kDevCapacity);
-      s_len[s] = len;
-      s_new[s] = n;
-      s_pre[s + 1] = n > 0 ? (len + n + kKeys - 1) / kKeys : 0;
-      mine += s_pre[s + 1];
-    }
-    int v = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += u;
-    }
-    if (lane == 31) s_warp[warp] = v;
-    __syncthreads();
-    int before = v - mine;
-    for (int w = 0; w < warp; ++w) before += s_warp[w];
-    for (int s = s0; s < s1; ++s) {
-      before += s_pre[s + 1];
-      s_pre[s + 1] = before;
-    }
-    if (tid == 0) s_pre[0] = 0;
-    __syncthreads();
-  }
-  if (blockIdx.x == 0)
-    for (int s = tid; s <= P.batch; s += L::kThreads) P.prefix[s] = s_pre[s];
+  count_tiles<L::kThreads>(P, s_pre, s_len, s_new, s_warp);
   const int batch = P.batch, nkv = P.nkv, grp = P.nq / nkv;
   const long long T = static_cast<long long>(nkv) * s_pre[batch];
   const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), T));
   const int cta = blockIdx.x;
   if (cta >= G) return;
   const long long T0 = range_begin(cta, T, G), T1 = range_begin(cta + 1, T, G);
-  // list position u -> sequence s, KV head g, tile t of the pair's nt
-  auto locate = [&](long long u, int& s, int& g, int& t, int& nt) {
-    int lo = 0, hi = batch - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (static_cast<long long>(nkv) * s_pre[mid] <= u) lo = mid;
-      else hi = mid - 1;
-    }
-    s = lo;
-    nt = s_pre[s + 1] - s_pre[s];
-    const long long rest = u - static_cast<long long>(nkv) * s_pre[s];
-    g = static_cast<int>(quotient(rest, nt));
-    t = static_cast<int>(rest - static_cast<long long>(g) * nt);
-  };
   // Every wait is bounded: past the limit the flag is set, later waits pass at once and the
   // CTA walks to its end without results.
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -265,8 +153,8 @@ __global__ void __launch_bounds__(Layout<D, RG, KG, STAGES>::kThreads, 1) paged_
     int i = 0, seg_no = 0;
     int q_issued = 0, kv_issued = 0;  // of the segments and tiles walked so far
     for (long long u = T0; u < T1; ++seg_no) {
-      int s, g, t0, nt;
-      locate(u, s, g, t0, nt);
+      const Place at = locate(s_pre, batch, nkv, u);
+      const int s = at.s, g = at.g, t0 = at.t, nt = at.nt;
       const int seg = static_cast<int>(min(T1 - u, static_cast<long long>(nt - t0)));
       const int n = s_new[s];
       const int qb = seg_no % L::kQBufs;
@@ -336,8 +224,8 @@ __global__ void __launch_bounds__(Layout<D, RG, KG, STAGES>::kThreads, 1) paged_
   const int mrow0 = rg * 16;  // first of the warp's rows
   int i = 0, seg_no = 0;
   for (long long u = T0; u < T1; ++seg_no) {
-    int s, g, t0, nt;
-    locate(u, s, g, t0, nt);
+    const Place at = locate(s_pre, batch, nkv, u);
+    const int s = at.s, g = at.g, t0 = at.t, nt = at.nt;
     const int seg = static_cast<int>(min(T1 - u, static_cast<long long>(nt - t0)));
     const int len = s_len[s], n_new = s_new[s];
     const int nk = len + n_new;
