@@ -667,8 +667,12 @@ int launch(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<D, BF16, W::RG, W::KG, W::ST>, p);
-  if (e != cudaSuccess) return static_cast<int>(e);
+#ifndef NO_TC
+  if (V >= 2) {
+    if (const int e = launch_paged_attn_tc(p, BF16, n_ctas, stream)) return e;
+  } else
+#endif
+  if (const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<D, BF16, W::RG, W::KG, W::ST>, p)) return static_cast<int>(e);
   cfg.gridDim = dim3(p.batch * p.nkv, (p.rows + 7) / 8);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
@@ -686,7 +690,7 @@ int paged_attn_set_attributes() {
                    set_attr<128, true, 0>(),  set_attr<128, true, 1>(),  set_attr<128, true, 2>(),  set_attr<128, true, 3>()};
   for (int x : e)
     if (x != 0) return x;
-  return 0;
+  return paged_attn_tc_set_attributes();
 }
 
 int launch_paged_attn(const PagedAttnParams& p, bool bf16, int n_ctas, cudaStream_t stream) {

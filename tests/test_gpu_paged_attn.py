@@ -130,7 +130,7 @@ def test_same_result_every_time(B):
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
-@pytest.mark.parametrize("nq,rows", [(4, 8), (8, 4), (1, 16)])
+@pytest.mark.parametrize("nq,rows", [(4, 8), (8, 4), (1, 16), (5, 9), (8, 8), (6, 16), (8, 16)])
 def test_keys_hidden_from_a_row_may_be_anything(B, dtype, nq, rows):
     """An infinite or NaN value (or key) in a new row's position reaches only the rows that see it."""
     for what, pool in ((INF, "v_pool"), (NAN, "v_pool"), (-INF, "v_pool"), (NAN, "k_pool"), (INF, "k_pool")):
