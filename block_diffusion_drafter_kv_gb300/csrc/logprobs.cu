@@ -34,6 +34,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "math.cuh"
 #include "ptx.cuh"
 #include "target.h"
 
@@ -53,11 +54,6 @@ constexpr int kListed = 1024;                // rows of a call whose tokens are 
 constexpr unsigned kAll = 0xffffffffu;
 using Key = unsigned long long;
 
-DEV float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // NaN if one of them is.
 DEV float max_nan(float a, float b) {
   float y;
@@ -69,23 +65,6 @@ DEV float warp_max_nan(float x) {
   asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
 }
-// Two fp32 operations in one instruction.
-DEV float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(*reinterpret_cast<unsigned long long*>(&d))
-      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
-        "l"(*reinterpret_cast<unsigned long long*>(&c)));
-  return d;
-}
-DEV float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(*reinterpret_cast<unsigned long long*>(&d))
-      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
-  return d;
-}
-
 // Order-preserving bits of a logit: NaN above all, -0 as +0.
 DEV uint32_t order_bits(float x) {
   if (x != x) return 0xffffffffu;

@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "math.cuh"
 #include "ptx.cuh"
 #include "target.h"
 
@@ -13,12 +14,6 @@ namespace dfl {
 namespace {
 
 constexpr int kKeys = kPagePos;  // keys per tile
-
-DEV float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // Two values as the cache's 16-bit type, the first in the low half.
 template <bool BF16>

@@ -395,20 +395,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
         const bool valid = s_valid[i & 15] >> hh & 1;
         const int key0 = t * kKeys;
         const bool edge = (w.at.t * kKeys) > len + 1;  // some row may not see some key of the step (the same for all threads)
-        float mx = -INFINITY;
-        if (valid && !edge) {
+        if (!valid || edge) {
 #pragma unroll
-          for (int k = 0; k < 64; ++k) {
-            sc[k] *= P.scale_log2;
-            mx = fmaxf(mx, sc[k]);
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 64; ++k) {
-            sc[k] = valid && key0 + k <= lim ? sc[k] * P.scale_log2 : -INFINITY;
-            mx = fmaxf(mx, sc[k]);
-          }
+          for (int k = 0; k < 64; ++k)
+            if (!valid || key0 + k > lim) sc[k] = -INFINITY;
         }
+        // one warp to a scheduler: four chains, not one
+        float top[4] = {sc[0], sc[1], sc[2], sc[3]};
+#pragma unroll
+        for (int k = 4; k < 64; ++k) top[k & 3] = fmaxf(top[k & 3], sc[k]);
+        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * P.scale_log2;
         const bool need = mx > m + kMove;
         if (__any_sync(0xffffffffu, need)) {
           const float corr = need && !first ? ex2(m - mx) : 1.f;
@@ -461,30 +457,31 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
               *at = make_uint4(0, 0, 0, 0);
             }
           }
-          float ls = 0.f;
-          const float base = m == -INFINITY ? 0.f : m;
+          if (odd) {
 #pragma unroll
-          for (int k = 0; k < 64; ++k) {
-            const int key = key0 + k;
-            const float p = ex2(sc[k] - base);
-            ls += p;
-            const bool out = odd && key >= len && key < nk;
-            if (out) {
-              s_z[key - len] = sc[k];
+            for (int k = 0; k < 64; ++k) {
+              const int key = key0 + k;
+              if (key < len || key >= nk) continue;
+              s_z[key - len] = sc[k] * P.scale_log2;
               kept |= 1u << (key - len);
+              l += ex2(sc[k] * P.scale_log2 - (m == -INFINITY ? 0.f : m));
+              sc[k] = -INFINITY;
             }
-            sc[k] = out ? 0.f : p;
           }
-          l += ls;
-        } else {
-          float ls[4] = {0.f, 0.f, 0.f, 0.f};
+        }
+        {
           const float base = m == -INFINITY ? 0.f : m;
+          const float2 scale2 = {P.scale_log2, P.scale_log2}, base2 = {-base, -base};
+          float2 ls[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
-          for (int k = 0; k < 64; ++k) {
-            sc[k] = ex2(sc[k] - base);
-            ls[k & 3] += sc[k];
+          for (int k = 0; k < 64; k += 2) {
+            const float2 x = fma2(float2{sc[k], sc[k + 1]}, scale2, base2);
+            sc[k] = ex2(x.x);
+            sc[k + 1] = ex2(x.y);
+            ls[k >> 1 & 1] = add2(ls[k >> 1 & 1], float2{sc[k], sc[k + 1]});
           }
-          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+          ls[0] = add2(ls[0], ls[1]);
+          l += ls[0].x + ls[0].y;
         }
         // P, once the previous step's product has read the buffer
         if (i > 0) wait(pvdone, (i - 1) & 1);
