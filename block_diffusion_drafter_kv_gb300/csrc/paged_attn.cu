@@ -14,15 +14,13 @@
 // small kernel joins those in CTA order: the result does not depend on timing, and no
 // counter has to be kept between calls.
 //
-// CTA. One producer warp walks the range: page ids a warp-load at a time, K/V tiles by TMA
-// into a ring of shared-memory stages, each segment's q rows by bulk copies. The compute
-// warps are RG row groups of 16 rows times KG key groups; a warp takes 32-key halves of tiles (of
-// every tile, or with four key groups of every second one) with a softmax state of its own, so
-// that warps meet only where a segment ends. S = q K^T and O += P V are mma.sync m16n8k16
-// with fp32 accumulation: the rows are few (4 in ordinary grouped decoding), so a
-// 128-row tcgen05 tile would be mostly padding, while the loads bound the kernel.
-#include <type_traits>
-
+// CTA (up to 16 rows; more rows: paged_attn_tc.cu). One producer warp walks the range: page ids a
+// warp-load at a time, K/V tiles by TMA into a ring of shared-memory stages, each segment's q
+// rows by bulk copies. Of the four compute warps two take one half each of every second tile, with
+// a softmax state of their own, so that warps meet only where a segment ends. S = q K^T and
+// O += P V are mma.sync m16n8k16 with fp32 accumulation: the rows are few (4 in ordinary
+// grouped decoding), so a 128-row tcgen05 tile would be mostly padding, while the loads bound
+// the kernel (0.92 of the measured copy rate at 4 sequences of 32768, fp32 sums included).
 #include "paged_attn.cuh"
 
 namespace dfl {
@@ -71,33 +69,34 @@ DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar)
                : "memory");
 }
 
-template <int D, int RG, int KG, int STAGES>
+constexpr int kRowsFew = 16;  // rows of a problem that this kernel takes
+constexpr int KG = 4;         // key groups: compute warps
+
+template <int D>
 struct Layout {
-  static constexpr int kWarps = RG * KG;
-  static constexpr int kThreads = 32 * (kWarps + 1);
-  static constexpr int kRows = 16 * RG;
-  static constexpr int kTileWarps = RG * (KG < 2 ? KG : 2);  // warps that use one tile
+  static constexpr int STAGES = D == 128 ? 4 : 8;
+  static constexpr int kThreads = 32 * (KG + 1);
+  static constexpr int kRows = kRowsFew;
   static constexpr int kTileBytes = kKeys * D * 2;          // one operand
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kQStride = D * 2 + 16;               // bytes; the pad keeps ldmatrix free of conflicts
-  static constexpr int kQBufs = kRows <= 64 ? 2 : 1;
-  static constexpr bool kAllAtOnce = kRows == 16;           // every key group's output exchanged at once
-  static constexpr int kCopies = kAllAtOnce ? KG : KG > 1 ? 1 : 0;
+  static constexpr int kQBufs = 2;
   static constexpr int kQOff = STAGES * kStageBytes;
   static constexpr int kXOff = kQOff + kQBufs * kRows * kQStride;
-  static constexpr int kMlOff = kXOff + kCopies * kRows * D * 4;
+  static constexpr int kMlOff = kXOff + KG * kRows * D * 4;
   static constexpr int kBarOff = kMlOff + KG * kRows * 8;   // full, empty [STAGES]; q full, q empty [kQBufs]
   static constexpr int kMetaOff = kBarOff + (2 * STAGES + 2 * kQBufs) * 8;
   static constexpr int kPreOff = kMetaOff + (STAGES + 4) * 4;  // stage valid flags, abort flag, scan scratch
   static constexpr int smem(int batch) { return 1024 + kPreOff + 64 + (3 * batch + 1) * 4; }
 };
 
-template <int D, bool BF16, int RG, int KG, int STAGES>
-__global__ void __launch_bounds__(Layout<D, RG, KG, STAGES>::kThreads, 1) paged_attn_kernel(const __grid_constant__ PagedAttnParams P) {
-  using L = Layout<D, RG, KG, STAGES>;
-  // With four key groups a stage has to serve the same two of them every time: a group that
-  // skipped a phase of a stage's barrier could take the phase before it for its own.
-  static_assert(KG != 4 || STAGES % 2 == 0, "stages of alternating tiles");
+template <int D, bool BF16>
+__global__ void __launch_bounds__(Layout<D>::kThreads, 1) paged_attn_kernel(const __grid_constant__ PagedAttnParams P) {
+  using L = Layout<D>;
+  constexpr int STAGES = L::STAGES;
+  // A stage has to serve the same two key groups every time: a group that skipped a phase of a
+  // stage's barrier could take the phase before it for its own.
+  static_assert(STAGES % 2 == 0, "stages of alternating tiles");
   constexpr int NT = D / 8;  // 8-dim column tiles of the output
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -118,11 +117,11 @@ __global__ void __launch_bounds__(Layout<D, RG, KG, STAGES>::kThreads, 1) paged_
   if (tid == 0) {
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], L::kTileWarps);
+      mbar_init(&empty[i], 2);  // the two key groups that take it
     }
     for (int i = 0; i < L::kQBufs; ++i) {
       mbar_init(&qfull[i], 1);
-      mbar_init(&qempty[i], L::kWarps);
+      mbar_init(&qempty[i], KG);
     }
     *s_abort = 0;
     fence_mbar_init();
@@ -145,7 +144,7 @@ __global__ void __launch_bounds__(Layout<D, RG, KG, STAGES>::kThreads, 1) paged_
     if (!mbar_try_wait(bar, parity)) wait_long(bar, parity, s_abort, P.err, P.wait_ns);
   };
 
-  if (warp == L::kWarps) {
+  if (warp == KG) {
     // ------------------------------------------------------------ producer warp
     // K/V are read once per call: streamed through L2, unless all of it (16 MB, one eighth of L2)
     // can stay there until it is read again
@@ -219,9 +218,8 @@ __global__ void __launch_bounds__(Layout<D, RG, KG, STAGES>::kThreads, 1) paged_
   }
 
   // -------------------------------------------------------------- compute warps
-  const int rg = warp / KG, kg = warp % KG;
+  const int kg = warp;
   const int r0 = lane >> 2, kq = (lane & 3) * 2, mi = lane >> 3;
-  const int mrow0 = rg * 16;  // first of the warp's rows
   int i = 0, seg_no = 0;
   for (long long u = T0; u < T1; ++seg_no) {
     const Place at = locate(s_pre, batch, nkv, u);
@@ -231,13 +229,13 @@ __global__ void __launch_bounds__(Layout<D, RG, KG, STAGES>::kThreads, 1) paged_
     const int nk = len + n_new;
     int lim[2];  // last key each of the thread's rows may see
 #pragma unroll
-    for (int h = 0; h < 2; ++h) lim[h] = len + (mrow0 + h * 8 + r0) / grp;
+    for (int h = 0; h < 2; ++h) lim[h] = len + (h * 8 + r0) / grp;
     const int qb = seg_no % L::kQBufs;
     wait(&qfull[qb], (seg_no / L::kQBufs) & 1);
     __syncwarp();
     uint32_t qa[D / 16][4];
     {
-      const uint32_t qbase = smem_u32(smem + L::kQOff + qb * L::kRows * L::kQStride) + (mrow0 + (lane & 15)) * L::kQStride + (lane >> 4) * 16;
+      const uint32_t qbase = smem_u32(smem + L::kQOff + qb * L::kRows * L::kQStride) + (lane & 15) * L::kQStride + (lane >> 4) * 16;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) ldsm4<false>(qbase + kk * 32, qa[kk]);
     }
@@ -245,16 +243,15 @@ __global__ void __launch_bounds__(Layout<D, RG, KG, STAGES>::kThreads, 1) paged_
 #pragma unroll
     for (int nt2 = 0; nt2 < NT; ++nt2) o[nt2][0] = o[nt2][1] = o[nt2][2] = o[nt2][3] = 0.f;
     for (int j = 0; j < seg; ++j, ++i) {
-      if (KG == 4 && (i & 1) != kg >> 1) continue;  // the other two key groups' tile
+      if ((i & 1) != kg >> 1) continue;  // the other two key groups' tile
       const int st = i % STAGES;
       wait(&full[st], (i / STAGES) & 1);
       const uint32_t kb = smem_u32(smem + st * L::kStageBytes), vb = kb + L::kTileBytes;
       // the whole warp takes the tile or skips it: the steps below are collective
       if (__all_sync(0xffffffffu, s_valid[st] != 0 && !*s_abort)) {
-#pragma unroll 1
-        for (int half = KG == 1 ? 0 : kg & 1; half < 2; half += KG == 1 ? 1 : 2) {
-          const int key0 = (t0 + j) * kKeys + half * kStep;  // position of the step's first key
-          if (key0 >= nk) break;
+        const int half = kg & 1;
+        const int key0 = (t0 + j) * kKeys + half * kStep;  // position of the step's first key
+        if (key0 < nk) {
           const bool edge = key0 + kStep - 1 > len;  // some row may not see some key
           float sc[4][4];
 #pragma unroll
@@ -420,17 +417,15 @@ __global__ void __launch_bounds__(Layout<D, RG, KG, STAGES>::kThreads, 1) paged_
     // (max, sum) of every row and group first, then the outputs, in fragment order
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      if ((lane & 3) == 0) s_ml[kg * L::kRows + mrow0 + h * 8 + r0] = make_float2(m_[h], l_[h]);
-    if (L::kAllAtOnce) {
+      if ((lane & 3) == 0) s_ml[kg * L::kRows + h * 8 + r0] = make_float2(m_[h], l_[h]);
 #pragma unroll
-      for (int nt2 = 0; nt2 < NT; ++nt2)
-        s_x[(kg * NT + nt2) * 32 + lane] = make_float4(o[nt2][0], o[nt2][1], o[nt2][2], o[nt2][3]);
-    }
-    named_bar_sync(1, 32 * L::kWarps);
+    for (int nt2 = 0; nt2 < NT; ++nt2)
+      s_x[(kg * NT + nt2) * 32 + lane] = make_float4(o[nt2][0], o[nt2][1], o[nt2][2], o[nt2][3]);
+    named_bar_sync(1, 32 * KG);
     float M[2], den[2], w[KG][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int row = mrow0 + h * 8 + r0;
+      const int row = h * 8 + r0;
       float top = -INFINITY, sum = 0.f;
 #pragma unroll
       for (int k = 0; k < KG; ++k) top = fmaxf(top, s_ml[k * L::kRows + row].x);
@@ -451,7 +446,7 @@ __global__ void __launch_bounds__(Layout<D, RG, KG, STAGES>::kThreads, 1) paged_
     float inv[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int row = mrow0 + h * 8 + r0, r = row / grp, hh = row - r * grp;
+      const int row = h * 8 + r0, r = row / grp, hh = row - r * grp;
       there[h] = row < n_new * grp;
       inv[h] = den[h] > 0.f ? 1.f / den[h] : (den[h] == 0.f ? 0.f : den[h]);
       dst[h] = static_cast<uint16_t*>(P.out) + ((static_cast<size_t>(s) * P.rows_per_seq + r) * P.nq + static_cast<size_t>(g) * grp + hh) * D;
@@ -463,70 +458,31 @@ __global__ void __launch_bounds__(Layout<D, RG, KG, STAGES>::kThreads, 1) paged_
         if (whole)
           *reinterpret_cast<uint32_t*>(dst[h] + nt2 * 8 + kq) = pack2<BF16>(v[2 * h] * inv[h], v[2 * h + 1] * inv[h]);
         else
-          __stcg(reinterpret_cast<float2*>(slot + static_cast<size_t>(mrow0 + h * 8 + r0) * D + nt2 * 8 + kq),
+          __stcg(reinterpret_cast<float2*>(slot + static_cast<size_t>(h * 8 + r0) * D + nt2 * 8 + kq),
                  make_float2(v[2 * h], v[2 * h + 1]));
       }
     };
-    if (L::kAllAtOnce) {
-      // each key group finishes its share of the columns
+    // each key group finishes its share of the columns
 #pragma unroll
-      for (int n4 = 0; n4 < NT / KG; ++n4) {
-        const int nt2 = kg * (NT / KG) + n4;
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int n4 = 0; n4 < NT / KG; ++n4) {
+      const int nt2 = kg * (NT / KG) + n4;
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < KG; ++k) {
-          const float4 x = s_x[(k * NT + nt2) * 32 + lane];
-          v[0] += w[k][0] * x.x;
-          v[1] += w[k][0] * x.y;
-          v[2] += w[k][1] * x.z;
-          v[3] += w[k][1] * x.w;
-        }
-        put(nt2, v);
+      for (int k = 0; k < KG; ++k) {
+        const float4 x = s_x[(k * NT + nt2) * 32 + lane];
+        v[0] += w[k][0] * x.x;
+        v[1] += w[k][0] * x.y;
+        v[2] += w[k][1] * x.z;
+        v[3] += w[k][1] * x.w;
       }
-    } else {
-      // one group after another through one buffer per row group, into group 0
-      float4* xb = s_x + static_cast<size_t>(rg) * NT * 32;
-#pragma unroll
-      for (int nt2 = 0; nt2 < NT; ++nt2) {
-        float w0 = w[0][0], w1 = w[0][1];
-#pragma unroll
-        for (int k = 1; k < KG; ++k)
-          if (kg == k) w0 = w[k][0], w1 = w[k][1];
-        o[nt2][0] *= w0;
-        o[nt2][1] *= w0;
-        o[nt2][2] *= w1;
-        o[nt2][3] *= w1;
-      }
-#pragma unroll
-      for (int k = 1; k < KG; ++k) {
-        if (kg == k) {
-#pragma unroll
-          for (int nt2 = 0; nt2 < NT; ++nt2) xb[nt2 * 32 + lane] = make_float4(o[nt2][0], o[nt2][1], o[nt2][2], o[nt2][3]);
-        }
-        named_bar_sync(1, 32 * L::kWarps);
-        if (kg == 0) {
-#pragma unroll
-          for (int nt2 = 0; nt2 < NT; ++nt2) {
-            const float4 x = xb[nt2 * 32 + lane];
-            o[nt2][0] += x.x;
-            o[nt2][1] += x.y;
-            o[nt2][2] += x.z;
-            o[nt2][3] += x.w;
-          }
-        }
-        if (k + 1 < KG) named_bar_sync(1, 32 * L::kWarps);
-      }
-      if (kg == 0) {
-#pragma unroll
-        for (int nt2 = 0; nt2 < NT; ++nt2) put(nt2, o[nt2]);
-      }
+      put(nt2, v);
     }
     if (kg == 0 && !whole && (lane & 3) == 0) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        __stcg(reinterpret_cast<float2*>(slot + static_cast<size_t>(L::kRows) * D) + mrow0 + h * 8 + r0, make_float2(M[h], den[h]));
+        __stcg(reinterpret_cast<float2*>(slot + static_cast<size_t>(L::kRows) * D) + h * 8 + r0, make_float2(M[h], den[h]));
     }
-    named_bar_sync(1, 32 * L::kWarps);  // the exchange buffers are the next segment's
+    named_bar_sync(1, 32 * KG);  // the exchange buffers are the next segment's
     u += seg;
   }
 }
@@ -610,97 +566,56 @@ __global__ void __launch_bounds__(256) paged_attn_join_kernel(const __grid_const
     *reinterpret_cast<uint32_t*>(dst + e) = pack2<BF16>(acc[e] * inv, acc[e + 1] * inv);
 }
 
-template <int D>
-struct Stages {
-  static constexpr int few = D == 128 ? 4 : 8, mid = D == 128 ? 4 : 8, many = D == 128 ? 5 : 10;
-};
-
-// Variants by rows of a problem: up to 16 rows as one row group and four key groups, 32 as two
-// and four, 64 as four and two, 128 as eight row groups.
-template <typename F>
-int with_variant(int rows, F&& f) {
-  if (rows <= 16) return f(std::integral_constant<int, 0>());
-  if (rows <= 32) return f(std::integral_constant<int, 1>());
-  if (rows <= 64) return f(std::integral_constant<int, 2>());
-  return f(std::integral_constant<int, 3>());
-}
-
-template <int D, int V>
-struct Variant;
-template <int D>
-struct Variant<D, 0> {
-  static constexpr int RG = 1, KG = 4, ST = Stages<D>::few;
-};
-template <int D>
-struct Variant<D, 1> {
-  static constexpr int RG = 2, KG = 4, ST = Stages<D>::few;
-};
-template <int D>
-struct Variant<D, 2> {
-  static constexpr int RG = 4, KG = 2, ST = Stages<D>::mid;
-};
-template <int D>
-struct Variant<D, 3> {
-  static constexpr int RG = 8, KG = 1, ST = Stages<D>::many;
-};
-
-template <int D, bool BF16, int V>
+template <int D, bool BF16>
 int set_attr() {
-  using W = Variant<D, V>;
-  using L = Layout<D, W::RG, W::KG, W::ST>;
-  static_assert(L::smem(kCacheMaxBatch) <= 232448, "shared memory of a CTA");
-  return static_cast<int>(cudaFuncSetAttribute(paged_attn_kernel<D, BF16, W::RG, W::KG, W::ST>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, L::smem(kCacheMaxBatch)));
+  static_assert(Layout<D>::smem(kCacheMaxBatch) <= 232448, "shared memory of a CTA");
+  return static_cast<int>(cudaFuncSetAttribute(paged_attn_kernel<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               Layout<D>::smem(kCacheMaxBatch)));
 }
 
-template <int D, bool BF16, int V>
+template <int D, bool BF16>
 int launch(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
-  using W = Variant<D, V>;
-  using L = Layout<D, W::RG, W::KG, W::ST>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(n_ctas);
-  cfg.blockDim = dim3(L::kThreads);
-  cfg.dynamicSmemBytes = L::smem(p.batch);
+  cfg.blockDim = dim3(Layout<D>::kThreads);
+  cfg.dynamicSmemBytes = Layout<D>::smem(p.batch);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-#ifndef NO_TC
-  if (V >= 2) {
-    if (const int e = launch_paged_attn_tc(p, BF16, n_ctas, stream)) return e;
-  } else
-#endif
-  if (const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<D, BF16, W::RG, W::KG, W::ST>, p)) return static_cast<int>(e);
+  // Up to 16 rows here, more on tcgen05. Measured (bf16, d 128, 32 query heads on 8 KV heads, us):
+  //   rows  1 x 2048  32 x 1000  4 x 32768       1 x 2048  32 x 1000  4 x 32768
+  //     16      12.1       32.1       86.6  here     18.2       53.9      102.5  tcgen05 (an earlier form)
+  //     20      15.0       43.1      103.5  here     15.6       36.5       91.1  tcgen05
+  //     64      17.6       60.3      146.8  here     17.4       48.3       99.1  tcgen05
+  const int e = p.rows <= kRowsFew ? static_cast<int>(cudaLaunchKernelEx(&cfg, paged_attn_kernel<D, BF16>, p))
+                                   : launch_paged_attn_tc(p, BF16, n_ctas, stream);
+  if (e != 0) return e;
   cfg.gridDim = dim3(p.batch * p.nkv, (p.rows + 7) / 8);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return static_cast<int>(cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<D, BF16>, p, n_ctas, static_cast<int>(L::kRows)));
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<D, BF16>, p, n_ctas, paged_attn_rows(p.rows)));
 }
 
 }  // namespace
 
-int paged_attn_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+int paged_attn_rows(int rows) { return rows <= kRowsFew ? kRowsFew : rows <= 64 ? 64 : 128; }
 
 int paged_attn_set_attributes() {
-  const int e[] = {set_attr<64, false, 0>(),  set_attr<64, false, 1>(),  set_attr<64, false, 2>(),  set_attr<64, false, 3>(),
-                   set_attr<64, true, 0>(),   set_attr<64, true, 1>(),   set_attr<64, true, 2>(),   set_attr<64, true, 3>(),
-                   set_attr<128, false, 0>(), set_attr<128, false, 1>(), set_attr<128, false, 2>(), set_attr<128, false, 3>(),
-                   set_attr<128, true, 0>(),  set_attr<128, true, 1>(),  set_attr<128, true, 2>(),  set_attr<128, true, 3>()};
+  const int e[] = {set_attr<64, false>(), set_attr<64, true>(), set_attr<128, false>(), set_attr<128, true>(),
+                   paged_attn_tc_set_attributes()};
   for (int x : e)
     if (x != 0) return x;
-  return paged_attn_tc_set_attributes();
+  return 0;
 }
 
 int launch_paged_attn(const PagedAttnParams& p, bool bf16, int n_ctas, cudaStream_t stream) {
   if (p.batch < 1 || p.batch > kCacheMaxBatch || n_ctas < 1 || n_ctas > kPagedMaxCtas || p.rows > 128)
     return static_cast<int>(cudaErrorInvalidValue);
-  return with_variant(p.rows, [&](auto v) {
-    constexpr int V = decltype(v)::value;
-    if (p.d == 128) return bf16 ? launch<128, true, V>(p, n_ctas, stream) : launch<128, false, V>(p, n_ctas, stream);
-    return bf16 ? launch<64, true, V>(p, n_ctas, stream) : launch<64, false, V>(p, n_ctas, stream);
-  });
+  if (p.d == 128) return bf16 ? launch<128, true>(p, n_ctas, stream) : launch<128, false>(p, n_ctas, stream);
+  return bf16 ? launch<64, true>(p, n_ctas, stream) : launch<64, false>(p, n_ctas, stream);
 }
 
 }  // namespace dfl

@@ -1,5 +1,5 @@
-// The attention over a paged cache on the tcgen05 tensor cores, for problems of more than 32
-// rows (a block to verify times the query heads of a KV head), whose mma.sync form is bound by
+// The attention over a paged cache on the tcgen05 tensor cores, for problems of more than 16
+// rows (a block to verify times the query heads of a KV head), whose mma.sync form was bound by
 // its fragments' trips through ldmatrix. The same list of tiles, cut and parts as in
 // paged_attn.cu, whose join follows.
 //
@@ -12,10 +12,14 @@
 // overlapped between steps.
 //
 //   S   two TMEM buffers of N columns: the next step's Q K^T runs under this one's softmax
-//   P   one shared-memory buffer, written once the previous step's P V has read it
+//   Q, P  in TMEM too, as the products' A operands: with them in shared memory (64 KB) the rings
+//       held two steps instead of three, and a step waited for its copies (104 us against the
+//       figure below at 4 sequences of 32768, blocks of 16)
 //   O   TMEM, kept over the segment. A row's reference moves only where a score passes it by more
 //       than 8 binary orders; that row of O is then rescaled in TMEM between two products
 //   K, V  rings of their own: a K stage is free after its Q K^T, a V stage after its P V
+// The next segment's q is fetched while a segment ends (the producer has asked for it in L2
+// when it began the segment's copies), so that its first product runs under the output.
 // Warps 0-3: softmax and output, a row per thread; warp 4: MMA issuer; warp 5: producer. Every
 // wait is bounded; past the limit the later ones pass at once and the softmax warps walk to
 // the end without results, so that none of their barriers and collective steps is missed.
@@ -32,6 +36,15 @@ namespace dfl {
 namespace {
 
 // ---------------------------------------------------------------- tensor memory, descriptors
+// D[tmem] (+)= A[tmem] * B[smem]: A is a row per lane, two 16-bit values to a column.
+DEV void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 // kind::f16: fp32 accumulator, both operands fp16 or both bf16, A K-major, B K-major or MN-major.
 constexpr uint32_t idesc_f32(bool bf16, int M, int N, bool b_mn) {
   return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
@@ -82,21 +95,20 @@ struct TcLayout {
   static constexpr int kTile = kKeys * 128;                // one 64-dim box of one tile
   static constexpr int kBox = H * kTile;                   // of a step's tiles
   static constexpr int kOperand = D / 64 * kBox;           // K, or V, of a step
-  static constexpr int kSlots = D == 128 ? (H == 2 ? 2 : 4) : (H == 2 ? 4 : 8);  // of each ring
-  static constexpr int kQ = 0;                             // D / 64 boxes of 128 rows
-  static constexpr int kP = kQ + D / 64 * kLanes * 128;    // H boxes of 128 rows x 64 keys
-  static constexpr int kK = kP + H * kLanes * 128;
+  static constexpr int kSlots = D == 128 ? (H == 2 ? 3 : 6) : (H == 2 ? 6 : 8);  // of each ring
+  static constexpr int kK = 0;
   static constexpr int kV = kK + kSlots * kOperand;
   static constexpr int kZ = kV + kSlots * kOperand;        // values of new keys that left the products
   static constexpr int kZs = kZ + kNewKeys * D * 2;        // their scores [128][16]
-  static constexpr int kMl = kZs + kLanes * kNewKeys * 4;  // states that meet at a segment's end
+  static constexpr int kX = kZs + kLanes * kNewKeys * 4;   // outputs that meet at a segment's end: two rounds of 16 columns
+  static constexpr int kMl = kX + (H == 2 ? 8192 : 0);     // and their (max, sum)
   static constexpr int kBar = kMl + kLanes * 8;
   static constexpr int kBars = 4 * kSlots + 2 + 2 + 4;     // K full, empty; V full, empty; S ready, free [2]; P, PV, Q, done
   static constexpr int kFlags = kBar + kBars * 8;          // [0] abort, [1] TMEM base, [2..3] odd values, [4..19] valid tiles of steps
   static constexpr int kWarpSums = kFlags + 80;
   static constexpr int kPre = kWarpSums + 32;
   static constexpr int smem(int batch) { return 1024 + kPre + (3 * batch + 1) * 4; }
-  static constexpr uint32_t kS = 0, kO = 256;              // TMEM columns: S buffers at 0 and kN, O
+  static constexpr uint32_t kS = 0, kO = 256, kQ = 384, kP = 448;  // TMEM columns: S buffers at 0 and kN
 };
 
 template <int D, bool BF16, int H>
@@ -191,6 +203,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
       if (w.left == 0) {
         begin_segment(w);
         id0 = 32;
+        if (lane < s_new[w.at.s])  // the segment's q, a new row a lane
+          bulk_prefetch_l2(static_cast<const uint16_t*>(P.q) +
+                               ((static_cast<size_t>(w.at.s) * P.rows_per_seq + lane) * P.nq + static_cast<size_t>(w.at.g) * grp) * D,
+                           grp * D * 2);
       }
       int page[2] = {-1, -1};
       const int cnt = min(H, w.left);
@@ -270,35 +286,34 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
       auto qk = [&](int i) {  // S[i & 1] = Q K^T
         const int st = i % L::kSlots;
         tc_fence_after();
-        const uint32_t q0 = smem_u32(smem + L::kQ), k0 = smem_u32(smem + L::kK + st * L::kOperand);
+        const uint32_t k0 = smem_u32(smem + L::kK + st * L::kOperand);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          tc_mma_bf16(tmem + L::kS + (i & 1) * L::kN, smem_desc_k_sw128(q0 + (kk >> 2) * (kLanes * 128) + (kk & 3) * 32),
-                      smem_desc_k_sw128(k0 + (kk >> 2) * L::kBox + (kk & 3) * 32), kQk, kk > 0 ? 1u : 0u);
+          mma_ts(tmem + L::kS + (i & 1) * L::kN, tmem + L::kQ + kk * 8, smem_desc_k_sw128(k0 + (kk >> 2) * L::kBox + (kk & 3) * 32),
+                 kQk, kk > 0 ? 1u : 0u);
         tc_commit(&sready[i & 1]);
         tc_commit(&kempty[st]);
       };
       auto pv = [&](int i, bool first) {  // O (+)= P V
         const int st = i % L::kSlots;
         tc_fence_after();
-        const uint32_t p0 = smem_u32(smem + L::kP), v0 = smem_u32(smem + L::kV + st * L::kOperand);
+        const uint32_t v0 = smem_u32(smem + L::kV + st * L::kOperand);
 #pragma unroll
         for (int kk = 0; kk < L::kN / 16; ++kk)
-          tc_mma_bf16(tmem + L::kO, smem_desc_k_sw128(p0 + (kk >> 2) * (kLanes * 128) + (kk & 3) * 32),
-                      desc_mn_sw128(v0 + kk * 2048, L::kBox), kPv, (kk > 0 || !first) ? 1u : 0u);
+          mma_ts(tmem + L::kO, tmem + L::kP + kk * 8, desc_mn_sw128(v0 + kk * 2048, L::kBox), kPv, (kk > 0 || !first) ? 1u : 0u);
         tc_commit(pvdone);
         tc_commit(&vempty[st]);
       };
       // Whichever product's inputs are ready goes next, so that neither waits behind the other's.
       Walk w{T0, 0, {}};
       int nqk = 0, npv = 0, segs = 0;
-      bool first_of[2] = {false, false};
+      bool first_of[4] = {};
       uint64_t idle_since = globaltimer_ns();
       uint32_t spins = 0;
       bool start = true;
       while (w.u < T1 || npv < nqk) {
         bool moved = false;
-        if (w.u < T1 && nqk <= npv + 1) {
+        if (w.u < T1 && nqk <= npv + 2) {
           if (w.left == 0) {
             begin_segment(w);
             start = true;
@@ -306,7 +321,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
           if (mbar_try_wait(&kfull[nqk % L::kSlots], (nqk / L::kSlots) & 1) &&
               (nqk < 2 || mbar_try_wait(&sfree[nqk & 1], ((nqk >> 1) - 1) & 1)) && (!start || mbar_try_wait(qready, segs & 1))) {
             qk(nqk);
-            first_of[nqk & 1] = start;
+            first_of[nqk & 3] = start;
             segs += start;
             start = false;
             const int cnt = min(H, w.left);
@@ -317,7 +332,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
           }
         }
         if (npv < nqk && mbar_try_wait(pready, npv & 1) && mbar_try_wait(&vfull[npv % L::kSlots], (npv / L::kSlots) & 1)) {
-          pv(npv, first_of[npv & 1]);
+          pv(npv, first_of[npv & 3]);
           ++npv;
           moved = true;
         }
@@ -345,32 +360,50 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
       if (!mbar_try_wait(bar, parity)) wait_long(bar, parity, flag, P.err, WL);
       __syncwarp();
     };
+    // a segment's row of q; rows that are not there are zero
+    uint4 qrow[D / 8];
+    auto load_q = [&](const Place& p) {
+      const int r = row / grp;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          static_cast<const uint16_t*>(P.q) +
+          ((static_cast<size_t>(p.s) * P.rows_per_seq + r) * P.nq + p.g * grp + row - r * grp) * D);
+      const bool there = row < s_new[p.s] * grp;
+#pragma unroll
+      for (int ch = 0; ch < D / 8; ++ch) qrow[ch] = there ? __ldcg(src + ch) : make_uint4(0, 0, 0, 0);
+    };
+    auto store_q = [&]() {  // once the products with the q before it are done
+      __syncwarp();
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t u[16];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint4 v = qrow[c * 4 + k];
+          u[4 * k] = v.x, u[4 * k + 1] = v.y, u[4 * k + 2] = v.z, u[4 * k + 3] = v.w;
+        }
+        tmem_store16(tmem + lanes + L::kQ + c * 16, u);
+      }
+      tmem_wait_stores();
+      tc_fence_before();
+      mbar_arrive(qready);
+    };
+    if (H == 2) {  // the weights of the other tile's keys stay zero
+      const uint32_t zero[16] = {};
+      tmem_store16(tmem + lanes + L::kP + (1 - hh) * 32, zero);
+      tmem_store16(tmem + lanes + L::kP + (1 - hh) * 32 + 16, zero);
+    }
     int i = 0, seg_no = 0;
-    for (Walk w{T0, 0, {}}; w.u < T1; ++seg_no) {
-      begin_segment(w);
+    Walk w{T0, 0, {}};
+    begin_segment(w);
+    load_q(w.at);
+    store_q();
+    for (; w.u < T1; ++seg_no) {
       const int s = w.at.s, g = w.at.g, t0 = w.at.t;
       const bool whole = t0 == 0 && w.left == w.at.nt;
       const int len = s_len[s], n_new = s_new[s], nk = len + n_new;
       const int r = row / grp, head = g * grp + row - r * grp;
       const bool there = row < n_new * grp;
       const int lim = len + r;  // last key the row may see
-      // the row of q into the swizzled boxes; rows that are not there are zero
-      {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.q) +
-                                                          ((static_cast<size_t>(s) * P.rows_per_seq + r) * P.nq + head) * D);
-#pragma unroll
-        for (int ch = 0; ch < D / 8; ++ch) {
-          const uint4 v = there ? __ldcg(src + ch) : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(smem + L::kQ + (ch >> 3) * (kLanes * 128) + sw128(tid, ch & 7)) = v;
-        }
-        if (H == 2) {  // the weights of the other tile's keys stay zero
-#pragma unroll
-          for (int ch = 0; ch < 8; ++ch)
-            *reinterpret_cast<uint4*>(smem + L::kP + (1 - hh) * (kLanes * 128) + sw128(tid, ch)) = make_uint4(0, 0, 0, 0);
-        }
-        fence_async_shared();
-        mbar_arrive(qready);
-      }
       float m = -INFINITY, l = 0.f;
       uint32_t kept = 0;  // new keys whose values are added at the end
       bool first = true;
@@ -483,20 +516,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
           ls[0] = add2(ls[0], ls[1]);
           l += ls[0].x + ls[0].y;
         }
-        // P, once the previous step's product has read the buffer
+        // P, once the previous step's product has read it
         if (i > 0) wait(pvdone, (i - 1) & 1);
+        __syncwarp();
+        tc_fence_after();
 #pragma unroll
-        for (int ch = 0; ch < 8; ++ch) {
-          uint4 v;
-          v.x = pack2<BF16>(sc[8 * ch], sc[8 * ch + 1]);
-          v.y = pack2<BF16>(sc[8 * ch + 2], sc[8 * ch + 3]);
-          v.z = pack2<BF16>(sc[8 * ch + 4], sc[8 * ch + 5]);
-          v.w = pack2<BF16>(sc[8 * ch + 6], sc[8 * ch + 7]);
-          *reinterpret_cast<uint4*>(smem + L::kP + hh * (kLanes * 128) + sw128(tid, ch)) = v;
+        for (int c = 0; c < 2; ++c) {
+          uint32_t u[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) u[k] = pack2<BF16>(sc[32 * c + 2 * k], sc[32 * c + 2 * k + 1]);
+          tmem_store16(tmem + lanes + L::kP + hh * 32 + c * 16, u);
         }
-        fence_async_shared();
+        tmem_wait_stores();
+        fence_async_shared();  // (cleared values)
         tc_fence_before();
         mbar_arrive(pready);
+      }
+      // the next segment's q: every score of this one has been read
+      const bool more = w.u < T1;
+      if (more) {
+        begin_segment(w);
+        load_q(w.at);
+        store_q();
       }
       wait(pvdone, (i - 1) & 1);
       tc_fence_after();
@@ -534,49 +575,52 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
       const float inv = den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den);
       float* slot = P.part + (2 * static_cast<size_t>(cta) + (seg_no == 0 ? 0 : 1)) * static_cast<size_t>(L::kRows) * (D + 2);
       uint16_t* dst = static_cast<uint16_t*>(P.out) + ((static_cast<size_t>(s) * P.rows_per_seq + r) * P.nq + head) * D;
-      float4* xch = reinterpret_cast<float4*>(smem + L::kP);  // [columns / 4][64 rows]
-      if (H == 2) {
-        if (hh == 1) {
-#pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
-            float o[16];
-            load_o(c, o);
+      auto put = [&](int c, const float (&o)[16]) {
+        if (!there) return;
+        if (whole) {
+          uint4 v[2];
+          uint32_t* b = reinterpret_cast<uint32_t*>(v);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) xch[(c * 4 + q) * 64 + row] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-          }
+          for (int k = 0; k < 8; ++k) b[k] = pack2<BF16>(o[2 * k] * inv, o[2 * k + 1] * inv);
+          *reinterpret_cast<uint4*>(dst + c * 16) = v[0];
+          *reinterpret_cast<uint4*>(dst + c * 16 + 8) = v[1];
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            __stcg(reinterpret_cast<float4*>(slot + static_cast<size_t>(row) * D + c * 16 + 4 * q),
+                   make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]));
         }
-        named_bar_sync(1, kLanes);
-      }
-      if (hh == 0) {
-        const float w_other = H == 2 ? weight_of(s_ml[tid + (H == 2 ? 64 : 0)], M) : 0.f;
+      };
+      if (H == 2) {
+        // each half of the rows' threads finishes half of the columns, 16 a round, with the other's from shared memory
+        float4* xch = reinterpret_cast<float4*>(smem + L::kX);  // [2 halves][4][64 rows]
+        const float w_other = weight_of(s_ml[tid ^ 64], M);
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          const int own = hh * (D / 32) + c, other = (1 - hh) * (D / 32) + c;
+          float o[16];
+          load_o(other, o);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) xch[(hh * 4 + q) * 64 + row] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          load_o(own, o);
+          named_bar_sync(1, kLanes);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float4 x = xch[((1 - hh) * 4 + q) * 64 + row];
+            o[4 * q] = o[4 * q] * w_own + x.x * w_other;
+            o[4 * q + 1] = o[4 * q + 1] * w_own + x.y * w_other;
+            o[4 * q + 2] = o[4 * q + 2] * w_own + x.z * w_other;
+            o[4 * q + 3] = o[4 * q + 3] * w_own + x.w * w_other;
+          }
+          put(own, o);
+          named_bar_sync(1, kLanes);
+        }
+      } else {
 #pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {
           float o[16];
           load_o(c, o);
-          if (H == 2) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float4 x = xch[(c * 4 + q) * 64 + row];
-              o[4 * q] = o[4 * q] * w_own + x.x * w_other;
-              o[4 * q + 1] = o[4 * q + 1] * w_own + x.y * w_other;
-              o[4 * q + 2] = o[4 * q + 2] * w_own + x.z * w_other;
-              o[4 * q + 3] = o[4 * q + 3] * w_own + x.w * w_other;
-            }
-          }
-          if (!there) continue;
-          if (whole) {
-            uint4 v[2];
-            uint32_t* b = reinterpret_cast<uint32_t*>(v);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) b[k] = pack2<BF16>(o[2 * k] * inv, o[2 * k + 1] * inv);
-            *reinterpret_cast<uint4*>(dst + c * 16) = v[0];
-            *reinterpret_cast<uint4*>(dst + c * 16 + 8) = v[1];
-          } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              __stcg(reinterpret_cast<float4*>(slot + static_cast<size_t>(row) * D + c * 16 + 4 * q),
-                     make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]));
-          }
+          put(c, o);
         }
       }
       if (hh == 0 && there && !whole)

@@ -72,7 +72,7 @@ struct PagedAttnParams {
 int paged_attn_rows(int rows);  // rows of a partial slot: `rows` rounded up to what a kernel variant holds
 int paged_attn_set_attributes();
 int launch_paged_attn(const PagedAttnParams& p, bool bf16, int n_ctas, cudaStream_t stream);
-// The first kernel's tcgen05 form, for more than 32 rows; called by the above.
+// The first kernel's tcgen05 form, for more than 16 rows; called by the above.
 int paged_attn_tc_set_attributes();
 int launch_paged_attn_tc(const PagedAttnParams& p, bool bf16, int n_ctas, cudaStream_t stream);
 
