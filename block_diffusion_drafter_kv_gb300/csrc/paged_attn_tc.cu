@@ -79,6 +79,19 @@ DEV void tmem_store16(uint32_t taddr, const uint32_t (&r)[16]) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+// Whether a phase is complete, without the suspension that a try_wait may take: for a thread that
+// watches several barriers.
+DEV bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 DEV void tmem_wait_loads() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 DEV void tmem_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -286,21 +299,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
       auto qk = [&](int i) {  // S[i & 1] = Q K^T
         const int st = i % L::kSlots;
         tc_fence_after();
-        const uint32_t k0 = smem_u32(smem + L::kK + st * L::kOperand);
+        // one descriptor and constant steps of its address field: building each one took longer
+        // than the product it describes
+        const uint64_t k0 = smem_desc_k_sw128(smem_u32(smem + L::kK + st * L::kOperand));
+        const uint32_t d = tmem + L::kS + (i & 1) * L::kN;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          mma_ts(tmem + L::kS + (i & 1) * L::kN, tmem + L::kQ + kk * 8, smem_desc_k_sw128(k0 + (kk >> 2) * L::kBox + (kk & 3) * 32),
-                 kQk, kk > 0 ? 1u : 0u);
+          mma_ts(d, tmem + L::kQ + kk * 8, k0 + (((kk >> 2) * L::kBox + (kk & 3) * 32) >> 4), kQk, kk > 0 ? 1u : 0u);
         tc_commit(&sready[i & 1]);
         tc_commit(&kempty[st]);
       };
       auto pv = [&](int i, bool first) {  // O (+)= P V
         const int st = i % L::kSlots;
         tc_fence_after();
-        const uint32_t v0 = smem_u32(smem + L::kV + st * L::kOperand);
+        const uint64_t v0 = desc_mn_sw128(smem_u32(smem + L::kV + st * L::kOperand), L::kBox);
 #pragma unroll
         for (int kk = 0; kk < L::kN / 16; ++kk)
-          mma_ts(tmem + L::kO, tmem + L::kP + kk * 8, desc_mn_sw128(v0 + kk * 2048, L::kBox), kPv, (kk > 0 || !first) ? 1u : 0u);
+          mma_ts(tmem + L::kO, tmem + L::kP + kk * 8, v0 + (kk * 2048 >> 4), kPv, (kk > 0 || !first) ? 1u : 0u);
         tc_commit(pvdone);
         tc_commit(&vempty[st]);
       };
@@ -308,7 +323,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
       Walk w{T0, 0, {}};
       int nqk = 0, npv = 0, segs = 0;
       bool first_of[4] = {};
-      uint64_t idle_since = globaltimer_ns();
+      uint64_t idle_since = 0;
       uint32_t spins = 0;
       bool start = true;
       while (w.u < T1 || npv < nqk) {
@@ -318,8 +333,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
             begin_segment(w);
             start = true;
           }
-          if (mbar_try_wait(&kfull[nqk % L::kSlots], (nqk / L::kSlots) & 1) &&
-              (nqk < 2 || mbar_try_wait(&sfree[nqk & 1], ((nqk >> 1) - 1) & 1)) && (!start || mbar_try_wait(qready, segs & 1))) {
+          if (mbar_test(&kfull[nqk % L::kSlots], (nqk / L::kSlots) & 1) &&
+              (nqk < 2 || mbar_test(&sfree[nqk & 1], ((nqk >> 1) - 1) & 1)) && (!start || mbar_test(qready, segs & 1))) {
             qk(nqk);
             first_of[nqk & 3] = start;
             segs += start;
@@ -331,17 +346,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
             moved = true;
           }
         }
-        if (npv < nqk && mbar_try_wait(pready, npv & 1) && mbar_try_wait(&vfull[npv % L::kSlots], (npv / L::kSlots) & 1)) {
+        if (npv < nqk && mbar_test(pready, npv & 1) && mbar_test(&vfull[npv % L::kSlots], (npv / L::kSlots) & 1)) {
           pv(npv, first_of[npv & 3]);
           ++npv;
           moved = true;
         }
+        // (reading the timer takes some 600 cycles: only where nothing has moved for a while)
         if (moved) {
-          idle_since = globaltimer_ns();
-        } else if ((++spins & 63u) == 0 && (flag[0] || globaltimer_ns() - idle_since > WL)) {
-          if (!flag[0]) raise_flag(P.err, kDevTimeout);
-          flag[0] = 1;
-          break;
+          spins = 0;
+        } else if ((++spins & 1023u) == 0) {
+          const uint64_t now = globaltimer_ns();
+          if (spins == 1024) idle_since = now;
+          if (flag[0] || now - idle_since > WL) {
+            if (!flag[0]) raise_flag(P.err, kDevTimeout);
+            flag[0] = 1;
+            break;
+          }
         }
       }
       tc_commit(mdone);
