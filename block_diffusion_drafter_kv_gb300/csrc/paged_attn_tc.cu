@@ -7,14 +7,17 @@
 // is one M = 128, N = 128 product with the rows twice in Q, once for each tile, so that all
 // 128 lanes of the softmax have a row of 64 scores; P keeps zeros where a row's other tile is, and
 // O += P V (M = 128, K = 128 keys) adds up two states per row, which meet at the segment's
-// end. With 65 to 128 rows a step is one tile. Against the step's 2750 cycles of HBM time (64 KB)
-// the products take about 1000 and the softmax 800, one after another for one step and
-// overlapped between steps.
+// end. With 65 to 128 rows a step is one tile. Measured (bf16, 32 query heads on 8 KV heads, 4
+// sequences of 32768, d 128): 91 us with 20 rows, 99 with 64 (80% of the copy rate), 120 with 128;
+// against a two-tile step's 2750 cycles of HBM time (64 KB) issuing its products takes 1250 and its
+// softmax 1100, overlapped between steps, so that it waits for copies; a one-tile step (1400 cycles of
+// HBM time) waits for the chain of its products and softmax (1700), d 64 likewise. Short caches (128
+// sequences of 500: 123 us with 64 rows, 36%) are bound by the segments' ends: q, output.
 //
 //   S   two TMEM buffers of N columns: the next step's Q K^T runs under this one's softmax
 //   Q, P  in TMEM too, as the products' A operands: with them in shared memory (64 KB) the rings
-//       held two steps instead of three, and a step waited for its copies (104 us against the
-//       figure below at 4 sequences of 32768, blocks of 16)
+//       held two steps instead of three, and a step waited for its copies (104 us against 99
+//       at 4 sequences of 32768, 64 rows)
 //   O   TMEM, kept over the segment. A row's reference moves only where a score passes it by more
 //       than 8 binary orders; that row of O is then rescaled in TMEM between two products
 //   K, V  rings of their own: a K stage is free after its Q K^T, a V stage after its P V
@@ -510,7 +513,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
               *at = make_uint4(0, 0, 0, 0);
             }
           }
-          if (odd) {
+          if (odd && valid) {  // (a tile of another CTA's has its new keys looked after there)
 #pragma unroll
             for (int k = 0; k < 64; ++k) {
               const int key = key0 + k;

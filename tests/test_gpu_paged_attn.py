@@ -155,6 +155,27 @@ def test_keys_hidden_from_a_row_may_be_anything(B, dtype, nq, rows):
             assert bool(torch.isfinite(rest[..., :7]).all()) and bool(torch.isfinite(rest[..., 8:]).all())
 
 
+@pytest.mark.parametrize("nq,rows", [(4, 4), (4, 8), (8, 16)])
+def test_new_rows_on_two_pages_with_an_infinite_value_on_the_first(B, nq, rows):
+    """Each page in a CTA of its own: the rows that do not see the value get their result."""
+    full = Case(B, nq, 1, 128, torch.bfloat16, [0] * 200, [rows] * 200, rows)
+    full.cache.v_pool.fill_(NAN)               # every CTA meets NaN among its new values
+    full.attend()
+    c = Case(B, nq, 1, 128, torch.bfloat16, [62, 62], [rows] * 2, rows, seed=1)
+    c.attend()
+    want = c.out.clone()
+    c.cache.v_pool[0, c.at(0)[63], 0, 9] = INF
+    c.out.fill_(3.0)
+    c.attend()
+    got = c.out.reshape(2, rows, nq, 128)
+    assert torch.equal(got[1], want.reshape(2, rows, nq, 128)[1])
+    off = (got[0, 0].double() - want.reshape(2, rows, nq, 128)[0, 0].double()).abs()
+    assert bool((off <= 8 * HALF[torch.bfloat16] * 6).all())
+    rest = got[0, 1:].float()
+    assert not bool(torch.isfinite(rest[..., 9]).any())
+    assert bool(torch.isfinite(rest[..., :9]).all()) and bool(torch.isfinite(rest[..., 10:]).all())
+
+
 def test_nothing_but_nan_is_nan(B):
     """A sequence whose every key is NaN, in one CTA and split over several."""
     c = Case(B, 4, 2, 128, torch.float16, [0, 3000, 5], [1, 1, 1], 1)
