@@ -81,7 +81,7 @@ int dflash_cache_config_check(const dflash_cache_config* c) {
       c->max_batch <= kCacheMaxBatch && static_cast<long long>(c->max_batch) * c->pages_per_seq < (1LL << 31) &&
       c->rope_dim >= 0 && c->rope_dim <= c->head_dim && c->rope_dim % 16 == 0 &&
       (c->rope_interleaved == 0 || c->rope_interleaved == 1) && (c->rope_dim == 0 || c->rope_positions >= 1) &&
-      std::isfinite(c->scale) && c->scale >= 0.f;
+      c->scale >= 0.f && c->scale <= 1e38f;
   return ok ? DFLASH_OK : DFLASH_E_CONFIG;
 }
 

@@ -931,7 +931,7 @@ int dflash_logprobs(dflash_handle* h, const void* logits, int32_t dtype, int64_t
   if (!h->bound) return DFLASH_E_STATE;
   const int V = h->cfg.vocab;
   if (!logits || !entropy || rows < 1 || n_top < 0 || n_top > kLpMaxTop || n_top > V || row_stride < V ||
-      !(temperature > 0.f) || !std::isfinite(temperature) || !tokens != !logprob || (n_top > 0 && (!top_ids || !top_logprobs)))
+      !(temperature >= 1.17549435e-38f) || !std::isfinite(temperature) || !tokens != !logprob || (n_top > 0 && (!top_ids || !top_logprobs)))
     return DFLASH_E_INVAL;
   if (dtype != DFLASH_F32 && dtype != DFLASH_F16 && dtype != DFLASH_BF16) return DFLASH_E_INVAL;
   const int elem = dtype == DFLASH_F32 ? 4 : 2;

@@ -11,7 +11,7 @@
 namespace dfl {
 
 constexpr int kPagePos = 64;          // positions per page, and keys per attention tile
-constexpr int kPoolMaxBatch = 4096;   // sequences per page-pool call (two shared-memory arrays)
+constexpr int kPoolMaxBatch = 4096;   // sequences per page-pool call (five integers each in shared memory)
 constexpr int kCacheMaxBatch = 1024;  // sequences per attention call (a shared-memory prefix table)
 constexpr int kPagedMaxCtas = 256;    // attention partial slots are sized for this many CTAs
 

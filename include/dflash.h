@@ -250,7 +250,7 @@ int dflash_verify_greedy_hidden(dflash_handle* h, const void* target_hidden, con
  *                 token, which is not read: logprob and entropy 0, top_ids -1, top_logprobs
  *                 0. Other values outside [0, vocab) do the same and set DFLASH_DEV_TOKEN.
  *   rows          >= 1; any number (not bound by max_batch and max_block)
- *   temperature   > 0
+ *   temperature   finite, at least 2^-126
  *   n_top         0..32, at most vocab
  *   logprob, entropy   fp32 [rows] out
  *   top_ids            int32 [rows][n_top] out, or NULL with n_top 0
@@ -460,7 +460,7 @@ typedef struct dflash_cache_config {
   int32_t rope_dim;         /* dims of each head that are rotated: 0..d, a multiple of 16 */
   int32_t rope_interleaved; /* pairs (2j, 2j + 1) instead of (j, j + rope_dim / 2) */
   int32_t rope_positions;   /* rows of the rotary tables */
-  float scale;              /* of the scores; 0: 1 / sqrt(d) */
+  float scale;              /* of the scores, 0 <= scale <= 1e38; 0: 1 / sqrt(d) */
 } dflash_cache_config;
 
 typedef struct dflash_cache dflash_cache;
@@ -509,12 +509,13 @@ int dflash_cache_append(dflash_cache* c, int32_t layer, const void* q, const voi
  * decoding, a block of rows is verification.
  *   q        [batch * rows_per_seq][nq][d] of the cache's dtype
  *   n_new    int32 [batch] on the device, 0 <= n_new[s] <= rows_per_seq <= max_block
- *   out      [batch * rows_per_seq][nq][d] of the cache's dtype. Rows past n_new[s] are left
- *            as they were.
+ *   out      [batch * rows_per_seq][nq][d] of the cache's dtype, not overlapping q. Rows past
+ *            n_new[s] are left as they were.
  * The positions of the new rows are in the cache already. What lies in the cache behind
  * them is never used, whatever its value. A sequence whose lengths are out of range or pass
  * pages_per_seq * 64 is left out, and a page id outside [0, n_pages) drops that page's
- * positions (a row with none left is 0); both set DFLASH_DEV_CAPACITY. */
+ * positions (a row with none left is 0); both set DFLASH_DEV_CAPACITY. A row that sees an
+ * infinite or NaN value has an infinity or NaN in that column: which of them is open. */
 int dflash_cache_attend(dflash_cache* c, int32_t layer, const void* q, const int32_t* n_new, int32_t batch,
                         int32_t rows_per_seq, void* out, void* stream);
 

@@ -168,6 +168,51 @@ def test_sorted_logits(make, V, rows):
         check(up, t, call(make(V), up, t, n), n)
 
 
+@pytest.mark.parametrize("n", [8, 32])
+def test_a_row_whose_late_values_count_before_a_higher_row(make, n):
+    """Rows of one CTA, high after low: a low row's n-th largest stands in its last stage, where a
+    warp without candidates is already at the high row."""
+    V, rows = 32768, 1000
+    e = torch.arange(V, device="cuda")
+    owner = e // 128 % 8                       # the warp that reads it
+    low = -1.0 - e.float() / V
+    per = n // 8
+    for w in range(1, 8):                      # all warps but 0 have their share of the largest early
+        low[(owner == w).nonzero()[:per, 0]] = 10.0 + torch.arange(per, device="cuda") + 0.1 * w
+    low[-700:] = torch.where(owner[-700:] > 0, 5.0 + e[-700:] % 50 / 10, low[-700:])   # the rest of them late
+    z = low.expand(rows, V).contiguous()
+    z[1::2] += 100.0
+    t = torch.full((rows,), V - 1, dtype=torch.int32, device="cuda")
+    for _ in range(5):
+        check(z, t, call(make(V), z, t, n), n)
+
+
+def test_one_certain_token_and_extreme_temperatures(make):
+    """An entropy is not negative; the smallest and largest temperatures give the limits."""
+    V = 20000
+    z, t = logits(64, V, torch.float32, seed=5)
+    z[torch.arange(64, device="cuda"), t.long()] = 60 + torch.arange(64, device="cuda") * 0.37
+    lp, h, ids, top = call(make(V), z, t, 2)
+    assert bool((h >= 0).all()) and bool((h < 1e-6).all()) and torch.equal(ids[:, 0], t)
+    lp, h, ids, top = call(make(V), z, t, 2, 2.0 ** -126)
+    assert bool((lp == 0).all()) and bool((h == 0).all()) and bool((top[:, 0] == 0).all()) and bool((top[:, 1] < -1e30).all())
+    lp, h, ids, top = call(make(V), z, t, 2, 3e38)
+    for x, want in ((lp, -math.log(V)), (h, math.log(V))):
+        assert bool(((x - want).abs() < 1e-4).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+def test_masked_logits_at_high_temperatures(make, dtype):
+    """-inf stays out of a distribution that is nearly uniform."""
+    V = 5000
+    z, t = logits(8, V, dtype, seed=7)
+    keep = torch.rand(8, V, generator=torch.Generator(device="cuda").manual_seed(8), device="cuda") < 0.3
+    keep[torch.arange(8, device="cuda"), t.long()] = True
+    z = torch.where(keep, z, torch.tensor(-INF, dtype=dtype, device="cuda"))
+    for temperature in (300.0, 600.0, 20000.0, 1e20, 1e30):
+        check(z, t, call(make(V), z, t, 4, temperature), 4, temperature)
+
+
 def test_masked_logits(make):
     """-inf masks, masks of the type's lowest value, rows with one token left, and rows with none."""
     V = 20000
@@ -244,5 +289,7 @@ def test_bad_arguments_are_refused_before_a_launch(make):
                 dict(n=33), dict(ids=None), dict(top=None), dict(tokens=t.data_ptr() + 1), dict(ids=p + 2), dict(h=p + 1)):
         assert c(**bad) == -1, bad
     assert bool((o == 0).all())
+    for bad in (1e-39, 2.0 ** -149):           # 1 / T overflows
+        assert c(temp=bad) == -1
     tiny = make(2)
     assert tiny.L.dflash_logprobs(tiny.h, z.data_ptr(), B.F32, 2, t.data_ptr(), 2, 1.0, 3, p, p, p, p, None) == -1

@@ -76,6 +76,10 @@ def test_cache_config_check_rejects(L, bad):
     assert L.dflash_cache_create(cfg(**bad), ctypes.byref(h)) == -2
 
 
+def test_cache_config_check_rejects_a_scale_that_overflows(L):
+    assert L.dflash_cache_config_check(cfg(scale=2e38)) == -2 and L.dflash_cache_config_check(cfg(scale=1e38)) == 0
+
+
 def test_cache_config_check_accepts(L):
     for kw in (dict(), dict(head_dim=64, rope_dim=64, dtype=B.BF16), dict(n_heads=16, max_block=16), dict(n_heads=256, max_block=1),
                dict(rope_dim=0, rope_positions=0), dict(rope_dim=32, rope_interleaved=1), dict(scale=0.25), dict(max_batch=1024)):
