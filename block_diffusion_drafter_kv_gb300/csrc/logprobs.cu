@@ -47,12 +47,15 @@ namespace {
 
 constexpr int kWarps = 8;                    // consumer warps
 constexpr int kConsumers = 32 * kWarps;
-constexpr int kThreads = kConsumers + 32;
 constexpr int kUnitWords = kConsumers;       // 16-byte words of a unit: one per consumer thread
 constexpr int kStageUnits = 4;
 constexpr int kStageWords = kStageUnits * kUnitWords;
-constexpr int kStages = 4;
-constexpr int kCtasPerSm = 3;
+// CTAs of an SM, and stages of 16 KB of each one's ring
+template <bool TOP>
+struct Shape {
+  static constexpr int kCtasPerSm = TOP ? 2 : 3, kStages = TOP ? 6 : 4;
+  static constexpr int kThreads = kConsumers + (TOP ? 64 : 32);  // and the producer, and the threshold's warp
+};
 constexpr int kListed = 1024;                // rows of a call whose tokens are looked through before the list is cut
 constexpr unsigned kAll = 0xffffffffu;
 using Key = unsigned long long;
@@ -128,49 +131,6 @@ constexpr int kWaiting = 96;
 __device__ __noinline__ Key sort_into(Key list, const Key* waiting, int count) {  // count <= 32
   const int lane = threadIdx.x & 31;
   return merge_desc(list, sort_desc(lane < count ? waiting[lane] : 0));
-}
-// Candidates of a warp, the values not below `floor` of the lanes in `votes`: their NW words of a
-// lane are read again by the whole warp, an element each. Lane 0's words start at `vals` and lie
-// `stride` apart there and in the row, from `index` on; elements from `limit` on do not count.
-// Returns the new count of waiting keys. (A chain of latencies on the streaming path: the lanes'
-// numbers go through shared memory, and two rounds of loads and votes are in flight together.)
-template <typename T, int NW>
-__device__ __noinline__ int note_candidates(Key& list, Key* waiting, uint8_t* lanes, int count, unsigned votes, float floor,
-                                            const T* vals, int stride, int index, int limit) {
-  constexpr int VE = 16 / sizeof(T), N = NW * VE;  // elements of a lane: 32 or 16
-  const int lane = threadIdx.x & 31, sub = lane % N;
-  const unsigned below = (1u << lane) - 1;
-  if (votes >> lane & 1) lanes[__popc(votes & below)] = static_cast<uint8_t>(lane);
-  __syncwarp();
-  const int total = __popc(votes);
-  for (int done = 0; done < total; done += 2 * (32 / N)) {
-    float x[2];
-    int at[2];
-    unsigned in[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int who = done + i * (32 / N) + lane / N;
-      const int off = (who < total ? lanes[who] : 0) * VE + sub / VE * stride + sub % VE;
-      at[i] = who < total && index + off < limit ? index + off : -1;
-      x[i] = widen1(vals[off]);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) in[i] = __ballot_sync(kAll, at[i] >= 0 && !(x[i] < floor));
-    int n = count;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (in[i] >> lane & 1) waiting[n + __popc(in[i] & below)] = make_key(order_bits(x[i]), at[i]);
-      n += __popc(in[i]);
-    }
-    count = n;
-    __syncwarp();
-    while (count >= 32) {  // (at most 31 + 64)
-      count -= 32;
-      list = sort_into(list, waiting + count, 32);
-      __syncwarp();
-    }
-  }
-  return count;
 }
 
 // Sums relative to the maximum M.
@@ -267,6 +227,55 @@ struct Word<__half> : Word16<__half2> {
   DEV static uint4 raised(const uint4& q) { return Word16::raised(q, __float2half2_rn(kFloor)); }
 };
 
+// Candidates of a warp, the values not below `floor` of the lanes in `votes`: their NW words of a
+// lane are read again by the whole warp, an element each. Lane 0's words start at `vals` and lie
+// `stride` apart there and in the row, from `index` on; elements from `limit` on do not count.
+// (A chain of latencies on the streaming path: the lanes' numbers go through shared memory, and two
+// rounds of loads and votes are in flight together. Compact, too: a ballot for each of the words'
+// elements in registers is fewer steps, but so much code that it waits for its instructions, 49 us
+// against 41.)
+struct Noted {
+  Key list;
+  int waiting;  // keys that wait now
+};
+template <typename T, int NW>
+__device__ __noinline__ Noted note_candidates(Noted to, Key* waiting, uint8_t* lanes, unsigned votes, float floor, const T* vals,
+                                              int stride, int index, int limit) {
+  constexpr int VE = 16 / sizeof(T), N = NW * VE;  // elements of a lane: 32 or 16
+  const int lane = threadIdx.x & 31, sub = lane % N;
+  const unsigned below = (1u << lane) - 1;
+  if (votes >> lane & 1) lanes[__popc(votes & below)] = static_cast<uint8_t>(lane);
+  __syncwarp();
+  const int total = __popc(votes);
+#pragma unroll 1
+  for (int done = 0; done < total; done += 2 * (32 / N)) {
+    float x[2];
+    int at[2];
+    unsigned in[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int who = done + i * (32 / N) + lane / N;
+      const int off = (who < total ? lanes[who] : 0) * VE + sub / VE * stride + sub % VE;
+      at[i] = who < total && index + off < limit ? index + off : -1;
+      x[i] = widen1(vals[off]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) in[i] = __ballot_sync(kAll, at[i] >= 0 && !(x[i] < floor));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (in[i] >> lane & 1) waiting[to.waiting + __popc(in[i] & below)] = make_key(order_bits(x[i]), at[i]);
+      to.waiting += __popc(in[i]);
+    }
+    __syncwarp();
+    while (to.waiting >= 32) {  // (at most 31 + 64)
+      to.waiting -= 32;
+      to.list = sort_into(to.list, waiting + to.waiting, 32);
+      __syncwarp();
+    }
+  }
+  return to;
+}
+
 // A row's words of 16 bytes: `lead` logits before the first whole aligned word, `words` whole
 // ones, the rest behind them.
 template <typename T>
@@ -281,23 +290,96 @@ struct RowWords {
   }
 };
 
-// First unit of CTA c's range, and the CTA whose range holds unit u (G <= U: none is empty).
-DEV long long range_begin(long long c, long long U, int G) { return c * U / G; }
-DEV int cta_of(long long u, long long U, int G) { return static_cast<int>(((u + 1) * G - 1) / U); }
+DEV int add_acq_rel(int* p, int v) {
+  int old;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
+}
 
-struct Shared {
-  uint4 ring[kStages][kStageWords];
-  Key waiting[kWarps][kWaiting];
-  uint8_t lanes[kWarps][32];
-  Key list[kWarps][32];         // the warps' results of a segment
+template <int STAGES, bool TOP>
+struct SharedOf {
+  uint4 ring[STAGES][kStageWords];
+  static constexpr int kLists = TOP ? kWarps : 1;
+  Key waiting[kLists][kWaiting];
+  Key list[kLists][32];         // the warps' results of a segment
   Part part[kWarps];
-  uint64_t full[kStages], empty[kStages], ready, taken;
-  volatile uint32_t thr[2][kWarps];  // by segment mod 2: a warp can be one segment ahead of another
+  uint64_t full[STAGES], empty[STAGES], ready, taken;
+  // by segment mod 2, since a warp can be one segment ahead of another:
+  uint8_t lanes[kLists][32];
+  uint32_t best[2][kLists][32];      // each lane's largest value
+  uint4 tops[2][kWarps];             // the four largest of each warp after its first stage
+  unsigned long long thr;            // (segment + 1, bits of a value that no candidate of it lies below)
+  volatile uint32_t started;         // the last segment of which all warps have stored their first `best`
+  volatile uint32_t events;          // stores to `best` so far
+  volatile int done;
+  float z_token[2];                  // the token's logit, of the row this CTA begins with, of the row it ends with
   volatile int abort;
   volatile int last[2];         // whether this CTA arrived last at the row it begins with, at the row it ends with
-  int warp_rows[kWarps + 1];
+  int warp_rows[kWarps + 2];
   uint16_t rows[2];             // [min(rows, kListed)] the rows that have a token
 };
+
+// The threshold that a segment starts with: the k-th largest of the four largest lane maxima of
+// each warp, which the warps leave before a barrier and each looks at behind it.
+template <typename Shared>
+__device__ __noinline__ void publish_tops(Shared& sh, int par, uint32_t best) {
+  static_assert(kLpMaxTop == 4 * kWarps, "four of each warp make the longest list");
+  const int lane = threadIdx.x & 31;
+  uint32_t t[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    t[i] = __reduce_max_sync(kAll, best);
+    if (lane == __ffs(__ballot_sync(kAll, best == t[i])) - 1) best = 0;
+  }
+  if (lane == 0) sh.tops[par][threadIdx.x >> 5] = make_uint4(t[0], t[1], t[2], t[3]);
+  __syncwarp();
+}
+template <typename Shared>
+__device__ __noinline__ uint32_t first_threshold(const Shared& sh, int par, int k) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t mine = reinterpret_cast<const uint32_t*>(sh.tops[par])[lane];
+  int above = 0;  // values before this one in descending order
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const uint32_t v = __shfl_sync(kAll, mine, i);
+    above += v > mine || (v == mine && i < lane);
+  }
+  return __shfl_sync(kAll, mine, __ffs(__ballot_sync(kAll, above == k - 1)) - 1);
+}
+// The k-th largest of the 256 lane maxima of the segment that runs, again and again while they change:
+// k values of the row are not below it. (Maxima that change meanwhile only grow. A segment's name goes
+// with its threshold, so that one that is late for it is not taken for the next.)
+template <typename Shared>
+DEV void keep_threshold(Shared& sh, int k) {
+  const int lane = threadIdx.x & 31;
+  uint32_t seen = 0;
+  while (true) {
+    const uint32_t events = __shfl_sync(kAll, sh.events, 0);
+    if (__any_sync(kAll, sh.done != 0)) return;
+    if (events == seen) {
+      __nanosleep(100);
+      continue;
+    }
+    seen = events;
+    const uint32_t seg = __shfl_sync(kAll, sh.started, 0);
+    __threadfence_block();
+    uint32_t v[kWarps], top = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v[w] = *const_cast<volatile uint32_t*>(&sh.best[seg & 1][w][lane]);
+#pragma unroll 1
+    for (int i = 0; i < k; ++i) {
+      uint32_t mine = v[0];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) mine = max(mine, v[w]);
+      top = __reduce_max_sync(kAll, mine);
+      bool drop = lane == __ffs(__ballot_sync(kAll, mine == top)) - 1;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w)
+        if (drop && v[w] == top) v[w] = 0, drop = false;
+    }
+    if (lane == 0) atomicMax(&sh.thr, static_cast<Key>(seg + 1) << 32 | top);
+  }
+}
 
 __device__ __noinline__ void wait_long(uint64_t* bar, uint32_t parity, volatile int* abort, int* err, unsigned long long limit_ns) {
   if (*abort) return;
@@ -308,7 +390,9 @@ __device__ __noinline__ void wait_long(uint64_t* bar, uint32_t parity, volatile 
 }
 
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const LogprobParams P) {
+__global__ void __launch_bounds__(Shape<TOP>::kThreads, Shape<TOP>::kCtasPerSm) logprobs_kernel(const LogprobParams P) {
+  using Shared = SharedOf<Shape<TOP>::kStages, TOP>;
+  constexpr int kStages = Shape<TOP>::kStages, kThreads = Shape<TOP>::kThreads;
   constexpr int VE = Word<T>::N;
   constexpr float kLn2 = 0.6931471805599453f;
   extern __shared__ uint8_t smem_raw[];
@@ -324,6 +408,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
     mbar_init(&sh.ready, kWarps);
     mbar_init(&sh.taken, 1);
     sh.abort = sh.last[0] = sh.last[1] = 0;
+    sh.thr = 0;
+    sh.started = sh.events = 0;
+    sh.done = 0;
     fence_mbar_init();
   }
   __syncthreads();
@@ -374,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
     int at = upto - __popc(in);
     n_rows = 0;
 #pragma unroll
-    for (int w = 0; w <= kWarps; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) at += sh.warp_rows[w];
       n_rows += sh.warp_rows[w];
     }
@@ -385,16 +472,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
   }
   const int per_row = P.units;  // units of a row
   const long long U = static_cast<long long>(n_rows) * per_row;
-  // two stages a CTA at least; where every row goes to eight or more CTAs, the same number for each
-  int G = static_cast<int>(min(static_cast<long long>(gridDim.x), (U + 2 * kStageUnits - 1) / (2 * kStageUnits)));
+  // at most one CTA for every two stages of a row; where rows go to eight or more CTAs each, to the same number
+  int G = static_cast<int>(min(static_cast<long long>(gridDim.x), static_cast<long long>(n_rows) * ((per_row + 2 * kStageUnits - 1) / (2 * kStageUnits))));
   if (G >= 8 * n_rows && n_rows > 0) G -= G % n_rows;
   const int cta = blockIdx.x;
   if (cta >= G) return;
   const long long U0 = range_begin(cta, U, G), U1 = range_begin(cta + 1, U, G);
   // The walk of both roles: the rows of this range from rank r0 on (the first from its unit u00),
-  // with their first and last unit in the range. No division past the first: a 64-bit one is
-  // a hundred instructions, for every warp and row.
-  const int r0 = static_cast<int>(U0 / per_row), u00 = static_cast<int>(U0 - static_cast<long long>(r0) * per_row);
+  // with their first and last unit in the range: no division past the first.
+  const int r0 = static_cast<int>(quotient(U0, per_row)), u00 = static_cast<int>(U0 - static_cast<long long>(r0) * per_row);
   auto row_of = [&](int rank) { return listed && P.tokens ? static_cast<int>(sh.rows[rank]) : rank; };
   auto token_of = [&](int row) { return P.tokens ? __ldcg(P.tokens + row) : 0; };
 
@@ -435,14 +521,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
     return;
   }
 
+  if (TOP && warp == kWarps + 1) {
+    // ------------------------------------------------------------ the threshold's warp
+    keep_threshold(sh, k);
+    return;
+  }
+
   // -------------------------------------------------------------- consumer warps
   const Scale sc = {P.scale, Word<T>::kFloor / 16};
-  const int m = (k + kWarps - 1) / kWarps;  // a warp's share of the n_top largest
   float M = -INFINITY;                       // the warp's, the same in every lane
   float2 S2 = {0.f, 0.f}, W2 = {0.f, 0.f};   // the thread's
   Key list = 0;
   int waiting = 0;                           // keys that are not in the list yet
   uint32_t best = 0;                         // the lane's largest value in the segment
+  uint32_t thr = 0;                          // the threshold as last read
   bool fresh = true;
   int seg_no = 0;
 
@@ -465,8 +557,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
     float top = Word<T>::top(q[0]);
 #pragma unroll
     for (int w = 1; w < NW; ++w) top = max_nan(top, Word<T>::top(q[w]));
-    const float wtop = warp_max_nan(top);
-    rebase(wtop);
+    if (__any_sync(kAll, !(top <= M))) rebase(warp_max_nan(top));
     if (sc.fast(M)) {
       const float B = __fmul_rn(M, sc.c);
       const float2 c2 = {sc.c, sc.c}, b2 = {-B, -B};
@@ -500,49 +591,39 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
     }
     if (TOP) {
       best = max(best, order_bits(top));
-      // what the warp knows of the threshold: the m-th largest of its lanes' maxima
-      auto publish = [&]() {
-        uint32_t rest = best, found = 0;
-        int left = m;
-#pragma unroll
-        for (int i = 0; i < kLpMaxTop / kWarps; ++i) {
-          const uint32_t top_rest = __reduce_max_sync(kAll, rest);
-          if (left > 0) found = top_rest;
-          left -= __popc(__ballot_sync(kAll, rest == top_rest));
-          if (rest == top_rest) rest = 0;
-        }
-        if (lane == 0) sh.thr[seg_no & 1][warp] = found;
-      };
       if (fresh) {
-        publish();
+        sh.best[seg_no & 1][warp][lane] = best;
+        publish_tops(sh, seg_no & 1, best);
         named_bar_sync(1, kConsumers);
+        if (tid == 0) sh.started = seg_no;
+        thr = first_threshold(sh, seg_no & 1, k);
         fresh = false;
       }
-      const uint32_t thr = __reduce_min_sync(kAll, sh.thr[seg_no & 1][lane & (kWarps - 1)]);
-      const float thr_f = from_order_bits(thr);  // NaN bits where there is none yet
-      if (!(wtop < thr_f)) {
-        waiting = note_candidates<T, NW>(list, sh.waiting[warp], sh.lanes[warp], waiting, __ballot_sync(kAll, !(top < thr_f)), thr_f, vals,
-                                         kUnitWords * VE, index, limit);
-        publish();
+      const float thr_f = from_order_bits(thr);
+      const unsigned votes = __ballot_sync(kAll, !(top < thr_f));
+      if (votes) {
+        const Noted to = note_candidates<T, NW>({list, waiting}, sh.waiting[warp], sh.lanes[warp], votes, thr_f, vals, kUnitWords * VE, index, limit);
+        list = to.list, waiting = to.waiting;
+        sh.best[seg_no & 1][warp][lane] = best;
         __syncwarp();
+        if (lane == 0) atomicAdd(const_cast<uint32_t*>(&sh.events), 1u);
       }
     }
   };
-  // The parts of the first `lanes` lanes (a power of two) into one, in all lanes.
+  // The parts of the first `lanes` lanes into one, in all lanes; what the others up to the next power
+  // of two hold has no mass.
   auto join_lanes = [&](Part p, int lanes) {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-      if (o >= lanes) continue;
+#pragma unroll 1
+    for (int o = 1; o < min(lanes, 32); o <<= 1)
       p = sc.join(p, Part{__shfl_xor_sync(kAll, p.M, o), __shfl_xor_sync(kAll, p.S, o), __shfl_xor_sync(kAll, p.W, o)});
-    }
-    return p;
+    return Part{__shfl_sync(kAll, p.M, 0), __shfl_sync(kAll, p.S, 0), __shfl_sync(kAll, p.W, 0)};
   };
-  auto write_row = [&](int row, const T* z, const Part& p) {  // one warp; its list is the row's
+  auto write_row = [&](int row, float z_token, const Part& p) {  // one warp; its list is the row's, lane 0 has the token's logit
     const bool empty = p.S == 0.f;  // every logit -inf
     const float top = p.M == -INFINITY ? 0.f : p.M;
     const float ls = kLn2 * (log2f(p.S) - (p.M == -INFINITY ? 0.f : sc.residual(p.M)));
     if (lane == 0) {
-      if (P.logprob) P.logprob[row] = empty ? -INFINITY : (widen1(z[token_of(row)]) - top) * P.inv_temp - ls;
+      if (P.logprob) P.logprob[row] = empty ? -INFINITY : (z_token - top) * P.inv_temp - ls;
       P.entropy[row] = empty ? 0.f : max_nan(kLn2 * (log2f(p.S) - p.W / p.S), 0.f);  // (rounding could leave -1e-7)
     }
     if (lane < k) {
@@ -569,9 +650,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
     else if (warp == 0 && lane < 2 * VE) edge = rw.lead + rw.words * VE + lane - VE;
     if (edge >= V || (lane >= VE && u1 < per_row)) edge = -1;
     const float edge_x = edge >= 0 ? widen1(rw.z[edge]) : -INFINITY;
+    const int finisher = seg_no % kWarps;
+    float z_token = 0.f;  // asked for now, used at the segment's end
+    if (warp == finisher && lane == 0 && P.logprob) z_token = widen1(rw.z[token_of(row)]);
     const int end = min(u1 * kUnitWords, rw.words);
     for (int w0 = u0 * kUnitWords; w0 < end; w0 += kStageWords, ++n) {
       const int st = n % kStages, words = min(kStageWords, end - w0);
+      if (TOP && !fresh) {
+        const Key now = *const_cast<volatile Key*>(&sh.thr);
+        if (static_cast<uint32_t>(now >> 32) == static_cast<uint32_t>(seg_no) + 1) thr = max(thr, static_cast<uint32_t>(now));
+      }
       wait(&sh.full[st], (n / kStages) & 1);
       __syncwarp();
       constexpr int L = kStageUnits;  // words of a thread at a time
@@ -602,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
         W2.x = fmaf(e, fmaxf(d, -200.f), W2.x);
       }
       if (TOP) {
-        const uint32_t thr = fresh ? 0 : __reduce_min_sync(kAll, sh.thr[seg_no & 1][lane & (kWarps - 1)]);
+        if (fresh) thr = 0;
         const bool in = edge >= 0 && order_bits(edge_x) >= thr;
         const unsigned votes = __ballot_sync(kAll, in);
         if (in) sh.waiting[warp][waiting + __popc(votes & ((1u << lane) - 1))] = make_key(order_bits(edge_x), edge);
@@ -626,7 +714,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
       W += __shfl_xor_sync(kAll, W, o);
     }
     // The warps hand their results to one of them, another for each segment, and go on.
-    const int finisher = seg_no % kWarps;
     if (seg_no >= 1) wait(&sh.taken, (seg_no - 1) & 1);
     __syncwarp();
     if (lane == 0) sh.part[warp] = {M, S, W};
@@ -639,25 +726,28 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
     best = 0;
     const uint32_t round = seg_no++;
     if (warp == finisher) {
+      const bool whole = u0 == 0 && u1 == per_row;
+      const long long base = static_cast<long long>(rank) * per_row;
+      int c0 = 0, c1 = 0;
+      if (!whole) c0 = cta_of(base, U, G), c1 = cta_of(base + per_row - 1, U, G);
       wait(&sh.ready, round & 1);
       __syncwarp();
       if (TOP) list = merge_eight(sh.list);
       const Part p = join_lanes(sh.part[lane & (kWarps - 1)], kWarps);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.taken);
-      if (u0 == 0 && u1 == per_row) {
-        write_row(row, rw.z, p);
+      if (whole) {
+        write_row(row, z_token, p);
       } else {
-        const long long base = static_cast<long long>(rank) * per_row;
-        const int c0 = cta_of(base, U, G), c1 = cta_of(base + per_row - 1, U, G);
         float* slot = slot_of(cta, base > U0);
         if (lane == 0) __stcg(reinterpret_cast<float4*>(slot), make_float4(p.M, p.S, p.W, 0.f));
         if (lane < k) __stcg(reinterpret_cast<Key*>(slot + 4) + lane, list);
-        __threadfence();
         __syncwarp();
-        if (lane == 0 && atomicAdd(P.row_cnt + c0, 1) == c1 - c0) {
+        // releases the warp's part, and acquires the others' for the CTA (by way of the barrier below)
+        if (lane == 0 && add_acq_rel(P.row_cnt + c0, 1) == c1 - c0) {
           P.row_cnt[c0] = 0;
           sh.last[base > U0] = 1;
+          sh.z_token[base > U0] = z_token;
         }
       }
     }
@@ -665,11 +755,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
   }
   // ---- the rows that this CTA shares with others and was the last to arrive at, by all warps
   named_bar_sync(1, kConsumers);
+  if (tid == 0) sh.done = 1;
 #pragma unroll 1
   for (int which = 0; which < 2; ++which) {
     if (!sh.last[which]) continue;
-    __threadfence();
-    const int rank = which == 0 ? r0 : static_cast<int>((U1 - 1) / per_row), row = row_of(rank);
+    const int rank = which == 0 ? r0 : static_cast<int>(quotient(U1 - 1, per_row)), row = row_of(rank);
     const long long base = static_cast<long long>(rank) * per_row;
     const int c0 = cta_of(base, U, G), c1 = cta_of(base + per_row - 1, U, G);
     // the row is the first of every CTA that has a part of it but perhaps c0
@@ -685,7 +775,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
           other[i] = from <= c1 && lane < k ? __ldcg(reinterpret_cast<const Key*>(slot_of(from, from == c0 ? c0_which : 0) + 4) + lane) : 0;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) list = merge_lists(list, other[i]);
+        for (int i = 0; i < 4; ++i)
+          if (c + i * kWarps <= c1) list = merge_lists(list, other[i]);
       }
       sh.list[warp][lane] = list;
       named_bar_sync(1, kConsumers);
@@ -695,24 +786,30 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
       Part p = {-INFINITY, 0.f, 0.f};
       for (int c = c0 + lane; c <= c1; c += 32) {
         const float4 q = __ldcg(reinterpret_cast<const float4*>(slot_of(c, c == c0 ? c0_which : 0)));
-        p = sc.join(p, Part{q.x, q.y, q.z});
+        p = c - c0 < 32 ? Part{q.x, q.y, q.z} : sc.join(p, Part{q.x, q.y, q.z});
       }
-      p = join_lanes(p, 32);
-      write_row(row, RowWords<T>(P, row).z, p);
+      p = join_lanes(p, c1 - c0 + 1);
+      write_row(row, sh.z_token[which], p);
     }
     if (TOP) named_bar_sync(1, kConsumers);  // the lists' buffer is the other row's
   }
 }
 
-int smem_bytes(int rows) { return static_cast<int>(sizeof(Shared)) + 128 + 2 * rows; }
-static_assert(sizeof(Shared) + 128 + 2 * kListed + 1024 <= 233472 / kCtasPerSm, "shared memory of an SM");
+template <bool TOP>
+int smem_bytes(int rows) {
+  using Shared = SharedOf<Shape<TOP>::kStages, TOP>;
+  static_assert(sizeof(Shared) + 128 + 2 * kListed + 1024 <= 233472 / Shape<TOP>::kCtasPerSm, "shared memory of an SM");
+  return static_cast<int>(sizeof(Shared)) + 128 + 2 * rows;
+}
 
 template <typename T, bool TOP>
-cudaError_t launch(const LogprobParams& p, int n_ctas, cudaStream_t stream) {
+cudaError_t launch(const LogprobParams& p, int n_sms, cudaStream_t stream) {
+  const long long stages = (static_cast<long long>(p.rows) * p.units + kStageUnits - 1) / kStageUnits;
+  const int most = std::min(Shape<TOP>::kCtasPerSm * n_sms, kLpMaxCtas);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(n_ctas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes(p.rows <= kListed ? p.rows : 0);
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(stages, most)));
+  cfg.blockDim = dim3(Shape<TOP>::kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<TOP>(p.rows <= kListed ? p.rows : 0);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -724,7 +821,7 @@ cudaError_t launch(const LogprobParams& p, int n_ctas, cudaStream_t stream) {
 
 template <typename T, bool TOP>
 cudaError_t set_attr() {
-  return cudaFuncSetAttribute(logprobs_kernel<T, TOP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(kListed));
+  return cudaFuncSetAttribute(logprobs_kernel<T, TOP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<TOP>(kListed));
 }
 
 }  // namespace
@@ -740,14 +837,11 @@ int logprob_set_attributes() {
 int launch_logprobs(LogprobParams p, int dtype, int n_sms, cudaStream_t stream) {
   const long long bytes = static_cast<long long>(p.V) * (dtype == DFLASH_F32 ? 4 : 2);
   p.units = static_cast<int>((bytes + 16 * kUnitWords - 1) / (16 * kUnitWords));
-  const long long stages = (static_cast<long long>(p.rows) * p.units + kStageUnits - 1) / kStageUnits;
-  const int most = std::min(kCtasPerSm * n_sms, kLpMaxCtas);
-  const int ctas = static_cast<int>(std::min<long long>(stages, most));
   const bool top = p.n_top > 0;
   cudaError_t e;
-  if (dtype == DFLASH_F32) e = top ? launch<float, true>(p, ctas, stream) : launch<float, false>(p, ctas, stream);
-  else if (dtype == DFLASH_F16) e = top ? launch<__half, true>(p, ctas, stream) : launch<__half, false>(p, ctas, stream);
-  else e = top ? launch<__nv_bfloat16, true>(p, ctas, stream) : launch<__nv_bfloat16, false>(p, ctas, stream);
+  if (dtype == DFLASH_F32) e = top ? launch<float, true>(p, n_sms, stream) : launch<float, false>(p, n_sms, stream);
+  else if (dtype == DFLASH_F16) e = top ? launch<__half, true>(p, n_sms, stream) : launch<__half, false>(p, n_sms, stream);
+  else e = top ? launch<__nv_bfloat16, true>(p, n_sms, stream) : launch<__nv_bfloat16, false>(p, n_sms, stream);
   return static_cast<int>(e);
 }
 

@@ -5,6 +5,15 @@
 
 namespace dfl {
 
+// A list of T units cut evenly over G CTAs (G <= T: none is empty): the first unit of CTA c, and the
+// CTA whose range holds unit u. (A 64-bit division is a hundred instructions in a chain: products
+// that fit take the 32-bit one.)
+DEV long long quotient(long long a, long long b) {
+  return static_cast<unsigned long long>(a | b) < (1ull << 32) ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
+DEV long long range_begin(long long c, long long T, int G) { return quotient(c * T, G); }
+DEV int cta_of(long long u, long long T, int G) { return static_cast<int>(quotient((u + 1) * G - 1, T)); }
+
 // 2^x by the multi-function unit (relative error about 2^-22).
 DEV float ex2(float x) {
   float y;

@@ -44,14 +44,6 @@ DEV float weight_of(float2 ml, float top) {
   return ex2(ml.x - top);
 }
 
-// First tile of CTA c's range, and the CTA whose range holds tile u (G <= T: none is empty).
-// (A 64-bit division is a hundred instructions in a chain: products that fit take the 32-bit one.)
-DEV long long quotient(long long a, long long b) {
-  return static_cast<unsigned long long>(a | b) < (1ull << 32) ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
-}
-DEV long long range_begin(long long c, long long T, int G) { return quotient(c * T, G); }
-DEV int cta_of(long long u, long long T, int G) { return static_cast<int>(quotient((u + 1) * G - 1, T)); }
-
 // Sequence s's rows of this call: 0 where its lengths are out of range.
 DEV int rows_of(const PagedAttnParams& P, int s, int& len, bool& bad) {
   len = __ldcg(P.len + s);
