@@ -9,28 +9,31 @@
 // overflow, and every base involved stands for its exact c max z.
 //
 // Bound: reading the logits, once, at 2 or 4 bytes each.
-// Split. The rows that have a token, in units of 4 KB of logits, form one list that is cut
-// evenly over three persistent CTAs per SM: rows without a token cost nothing, no wave is left
-// half full, few rows are split over all SMs, and a CTA has at most two rows that it shares with
-// others. Those join in CTA order in the CTA that arrives last at the row, which does not depend
-// on who that is; a row inside one range never leaves its CTA. (Chunks of 64 KB taken from a
-// counter, each joined through global memory, took 129 us for 293 rows of 151936 fp32 against 46:
-// fence, counter and parts are microseconds of latency, too many for 1.4 us of copying.)
+// Split. The rows that have a token, in units of 4 KB of logits, form one list that is cut evenly
+// over persistent CTAs: rows without a token cost nothing, no wave is left half full, few rows are
+// split over all SMs, and a CTA has at most two rows that it shares with others. Those join in CTA
+// order in the CTA that arrives last at the row, which does not depend on who that is; a row
+// inside one range never leaves its CTA. (Chunks of 64 KB taken from a counter, each joined through
+// global memory, took 129 us for 293 rows of 151936 fp32 against 46 then: fence, counter and parts
+// are microseconds of latency, too many for 1.4 us of copying.)
 // In a CTA a producer warp keeps a ring of 16 KB stages full by bulk copies across rows, and
-// eight consumer warps share each stage.
+// eight consumer warps share each stage. Two CTAs per SM with six stages where alternatives are
+// wanted (registers), three with four where they are not (more warps for the arithmetic of 16-bit
+// logits): 40.7 us and 45.1 us, 28.9 us and 27.2 us for the cases below.
 //
 // The n_top largest: every warp keeps the best of what it has read as a sorted list of 64-bit
 // keys, one per lane, (order-preserving bits of the logit, ~index): ties go to the lowest
-// index and all keys differ. What keeps this off the streaming path is a threshold that the
-// warps share: each publishes the ceil(n_top / 8)-th largest of its lanes' maxima, and the least
-// of the eight bounds the n_top-th largest of the row from below, so that after the first stage
-// few values are candidates. Those wait in a buffer until 32 can be sorted and merged into
-// the list at once: sorted logits, where every value is a candidate, take the same path.
+// index and all keys differ. What keeps this off the streaming path is a threshold: n_top values of
+// the row are not below it, so that few values are candidates. A row starts with one from the first
+// stage's lane maxima; then a warp of its own takes the n_top-th largest of all 256 lane maxima
+// while they change (each warp raising it for itself, from four maxima a warp: 44.4 us against 40.7).
+// Candidates wait in a buffer until 32 can be sorted and merged into the list at once: sorted
+// logits, where every value is a candidate, take the same path.
 //
-// Measured: 293 of 512 rows of 151936 fp32, n_top 20, 47 us (55% of the copy rate; issue slots half
-// busy, the rest waits between a row's end and the next one's first values); 1000 rows of
-// 50257 bf16 without alternatives 29 us (51%: two exponentials' worth of arithmetic per 2 bytes);
-// 16 rows, n_top 20, 17 us, a chain of latencies: token list, first copy, sums, sort, join.
+// Measured: 293 of 512 rows of 151936 fp32, n_top 5, 40.7 us (64% of the copy rate; 32.1 us without
+// alternatives: a row's first stages have many candidates); 1000 rows of 50257 bf16 without
+// alternatives 27.2 us (54%: 3.7 us of it are the sums, 3 the join of cut rows at the end);
+// 16 rows, n_top 20, 13.6 us, a chain of latencies: token list, first copy, sums, sort, join.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
