@@ -365,10 +365,20 @@ def _require_on(t, dtype, numel, name, device):
 
 
 def _stream_on(stream, device) -> int:
-    import torch
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return _torch_calls()[0](device.index) if stream is None else stream.cuda_stream
+
+
+_calls = None
+
+
+def _torch_calls():
+    """(raw handle of a device's current stream, index of the current device, int32), looked up once:
+    the small calls below take a few microseconds in all."""
+    global _calls
+    if _calls is None:
+        import torch
+        _calls = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, torch.int32
+    return _calls
 
 
 _DTYPES = {"torch.float32": F32, "torch.float16": F16, "torch.bfloat16": BF16}
@@ -400,18 +410,17 @@ class PagePool:
         """Pages for positions [length[s], length[s] + n_new[s]) of every sequence; `slots` (int32
         [batch * rows_per_seq]) gets their cache rows, -1 for rows past n_new[s] and for
         sequences that the pool has no pages for."""
-        import torch
-        _require_min(length, torch.int32, batch, "length", self.device)
-        _require_min(n_new, torch.int32, batch, "n_new", self.device)
+        i32 = _torch_calls()[2]
+        _require_min(length, i32, batch, "length", self.device)
+        _require_min(n_new, i32, batch, "n_new", self.device)
         if slots is not None:
-            _require_on(slots, torch.int32, batch * rows_per_seq, "slots", self.device)
+            _require_on(slots, i32, batch * rows_per_seq, "slots", self.device)
         self._call(self.L.dflash_pages_reserve, "dflash_pages_reserve", stream, length.data_ptr(), n_new.data_ptr(), batch,
                    rows_per_seq, _ptr(slots))
 
     def release(self, length, batch: int, stream=None):
         """Gives back every page past the first length[s] positions of each sequence (0: all)."""
-        import torch
-        _require_min(length, torch.int32, batch, "length", self.device)
+        _require_min(length, _torch_calls()[2], batch, "length", self.device)
         self._call(self.L.dflash_pages_release, "dflash_pages_release", stream, length.data_ptr(), batch)
 
     def device_error(self, clear: bool = True) -> int:
@@ -422,10 +431,10 @@ class PagePool:
         return v
 
     def _call(self, f, what, stream, *args):
-        import torch
-        if torch.cuda.current_device() == self.device.index:
+        if _torch_calls()[1]() == self.device.index:
             check(f(self._ref, *args, _stream_on(stream, self.device)), what)
         else:
+            import torch
             with torch.cuda.device(self.device):
                 check(f(self._ref, *args, _stream_on(stream, self.device)), what)
 
@@ -481,12 +490,11 @@ class PagedCache:
         PagePool.reserve), the rotated q to q_out. q, k, v: fp16 or bf16 [batch * rows_per_seq]
         rows of heads x dims, rows a stride apart (slices of one fused projection are fine);
         q and q_out may be None."""
-        import torch
         rows, dev, dt = batch * rows_per_seq, self.device, k.dtype
         q_stride = 0 if q is None else _row_stride(q, dt, rows, self._q_row, "q", dev)
         k_stride = _row_stride(k, dt, rows, self._kv_row, "k", dev)
         v_stride = _row_stride(v, dt, rows, self._kv_row, "v", dev)
-        _require_on(slots, torch.int32, rows, "slots", dev)
+        _require_on(slots, _torch_calls()[2], rows, "slots", dev)
         _require_on(q_out, self.dtype, rows * self._q_row, "q_out", dev)
         check(self.L.dflash_cache_append(self.c, layer, _ptr(q), k.data_ptr(), v.data_ptr(), _DTYPES.get(str(dt), -1),
                                          q_stride, k_stride, v_stride, slots.data_ptr(), batch, rows_per_seq, _ptr(q_out),
@@ -496,11 +504,10 @@ class PagedCache:
         """Causal attention of row r of every sequence (position length[s] + r, r < n_new[s]) over
         the cache; q and out: contiguous [batch * rows_per_seq][n_heads][head_dim] of the
         cache's dtype. Rows past n_new[s] of out are left as they were."""
-        import torch
         numel = batch * rows_per_seq * self._q_row
         _require_on(q, self.dtype, numel, "q", self.device)
         _require_on(out, self.dtype, numel, "out", self.device)
-        _require_min(n_new, torch.int32, batch, "n_new", self.device)
+        _require_min(n_new, _torch_calls()[2], batch, "n_new", self.device)
         check(self.L.dflash_cache_attend(self.c, layer, q.data_ptr(), n_new.data_ptr(), batch, rows_per_seq, out.data_ptr(),
                                          _stream_on(stream, self.device)), "dflash_cache_attend")
 
@@ -533,12 +540,15 @@ def _row_stride(t, dtype, rows: int, row: int, name, device) -> int:
     has to be dense."""
     shape, stride = t.shape, t.stride()
     if len(shape) == 3:
-        dense = shape[1] * shape[2] == row and stride[2] == 1 and (shape[1] == 1 or stride[1] == shape[2])
+        n, heads, dims = shape
+        step, per_head, one = stride
+        dense = heads * dims == row and one == 1 and (heads == 1 or per_head == dims)
     else:
+        n, step = shape[0] if shape else 0, stride[0] if stride else 0
         dense = len(shape) == 2 and shape[1] == row and stride[1] == 1
-    if not dense or shape[0] != rows or t.dtype != dtype or t.device != device:
+    if not dense or n != rows or t.dtype != dtype or t.device != device:
         raise DFlashError(DFLASH_E_INVAL, f"{name} must be {rows} dense rows of {row} values of one type on {device}")
-    return stride[0] if rows > 1 else max(row, stride[0] // 8 * 8)   # a single row's stride means nothing
+    return step if rows > 1 else max(row, step // 8 * 8)   # a single row's stride means nothing
 
 
 def rope_tables(n_positions: int, rope_dim: int, theta: float, linear: float = 1.0, bands=None, attention_factor: float = 1.0,
