@@ -492,16 +492,37 @@ __global__ void __launch_bounds__(Layout<D>::kThreads, 1) paged_attn_kernel(cons
 // ranges the pair lies in, in CTA order.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) paged_attn_join_kernel(const __grid_constant__ PagedAttnParams P, int n_ctas, int slot_rows) {
-  pdl_wait();
-  pdl_launch_dependents();
   const int pair = blockIdx.x, s = pair / P.nkv, g = pair - s * P.nkv;
   const int lane = threadIdx.x & 31;
   const int grp = P.nq / P.nkv;
   const int row = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int p0 = __ldcg(P.prefix + s), p1 = __ldcg(P.prefix + s + 1);
-  const long long T = static_cast<long long>(P.nkv) * __ldcg(P.prefix + P.batch);
+  // The tiles before the pair, and its own. What the lengths say is known before the first kernel ends
+  // (it let this one start once all before it had finished): with a sequence a lane, from them.
+  int p0, p1, all, n_new;
+  if (P.batch <= 32) {
+    int len;
+    bool bad;
+    const int n = lane < P.batch ? rows_of(P, lane, len, bad) : 0;
+    int upto = n > 0 ? (len + n + kKeys - 1) / kKeys : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    n_new = __shfl_sync(0xffffffffu, n, s);
+    p1 = __shfl_sync(0xffffffffu, upto, s);
+    p0 = s > 0 ? __shfl_sync(0xffffffffu, upto, s - 1) : 0;
+    all = __shfl_sync(0xffffffffu, upto, 31);
+    pdl_wait();
+  } else {
+    pdl_wait();
+    p0 = __ldcg(P.prefix + s), p1 = __ldcg(P.prefix + s + 1), all = __ldcg(P.prefix + P.batch);
+    n_new = __ldcg(P.n_new + s);
+  }
+  pdl_launch_dependents();
+  const long long T = static_cast<long long>(P.nkv) * all;
   const int nt = p1 - p0;
-  if (nt == 0 || row >= __ldcg(P.n_new + s) * grp) return;
+  if (nt == 0 || row >= n_new * grp) return;
   const int G = static_cast<int>(min(static_cast<long long>(n_ctas), T));
   const long long base = static_cast<long long>(P.nkv) * p0 + static_cast<long long>(g) * nt;
   const int c0 = cta_of(base, T, G), c1 = cta_of(base + nt - 1, T, G);
