@@ -8,8 +8,9 @@ namespace dfl {
 // A list of T units cut evenly over G CTAs (G <= T: none is empty): the first unit of CTA c, and the
 // CTA whose range holds unit u. (A 64-bit division is a hundred instructions in a chain: products
 // that fit take the 32-bit one.)
+static __device__ __noinline__ long long wide_quotient(long long a, long long b) { return a / b; }
 DEV long long quotient(long long a, long long b) {
-  return static_cast<unsigned long long>(a | b) < (1ull << 32) ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+  return static_cast<unsigned long long>(a | b) < (1ull << 32) ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : wide_quotient(a, b);
 }
 DEV long long range_begin(long long c, long long T, int G) { return quotient(c * T, G); }
 DEV int cta_of(long long u, long long T, int G) { return static_cast<int>(quotient((u + 1) * G - 1, T)); }

@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(Layout<D>::kThreads, 1) paged_attn_kernel(cons
     tma_prefetch_desc(&P.kmap);
     tma_prefetch_desc(&P.vmap);
   }
+  __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
 
@@ -500,18 +501,13 @@ __global__ void __launch_bounds__(256) paged_attn_join_kernel(const __grid_const
   // (it let this one start once all before it had finished): with a sequence a lane, from them.
   int p0, p1, all, n_new;
   if (P.batch <= 32) {
-    int len;
+    int len = 0, upto;
     bool bad;
     const int n = lane < P.batch ? rows_of(P, lane, len, bad) : 0;
-    int upto = n > 0 ? (len + n + kKeys - 1) / kKeys : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += v;
-    }
+    const int before = scan_tiles(n, len, lane, upto);
     n_new = __shfl_sync(0xffffffffu, n, s);
+    p0 = __shfl_sync(0xffffffffu, before, s);
     p1 = __shfl_sync(0xffffffffu, upto, s);
-    p0 = s > 0 ? __shfl_sync(0xffffffffu, upto, s - 1) : 0;
     all = __shfl_sync(0xffffffffu, upto, 31);
     pdl_wait();
   } else {

@@ -53,12 +53,39 @@ DEV int rows_of(const PagedAttnParams& P, int s, int& len, bool& bad) {
   return bad ? 0 : n;
 }
 
-// The lengths of the call in shared memory, and the tiles per head before each sequence: each
-// thread a run of sequences, then a scan over the block's THREADS threads. CTA 0 leaves the
-// prefix for the join.
+// With up to 32 sequences, one a lane: the tiles per head of those before the lane's, and with its own.
+DEV int scan_tiles(int n, int len, int lane, int& upto) {
+  const int mine = n > 0 ? (len + n + kKeys - 1) / kKeys : 0;
+  upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  return upto - mine;
+}
+
+// The lengths of the call in shared memory, and the tiles per head before each sequence: with more
+// sequences each thread a run of them, then a scan over the block's THREADS threads, and CTA 0
+// leaves the prefix for the join.
 template <int THREADS>
 DEV void count_tiles(const PagedAttnParams& P, int* s_pre, int* s_len, int* s_new, int* s_warp) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (P.batch <= 32) {  // a sequence a lane, in every warp for itself: the same values, and no barrier
+    int len = 0, upto = 0;
+    bool bad = false;
+    const int n = lane < P.batch ? rows_of(P, lane, len, bad) : 0;
+    if (bad && blockIdx.x == 0 && warp == 0) raise_flag(P.err, kDevCapacity);
+    const int before = scan_tiles(n, len, lane, upto);
+    if (lane < P.batch) {
+      s_len[lane] = len;
+      s_new[lane] = n;
+      s_pre[lane] = before;
+    }
+    if (lane == P.batch - 1) s_pre[P.batch] = upto;
+    __syncwarp();
+    return;
+  }
   const int per = (P.batch + THREADS - 1) / THREADS;
   const int s0 = min(tid * per, P.batch), s1 = min(s0 + per, P.batch);
   int mine = 0;
