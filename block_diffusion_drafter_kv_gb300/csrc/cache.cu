@@ -227,7 +227,9 @@ int dflash_cache_attend(dflash_cache* c, int32_t layer, const void* q, const int
   P.d = f.head_dim;
   P.n_pages = f.n_pages;
   P.pages_per_seq = f.pages_per_seq;
-  P.rows = f.n_heads / f.n_kv_heads * rows_per_seq;
+  P.group = f.n_heads / f.n_kv_heads;
+  P.group_inv = 1.f / static_cast<float>(P.group);
+  P.rows = P.group * rows_per_seq;
   P.scale_log2 = static_cast<float>(1.4426950408889634 * f.scale);
   P.wait_ns = kDefaultWaitLimitNs;
   return launch_paged_attn(P, f.dtype == DFLASH_BF16, std::min(c->n_sms, kPagedMaxCtas),

@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(Layout<D>::kThreads, 1) paged_attn_kernel(cons
   pdl_launch_dependents();
 
   count_tiles<L::kThreads>(P, s_pre, s_len, s_new, s_warp);
-  const int batch = P.batch, nkv = P.nkv, grp = P.nq / nkv;
+  const int batch = P.batch, nkv = P.nkv, grp = P.group;
   const long long T = static_cast<long long>(nkv) * s_pre[batch];
   const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), T));
   const int cta = blockIdx.x;
@@ -158,6 +158,9 @@ __global__ void __launch_bounds__(Layout<D>::kThreads, 1) paged_attn_kernel(cons
       const int seg = static_cast<int>(min(T1 - u, static_cast<long long>(nt - t0)));
       const int n = s_new[s];
       const int qb = seg_no % L::kQBufs;
+      // page ids, one a lane: the next 32, asked for before q's copies
+      auto ids = [&](int b0) { return b0 + lane < seg ? __ldcg(P.page_table + static_cast<size_t>(s) * P.pages_per_seq + t0 + b0 + lane) : 0; };
+      int page = ids(0);
       if (seg_no >= L::kQBufs) wait(&qempty[qb], (seg_no / L::kQBufs - 1) & 1);
       if (__all_sync(0xffffffffu, !*s_abort)) {
         q_issued = seg_no + 1;
@@ -166,20 +169,17 @@ __global__ void __launch_bounds__(Layout<D>::kThreads, 1) paged_attn_kernel(cons
         const uint32_t qdst = smem_u32(smem + L::kQOff + qb * L::kRows * L::kQStride);
         const uint16_t* q = static_cast<const uint16_t*>(P.q);
         for (int m = lane; m < n * grp; m += 32) {
-          const int r = m / grp, hh = m - r * grp;
+          const int r = new_row(P, m), hh = m - r * grp;
           bulk_load(qdst + m * L::kQStride,
                     q + ((static_cast<size_t>(s) * P.rows_per_seq + r) * P.nq + static_cast<size_t>(g) * grp + hh) * D,
                     D * 2, &qfull[qb]);
         }
       }
       for (int b0 = 0; b0 < seg; b0 += 32) {
-        int page = -1;
-        if (b0 + lane < seg) {
-          page = __ldcg(P.page_table + static_cast<size_t>(s) * P.pages_per_seq + t0 + b0 + lane);
-          if (page < 0 || page >= P.n_pages) {
-            raise_flag(P.err, kDevCapacity);
-            page = -1;
-          }
+        if (b0 > 0) page = ids(b0);
+        if (page < 0 || page >= P.n_pages) {
+          raise_flag(P.err, kDevCapacity);
+          page = -1;
         }
         const int cnt = min(32, seg - b0);
         for (int k = 0; k < cnt; ++k, ++i) {
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(Layout<D>::kThreads, 1) paged_attn_kernel(cons
     const int nk = len + n_new;
     int lim[2];  // last key each of the thread's rows may see
 #pragma unroll
-    for (int h = 0; h < 2; ++h) lim[h] = len + (h * 8 + r0) / grp;
+    for (int h = 0; h < 2; ++h) lim[h] = len + new_row(P, h * 8 + r0);
     const int qb = seg_no % L::kQBufs;
     wait(&qfull[qb], (seg_no / L::kQBufs) & 1);
     __syncwarp();
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(Layout<D>::kThreads, 1) paged_attn_kernel(cons
     float inv[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int row = h * 8 + r0, r = row / grp, hh = row - r * grp;
+      const int row = h * 8 + r0, r = new_row(P, row), hh = row - r * grp;
       there[h] = row < n_new * grp;
       inv[h] = den[h] > 0.f ? 1.f / den[h] : (den[h] == 0.f ? 0.f : den[h]);
       dst[h] = static_cast<uint16_t*>(P.out) + ((static_cast<size_t>(s) * P.rows_per_seq + r) * P.nq + static_cast<size_t>(g) * grp + hh) * D;
@@ -495,7 +495,7 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(256) paged_attn_join_kernel(const __grid_constant__ PagedAttnParams P, int n_ctas, int slot_rows) {
   const int pair = blockIdx.x, s = pair / P.nkv, g = pair - s * P.nkv;
   const int lane = threadIdx.x & 31;
-  const int grp = P.nq / P.nkv;
+  const int grp = P.group;
   const int row = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
   // The tiles before the pair, and its own. What the lengths say is known before the first kernel ends
   // (it let this one start once all before it had finished): with a sequence a lane, from them.
@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(256) paged_attn_join_kernel(const __grid_const
     }
   }
   const float inv = den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den);
-  const int r = row / grp, hh = row - r * grp;
+  const int r = new_row(P, row), hh = row - r * grp;
   uint16_t* dst = static_cast<uint16_t*>(P.out) +
                   ((static_cast<size_t>(s) * P.rows_per_seq + r) * P.nq + static_cast<size_t>(g) * grp + hh) * D + lane * E;
 #pragma unroll

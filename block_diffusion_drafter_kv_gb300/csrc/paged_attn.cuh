@@ -119,6 +119,10 @@ DEV void count_tiles(const PagedAttnParams& P, int* s_pre, int* s_len, int* s_ne
     for (int s = tid; s <= P.batch; s += THREADS) P.prefix[s] = s_pre[s];
 }
 
+// The new row that row x < 256 of a problem belongs to, x / group: (x + 1/2) / group is 1 / 512 or more
+// from the next integers, far more than a product of floats is off.
+DEV int new_row(const PagedAttnParams& P, int x) { return static_cast<int>((static_cast<float>(x) + 0.5f) * P.group_inv); }
+
 // List position u: sequence s, KV head g, tile t of the pair's nt.
 struct Place {
   int s, g, t, nt;

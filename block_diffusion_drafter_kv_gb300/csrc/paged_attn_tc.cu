@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
   pdl_wait();
   pdl_launch_dependents();
   count_tiles<kTcThreads>(P, s_pre, s_len, s_new, s_warp);
-  const int batch = P.batch, nkv = P.nkv, grp = P.nq / nkv;
+  const int batch = P.batch, nkv = P.nkv, grp = P.group;
   const long long T = static_cast<long long>(nkv) * s_pre[batch];
   const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), T));
   const int cta = blockIdx.x;
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
     // a segment's row of q; rows that are not there are zero
     uint4 qrow[D / 8];
     auto load_q = [&](const Place& p) {
-      const int r = row / grp;
+      const int r = new_row(P, row);
       const uint4* src = reinterpret_cast<const uint4*>(
           static_cast<const uint16_t*>(P.q) +
           ((static_cast<size_t>(p.s) * P.rows_per_seq + r) * P.nq + p.g * grp + row - r * grp) * D);
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
       const int s = w.at.s, g = w.at.g, t0 = w.at.t;
       const bool whole = t0 == 0 && w.left == w.at.nt;
       const int len = s_len[s], n_new = s_new[s], nk = len + n_new;
-      const int r = row / grp, head = g * grp + row - r * grp;
+      const int r = new_row(P, row), head = g * grp + row - r * grp;
       const bool there = row < n_new * grp;
       const int lim = len + r;  // last key the row may see
       float m = -INFINITY, l = 0.f;

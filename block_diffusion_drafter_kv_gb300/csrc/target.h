@@ -66,6 +66,8 @@ struct PagedAttnParams {
   float* part;       // [2 * CTAs] slots of rows * d outputs, then (max, sum) per row
   int batch, rows_per_seq, nq, nkv, d, n_pages, pages_per_seq;
   int rows;          // (nq / nkv) * rows_per_seq
+  int group;         // nq / nkv
+  float group_inv;   // its inverse
   float scale_log2;  // scale * log2(e)
   unsigned long long wait_ns;
 };
