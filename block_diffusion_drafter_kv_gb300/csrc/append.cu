@@ -5,7 +5,12 @@
 // A thread owns 16 dims of a head that are closed under the rotation: [8i, 8i + 8) and its
 // partners rope_dim / 2 further on (half layout), or the eight pairs of [16i, 16i + 16)
 // (interleaved), or 16 plain dims past rope_dim. Its eight angles are the same for every
-// head of the row, so it keeps their cos and sin in registers and walks the row's heads.
+// head of the row, so it keeps their cos and sin in registers and walks the row's heads. A CTA a
+// row: many rows fill the SMs with small CTAs, whose loads overlap each other's latency.
+//
+// Measured (bf16, 32 query heads on 8 KV heads, d 128): a prompt of 8191 rows 33.0 us, 90% of the
+// copy rate (102.8 MB read, as much written, most of it still in L2 at the end); 32 blocks of 16
+// rows 4.1 us and one row 2.1 us, a launch and the latencies slot, tables, values.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -9,6 +9,10 @@
 // same call hands out are read from the free list, not from the table, so that no CTA waits
 // for another's writes; the held counts and the length of the list, which every CTA reads,
 // are written by the CTA that arrives last.
+//
+// Bound: latency (a few hundred bytes to read, 4 bytes a new row to write): lengths, prefix sum,
+// list, slots, and with more than one CTA the counter. Measured, reserve and release together: 32
+// blocks of 16 rows 6.8 us, 256 prompts of up to 2048 rows (2 MB of slots) 11.1 us.
 #include "ptx.cuh"
 #include "target.h"
 
