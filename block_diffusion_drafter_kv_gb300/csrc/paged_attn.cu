@@ -20,7 +20,9 @@
 // a softmax state of their own, so that warps meet only where a segment ends. S = q K^T and
 // O += P V are mma.sync m16n8k16 with fp32 accumulation: the rows are few (4 in ordinary
 // grouped decoding), so a 128-row tcgen05 tile would be mostly padding, while the loads bound
-// the kernel (0.92 of the measured copy rate at 4 sequences of 32768, fp32 sums included).
+// the kernel: 4 rows over 4 sequences of 32768 keys take 85 to 89 us (0.89 to 0.93 of the measured
+// copy rate), 32 ragged sequences of 512 to 8192 keys 91 to 94 us (0.89 to 0.91). One sequence of 2048
+// takes 8.5 us: two launches, lengths, page ids, q, K/V, softmax, parts, one latency after another.
 #include "paged_attn.cuh"
 
 namespace dfl {
@@ -604,9 +606,9 @@ int launch(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
   cfg.numAttrs = 1;
   // Up to 16 rows here, more on tcgen05. Measured (bf16, d 128, 32 query heads on 8 KV heads, us):
   //   rows  1 x 2048  32 x 1000  4 x 32768       1 x 2048  32 x 1000  4 x 32768
-  //     16      12.1       32.1       86.6  here     18.2       53.9      102.5  tcgen05 (an earlier form)
-  //     20      15.0       43.1      103.5  here     15.6       36.5       91.1  tcgen05
-  //     64      17.6       60.3      146.8  here     17.4       48.3       99.1  tcgen05
+  //     16      11.0       30.1       87.6  here     18.2       53.9      102.5  tcgen05 (an earlier form)
+  //     20      15.0       43.1      103.5  here     14.4       33.9       89.6  tcgen05 (here: an earlier
+  //     64      17.6       60.3      146.8  here     16.5       45.2       97.3  tcgen05  form with more rows)
   const int e = p.rows <= kRowsFew ? static_cast<int>(cudaLaunchKernelEx(&cfg, paged_attn_kernel<D, BF16>, p))
                                    : launch_paged_attn_tc(p, BF16, n_ctas, stream);
   if (e != 0) return e;

@@ -8,15 +8,15 @@
 // 128 lanes of the softmax have a row of 64 scores; P keeps zeros where a row's other tile is, and
 // O += P V (M = 128, K = 128 keys) adds up two states per row, which meet at the segment's
 // end. With 65 to 128 rows a step is one tile. Measured (bf16, 32 query heads on 8 KV heads, 4
-// sequences of 32768, d 128): 91 us with 20 rows, 99 with 64 (80% of the copy rate), 120 with 128;
+// sequences of 32768, d 128): 90 us with 20 rows, 97 with 64 (81% of the copy rate), 119 with 128;
 // against a two-tile step's 2750 cycles of HBM time (64 KB) issuing its products takes 1250 and its
 // softmax 1100, overlapped between steps, so that it waits for copies; a one-tile step (1400 cycles of
 // HBM time) waits for the chain of its products and softmax (1700), d 64 likewise. Short caches (128
-// sequences of 500: 123 us with 64 rows, 36%) are bound by the segments' ends: q, output.
+// sequences of 500: 119 us with 64 rows, 37%) are bound by the segments' ends: q, output.
 //
 //   S   two TMEM buffers of N columns: the next step's Q K^T runs under this one's softmax
 //   Q, P  in TMEM too, as the products' A operands: with them in shared memory (64 KB) the rings
-//       held two steps instead of three, and a step waited for its copies (104 us against 99
+//       held two steps instead of three, and a step waited for its copies (104 us against 99 then
 //       at 4 sequences of 32768, 64 rows)
 //   O   TMEM, kept over the segment. A row's reference moves only where a score passes it by more
 //       than 8 binary orders; that row of O is then rescaled in TMEM between two products
