@@ -26,7 +26,7 @@ CacheLayout layout_of(const dflash_cache_config& c) {
   CacheLayout L{};
   L.err = 0;
   L.prefix = 256;
-  L.part = L.prefix + up256((static_cast<size_t>(c.max_batch) + 1) * 4);
+  L.part = L.prefix + up256((std::min<size_t>(c.max_batch, kAttnMaxBatch) + 1) * 4);
   const size_t rows = paged_attn_rows(c.n_heads / c.n_kv_heads * c.max_block);
   L.total = L.part + up256(2 * kPagedMaxCtas * rows * (c.head_dim + 2) * 4);
   return L;
@@ -78,7 +78,7 @@ int dflash_cache_config_check(const dflash_cache_config* c) {
       (c->dtype == DFLASH_F16 || c->dtype == DFLASH_BF16) && c->n_pages >= 1 &&
       static_cast<long long>(c->n_pages) * kPagePos < (1LL << 31) && c->pages_per_seq >= 1 &&
       static_cast<long long>(c->pages_per_seq) * kPagePos < (1LL << 31) && c->max_batch >= 1 &&
-      c->max_batch <= kCacheMaxBatch && static_cast<long long>(c->max_batch) * c->pages_per_seq < (1LL << 31) &&
+      c->max_batch <= kMaxBatch && static_cast<long long>(c->max_batch) * c->pages_per_seq < (1LL << 31) &&
       c->rope_dim >= 0 && c->rope_dim <= c->head_dim && c->rope_dim % 16 == 0 &&
       (c->rope_interleaved == 0 || c->rope_interleaved == 1) && (c->rope_dim == 0 || c->rope_positions >= 1) &&
       c->scale >= 0.f && c->scale <= 1e38f;
@@ -212,15 +212,9 @@ int dflash_cache_attend(dflash_cache* c, int32_t layer, const void* q, const int
   PagedAttnParams P{};
   P.kmap = c->kmap[layer];
   P.vmap = c->vmap[layer];
-  P.q = q;
-  P.out = out;
-  P.len = c->len;
-  P.n_new = n_new;
-  P.page_table = c->page_table;
   P.err = c->err();
   P.prefix = reinterpret_cast<int*>(c->ws + c->L.prefix);
   P.part = reinterpret_cast<float*>(c->ws + c->L.part);
-  P.batch = batch;
   P.rows_per_seq = rows_per_seq;
   P.nq = f.n_heads;
   P.nkv = f.n_kv_heads;
@@ -232,10 +226,18 @@ int dflash_cache_attend(dflash_cache* c, int32_t layer, const void* q, const int
   P.rows = P.group * rows_per_seq;
   P.scale_log2 = static_cast<float>(1.4426950408889634 * f.scale);
   P.wait_ns = kDefaultWaitLimitNs;
-  return launch_paged_attn(P, f.dtype == DFLASH_BF16, std::min(c->n_sms, kPagedMaxCtas),
-                           static_cast<cudaStream_t>(stream)) == 0
-             ? DFLASH_OK
-             : DFLASH_E_CUDA;
+  const size_t seq_bytes = static_cast<size_t>(rows_per_seq) * f.n_heads * f.head_dim * 2;
+  for (int s = 0; s < batch; s += kAttnMaxBatch) {
+    P.q = static_cast<const uint8_t*>(q) + s * seq_bytes;
+    P.out = static_cast<uint8_t*>(out) + s * seq_bytes;
+    P.len = c->len + s;
+    P.n_new = n_new + s;
+    P.page_table = c->page_table + static_cast<size_t>(s) * f.pages_per_seq;
+    P.batch = std::min(batch - s, kAttnMaxBatch);
+    if (launch_paged_attn(P, f.dtype == DFLASH_BF16, std::min(c->n_sms, kPagedMaxCtas), static_cast<cudaStream_t>(stream)) != 0)
+      return DFLASH_E_CUDA;
+  }
+  return DFLASH_OK;
 }
 
 int dflash_cache_read_error(dflash_cache* c, int32_t* flags, int32_t clear, void* stream) {

@@ -587,9 +587,9 @@ __global__ void __launch_bounds__(256) paged_attn_join_kernel(const __grid_const
 
 template <int D, bool BF16>
 int set_attr() {
-  static_assert(Layout<D>::smem(kCacheMaxBatch) <= 232448, "shared memory of a CTA");
+  static_assert(Layout<D>::smem(kAttnMaxBatch) <= 232448, "shared memory of a CTA");
   return static_cast<int>(cudaFuncSetAttribute(paged_attn_kernel<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               Layout<D>::smem(kCacheMaxBatch)));
+                                               Layout<D>::smem(kAttnMaxBatch)));
 }
 
 template <int D, bool BF16>
@@ -631,7 +631,7 @@ int paged_attn_set_attributes() {
 }
 
 int launch_paged_attn(const PagedAttnParams& p, bool bf16, int n_ctas, cudaStream_t stream) {
-  if (p.batch < 1 || p.batch > kCacheMaxBatch || n_ctas < 1 || n_ctas > kPagedMaxCtas || p.rows > 128)
+  if (p.batch < 1 || p.batch > kAttnMaxBatch || n_ctas < 1 || n_ctas > kPagedMaxCtas || p.rows > 128)
     return static_cast<int>(cudaErrorInvalidValue);
   if (p.d == 128) return bf16 ? launch<128, true>(p, n_ctas, stream) : launch<128, false>(p, n_ctas, stream);
   return bf16 ? launch<64, true>(p, n_ctas, stream) : launch<64, false>(p, n_ctas, stream);

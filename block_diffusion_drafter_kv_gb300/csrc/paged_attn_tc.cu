@@ -665,9 +665,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
 
 template <int D, bool BF16, int H>
 int set_tc_attr() {
-  static_assert(TcLayout<D, H>::smem(kCacheMaxBatch) <= 232448, "shared memory of a CTA");
+  static_assert(TcLayout<D, H>::smem(kAttnMaxBatch) <= 232448, "shared memory of a CTA");
   return static_cast<int>(cudaFuncSetAttribute(paged_attn_tc_kernel<D, BF16, H>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               TcLayout<D, H>::smem(kCacheMaxBatch)));
+                                               TcLayout<D, H>::smem(kAttnMaxBatch)));
 }
 template <int D, bool BF16, int H>
 int launch_tc(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {

@@ -258,7 +258,7 @@ bool pool_ok(const dflash_page_pool* p) {
   auto at4 = [](const void* q) { return q && (reinterpret_cast<uintptr_t>(q) & 3) == 0; };
   return p && p->n_pages >= 1 && static_cast<long long>(p->n_pages) * kPagePos < (1LL << 31) && p->pages_per_seq >= 1 &&
          static_cast<long long>(p->pages_per_seq) * kPagePos < (1LL << 31) && p->max_batch >= 1 &&
-         p->max_batch <= kPoolMaxBatch && at4(p->page_table) && at4(p->held) && at4(p->free_list) && at4(p->state);
+         p->max_batch <= kMaxBatch && at4(p->page_table) && at4(p->held) && at4(p->free_list) && at4(p->state);
 }
 
 template <typename K, typename A>

@@ -11,8 +11,8 @@
 namespace dfl {
 
 constexpr int kPagePos = 64;          // positions per page, and keys per attention tile
-constexpr int kPoolMaxBatch = 4096;   // sequences per page-pool call (five integers each in shared memory)
-constexpr int kCacheMaxBatch = 1024;  // sequences per attention call (a shared-memory prefix table)
+constexpr int kMaxBatch = 8192;       // sequences of a pool and of a cache (a pool call keeps five integers each in shared memory)
+constexpr int kAttnMaxBatch = 1024;   // sequences of an attention launch (three integers each beside its rings)
 constexpr int kPagedMaxCtas = 256;    // attention partial slots are sized for this many CTAs
 
 // Makes a handle's device current for a call, and the caller's again afterwards.

@@ -409,7 +409,7 @@ int dflash_verify_greedy_noalloc(const float* target_logits, const int32_t* draf
 typedef struct dflash_page_pool {
   int32_t n_pages;       /* >= 1, n_pages * 64 < 2^31 */
   int32_t pages_per_seq; /* >= 1 */
-  int32_t max_batch;     /* 1..4096 */
+  int32_t max_batch;     /* 1..8192 */
   int32_t reserved;      /* 0 */
   int32_t* page_table;
   int32_t* held;
@@ -455,7 +455,7 @@ typedef struct dflash_cache_config {
   int32_t dtype;            /* DFLASH_F16 or DFLASH_BF16: the pools, and q of the attention */
   int32_t n_pages;          /* pages of 64 positions per layer, n_pages * 64 < 2^31 */
   int32_t pages_per_seq;    /* columns of the page table */
-  int32_t max_batch;        /* 1..1024 */
+  int32_t max_batch;        /* 1..8192; the attention takes 1024 sequences a launch */
   int32_t max_block;        /* new rows per sequence that one attention call takes, 1..16 */
   int32_t rope_dim;         /* dims of each head that are rotated: 0..d, a multiple of 16 */
   int32_t rope_interleaved; /* pairs (2j, 2j + 1) instead of (j, j + rope_dim / 2) */

@@ -102,7 +102,7 @@ def test_types_and_layouts(B, x, y, d, rope, interleaved):
 
 
 @pytest.mark.parametrize("nq,nkv,lens,rows,pad,layers", [(1, 1, [0], 1, 0, 1), (32, 8, [1000], 1, 8, 2), (5, 5, [63, 64, 127], 2, 24, 3),
-                                                         (40, 8, [0], 777, 0, 1), (8, 1, list(range(0, 330, 11)), 16, 16, 1)])
+                                                         (40, 8, [0], 777, 0, 1), (8, 1, list(range(0, 330, 11)), 16, 16, 1), (2, 1, [n % 300 for n in range(8192)], 1, 0, 1)])
 def test_sizes_and_strides(B, nq, nkv, lens, rows, pad, layers):
     c = Case(B, nq, nkv, 128, torch.bfloat16, torch.float16, 128, False, lens, [rows] * len(lens), rows, layers, layers - 1, pad=pad)
     c.append()

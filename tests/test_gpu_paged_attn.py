@@ -109,7 +109,8 @@ def test_tile_edges(B, rows):
 
 @pytest.mark.parametrize("nq,nkv,rows,lens", [(8, 2, 1, [40000]), (8, 8, 1, [9000, 1, 3000]), (32, 8, 16, [5000, 64, 0, 777]),
                                               (32, 8, 1, [n * 997 % 8000 for n in range(32)]), (12, 4, 5, [n * 641 % 6000 for n in range(40)]),
-                                              (4, 2, 1, [n * 37 % 900 for n in range(400)]), (8, 4, 2, list(range(1024)))])
+                                              (4, 2, 1, [n * 37 % 900 for n in range(400)]), (8, 4, 2, list(range(1024))),
+                                              (2, 1, 1, [n % 70 for n in range(2500)])])
 def test_long_ragged_and_many(B, nq, nkv, rows, lens):
     """Long caches split over every CTA, ragged batches whose CTAs walk many tiles and segments, and
     as many sequences as a call takes."""

@@ -69,7 +69,7 @@ def ints(v):
     return torch.tensor(v, dtype=torch.int32, device="cuda")
 
 
-@pytest.mark.parametrize("n_pages,cols,batch", [(1, 1, 1), (40, 3, 7), (700, 40, 33), (5000, 17, 300), (9000, 5, 4096)])
+@pytest.mark.parametrize("n_pages,cols,batch", [(1, 1, 1), (40, 3, 7), (700, 40, 33), (5000, 17, 300), (9000, 5, 4096), (9000, 5, 8192)])
 def test_random_steps(B, n_pages, cols, batch):
     rng = random.Random(n_pages * 7 + batch)
     p, m = B.PagePool(n_pages, cols, batch), Model(n_pages, cols, batch)

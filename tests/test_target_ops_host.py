@@ -31,7 +31,7 @@ def test_struct_layouts():
 
 
 @pytest.mark.parametrize("bad", [dict(n_pages=0), dict(n_pages=1 << 25), dict(pages_per_seq=0), dict(pages_per_seq=1 << 25),
-                                 dict(max_batch=0), dict(max_batch=4097), dict(page_table=None), dict(held=None),
+                                 dict(max_batch=0), dict(max_batch=8193), dict(page_table=None), dict(held=None),
                                  dict(free_list=None), dict(state=None), dict(state=P4 + 2), dict(held=P4 + 1)])
 def test_page_pool_refuses_a_bad_pool(L, bad):
     assert L.dflash_pages_init(pool(**bad), None) == -1
@@ -65,7 +65,7 @@ def cfg(**kw):
 
 @pytest.mark.parametrize("bad", [dict(n_layers=0), dict(n_kv_heads=0), dict(n_heads=9), dict(n_heads=0), dict(n_heads=34),
                                  dict(head_dim=96), dict(dtype=B.F32), dict(dtype=-1), dict(n_pages=0), dict(n_pages=1 << 25),
-                                 dict(pages_per_seq=0), dict(max_batch=0), dict(max_batch=1025), dict(max_block=0),
+                                 dict(pages_per_seq=0), dict(max_batch=0), dict(max_batch=8193), dict(max_block=0),
                                  dict(max_block=17), dict(rope_dim=24), dict(rope_dim=144), dict(rope_dim=-16),
                                  dict(rope_interleaved=2), dict(rope_positions=0), dict(scale=-1.0), dict(scale=float("nan")),
                                  dict(scale=float("inf"))])
@@ -82,7 +82,7 @@ def test_cache_config_check_rejects_a_scale_that_overflows(L):
 
 def test_cache_config_check_accepts(L):
     for kw in (dict(), dict(head_dim=64, rope_dim=64, dtype=B.BF16), dict(n_heads=16, max_block=16), dict(n_heads=256, max_block=1),
-               dict(rope_dim=0, rope_positions=0), dict(rope_dim=32, rope_interleaved=1), dict(scale=0.25), dict(max_batch=1024)):
+               dict(rope_dim=0, rope_positions=0), dict(rope_dim=32, rope_interleaved=1), dict(scale=0.25), dict(max_batch=8192)):
         assert L.dflash_cache_config_check(cfg(**kw)) == 0, kw
         assert 0 < L.dflash_cache_workspace_size(cfg(**kw)) < 1 << 28
 
