@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
       const int lim = len + r;  // last key the row may see
       float m = -INFINITY, l = 0.f;
       uint32_t kept = 0;  // new keys whose values are added at the end
-      bool first = true;
+      bool first = true, huge = false;
       for (; w.left > 0; ++i, first = false) {
         const int cnt = min(H, w.left), t = w.at.t + hh;
         w.u += cnt;
@@ -483,6 +483,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
             l *= corr;
             m = mx;
           }
+          huge = __any_sync(0xffffffffu, fabsf(m) > 1048576.f && fabsf(m) < INFINITY);
         }
         if (edge) {
           // The step's V rows behind the last key are cleared; new keys are looked through, a key
@@ -527,7 +528,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
         }
         {
           const float base = m == -INFINITY ? 0.f : m;
-          const float2 scale2 = {P.scale_log2, P.scale_log2}, base2 = {-base, -base};
+          // One rounding of score times scale less base. Past 2^20 the base's own rounding would show
+          // in it (a weight of 2^32 at scores of 2^30): there the product is rounded as the base was.
+          if (huge)
+#pragma unroll
+            for (int k = 0; k < 64; ++k) sc[k] *= P.scale_log2;
+          const float scale = huge ? 1.f : P.scale_log2;
+          const float2 scale2 = {scale, scale}, base2 = {-base, -base};
           float2 ls[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
           for (int k = 0; k < 64; k += 2) {

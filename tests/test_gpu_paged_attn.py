@@ -200,6 +200,22 @@ def test_large_and_equal_scores(B):
     c.check()
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("nq,rows", [(4, 1), (4, 8), (8, 16)])
+def test_scores_of_billions(B, dtype, nq, rows):
+    """One key takes all where its score is 2^30 and more and the next a millionth less."""
+    c = Case(B, nq, 1, 128, dtype, [300, 7], [rows] * 2, rows, seed=rows)
+    c.q.copy_(torch.where(c.q > 0, 59648.0, 58880.0).to(dtype))     # 233 and 230 times 256: exact in both types
+    for s in range(2):
+        at = c.at(s)
+        c.cache.k_pool[0, at] = (torch.arange(len(at), device="cuda") * 37 % len(at) * 0.25 + 40000.0).to(dtype)[:, None, None].expand(-1, 1, 128)
+        c.cache.k_pool[0, at[3]] = 50176.0
+    c.attend()
+    for s in range(2):
+        want = c.cache.v_pool[0, c.at(s)[3], 0]
+        assert torch.equal(c.out[s * rows:(s + 1) * rows], want.expand(rows, nq, 128))
+
+
 def test_layers_and_spare_columns(B):
     c = Case(B, 8, 2, 128, torch.float16, [100, 300], [2, 2], 2, layers=3, layer=2, spare_cols=5)
     c.attend()
