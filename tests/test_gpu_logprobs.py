@@ -277,6 +277,34 @@ def test_captured_replayed_and_repeated(make):
     assert dr.last_launch_count() == 1
 
 
+def test_two_handles_on_two_streams_at_once(make):
+    """Each with its own workspace, one replaying a graph while the other is called."""
+    V = (60000, 60001)
+    sets = []
+    for i in range(2):
+        z, t = logits(40 + i, V[i], torch.float32, seed=20 + i)
+        out = call(make(V[i]), z, t, 6)
+        sets.append((make(V[i]), z, t, out, [x.clone() for x in out], torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    dr, z, t, out, _, _ = sets[0]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dr.logprobs(z, t, *out)
+    for _ in range(30):
+        with torch.cuda.stream(sets[0][5]):
+            for x in out:
+                x.zero_()
+            g.replay()
+        dr1, z1, t1, out1, _, s1 = sets[1]
+        with torch.cuda.stream(s1):
+            for x in out1:
+                x.zero_()
+            dr1.logprobs(z1, t1, *out1, stream=s1)
+    torch.cuda.synchronize()
+    for dr, z, t, out, want, _ in sets:
+        assert all(torch.equal(a, b) for a, b in zip(out, want)) and dr.device_error() == 0
+
+
 def test_bad_arguments_are_refused_before_a_launch(make):
     dr, B = make(1000), make.B
     z, t = logits(2, 1000, torch.float32)
