@@ -279,7 +279,8 @@ __global__ void __launch_bounds__(Layout<D>::kThreads, 1) paged_attn_kernel(cons
           for (int n8 = 0; n8 < 4; ++n8)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              float v = sc[n8][c] * P.scale_log2;
+              // (rounded here, not in one step with the base below: the maximum is of rounded scores)
+              float v = __fmul_rn(sc[n8][c], P.scale_log2);
               if (edge && key0 + n8 * 8 + kq + (c & 1) > lim[c >> 1]) v = -INFINITY;
               sc[n8][c] = v;
               mx[c >> 1] = fmaxf(mx[c >> 1], v);

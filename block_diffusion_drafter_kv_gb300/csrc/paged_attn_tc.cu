@@ -460,7 +460,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
         float top[4] = {sc[0], sc[1], sc[2], sc[3]};
 #pragma unroll
         for (int k = 4; k < 64; ++k) top[k & 3] = fmaxf(top[k & 3], sc[k]);
-        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * P.scale_log2;
+        // (a rounded product: wherever it is used, it is the same number)
+        const float mx = __fmul_rn(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), P.scale_log2);
         const bool need = mx > m + kMove;
         if (__any_sync(0xffffffffu, need)) {
           const float corr = need && !first ? ex2(m - mx) : 1.f;
@@ -515,13 +516,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
             }
           }
           if (odd && valid) {  // (a tile of another CTA's has its new keys looked after there)
+            const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
             for (int k = 0; k < 64; ++k) {
               const int key = key0 + k;
               if (key < len || key >= nk) continue;
-              s_z[key - len] = sc[k] * P.scale_log2;
+              // The rounded product for the sum here and for the weight at the segment's end: a product
+              // fused with the subtraction would differ from it by the product's rounding.
+              const float z = __fmul_rn(sc[k], P.scale_log2);
+              s_z[key - len] = z;
               kept |= 1u << (key - len);
-              l += ex2(sc[k] * P.scale_log2 - (m == -INFINITY ? 0.f : m));
+              l += ex2(z - base);
               sc[k] = -INFINITY;
             }
           }
