@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(Shape<TOP>::kThreads, Shape<TOP>::kCtasPerSm) 
   const long long U = static_cast<long long>(n_rows) * per_row;
   // at most one CTA for every two stages of a row; where rows go to eight or more CTAs each, to the same number
   int G = static_cast<int>(min(static_cast<long long>(gridDim.x), static_cast<long long>(n_rows) * ((per_row + 2 * kStageUnits - 1) / (2 * kStageUnits))));
-  if (G >= 8 * n_rows && n_rows > 0) G -= G % n_rows;
+  if (n_rows > 0 && G / 8 >= n_rows) G -= G % n_rows;
   const int cta = blockIdx.x;
   if (cta >= G) return;
   const long long U0 = range_begin(cta, U, G), U1 = range_begin(cta + 1, U, G);
