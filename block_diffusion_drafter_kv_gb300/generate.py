@@ -55,7 +55,23 @@ def spec_generate(drafter, target, input_ids, max_new_tokens: int, temperature: 
     temperature > 0 verifies by speculative sampling with uniforms drawn from `generator`.
     logprobs=n (0..32) also collects every new token's log probability, the entropy of its
     distribution and the n most likely tokens at its place in the stats. A drafter bound with
-    `pages` gets its pages as the sequence grows. Returns (new tokens as a list of ints, GenerationStats)."""
+    `pages` gets its pages as the sequence grows. With a `stream` (torch.cuda.Stream) all of it, the
+    target's calls included, runs on that stream, after what the current one has queued and before
+    what it queues next. Returns (new tokens as a list of ints, GenerationStats)."""
+    if stream is None:
+        return _generate(drafter, target, input_ids, max_new_tokens, temperature, stop_token_ids, block, generator, logprobs)
+    caller = torch.cuda.current_stream(stream.device)
+    stream.wait_stream(caller)
+    try:
+        # the library's calls take the current stream, so that they, torch's and the target's are in one order
+        with torch.cuda.stream(stream):
+            return _generate(drafter, target, input_ids, max_new_tokens, temperature, stop_token_ids, block, generator, logprobs)
+    finally:
+        caller.wait_stream(stream)
+
+
+def _generate(drafter, target, input_ids, max_new_tokens, temperature, stop_token_ids, block, generator, logprobs):
+    """spec_generate on the current stream."""
     dev = drafter.last_token.device
     B = block or drafter.cfg.max_block
     V = drafter.shape.vocab
@@ -77,7 +93,7 @@ def spec_generate(drafter, target, input_ids, max_new_tokens: int, temperature: 
         n = rows.shape[0]
         lp, ent, tv = (torch.empty(k, dtype=torch.float32, device=dev) for k in (n, n, n * logprobs))
         ti = torch.empty(n * logprobs, dtype=torch.int32, device=dev)
-        drafter.logprobs(rows, tokens, lp, ent, ti if logprobs else None, tv if logprobs else None, stream=stream)
+        drafter.logprobs(rows, tokens, lp, ent, ti if logprobs else None, tv if logprobs else None)
         alts = [list(zip(i, v)) for i, v in zip(ti.reshape(n, logprobs).tolist(), tv.reshape(n, logprobs).tolist())]
         return list(zip(lp.tolist(), ent.tolist(), alts))
 
@@ -99,9 +115,9 @@ def spec_generate(drafter, target, input_ids, max_new_tokens: int, temperature: 
     drafter.len.zero_()
     n_prompt = torch.tensor([P], dtype=torch.int32, device=dev)
     if pages is not None:
-        pages.release(drafter.len, 1, stream)   # what an earlier sequence in the slot still holds
-        pages.reserve(drafter.len, n_prompt, P, 1, stream=stream)
-    drafter.inject(tapped.contiguous(), P, n_prompt, 1, stream)
+        pages.release(drafter.len, 1)   # what an earlier sequence in the slot still holds
+        pages.reserve(drafter.len, n_prompt, P, 1)
+    drafter.inject(tapped.contiguous(), P, n_prompt, 1)
     first = pick(logits.reshape(-1))
     drafter.last_token[0] = first
     scores = None
@@ -115,23 +131,23 @@ def spec_generate(drafter, target, input_ids, max_new_tokens: int, temperature: 
     n_cached = P
     while True:
         if pages is not None:
-            pages.reserve(drafter.len, room, B, 1, stream=stream)
-        drafter.draft(1, B, drafted, stream=stream)
+            pages.reserve(drafter.len, room, B, 1)
+        drafter.draft(1, B, drafted)
         block_tokens = torch.cat([drafter.last_token[:1].to(torch.int64), drafted[0, : B - 1].to(torch.int64)])
         tapped, logits = target.forward_block(block_tokens)
         logits = logits.to(torch.float32).reshape(1, B, V).contiguous()
         if temperature > 0:
             u = torch.rand(1, B, generator=generator, device=dev, dtype=torch.float32)
-            drafter.verify_sampling(logits, drafted, u, temperature, 1, B, acc, com, stream)
+            drafter.verify_sampling(logits, drafted, u, temperature, 1, B, acc, com)
         else:
-            drafter.verify(logits, drafted, 1, B, acc, com, stream)
+            drafter.verify(logits, drafted, 1, B, acc, com)
         tau = int(acc[0])
         stats.steps += 1
         stats.accept_lens.append(tau)
         target.truncate(n_cached + tau)   # keep slot 0 and the accepted drafts
         rows = torch.zeros(tapped.shape[0], B, tapped.shape[2], dtype=torch.bfloat16, device=dev)
         rows[:, :tau] = tapped[:, :tau]
-        drafter.inject(rows, B, acc, 1, stream)
+        drafter.inject(rows, B, acc, 1)
         n_cached += tau
         if logprobs is not None:
             scores = score(logits[0], com[0])
