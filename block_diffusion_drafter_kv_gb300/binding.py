@@ -15,6 +15,7 @@ from .build import LIB_PATH
 
 DFLASH_OK = 0
 DFLASH_E_INVAL = -1
+DFLASH_E_CAPACITY = -3
 STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported drafter shape", -3: "capacity exceeded",
           -4: "CUDA error", -5: "state not bound"}
 DEV_TIMEOUT, DEV_CAPACITY, DEV_TOKEN = 1, 2, 4

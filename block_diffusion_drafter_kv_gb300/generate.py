@@ -31,6 +31,8 @@ from typing import List, Optional, Sequence, Tuple
 
 import torch
 
+from .binding import DFLASH_E_CAPACITY, PAGE_POSITIONS, DFlashError
+
 
 @dataclass
 class GenerationStats:
@@ -55,7 +57,10 @@ def spec_generate(drafter, target, input_ids, max_new_tokens: int, temperature: 
     temperature > 0 verifies by speculative sampling with uniforms drawn from `generator`.
     logprobs=n (0..32) also collects every new token's log probability, the entropy of its
     distribution and the n most likely tokens at its place in the stats. A drafter bound with
-    `pages` gets its pages as the sequence grows. With a `stream` (torch.cuda.Stream) all of it, the
+    `pages` gets its pages as the sequence grows. Where the pool or the table has no further page for
+    it, blocks shrink to what is left of its last one; where nothing is left, or the prompt has no
+    room, DFlashError (capacity exceeded) is raised before drafter and target go on. The pool's flag
+    is set in either case. With a `stream` (torch.cuda.Stream) all of it, the
     target's calls included, runs on that stream, after what the current one has queued and before
     what it queues next. Returns (new tokens as a list of ints, GenerationStats)."""
     if stream is None:
@@ -108,16 +113,24 @@ def _generate(drafter, target, input_ids, max_new_tokens, temperature, stop_toke
         return False
 
     pages = getattr(drafter, "pages", None)
-    room = None if pages is None else torch.full((1,), B, dtype=torch.int32, device=dev)
+    n_cached = 0
+
+    def make_room(n: int) -> int:
+        """Pages for the next n positions; returns how many of them there is room for. A refused sequence
+        has -1 in its slots (the pool's flag would also tell of other sequences than this one)."""
+        n_new, slots = torch.full((1,), n, dtype=torch.int32, device=dev), torch.zeros(n, dtype=torch.int32, device=dev)
+        pages.reserve(drafter.len, n_new, n, 1, slots)
+        return n if int(slots[0]) >= 0 else min(n, -n_cached % PAGE_POSITIONS)
+
     ids = torch.as_tensor(input_ids, dtype=torch.int64, device=dev).reshape(-1)
-    tapped, logits = target.prefill(ids)
     P = ids.numel()
     drafter.len.zero_()
-    n_prompt = torch.tensor([P], dtype=torch.int32, device=dev)
     if pages is not None:
         pages.release(drafter.len, 1)   # what an earlier sequence in the slot still holds
-        pages.reserve(drafter.len, n_prompt, P, 1)
-    drafter.inject(tapped.contiguous(), P, n_prompt, 1)
+        if make_room(P) < P:
+            raise DFlashError(DFLASH_E_CAPACITY, f"no pages for a prompt of {P} positions")
+    tapped, logits = target.prefill(ids)
+    drafter.inject(tapped.contiguous(), P, torch.tensor([P], dtype=torch.int32, device=dev), 1)
     first = pick(logits.reshape(-1))
     drafter.last_token[0] = first
     scores = None
@@ -129,27 +142,30 @@ def _generate(drafter, target, input_ids, max_new_tokens, temperature, stop_toke
     acc = torch.zeros(1, dtype=torch.int32, device=dev)
     com = torch.zeros(1, B, dtype=torch.int32, device=dev)
     n_cached = P
+    n = B   # slots of the block
     while True:
         if pages is not None:
-            pages.reserve(drafter.len, room, B, 1)
-        drafter.draft(1, B, drafted)
-        block_tokens = torch.cat([drafter.last_token[:1].to(torch.int64), drafted[0, : B - 1].to(torch.int64)])
+            n = make_room(B)
+            if n == 0:
+                raise DFlashError(DFLASH_E_CAPACITY, f"no pages for a block after {len(out)} new tokens")
+        drafter.draft(1, n, drafted)
+        block_tokens = torch.cat([drafter.last_token[:1].to(torch.int64), drafted[0, : n - 1].to(torch.int64)])
         tapped, logits = target.forward_block(block_tokens)
-        logits = logits.to(torch.float32).reshape(1, B, V).contiguous()
+        logits = logits.to(torch.float32).reshape(1, n, V).contiguous()
         if temperature > 0:
-            u = torch.rand(1, B, generator=generator, device=dev, dtype=torch.float32)
-            drafter.verify_sampling(logits, drafted, u, temperature, 1, B, acc, com)
+            u = torch.rand(1, n, generator=generator, device=dev, dtype=torch.float32)
+            drafter.verify_sampling(logits, drafted, u, temperature, 1, n, acc, com)
         else:
-            drafter.verify(logits, drafted, 1, B, acc, com)
+            drafter.verify(logits, drafted, 1, n, acc, com)
         tau = int(acc[0])
         stats.steps += 1
         stats.accept_lens.append(tau)
         target.truncate(n_cached + tau)   # keep slot 0 and the accepted drafts
-        rows = torch.zeros(tapped.shape[0], B, tapped.shape[2], dtype=torch.bfloat16, device=dev)
+        rows = torch.zeros(tapped.shape[0], n, tapped.shape[2], dtype=torch.bfloat16, device=dev)
         rows[:, :tau] = tapped[:, :tau]
-        drafter.inject(rows, B, acc, 1)
+        drafter.inject(rows, n, acc, 1)
         n_cached += tau
         if logprobs is not None:
-            scores = score(logits[0], com[0])
+            scores = score(logits[0], com[0, :n])
         if emit(com[0, :tau].tolist(), scores):
             return out, stats
