@@ -124,7 +124,7 @@ def _generate(drafter, target, input_ids, max_new_tokens, temperature, stop_toke
 
     ids = torch.as_tensor(input_ids, dtype=torch.int64, device=dev).reshape(-1)
     P = ids.numel()
-    drafter.len.zero_()
+    drafter.len[:1].zero_()
     if pages is not None:
         pages.release(drafter.len, 1)   # what an earlier sequence in the slot still holds
         if make_room(P) < P:
