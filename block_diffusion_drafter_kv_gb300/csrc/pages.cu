@@ -261,14 +261,18 @@ bool pool_ok(const dflash_page_pool* p) {
          p->max_batch <= kMaxBatch && at4(p->page_table) && at4(p->held) && at4(p->free_list) && at4(p->state);
 }
 
+// ints: the kernel's integers in shared memory for each of `batch` sequences.
 template <typename K, typename A>
-int launch(K kernel, long long items, size_t smem, const A& arg, void* stream) {
+int launch(K kernel, long long items, int ints, int batch, const A& arg, void* stream) {
   cudaLaunchConfig_t cfg = {};
   // a thread per item up to 512 CTAs (each repeats the prefix sum), then more items a thread
   const long long ctas = (items + kThreads - 1) / kThreads;
   cfg.gridDim = dim3(static_cast<unsigned>(ctas < 1 ? 1 : ctas > 512 ? 512 : ctas));
-  if (smem > 40 * 1024 &&  // with the static part past the 48 KB that need no asking
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+  const size_t smem = sizeof(int) * ints * batch;
+  // With the static part past the 48 KB that need no asking. The limit belongs to the kernel, not to the
+  // call: always the same one, so that host threads with pools of their own cannot lower each other's.
+  if (smem > 40 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(sizeof(int)) * ints * kMaxBatch) != cudaSuccess)
     return DFLASH_E_CUDA;
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
@@ -290,7 +294,7 @@ bool at4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 extern "C" int dflash_pages_init(const dflash_page_pool* p, void* stream) {
   if (!dfl::pool_ok(p)) return DFLASH_E_INVAL;
   const long long entries = static_cast<long long>(p->max_batch) * p->pages_per_seq;
-  return dfl::launch(dfl::pages_init_kernel, entries > p->n_pages ? entries : p->n_pages, 0, *p, stream);
+  return dfl::launch(dfl::pages_init_kernel, entries > p->n_pages ? entries : p->n_pages, 0, 0, *p, stream);
 }
 
 extern "C" int dflash_pages_reserve(const dflash_page_pool* p, const int32_t* len, const int32_t* n_new, int32_t batch,
@@ -310,7 +314,7 @@ extern "C" int dflash_pages_reserve(const dflash_page_pool* p, const int32_t* le
   // four slots a thread; without slots, a thread for about every page
   const long long rows = static_cast<long long>(batch) * rows_per_seq;
   return dfl::launch(dfl::pages_reserve_kernel, slots ? (rows + 3) / 4 : rows / dfl::kPagePos + batch,
-                     5 * sizeof(int) * batch, P, stream);
+                     5, batch, P, stream);
 }
 
 extern "C" int dflash_pages_release(const dflash_page_pool* p, const int32_t* len, int32_t batch, void* stream) {
@@ -322,6 +326,6 @@ extern "C" int dflash_pages_release(const dflash_page_pool* p, const int32_t* le
   P.batch = batch;
   // at most the pool's pages come back, and at most what the sequences can hold
   const long long most = static_cast<long long>(batch) * p->pages_per_seq;
-  return dfl::launch(dfl::pages_release_kernel, (most < p->n_pages ? most : p->n_pages) / 2, 3 * sizeof(int) * batch, P,
+  return dfl::launch(dfl::pages_release_kernel, (most < p->n_pages ? most : p->n_pages) / 2, 3, batch, P,
                      stream);
 }
