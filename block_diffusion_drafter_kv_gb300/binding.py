@@ -169,6 +169,8 @@ class Drafter:
         if pages is not None:
             if n_pages or page_table is not None or pages.max_batch < max_batch:
                 raise DFlashError(DFLASH_E_INVAL, "pages: a pool of at least max_batch sequences, without n_pages or page_table")
+            if pages.device != weights.w_fc.device:
+                raise DFlashError(DFLASH_E_INVAL, f"pages on {pages.device}, the weights on {weights.w_fc.device}")
             n_pages, page_table = pages.n_pages, pages.page_table
         self.pages = pages
         self.L = lib()
