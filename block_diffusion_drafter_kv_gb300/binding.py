@@ -279,6 +279,7 @@ class Drafter:
         dtype = _DTYPES.get(str(logits.dtype), -1)
         if dtype < 0 or vocab != self.cfg.vocab or logits.stride(1) != 1 or logits.device != self.last_token.device:
             raise DFlashError(DFLASH_E_INVAL, "logits must be fp32, fp16 or bf16 [rows][vocab] on the drafter's device")
+        _require_31_bits(rows, "rows")
         n = 0 if top_ids is None else top_ids.numel() // max(rows, 1)
         for t, dt, size, name in ((tokens, torch.int32, rows, "tokens"), (logprob, torch.float32, rows, "logprob"),
                                   (entropy, torch.float32, rows, "entropy"), (top_ids, torch.int32, rows * n, "top_ids"),
@@ -397,6 +398,7 @@ class PagePool:
         self.n_pages, self.pages_per_seq, self.max_batch = n_pages, pages_per_seq, max_batch
         if min(n_pages, pages_per_seq, max_batch) < 1:
             raise DFlashError(DFLASH_E_INVAL, "PagePool")
+        _require_31_bits(max(n_pages, pages_per_seq, max_batch), "the pool's sizes")
         with torch.cuda.device(device):
             self.page_table = torch.empty(max_batch, pages_per_seq, dtype=torch.int32, device="cuda")
             self.held = torch.empty(max_batch, dtype=torch.int32, device="cuda")
@@ -418,6 +420,7 @@ class PagePool:
         _require_min(n_new, i32, batch, "n_new", self.device)
         if slots is not None:
             _require_on(slots, i32, batch * rows_per_seq, "slots", self.device)
+        _require_31_bits(rows_per_seq, "rows_per_seq")
         self._call(self.L.dflash_pages_reserve, "dflash_pages_reserve", stream, length.data_ptr(), n_new.data_ptr(), batch,
                    rows_per_seq, _ptr(slots))
 
@@ -531,6 +534,12 @@ class PagedCache:
             self.close()
         except Exception:
             pass
+
+
+def _require_31_bits(n: int, name) -> None:
+    """The library's arguments are int32, and ctypes would drop the bits above."""
+    if n >= 1 << 31:
+        raise DFlashError(DFLASH_E_CAPACITY, f"{name} ({n}) must be less than 2^31")
 
 
 def _require_min(t, dtype, numel, name, device):
