@@ -14,7 +14,7 @@
 // split over all SMs, and a CTA has at most two rows that it shares with others. Those join in CTA
 // order in the CTA that arrives last at the row, which does not depend on who that is; a row
 // inside one range never leaves its CTA. (Chunks of 64 KB taken from a counter, each joined through
-// global memory, took 129 us for 293 rows of 151936 fp32 against 46 then: fence, counter and parts
+// global memory, took 129 us for 289 rows of 151936 fp32 against 46 then: fence, counter and parts
 // are microseconds of latency, too many for 1.4 us of copying.)
 // In a CTA a producer warp keeps a ring of 16 KB stages full by bulk copies across rows, and
 // eight consumer warps share each stage. Two CTAs per SM with six stages where alternatives are
@@ -30,9 +30,10 @@
 // Candidates wait in a buffer until 32 can be sorted and merged into the list at once: sorted
 // logits, where every value is a candidate, take the same path.
 //
-// Measured: 293 of 512 rows of 151936 fp32, n_top 5, 40.7 us (64% of the copy rate; 32.1 us without
-// alternatives: a row's first stages have many candidates); 1000 rows of 50257 bf16 without
-// alternatives 27.2 us (54%: 3.7 us of it are the sums, 3 the join of cut rows at the end);
+// Measured: 289 of 512 rows of 151936 fp32, n_top 5, 41 us (63% of the copy rate; 32.8 us without
+// alternatives, 62 us with 32: a row's first stages have many candidates); 1000 rows of 50257 bf16 without
+// alternatives 27.7 us (53%: 3.7 us of it are the sums, 3 the join of cut rows at the end), with 5 of them
+// 55 us (27%: a row is six stages long, and most of it is its start);
 // 16 rows, n_top 20, 13.6 us, a chain of latencies: token list, first copy, sums, sort, join.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -59,7 +60,10 @@ struct Shape {
   static constexpr int kCtasPerSm = TOP ? 2 : 3, kStages = TOP ? 6 : 4;
   static constexpr int kThreads = kConsumers + (TOP ? 64 : 32);  // and the producer, and the threshold's warp
 };
-constexpr int kListed = 1024;                // rows of a call whose tokens are looked through before the list is cut
+// Rows of a call whose tokens are looked through before the list is cut: every CTA looks through all of
+// them, a few to a thread. Calls of more rows cut a list of all rows, and a CTA walks past those without a
+// token: 1107 of 2048 rows of 151936 fp32, n_top 5, 192 us (52% of the copy rate).
+constexpr int kListed = 1024;
 constexpr unsigned kAll = 0xffffffffu;
 using Key = unsigned long long;
 

@@ -20,9 +20,10 @@
 // a softmax state of their own, so that warps meet only where a segment ends. S = q K^T and
 // O += P V are mma.sync m16n8k16 with fp32 accumulation: the rows are few (4 in ordinary
 // grouped decoding), so a 128-row tcgen05 tile would be mostly padding, while the loads bound
-// the kernel: 4 rows over 4 sequences of 32768 keys take 85 to 89 us (0.89 to 0.93 of the measured
-// copy rate), 32 ragged sequences of 512 to 8192 keys 91 to 94 us (0.89 to 0.91). One sequence of 2048
-// takes 8.5 us: two launches, lengths, page ids, q, K/V, softmax, parts, one latency after another.
+// the kernel: 4 rows over 4 sequences of 32768 keys take 86 us (0.92 of the measured copy rate), 32
+// ragged sequences of 512 to 8192 keys 93 to 94 us (0.89 to 0.90). One sequence of 2048 takes 8.7 us:
+// two launches, lengths, page ids, q, K/V, softmax, parts, one latency after another. With d 64 a tile is
+// half the bytes for the same steps of the warps: 59 us (0.66), 68 us (0.61), 7.9 us.
 #include "paged_attn.cuh"
 
 namespace dfl {
@@ -149,8 +150,9 @@ __global__ void __launch_bounds__(Layout<D>::kThreads, 1) paged_attn_kernel(cons
 
   if (warp == KG) {
     // ------------------------------------------------------------ producer warp
-    // K/V are read once per call: streamed through L2, unless all of it (16 MB, one eighth of L2)
-    // can stay there until it is read again
+    // K/V are read once per call: streamed through L2, unless all of it (16 MB, one eighth of L2) can stay
+    // there until it is read again. Three caches in turn, one row (us), kept and streamed: 1 x 2048 (8.4
+    // MB each) 8.7 and 9.1, 1 x 3900 (16.0 MB) 9.6 and 10.4, 8 x 2048 (67 MB) 18.8 and 18.2.
     const uint64_t pol = T * L::kStageBytes > (16ll << 20) ? policy_evict_first() : policy_evict_last();
     int i = 0, seg_no = 0;
     int q_issued = 0, kv_issued = 0;  // of the segments and tiles walked so far
@@ -605,11 +607,13 @@ int launch(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // Up to 16 rows here, more on tcgen05. Measured (bf16, d 128, 32 query heads on 8 KV heads, us):
+  // Up to the 16 rows of an mma.sync tile here, more on tcgen05. Measured (bf16, d 128, 32 query heads on
+  // 8 KV heads, us):
   //   rows  1 x 2048  32 x 1000  4 x 32768       1 x 2048  32 x 1000  4 x 32768
-  //     16      11.0       30.1       87.6  here     18.2       53.9      102.5  tcgen05 (an earlier form)
-  //     20      15.0       43.1      103.5  here     14.4       33.9       89.6  tcgen05 (here: an earlier
-  //     64      17.6       60.3      146.8  here     16.5       45.2       97.3  tcgen05  form with more rows)
+  //      4       8.7       27.6       85.6  here     11.1       29.1       86.2  tcgen05
+  //      8      10.8       29.1       86.0  here     13.4       31.3       88.5  tcgen05
+  //     16      11.1       30.3       86.0  here     14.3       32.8       89.8  tcgen05
+  //     20                                           14.6       34.3       90.5  tcgen05
   const int e = p.rows <= kRowsFew ? static_cast<int>(cudaLaunchKernelEx(&cfg, paged_attn_kernel<D, BF16>, p))
                                    : launch_paged_attn_tc(p, BF16, n_ctas, stream);
   if (e != 0) return e;

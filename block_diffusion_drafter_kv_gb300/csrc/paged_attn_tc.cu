@@ -11,8 +11,9 @@
 // sequences of 32768, d 128): 90 us with 20 rows, 97 with 64 (81% of the copy rate), 119 with 128;
 // against a two-tile step's 2750 cycles of HBM time (64 KB) issuing its products takes 1250 and its
 // softmax 1100, overlapped between steps, so that it waits for copies; a one-tile step (1400 cycles of
-// HBM time) waits for the chain of its products and softmax (1700), d 64 likewise. Short caches (128
-// sequences of 500: 119 us with 64 rows, 37%) are bound by the segments' ends: q, output.
+// HBM time) waits for the chain of its products and softmax (1700), d 64 likewise (75 us with 64 rows, 53%).
+// Short caches (128 sequences of 500: 117 us with 64 rows, 38%, 168 us with 128 rows, 29%) are bound by the
+// segments' ends: q, output.
 //
 //   S   two TMEM buffers of N columns: the next step's Q K^T runs under this one's softmax
 //   Q, P  in TMEM too, as the products' A operands: with them in shared memory (64 KB) the rings
