@@ -22,7 +22,7 @@ DEV_TIMEOUT, DEV_CAPACITY, DEV_TOKEN = 1, 2, 4
 OPT_WAIT_LIMIT_NS, OPT_CHAIN_MAX, OPT_GEMV_VARIANT, OPT_ATTN_SPLIT, OPT_ATTN_KEY_GROUPS = 1, 2, 3, 4, 5
 OPT_INJECT_PASS_ROWS = 6
 OPT_ATTN_MODE = 7
-F32, F16, BF16 = 0, 1, 2
+F32, F16, BF16, E4M3_F16, E4M3_BF16 = 0, 1, 2, 3, 4
 PAGE_POSITIONS = 64
 
 
@@ -83,9 +83,19 @@ SIGNATURES = {
     "dflash_cache_destroy": (c_int32, [c_void_p]),
     "dflash_cache_bind": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                     c_size_t]),
+    "dflash_cache_bind_8bit": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                         c_void_p, c_size_t]),
     "dflash_cache_append": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_int32, ctypes.c_int64,
                                       ctypes.c_int64, ctypes.c_int64, c_void_p, c_int32, c_int32, c_void_p, c_void_p]),
     "dflash_cache_attend": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_void_p]),
+    "dflash_cache_append_shared": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_int32, ctypes.c_int64,
+                                             ctypes.c_int64, ctypes.c_int64, c_void_p, c_int32, c_int32, c_int32, c_void_p,
+                                             c_void_p]),
+    "dflash_cache_shared_workspace_size": (c_size_t, [POINTER(DflashCacheConfig), c_int32]),
+    "dflash_cache_attend_shared": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_int32, c_int32, c_void_p,
+                                             c_void_p, c_size_t, c_void_p]),
+    "dflash_cache_read": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_int32, c_int32, c_void_p, c_void_p,
+                                    c_void_p]),
     "dflash_cache_read_error": (c_int32, [c_void_p, POINTER(c_int32), c_int32, c_void_p]),
     "dflash_linear_bf16": (c_int32, [c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_int32, c_void_p,
                                      c_void_p]),
@@ -451,14 +461,26 @@ class PagedCache:
     `pages` keeps the page table; `length` (int32 CUDA [max_batch]) holds every sequence's
     positions before the new rows and stays the caller's to advance. k_pool / v_pool:
     [n_layers][n_pages * 64][n_kv_heads][head_dim] of `dtype` (fp16 or bf16), allocated here
-    unless given. rope_cos / rope_sin: fp32 [positions][rope_dim / 2] (see rope_tables)."""
+    unless given. rope_cos / rope_sin: fp32 [positions][rope_dim / 2] (see rope_tables).
+
+    bits=8: the pools hold e4m3 values (torch.float8_e4m3fn), each row of one position and KV head with a
+    power of two in `scales` (uint8 [n_layers][n_pages][n_kv_heads][2][64]: exponent + 127 of K, of V);
+    q and out stay of `dtype`.
+
+    Sequences that share a prefix: append and attend take `prefix`, the number of the sequence whose
+    positions come before those of every sequence of the call (one of the page table's that is not in the
+    batch, filled like any other). shared_rows: the most rows (batch * rows_per_seq) of such an attend;
+    its workspace is kept here."""
 
     def __init__(self, n_layers: int, n_heads: int, n_kv_heads: int, head_dim: int, pages: PagePool, length, dtype=None,
                  max_block: int = 0, rope_cos=None, rope_sin=None, rope_interleaved: bool = False, scale: float = 0.0,
-                 k_pool=None, v_pool=None):
+                 k_pool=None, v_pool=None, bits: int = 16, scales=None, shared_rows: int = 0):
         import torch
         self.L = lib()
         dtype = torch.float16 if dtype is None else dtype
+        if bits not in (8, 16) or (bits == 16 and scales is not None):
+            raise DFlashError(DFLASH_E_INVAL, "bits: 16, or 8 with scales")
+        _require_31_bits(shared_rows, "shared_rows")
         self.dtype, self.device, self.pages, self.length = dtype, pages.device, pages, length
         batch = min(length.numel(), pages.max_batch)
         _require_min(length, torch.int32, 1, "length", self.device)
@@ -469,16 +491,25 @@ class PagedCache:
             _require_on(t, torch.float32, positions * rope_dim // 2, n, self.device)
         if not max_block:  # as many rows as a call can take
             max_block = max(1, min(16, 128 // max(1, n_heads // max(1, n_kv_heads))))
-        self.cfg = DflashCacheConfig(n_layers, n_heads, n_kv_heads, head_dim, _DTYPES.get(str(dtype), -1), pages.n_pages,
-                                     pages.pages_per_seq, batch, max_block, rope_dim, int(rope_interleaved), positions,
-                                     float(scale))
+        code = _DTYPES.get(str(dtype), -1)
+        if bits == 8:
+            code = {F16: E4M3_F16, BF16: E4M3_BF16}.get(code, -1)
+        self.cfg = DflashCacheConfig(n_layers, n_heads, n_kv_heads, head_dim, code, pages.n_pages, pages.pages_per_seq, batch,
+                                     max_block, rope_dim, int(rope_interleaved), positions, float(scale))
         check(self.L.dflash_cache_config_check(ctypes.byref(self.cfg)), "dflash_cache_config_check")
         shape = (n_layers, pages.n_pages * PAGE_POSITIONS, n_kv_heads, head_dim)
         numel = shape[0] * shape[1] * shape[2] * shape[3]
-        _require_on(k_pool, dtype, numel, "k_pool", self.device)
-        _require_on(v_pool, dtype, numel, "v_pool", self.device)
-        self.k_pool = torch.zeros(shape, dtype=dtype, device=self.device) if k_pool is None else k_pool
-        self.v_pool = torch.zeros(shape, dtype=dtype, device=self.device) if v_pool is None else v_pool
+        pool_dtype = torch.float8_e4m3fn if bits == 8 else dtype
+        _require_on(k_pool, pool_dtype, numel, "k_pool", self.device)
+        _require_on(v_pool, pool_dtype, numel, "v_pool", self.device)
+        self.k_pool = torch.zeros(shape, dtype=pool_dtype, device=self.device) if k_pool is None else k_pool
+        self.v_pool = torch.zeros(shape, dtype=pool_dtype, device=self.device) if v_pool is None else v_pool
+        self.bits, self.scales = bits, scales
+        if bits == 8:
+            shape = (n_layers, pages.n_pages, n_kv_heads, 2, PAGE_POSITIONS)
+            _require_on(scales, torch.uint8, 2 * numel // head_dim, "scales", self.device)
+            if scales is None:
+                self.scales = torch.zeros(shape, dtype=torch.uint8, device=self.device)
         self.rope_cos, self.rope_sin = rope_cos, rope_sin
         nbytes = self.L.dflash_cache_workspace_size(ctypes.byref(self.cfg))
         with torch.cuda.device(self.device):
@@ -486,36 +517,70 @@ class PagedCache:
             h = c_void_p()
             check(self.L.dflash_cache_create(ctypes.byref(self.cfg), ctypes.byref(h)), "dflash_cache_create")
             self.c = h
-            check(self.L.dflash_cache_bind(h, self.k_pool.data_ptr(), self.v_pool.data_ptr(), pages.page_table.data_ptr(),
-                                           length.data_ptr(), _ptr(rope_cos), _ptr(rope_sin),
-                                           (self.workspace.data_ptr() + 255) // 256 * 256, nbytes), "dflash_cache_bind")
+            args = (pages.page_table.data_ptr(), length.data_ptr(), _ptr(rope_cos), _ptr(rope_sin),
+                    (self.workspace.data_ptr() + 255) // 256 * 256, nbytes)
+            if bits == 8:
+                check(self.L.dflash_cache_bind_8bit(h, self.k_pool.data_ptr(), self.v_pool.data_ptr(), self.scales.data_ptr(),
+                                                    *args), "dflash_cache_bind_8bit")
+            else:
+                check(self.L.dflash_cache_bind(h, self.k_pool.data_ptr(), self.v_pool.data_ptr(), *args), "dflash_cache_bind")
+            self._shared = None
+            if shared_rows:
+                self._shared_bytes = self.L.dflash_cache_shared_workspace_size(ctypes.byref(self.cfg), shared_rows)
+                self._shared = torch.empty(self._shared_bytes + 256, dtype=torch.uint8, device="cuda")
         self._q_row, self._kv_row = n_heads * head_dim, n_kv_heads * head_dim
 
-    def append(self, layer: int, q, k, v, slots, batch: int, rows_per_seq: int, q_out, stream=None):
+    def append(self, layer: int, q, k, v, slots, batch: int, rows_per_seq: int, q_out, stream=None, prefix: Optional[int] = None):
         """Rotary positions on q and k, k and v into the cache at `slots` (from
         PagePool.reserve), the rotated q to q_out. q, k, v: fp16 or bf16 [batch * rows_per_seq]
         rows of heads x dims, rows a stride apart (slices of one fused projection are fine);
-        q and q_out may be None."""
+        q and q_out may be None. With `prefix`, row r of a sequence is position
+        length[prefix] + length[s] + r."""
         rows, dev, dt = batch * rows_per_seq, self.device, k.dtype
         q_stride = 0 if q is None else _row_stride(q, dt, rows, self._q_row, "q", dev)
         k_stride = _row_stride(k, dt, rows, self._kv_row, "k", dev)
         v_stride = _row_stride(v, dt, rows, self._kv_row, "v", dev)
         _require_on(slots, _torch_calls()[2], rows, "slots", dev)
         _require_on(q_out, self.dtype, rows * self._q_row, "q_out", dev)
-        check(self.L.dflash_cache_append(self.c, layer, _ptr(q), k.data_ptr(), v.data_ptr(), _DTYPES.get(str(dt), -1),
-                                         q_stride, k_stride, v_stride, slots.data_ptr(), batch, rows_per_seq, _ptr(q_out),
-                                         _stream_on(stream, dev)), "dflash_cache_append")
+        args = (self.c, layer, _ptr(q), k.data_ptr(), v.data_ptr(), _DTYPES.get(str(dt), -1), q_stride, k_stride, v_stride,
+                slots.data_ptr(), batch, rows_per_seq)
+        if prefix is None:
+            check(self.L.dflash_cache_append(*args, _ptr(q_out), _stream_on(stream, dev)), "dflash_cache_append")
+        else:
+            check(self.L.dflash_cache_append_shared(*args, prefix, _ptr(q_out), _stream_on(stream, dev)), "dflash_cache_append_shared")
 
-    def attend(self, layer: int, q, n_new, batch: int, rows_per_seq: int, out, stream=None):
+    def attend(self, layer: int, q, n_new, batch: int, rows_per_seq: int, out, stream=None, prefix: Optional[int] = None):
         """Causal attention of row r of every sequence (position length[s] + r, r < n_new[s]) over
         the cache; q and out: contiguous [batch * rows_per_seq][n_heads][head_dim] of the
-        cache's dtype. Rows past n_new[s] of out are left as they were."""
+        cache's dtype. Rows past n_new[s] of out are left as they were. With `prefix`, every row sees
+        all length[prefix] positions of that sequence first; they are read once for the batch."""
         numel = batch * rows_per_seq * self._q_row
         _require_on(q, self.dtype, numel, "q", self.device)
         _require_on(out, self.dtype, numel, "out", self.device)
         _require_min(n_new, _torch_calls()[2], batch, "n_new", self.device)
-        check(self.L.dflash_cache_attend(self.c, layer, q.data_ptr(), n_new.data_ptr(), batch, rows_per_seq, out.data_ptr(),
-                                         _stream_on(stream, self.device)), "dflash_cache_attend")
+        if prefix is None:
+            check(self.L.dflash_cache_attend(self.c, layer, q.data_ptr(), n_new.data_ptr(), batch, rows_per_seq, out.data_ptr(),
+                                             _stream_on(stream, self.device)), "dflash_cache_attend")
+            return
+        if self._shared is None:
+            raise DFlashError(DFLASH_E_INVAL, "attention with a prefix needs a cache with shared_rows")
+        check(self.L.dflash_cache_attend_shared(self.c, layer, q.data_ptr(), n_new.data_ptr(), batch, rows_per_seq, prefix,
+                                                out.data_ptr(), (self._shared.data_ptr() + 255) // 256 * 256, self._shared_bytes,
+                                                _stream_on(stream, self.device)), "dflash_cache_attend_shared")
+
+    def read(self, layer: int, first, count, batch: int, rows_per_seq: int, k_out, v_out, stream=None):
+        """K and V of positions [first[s], first[s] + count[s]) of every sequence, dense: row
+        s * rows_per_seq + r of k_out and v_out (fp16 or bf16 [batch * rows_per_seq][n_kv_heads][head_dim])
+        is position first[s] + r. Rows past count[s] are left as they were."""
+        i32 = _torch_calls()[2]
+        numel = batch * rows_per_seq * self._kv_row
+        _require_min(first, i32, batch, "first", self.device)
+        _require_min(count, i32, batch, "count", self.device)
+        _require_on(k_out, k_out.dtype, numel, "k_out", self.device)
+        _require_on(v_out, k_out.dtype, numel, "v_out", self.device)
+        check(self.L.dflash_cache_read(self.c, layer, first.data_ptr(), count.data_ptr(), batch, rows_per_seq,
+                                       _DTYPES.get(str(k_out.dtype), -1), k_out.data_ptr(), v_out.data_ptr(),
+                                       _stream_on(stream, self.device)), "dflash_cache_read")
 
     def device_error(self, clear: bool = True, stream=None) -> int:
         """The device error flags once the work queued on `stream` has finished."""

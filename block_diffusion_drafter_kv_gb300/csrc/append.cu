@@ -14,8 +14,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "ptx.cuh"
-#include "target.h"
+#include "quant.cuh"
 
 namespace dfl {
 
@@ -52,9 +51,10 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams P) 
   const long long row = blockIdx.x;
   const int slot = __ldcg(P.slots + row);
   const int s = static_cast<int>(row / P.rows_per_seq);
-  const long long pos = static_cast<long long>(__ldcg(P.len + s)) + (row - static_cast<long long>(s) * P.rows_per_seq);
+  const int before = P.prefix_len ? __ldcg(P.prefix_len) : 0;
+  const long long pos = static_cast<long long>(__ldcg(P.len + s)) + (row - static_cast<long long>(s) * P.rows_per_seq) + before;
   if (slot == -1) return;
-  if (slot < 0 || slot >= P.pool_rows || (P.rope_dim > 0 && (pos < 0 || pos >= P.positions))) {
+  if (slot < 0 || slot >= P.pool_rows || before < 0 || (P.rope_dim > 0 && (pos < 0 || pos >= P.positions))) {
     if (threadIdx.x == 0) raise_flag(P.err, kDevCapacity);
     return;
   }
@@ -118,6 +118,98 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams P) 
   }
 }
 
+// The same for an 8-bit cache: q as above, K and V rows in e4m3 with a scale byte. The threads of a head
+// (4 or 8 neighbouring lanes) join their largest magnitude. The rotation's products and sums are
+// rounded one by one, not fused: a value next to a rounding border of e4m3 or of the scale then goes the
+// way that plain fp32 arithmetic takes it.
+template <typename X, typename Y>
+__global__ void __launch_bounds__(kThreads) append8_kernel(const AppendParams P) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const long long row = blockIdx.x;
+  const int slot = __ldcg(P.slots + row);
+  const int s = static_cast<int>(row / P.rows_per_seq);
+  const int before = P.prefix_len ? __ldcg(P.prefix_len) : 0;
+  const long long pos = static_cast<long long>(__ldcg(P.len + s)) + (row - static_cast<long long>(s) * P.rows_per_seq) + before;
+  if (slot == -1) return;
+  if (slot < 0 || slot >= P.pool_rows || before < 0 || (P.rope_dim > 0 && (pos < 0 || pos >= P.positions))) {
+    if (threadIdx.x == 0) raise_flag(P.err, kDevCapacity);
+    return;
+  }
+  const int items = P.d / 16;  // 4 or 8
+  const int item = threadIdx.x % items, h0 = threadIdx.x / items, step = kThreads / items;
+  const bool turn = item * 16 < P.rope_dim;
+  const int half = P.rope_dim / 2;
+  const int d0 = turn && !P.interleaved ? 8 * item : 16 * item;
+  const int d1 = turn && !P.interleaved ? d0 + half : d0 + 8;
+  float cs[8], sn[8];
+  if (turn) {
+    const float4* c4 = reinterpret_cast<const float4*>(P.cos + pos * half + 8 * item);
+    const float4* s4 = reinterpret_cast<const float4*>(P.sin + pos * half + 8 * item);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 c = __ldg(c4 + i), t = __ldg(s4 + i);
+      cs[4 * i] = c.x, cs[4 * i + 1] = c.y, cs[4 * i + 2] = c.z, cs[4 * i + 3] = c.w;
+      sn[4 * i] = t.x, sn[4 * i + 1] = t.y, sn[4 * i + 2] = t.z, sn[4 * i + 3] = t.w;
+    }
+  }
+  const int nq = P.q ? P.nq : 0, heads = nq + 2 * P.nkv;
+  // (the lanes of a warp walk together, past the last head too: the maxima are joined by shuffles)
+  for (int base = 0; base < heads; base += step) {
+    const int h = min(base + h0, heads - 1);
+    const bool there = base + h0 < heads;
+    const int which = h < nq ? -1 : h < nq + P.nkv ? 0 : 1, kv = h - nq - (which == 1 ? P.nkv : 0);
+    const X* src = which < 0 ? static_cast<const X*>(P.q) + row * P.q_stride + static_cast<size_t>(h) * P.d
+                             : static_cast<const X*>(which == 0 ? P.k : P.v) + row * (which == 0 ? P.k_stride : P.v_stride) +
+                                   static_cast<size_t>(kv) * P.d;
+    const uint4 in[2] = {__ldcs(reinterpret_cast<const uint4*>(src + d0)), __ldcs(reinterpret_cast<const uint4*>(src + d1))};
+    const X* x = reinterpret_cast<const X*>(in);
+    float y[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) y[e] = to_f32(x[e]);
+    if (turn && which != 1) {
+      auto pair = [&](float& a, float& b, int e) {
+        const float u = __fsub_rn(__fmul_rn(a, cs[e]), __fmul_rn(b, sn[e]));
+        b = __fadd_rn(__fmul_rn(b, cs[e]), __fmul_rn(a, sn[e]));
+        a = u;
+      };
+      if (P.interleaved) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) pair(y[2 * e], y[2 * e + 1], e);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) pair(y[e], y[e + 8], e);
+      }
+    }
+    uint32_t top = 0;  // the bits of a magnitude are ordered as it is, infinities and NaN above all others
+#pragma unroll
+    for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(y[e]) & 0x7fffffffu);
+    for (int o = 1; o < items; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (!there) continue;
+    if (which < 0) {
+      Y* dst = static_cast<Y*>(P.q_out) + (static_cast<size_t>(row) * P.nq + h) * P.d;
+      uint4 out[2];
+      Y* o = reinterpret_cast<Y*>(out);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[e] = from_f32<Y>(y[e]);
+      *reinterpret_cast<uint4*>(dst + d0) = out[0];
+      *reinterpret_cast<uint4*>(dst + d1) = out[1];
+      continue;
+    }
+    const int byte = scale_byte(top);
+    uint32_t out[4] = {0, 0, 0, 0};
+    if (byte != kScaleNan) {
+      const float f = exponent_value(kScaleBias - byte);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) out[e >> 1] |= to_e4m3x2(y[2 * e] * f, y[2 * e + 1] * f) << ((e & 1) * 16);
+    }
+    uint8_t* dst = static_cast<uint8_t*>(which == 0 ? P.k_pool : P.v_pool) + (static_cast<size_t>(slot) * P.nkv + kv) * P.d;
+    *reinterpret_cast<uint2*>(dst + d0) = make_uint2(out[0], out[1]);
+    *reinterpret_cast<uint2*>(dst + d1) = make_uint2(out[2], out[3]);
+    if (item == 0) P.scales[scale_index(slot, P.nkv, kv, which)] = static_cast<uint8_t>(byte);
+  }
+}
+
 }  // namespace
 
 int launch_append(const AppendParams& p, int x_dtype, int pool_dtype, cudaStream_t stream) {
@@ -130,9 +222,14 @@ int launch_append(const AppendParams& p, int x_dtype, int pool_dtype, cudaStream
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const bool xh = x_dtype == DFLASH_F16, yh = pool_dtype == DFLASH_F16;
+  const bool xh = x_dtype == DFLASH_F16, yh = pool_dtype == DFLASH_F16 || pool_dtype == DFLASH_E4M3_F16;
   cudaError_t e;
-  if (xh && yh) e = cudaLaunchKernelEx(&cfg, append_kernel<__half, __half>, p);
+  if (pool_dtype == DFLASH_E4M3_F16 || pool_dtype == DFLASH_E4M3_BF16) {
+    if (xh && yh) e = cudaLaunchKernelEx(&cfg, append8_kernel<__half, __half>, p);
+    else if (xh) e = cudaLaunchKernelEx(&cfg, append8_kernel<__half, __nv_bfloat16>, p);
+    else if (yh) e = cudaLaunchKernelEx(&cfg, append8_kernel<__nv_bfloat16, __half>, p);
+    else e = cudaLaunchKernelEx(&cfg, append8_kernel<__nv_bfloat16, __nv_bfloat16>, p);
+  } else if (xh && yh) e = cudaLaunchKernelEx(&cfg, append_kernel<__half, __half>, p);
   else if (xh) e = cudaLaunchKernelEx(&cfg, append_kernel<__half, __nv_bfloat16>, p);
   else if (yh) e = cudaLaunchKernelEx(&cfg, append_kernel<__nv_bfloat16, __half>, p);
   else e = cudaLaunchKernelEx(&cfg, append_kernel<__nv_bfloat16, __nv_bfloat16>, p);

@@ -45,12 +45,30 @@ struct AppendParams {
   void* q_out;
   void* k_pool;  // this layer's
   void* v_pool;
+  uint8_t* scales;        // this layer's, of an 8-bit cache
+  const int* prefix_len;  // positions before those that len counts, or null
   int* err;
   long long rows;
   int rows_per_seq, nq, nkv, d, rope_dim, interleaved, positions;
   int pool_rows;
 };
+// pool_dtype: DFLASH_F16, DFLASH_BF16, or an 8-bit cache's, whose q_out is of the type it names
 int launch_append(const AppendParams& p, int x_dtype, int pool_dtype, cudaStream_t stream);
+
+// ---------------------------------------------------------------- rows of the cache, dense
+struct ReadParams {
+  const uint8_t* k_pool;  // this layer's
+  const uint8_t* v_pool;
+  const uint8_t* scales;
+  const int* page_table;
+  const int* first;
+  const int* count;
+  void* k_out;
+  void* v_out;
+  int* err;
+  int batch, rows_per_seq, nkv, d, n_pages, pages_per_seq;
+};
+int launch_cache_read(const ReadParams& p, int pool_dtype, int out_dtype, int n_sms, cudaStream_t stream);
 
 // ---------------------------------------------------------------- paged attention
 struct PagedAttnParams {
@@ -70,7 +88,14 @@ struct PagedAttnParams {
   float group_inv;   // its inverse
   float scale_log2;  // scale * log2(e)
   unsigned long long wait_ns;
+  const uint8_t* k_pool;   // this layer's
+  const uint8_t* v_pool;
+  const uint8_t* scales;   // of an 8-bit cache
+  const int* prefix_len;   // a prefix that all sequences share, or null
+  const int* prefix_table; // its row of the page table
 };
+// Attention over an 8-bit cache, and with a shared prefix.
+int launch_paged_attn_rows(const PagedAttnParams& p, int dtype, cudaStream_t stream);
 int paged_attn_rows(int rows);  // rows of a partial slot: `rows` rounded up to what a kernel variant holds
 int paged_attn_set_attributes();
 int launch_paged_attn(const PagedAttnParams& p, bool bf16, int n_ctas, cudaStream_t stream);

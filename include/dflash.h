@@ -260,6 +260,8 @@ int dflash_verify_greedy_hidden(dflash_handle* h, const void* target_hidden, con
 #define DFLASH_F32 0
 #define DFLASH_F16 1
 #define DFLASH_BF16 2
+#define DFLASH_E4M3_F16 3  /* of a cache: K and V in 8 bits, q and out in fp16 */
+#define DFLASH_E4M3_BF16 4 /* of a cache: K and V in 8 bits, q and out in bf16 */
 int dflash_logprobs(dflash_handle* h, const void* logits, int32_t dtype, int64_t row_stride,
                     const int32_t* tokens, int32_t rows, float temperature, int32_t n_top, float* logprob,
                     float* entropy, int32_t* top_ids, float* top_logprobs, void* stream);
@@ -452,7 +454,8 @@ typedef struct dflash_cache_config {
   int32_t n_heads;          /* nq: query heads */
   int32_t n_kv_heads;       /* nkv; nq % nkv == 0, (nq / nkv) * max_block <= 128 */
   int32_t head_dim;         /* d: 64 or 128 */
-  int32_t dtype;            /* DFLASH_F16 or DFLASH_BF16: the pools, and q of the attention */
+  int32_t dtype;            /* DFLASH_F16 or DFLASH_BF16: the pools, and q of the attention; DFLASH_E4M3_F16
+                               or DFLASH_E4M3_BF16: pools in 8 bits (dflash_cache_bind_8bit) */
   int32_t n_pages;          /* pages of 64 positions per layer, n_pages * 64 < 2^31 */
   int32_t pages_per_seq;    /* columns of the page table */
   int32_t max_batch;        /* 1..8192; the attention takes 1024 sequences a launch */
@@ -487,6 +490,19 @@ int dflash_cache_destroy(dflash_cache* c);
 int dflash_cache_bind(dflash_cache* c, void* k_pool, void* v_pool, const int32_t* page_table, int32_t* len,
                       const float* rope_cos, const float* rope_sin, void* workspace, size_t workspace_bytes);
 
+/* As dflash_cache_bind, for a cache of 8 bits. A row of K or V (one position, one KV head) is
+ * values in e4m3 times 2^e: e is the least whole number for which the row's largest magnitude is at
+ * most 448 * 2^e, -40 at least; each value is rounded to nearest once, after rotation in fp32.
+ *   k_pool, v_pool  uint8 [L][n_pages * 64][nkv][d], e4m3
+ *   scales          uint8 [L][n_pages][nkv][2][64], 16-byte aligned: e + 127 of K's, then of V's 64
+ *                   positions of the page; 255 stands for a row of NaN: one with an infinity, a
+ *                   NaN or a magnitude past 448 * 2^40 is written so. Scales of positions that
+ *                   an append has not written may hold any value.
+ * The other calls are the same; q and out are of the type that the config's dtype names, and
+ * q_out of an append too. */
+int dflash_cache_bind_8bit(dflash_cache* c, void* k_pool, void* v_pool, void* scales, const int32_t* page_table, int32_t* len,
+                           const float* rope_cos, const float* rope_sin, void* workspace, size_t workspace_bytes);
+
 /* Rotary positions on q and k, and k and v into the cache, for one layer's new rows (any
  * number: a token, a block, a prompt). Row s * rows_per_seq + r is position len[s] + r.
  * u = x cos - y sin, v = y cos + x sin for each pair (x, y) of the head's first rope_dim
@@ -502,6 +518,15 @@ int dflash_cache_bind(dflash_cache* c, void* k_pool, void* v_pool, const int32_t
 int dflash_cache_append(dflash_cache* c, int32_t layer, const void* q, const void* k, const void* v,
                         int32_t x_dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride,
                         const int32_t* slots, int32_t batch, int32_t rows_per_seq, void* q_out, void* stream);
+
+/* The same for sequences that share a prefix (below): row s * rows_per_seq + r is position
+ * len[prefix] + len[s] + r.
+ *   prefix   a sequence of the page table that is none of the batch's: batch <= prefix < max_batch.
+ *            Where len[prefix] is negative every row is left out, and DFLASH_DEV_CAPACITY set. */
+int dflash_cache_append_shared(dflash_cache* c, int32_t layer, const void* q, const void* k, const void* v,
+                               int32_t x_dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                               const int32_t* slots, int32_t batch, int32_t rows_per_seq, int32_t prefix, void* q_out,
+                               void* stream);
 
 /* Causal attention of the new rows over the cache, one layer:
  *   out[s][r][h] = sum_j softmax_j(scale * q[s][r][h] . K_j) V_j,  j = 0 .. len[s] + r
@@ -522,6 +547,35 @@ int dflash_cache_append(dflash_cache* c, int32_t layer, const void* q, const voi
  * in fp16), of which the result's own rounding is 1.7e-3 (2.1e-4). */
 int dflash_cache_attend(dflash_cache* c, int32_t layer, const void* q, const int32_t* n_new, int32_t batch,
                         int32_t rows_per_seq, void* out, void* stream);
+
+/* Attention of sequences that share a prefix (a system prompt, one document's questions): the
+ * len[prefix] positions of sequence `prefix`, whose pages the page table's row `prefix` lists (it is
+ * filled as any other sequence's: dflash_pages_reserve, dflash_cache_append). Every new row of the
+ * batch sees all of them, then the positions 0 .. len[s] + r of its own sequence:
+ *   out[s][r][h] = sum_j softmax_j(scale * q[s][r][h] . K_j) V_j, j over both
+ * The prefix is read once for all sequences (of every 512), and its products are taken for many
+ * sequences at once. q, n_new, out and the rest as for dflash_cache_attend; where len[prefix] is out of
+ * range the whole batch is left out.
+ *   prefix     batch <= prefix < max_batch
+ *   workspace  dflash_cache_shared_workspace_size(cfg, batch * rows_per_seq) bytes or more, 256-byte
+ *              aligned, of any contents: it belongs to the call until that has run */
+size_t dflash_cache_shared_workspace_size(const dflash_cache_config* cfg, int32_t rows);
+int dflash_cache_attend_shared(dflash_cache* c, int32_t layer, const void* q, const int32_t* n_new, int32_t batch,
+                               int32_t rows_per_seq, int32_t prefix, void* out, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/* Rows of the cache, dense and in 16 bits (a prompt chunk's attention in the caller's own code, a
+ * sequence that leaves the card), one layer: position first[s] + r of sequence s < batch at row
+ * s * rows_per_seq + r, for r < count[s].
+ *   first, count  int32 [batch] on the device, 0 <= count[s] <= rows_per_seq
+ *   out_dtype     DFLASH_F16 or DFLASH_BF16; rounded once where it is not the cache's
+ *   k_out, v_out  [batch * rows_per_seq][nkv][d], 16-byte aligned. Rows past count[s] are left as
+ *                 they were, and so are all of a sequence whose numbers are out of range or pass
+ *                 pages_per_seq * 64 and the rows of a page id outside [0, n_pages); both set
+ *                 DFLASH_DEV_CAPACITY.
+ * len is not looked at: any positions whose pages are in the table can be read. */
+int dflash_cache_read(dflash_cache* c, int32_t layer, const int32_t* first, const int32_t* count, int32_t batch,
+                      int32_t rows_per_seq, int32_t out_dtype, void* k_out, void* v_out, void* stream);
 
 /* As dflash_read_device_error, for a cache handle. */
 int dflash_cache_read_error(dflash_cache* c, int32_t* flags, int32_t clear, void* stream);
