@@ -120,7 +120,7 @@ int dflash_cache_create(const dflash_cache_config* cfg, dflash_cache** out) {
   }
   if (cudaGetDevice(&c->device) != cudaSuccess ||
       cudaDeviceGetAttribute(&c->n_sms, cudaDevAttrMultiProcessorCount, c->device) != cudaSuccess ||
-      paged_attn_set_attributes() != 0) {
+      paged_attn_set_attributes() != 0 || paged_attn8_set_attributes() != 0) {
     delete c;
     return DFLASH_E_CUDA;
   }
@@ -277,7 +277,7 @@ static int attend(dflash_cache* c, int32_t layer, const void* q, const int32_t* 
   P.scales = c->layer_scales(layer);
   P.prefix_len = prefix >= 0 ? c->len + prefix : nullptr;
   P.prefix_table = prefix >= 0 ? c->page_table + static_cast<size_t>(prefix) * f.pages_per_seq : nullptr;
-  const bool plain = !bits8(f) && prefix < 0;
+  P.slot_rows = paged_attn_rows(P.rows);
   const size_t seq_bytes = static_cast<size_t>(rows_per_seq) * f.n_heads * f.head_dim * 2;
   for (int s = 0; s < batch; s += kAttnMaxBatch) {
     P.q = static_cast<const uint8_t*>(q) + s * seq_bytes;
@@ -287,8 +287,10 @@ static int attend(dflash_cache* c, int32_t layer, const void* q, const int32_t* 
     P.page_table = c->page_table + static_cast<size_t>(s) * f.pages_per_seq;
     P.batch = std::min(batch - s, kAttnMaxBatch);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if ((plain ? launch_paged_attn(P, f.dtype == DFLASH_BF16, std::min(c->n_sms, kPagedMaxCtas), st)
-               : launch_paged_attn_rows(P, f.dtype, st)) != 0)
+    const int ctas = std::min(c->n_sms, kPagedMaxCtas);
+    if ((prefix >= 0 ? launch_paged_attn_rows(P, f.dtype, st)
+         : bits8(f) ? launch_paged_attn8(P, io_bf16(f), ctas, st)
+                    : launch_paged_attn(P, io_bf16(f), ctas, st)) != 0)
       return DFLASH_E_CUDA;
   }
   return DFLASH_OK;

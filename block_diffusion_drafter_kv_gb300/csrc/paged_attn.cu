@@ -616,10 +616,20 @@ int launch(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
   //     20                                           14.6       34.3       90.5  tcgen05
   const int e = p.rows <= kRowsFew ? static_cast<int>(cudaLaunchKernelEx(&cfg, paged_attn_kernel<D, BF16>, p))
                                    : launch_paged_attn_tc(p, BF16, n_ctas, stream);
-  if (e != 0) return e;
+  return e != 0 ? e : launch_paged_attn_join(p, BF16, n_ctas, stream);
+}
+
+template <int D, bool BF16>
+int launch_join(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.batch * p.nkv, (p.rows + 7) / 8);
   cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = 0;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   return static_cast<int>(cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<D, BF16>, p, n_ctas, paged_attn_rows(p.rows)));
 }
 
@@ -633,6 +643,11 @@ int paged_attn_set_attributes() {
   for (int x : e)
     if (x != 0) return x;
   return 0;
+}
+
+int launch_paged_attn_join(const PagedAttnParams& p, bool bf16, int n_ctas, cudaStream_t stream) {
+  if (p.d == 128) return bf16 ? launch_join<128, true>(p, n_ctas, stream) : launch_join<128, false>(p, n_ctas, stream);
+  return bf16 ? launch_join<64, true>(p, n_ctas, stream) : launch_join<64, false>(p, n_ctas, stream);
 }
 
 int launch_paged_attn(const PagedAttnParams& p, bool bf16, int n_ctas, cudaStream_t stream) {

@@ -1,0 +1,761 @@
+// Causal attention of new rows over an 8-bit paged cache, on the fp8 tensor cores: the same list of
+// tiles, cut and parts as in paged_attn.cu, whose join follows.
+//
+//   out = sum_j w_j V_j / sum_j p_j,  p_j = 2^(s_j - m),  w_j = p_j 2^ev_j,  s_j = scale_log2 2^ek_j q . K_j
+//
+// with K_j, V_j the stored e4m3 values and ek_j, ev_j their rows' exponents. Bound: the cache's bytes,
+// 2 (d + 1) per key and KV head.
+//
+// The cache's bytes go from memory to the tensor cores as they are. Both products are taken with the
+// cache as the M operand, so that a step's cost goes with the rows there are, not with 128 of them:
+//   S^T = K Q^T   M = 128 keys (two tiles), N = rows;   K as loaded, K-major
+//   O^T += V^T P^T   M = dims, N = rows, K = 128 keys;  V as loaded, MN-major
+// What multiplies the cache is e4m3 too, split so that little is lost:
+//   q   a row is scaled by a power of two to a largest magnitude in [128, 256) and taken apart into
+//       2 (bf16) or 3 (fp16) numbers of 4 significant bits: exact, but for what lies below 2^-10
+//       of e4m3's scale there, 2^-17 of the row's largest value. Their products add up in one accumulator.
+//   w   as fp16, then 2 (bf16) or 3 (fp16) e4m3 numbers, each the sixteenfold rest of the one before, so
+//       that it reaches 2^-18 (2^-22) below the row's largest w_j; an accumulator each, N = pieces x rows.
+// A thread of the softmax has one key and all rows: the key's scales are its own two numbers, and so is
+// the first row that may see the key. The weights' reference m' is a running maximum of s_j + ev_j, so that
+// w_j <= 256 whatever the scales; p_j is w_j 2^-ev_j (|ev_j| <= 40: no overflow).
+//
+// CTA: one per SM, two softmax groups of 128 threads (one for more than 64 rows) that take alternate steps, each
+// with its own S, P, O and references, a warp that issues the products, a producer warp. Every wait is
+// bounded, as in paged_attn_tc.cu.
+#include "paged_attn.cuh"
+#include "quant.cuh"
+
+namespace dfl {
+
+namespace {
+
+constexpr int kStepKeys = 128;
+constexpr float kNone = -3e38f;     // a reference where no key has been seen
+constexpr float kHeadroom = 4.f;    // binary orders of the weights at their reference, and by which scores may pass it
+
+// ---------------------------------------------------------------- descriptors
+DEV void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// fp32 accumulator, both operands e4m3, each K-major or MN-major.
+constexpr uint32_t idesc_f8(int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+// An operand in rows of W bytes (32, 64 or 128, the width of its swizzle), 8 rows to an atom. K-major: a row an M
+// or N index, atoms 8 W apart. MN-major: a row a K index, the next W indices of M or N `mn_stride` bytes on.
+template <int W>
+DEV uint64_t desc_rows(uint32_t saddr, uint32_t mn_stride) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>((mn_stride >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>(8 * W >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(W == 128 ? 2 : W == 64 ? 4 : 6) << 61;
+  return d;
+}
+// Byte offset of 16-byte chunk `ch` of row `r` of such an operand.
+template <int W>
+DEV uint32_t chunk_at(int r, int ch) {
+  return static_cast<uint32_t>(r * W + ((ch ^ (W == 128 ? r & 7 : W == 64 ? (r >> 1) & 3 : (r >> 2) & 1)) << 4));
+}
+
+DEV void load16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+DEV void store16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+DEV void wait_loads() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+DEV void wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+DEV bool test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// A barrier of `n` threads that tells each of them whether one had `v`.
+DEV bool named_bar_any(int id, int n, bool v) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(v ? 1u : 0u), "r"(id), "r"(n)
+      : "memory");
+  return any != 0;
+}
+DEV float warp_max(float x) {  // NaN left out
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+DEV uint32_t half2_to_e4m3x2(__half2 v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&v)));
+  return r;
+}
+DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+DEV bool has_nan8(uint32_t v) { return (((v & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0; }
+
+// Sums of 16 values over the warp: lane L gets that of value L / 2.
+DEV float reduce16(float (&v)[16]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int h = 8; h >= 1; h >>= 1) {
+    const bool up = lane & (2 * h);
+#pragma unroll
+    for (int k = 0; k < h; ++k) {
+      const float keep = up ? v[k + h] : v[k], send = up ? v[k] : v[k + h];
+      v[k] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * h);
+    }
+  }
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
+
+// D: head dim; R: rows of a problem that fit (32, 64, 128).
+template <int D, int R, bool BF16>
+struct Layout8 {
+  static constexpr int kPieces = BF16 ? 2 : 3;              // of q, and of the weights
+  static constexpr int NG = R <= 64 ? 2 : 1;                // softmax groups
+  static constexpr int kThreads = NG * 128 + 64;
+  static constexpr int kOperand = kStepKeys * D;            // K, or V, of a step
+  static constexpr int STAGES = D == 64 ? 8 : R == 32 ? 5 : R == 64 || BF16 ? 4 : 3;
+  static constexpr int kPPiece = kStepKeys * R;
+  static constexpr int kQPiece = R * D;
+  static constexpr int kK = 0;
+  static constexpr int kV = kK + STAGES * kOperand;
+  static constexpr int kP = kV + STAGES * kOperand;
+  static constexpr int kQ = kP + NG * kPieces * kPPiece;
+  static constexpr int kSc = kQ + kPieces * kQPiece;        // scales of a step: two tiles' 128 bytes
+  static constexpr int kRef = kSc + STAGES * 256;           // [NG][R] references
+  static constexpr int kGain = kRef + NG * R * 4;           // [R] 1 / the power of two that q was scaled by
+  static constexpr int kCorr = kGain + R * 4;               // [NG][R] factors of a moved reference; weights of the groups at the end
+  static constexpr int kTop = kCorr + NG * R * 4;           // [NG][4][R] warps' maxima; sums at the end
+  static constexpr int kMl = kTop + NG * 4 * R * 4;         // [R] (max, sum)
+  static constexpr int kBar = kMl + R * 8;
+  static constexpr int kBars = 2 * STAGES + 4 * NG + 2;     // full, empty; S ready, free, P ready, PV done [NG]; Q, done
+  static constexpr int kFlags = kBar + kBars * 8;           // [0] abort, [1] TMEM base, [4..19] valid tiles of steps
+  static constexpr int kWarpSums = kFlags + 80;
+  static constexpr int kPre = kWarpSums + 64;
+  static constexpr int smem(int batch) { return 1024 + kPre + (3 * batch + 1) * 4; }
+  static constexpr uint32_t tS(int g) { return g * R; }     // TMEM columns
+  static constexpr uint32_t tO(int g) { return NG * R + g * kPieces * R; }
+  static_assert(NG * R * (1 + kPieces) <= 512, "tensor memory");
+};
+
+template <int D, int R, bool BF16>
+__global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_kernel(const __grid_constant__ PagedAttnParams P) {
+  using L = Layout8<D, R, BF16>;
+  constexpr int NG = L::NG, STAGES = L::STAGES, PC = L::kPieces;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
+  uint64_t* empty = full + STAGES;
+  uint64_t* sready = empty + STAGES;
+  uint64_t* sfree = sready + NG;
+  uint64_t* pready = sfree + NG;
+  uint64_t* pvdone = pready + NG;
+  uint64_t* qready = pvdone + NG;
+  uint64_t* mdone = qready + 1;
+  volatile int* flag = reinterpret_cast<volatile int*>(smem + L::kFlags);
+  volatile int* s_valid = flag + 4;  // bit h: tile h of the step is there; by step mod 16, more than the ring holds
+  int* s_warp = reinterpret_cast<int*>(smem + L::kWarpSums);
+  int* s_pre = reinterpret_cast<int*>(smem + L::kPre);
+  int* s_len = s_pre + P.batch + 1;
+  int* s_new = s_len + P.batch;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint64_t WL = P.wait_ns;
+
+  if (tid == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < NG; ++i) {
+      mbar_init(&sready[i], 1);
+      mbar_init(&sfree[i], 128);
+      mbar_init(&pready[i], 128);
+      mbar_init(&pvdone[i], 1);
+    }
+    mbar_init(qready, NG * 128);
+    mbar_init(mdone, 1);
+    flag[0] = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&P.kmap);
+    tma_prefetch_desc(&P.vmap);
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  count_tiles<L::kThreads>(P, s_pre, s_len, s_new, s_warp);
+  const int batch = P.batch, nkv = P.nkv, grp = P.group;
+  const long long T = static_cast<long long>(nkv) * s_pre[batch];
+  const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), T));
+  const int cta = blockIdx.x;
+  if (cta >= G) return;  // the whole CTA, before it holds any tensor memory
+  constexpr int kIssuer = NG * 4, kProducer = NG * 4 + 1;
+  if (warp == kIssuer) tmem_alloc(reinterpret_cast<uint32_t*>(smem + L::kFlags + 4), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = static_cast<uint32_t>(flag[1]);
+  const long long T0 = range_begin(cta, T, G), T1 = range_begin(cta + 1, T, G);
+
+  // The walk of every role: steps of up to two tiles of the segments of [T0, T1).
+  struct Walk {
+    long long u;
+    int left;  // tiles of the segment that are left
+    Place at;  // of the next tile
+  };
+  auto begin_segment = [&](Walk& w) {
+    w.at = locate(s_pre, batch, nkv, w.u);
+    w.left = static_cast<int>(min(T1 - w.u, static_cast<long long>(w.at.nt - w.at.t)));
+  };
+
+  if (warp == kProducer) {
+    // ------------------------------------------------------------------ producer
+    const uint64_t pol = T * (2 * kKeys * D) > (16ll << 20) ? policy_evict_first() : policy_evict_last();
+    int i = 0;       // step
+    bool go = true;  // the same in every lane
+    Walk w{T0, 0, {}};
+    int ids = -1, id0 = 0;  // page ids of the segment's next tiles, one a lane; the lane that has the next one
+    while (w.u < T1 && go) {
+      if (w.left == 0) {
+        begin_segment(w);
+        id0 = 32;
+      }
+      int page[2] = {-1, -1};
+      const int cnt = min(2, w.left);
+      for (int h = 0; h < cnt; ++h) {
+        if (id0 == 32) {
+          ids = -1;
+          if (lane < w.left - h) {
+            ids = __ldcg(P.page_table + static_cast<size_t>(w.at.s) * P.pages_per_seq + w.at.t + h + lane);
+            if (ids < 0 || ids >= P.n_pages) {
+              raise_flag(P.err, kDevCapacity);
+              ids = -1;
+            }
+          }
+          id0 = 0;
+        }
+        page[h] = __shfl_sync(0xffffffffu, ids, id0++);
+      }
+      const int st = i % STAGES;
+      if (i >= STAGES) {
+        bool ok = !flag[0];
+        if (ok && lane == 0 && !mbar_wait(&empty[st], (i / STAGES - 1) & 1, WL)) {
+          raise_flag(P.err, kDevTimeout);
+          flag[0] = 1;
+          ok = false;
+        }
+        go = __all_sync(0xffffffffu, ok);
+        if (!go) break;
+      }
+      if (lane == 0) {
+        const int valid = (page[0] >= 0) | (page[1] >= 0) << 1;
+        s_valid[i & 15] = valid;
+        if (valid) mbar_arrive_expect_tx(&full[st], (valid == 3 ? 2 : 1) * (2 * kKeys * D + 2 * kKeys));
+        else mbar_arrive(&full[st]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (page[h] >= 0) {
+            tma_load_3d(smem + L::kK + st * L::kOperand + h * kKeys * D, &P.kmap, &full[st], 0, w.at.g, page[h] * kKeys, pol);
+            tma_load_3d(smem + L::kV + st * L::kOperand + h * kKeys * D, &P.vmap, &full[st], 0, w.at.g, page[h] * kKeys, pol);
+            bulk_load(smem + L::kSc + st * 256 + h * 128, P.scales + (static_cast<size_t>(page[h]) * nkv + w.at.g) * 128, 128, &full[st]);
+          }
+      }
+      __syncwarp();
+      ++i;
+      w.u += cnt;
+      w.left -= cnt;
+      w.at.t += cnt;
+    }
+    // every copy issued has landed before the CTA leaves
+    if (lane == 0)
+      for (int k = max(0, i - STAGES); k < i; ++k) mbar_wait(&full[k % STAGES], (k / STAGES) & 1, WL);
+    __syncwarp();
+  } else if (warp == kIssuer) {
+    // ------------------------------------------------------------------ issuer of the products
+    if (lane == 0) {
+      constexpr uint32_t kQk = idesc_f8(128, R, false, false);
+      auto qk = [&](int i) {  // S^T = K Q^T
+        const int st = i % STAGES, g = i % NG;
+        tc_fence_after();
+        const uint64_t k0 = desc_rows<D>(smem_u32(smem + L::kK + st * L::kOperand), 16);
+        const uint64_t q0 = desc_rows<D>(smem_u32(smem + L::kQ), 16);
+        const uint32_t d = tmem + L::tS(g);
+#pragma unroll
+        for (int p = 0; p < PC; ++p)
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk)
+            mma_f8(d, k0 + (kk * 32 >> 4), q0 + ((p * L::kQPiece + kk * 32) >> 4), kQk, p + kk > 0 ? 1u : 0u);
+        tc_commit(&sready[g]);
+      };
+      auto pv = [&](int i, bool first) {  // O^T (+)= V^T P^T. With 64 dims M's upper half are the same dims again, unused.
+        const int st = i % STAGES, g = i % NG;
+        tc_fence_after();
+        const uint64_t v0 = desc_rows<D>(smem_u32(smem + L::kV + st * L::kOperand), 0);
+        const uint64_t p0 = desc_rows<R>(smem_u32(smem + L::kP + g * PC * L::kPPiece), L::kPPiece);
+        constexpr int N1 = PC * R <= 256 ? PC * R : 256, N2 = PC * R - N1;
+        constexpr uint32_t kPv1 = idesc_f8(128, N1, true, true);
+#pragma unroll
+        for (int kk = 0; kk < kStepKeys / 32; ++kk) {
+          const uint32_t acc = kk > 0 || !first ? 1u : 0u;
+          mma_f8(tmem + L::tO(g), v0 + (kk * 32 * D >> 4), p0 + (kk * 32 * R >> 4), kPv1, acc);
+          if constexpr (N2 > 0) {
+            constexpr uint32_t kPv2 = idesc_f8(128, N2, true, true);
+            mma_f8(tmem + L::tO(g) + N1, v0 + (kk * 32 * D >> 4), p0 + ((N1 / R * L::kPPiece + kk * 32 * R) >> 4), kPv2, acc);
+          }
+        }
+        tc_commit(&pvdone[g]);
+        tc_commit(&empty[st]);
+      };
+      // Whichever product's inputs are ready goes next, so that neither waits behind the other's.
+      Walk w{T0, 0, {}};
+      int nqk = 0, npv = 0, segs = 0;
+      int seg_of[8] = {}, last_seg[NG];  // segment of a step, and of the group's last product
+      for (int g = 0; g < NG; ++g) last_seg[g] = -1;
+      uint64_t idle_since = 0;
+      uint32_t spins = 0;
+      bool start = true;
+      while (w.u < T1 || npv < nqk) {
+        bool moved = false;
+        if (w.u < T1 && nqk < npv + 2 * NG) {
+          if (w.left == 0) {
+            begin_segment(w);
+            start = true;
+          }
+          if (test_wait(&full[nqk % STAGES], (nqk / STAGES) & 1) &&
+              (nqk < NG || test_wait(&sfree[nqk % NG], (nqk / NG - 1) & 1)) && (!start || test_wait(qready, segs & 1))) {
+            segs += start;
+            start = false;
+            qk(nqk);
+            seg_of[nqk & 7] = segs;
+            const int cnt = min(2, w.left);
+            w.u += cnt;
+            w.left -= cnt;
+            ++nqk;
+            moved = true;
+          }
+        }
+        if (npv < nqk && test_wait(&pready[npv % NG], (npv / NG) & 1)) {
+          const int seg = seg_of[npv & 7];
+          pv(npv, last_seg[npv % NG] != seg);
+          last_seg[npv % NG] = seg;
+          ++npv;
+          moved = true;
+        }
+        // (reading the timer takes some 600 cycles: only where nothing has moved for a while)
+        if (moved) {
+          spins = 0;
+        } else if ((++spins & 1023u) == 0) {
+          const uint64_t now = globaltimer_ns();
+          if (spins == 1024) idle_since = now;
+          if (flag[0] || now - idle_since > WL) {
+            if (!flag[0]) raise_flag(P.err, kDevTimeout);
+            flag[0] = 1;
+            break;
+          }
+        }
+      }
+      tc_commit(mdone);
+      if (!mbar_wait(mdone, 0, WL)) raise_flag(P.err, kDevTimeout);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------ softmax and output
+    const int g = tid >> 7, j = tid & 127, gw = warp & 3;  // group, key of the step, warp of the group
+    const uint32_t lanes = static_cast<uint32_t>(gw * 32) << 16;
+    const uint32_t ts = tmem + lanes + L::tS(g), to = tmem + lanes + L::tO(g);
+    float* s_ref = reinterpret_cast<float*>(smem + L::kRef) + g * R;
+    float* s_gain = reinterpret_cast<float*>(smem + L::kGain);
+    float* s_corr = reinterpret_cast<float*>(smem + L::kCorr) + g * R;
+    float* s_top = reinterpret_cast<float*>(smem + L::kTop) + g * 4 * R;
+    float2* s_ml = reinterpret_cast<float2*>(smem + L::kMl);
+    uint8_t* pbuf = smem + L::kP + g * PC * L::kPPiece;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (!mbar_try_wait(bar, parity)) wait_long(bar, parity, flag, P.err, WL);
+      __syncwarp();
+    };
+    // a segment's q, taken apart; rows up to the next multiple of 16 that are not there are zero
+    auto put_q = [&](const Place& p) {
+      constexpr int kParts = D / 16;  // threads of a row
+      const int live = s_new[p.s] * grp, rows = (live + 15) & ~15;
+      for (int item = tid; item < rows * kParts; item += NG * 128) {
+        const int row = item / kParts, part = item % kParts;
+        uint4 in[2] = {};
+        if (row < live) {
+          const int r = new_row(P, row);
+          const uint4* src = reinterpret_cast<const uint4*>(
+              static_cast<const uint16_t*>(P.q) +
+              ((static_cast<size_t>(p.s) * P.rows_per_seq + r) * P.nq + static_cast<size_t>(p.g) * grp + row - r * grp) * D + part * 16);
+          in[0] = __ldcg(src), in[1] = __ldcg(src + 1);
+        }
+        const uint32_t* u = reinterpret_cast<const uint32_t*>(in);
+        float x[16];
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float2 v = unpack2<BF16>(u[k]);
+          x[2 * k] = v.x, x[2 * k + 1] = v.y;
+          top = max(top, max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu));
+        }
+#pragma unroll
+        for (int o = 1; o < kParts; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const bool fine = top < 0x7f800000u;
+        const int e = max(static_cast<int>(top >> 23) - 127, -119);
+        const float f = fine ? exponent_value(7 - e) : 0.f;
+        if (part == 0) s_gain[row] = fine ? exponent_value(e - 7) : __uint_as_float(0x7fc00000u);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) x[k] = fine ? x[k] * f : 0.f;
+#pragma unroll
+        for (int p2 = 0; p2 < PC; ++p2) {
+          uint32_t out[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t b = to_e4m3x2(x[2 * k], x[2 * k + 1]);
+            out[k >> 1] |= b << ((k & 1) * 16);
+            const float2 v = __half22float2(from_e4m3x2(b));
+            x[2 * k] -= v.x, x[2 * k + 1] -= v.y;
+          }
+          *reinterpret_cast<uint4*>(smem + L::kQ + p2 * L::kQPiece + chunk_at<D>(row, part)) = make_uint4(out[0], out[1], out[2], out[3]);
+        }
+      }
+      fence_async_shared();
+      mbar_arrive(qready);
+    };
+
+    float2 l2[R / 2];  // the key's part of every row's sum
+    int i = 0, n_own = 0, seg_no = 0;  // step; steps of this group
+    Walk w{T0, 0, {}};
+    begin_segment(w);
+    put_q(w.at);
+    if (j < R) s_ref[j] = kNone;
+    named_bar_sync(1, NG * 128);
+    for (; w.u < T1; ++seg_no) {
+      const int s = w.at.s, kvh = w.at.g, t0 = w.at.t;
+      const bool whole = t0 == 0 && w.left == w.at.nt;
+      const int len = s_len[s], n_new = s_new[s], nk = len + n_new;
+      const int live = n_new * grp, chunks = (live + 15) >> 4;
+#pragma unroll
+      for (int k = 0; k < R / 2; ++k) l2[k] = {0.f, 0.f};
+      bool first = true;  // of the group's steps in the segment
+      for (; w.left > 0; ++i) {
+        const int cnt = min(2, w.left), t = w.at.t;
+        w.u += cnt;
+        w.left -= cnt;
+        w.at.t += cnt;
+        if (NG == 2 && (i & 1) != g) continue;
+        const int st = i % STAGES;
+        wait(&full[st], (i / STAGES) & 1);
+        // the thread's key: its scales, and the first row that sees it
+        const int valid = s_valid[i & 15];
+        const int key = t * kKeys + j;
+        const bool alive = (valid >> (j >> 6) & 1) && key < nk;
+        const uint8_t* sc = smem + L::kSc + st * 256 + (j >> 6) * 128 + (j & 63);
+        const uint32_t kb = sc[0], vb = sc[64];
+        const float f = P.scale_log2 * scale_value(kb);
+        float ev = vb == kScaleNan ? __uint_as_float(0x7fc00000u) : static_cast<float>(static_cast<int>(vb) - kScaleBias);
+        const float inv_v = scale_value(254u - min(vb, 253u));
+        const int rmin = !alive ? R : key <= len ? 0 : (key - len) * grp;
+        const bool edge = valid != 3 || (t + 2) * kKeys > len + 1;  // some row may not see some key of the step (the same for all threads)
+        if (edge) {
+          // Values that no row sees are cleared (0 * NaN is NaN); a key that some rows see and that has a NaN
+          // among its values becomes one of zeros whose scale is NaN.
+          uint4* vrow = reinterpret_cast<uint4*>(smem + L::kV + st * L::kOperand + j * D);
+          bool clear = !alive;
+          if (alive && key >= len && n_new > 1) {
+            bool nan = false;
+#pragma unroll
+            for (int ch = 0; ch < D / 16; ++ch) {
+              const uint4 v = vrow[ch];
+              nan |= has_nan8(v.x) || has_nan8(v.y) || has_nan8(v.z) || has_nan8(v.w);
+            }
+            if (nan) ev = __uint_as_float(0x7fc00000u);
+            clear = nan;
+          }
+          if (clear)
+#pragma unroll
+            for (int ch = 0; ch < D / 16; ++ch) vrow[ch] = make_uint4(0, 0, 0, 0);
+        }
+        wait(&sready[g], n_own & 1);
+        tc_fence_after();
+        // s_j + ev_j of 16 rows; what a row does not see is -inf
+        auto scores = [&](int c, float (&x)[16]) {
+          uint32_t u[16];
+          __syncwarp();
+          load16(ts + c * 16, u);
+          float gain[16];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 v = reinterpret_cast<const float4*>(s_gain)[c * 4 + k];
+            gain[4 * k] = v.x, gain[4 * k + 1] = v.y, gain[4 * k + 2] = v.z, gain[4 * k + 3] = v.w;
+          }
+          wait_loads();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float v = __fmaf_rn(__uint_as_float(u[k]), __fmul_rn(f, gain[k]), ev);
+            x[k] = edge && c * 16 + k < rmin ? -INFINITY : v;
+          }
+        };
+        float past = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+          float x[16];
+          scores(c, x);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) past = fmaxf(past, x[k] - s_ref[c * 16 + k]);
+        }
+        if (named_bar_any(2 + g, 128, past > kHeadroom)) {
+          // ---- references that move: the rows' maxima over the group, then O and the sums
+#pragma unroll 1
+          for (int c = 0; c < chunks; ++c) {
+            float x[16];
+            scores(c, x);
+            float mine = 0.f;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float top = warp_max(x[k]);
+              if (lane == k) mine = top;
+            }
+            if (lane < 16) s_top[gw * R + c * 16 + lane] = mine;
+          }
+          named_bar_sync(2 + g, 128);
+          if (j < chunks * 16) {
+            const float top = fmaxf(fmaxf(s_top[j], s_top[R + j]), fmaxf(s_top[2 * R + j], s_top[3 * R + j]));
+            const float old = s_ref[j];
+            const bool moves = top > old + kHeadroom;
+            s_corr[j] = moves ? ex2(old - top) : 1.f;
+            if (moves) s_ref[j] = top;
+          }
+          named_bar_sync(2 + g, 128);
+          if (!first) {
+            wait(&pvdone[g], (n_own - 1) & 1);
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < R / 16; ++c) {
+              if (c >= chunks) break;
+              float corr[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) corr[k] = s_corr[c * 16 + k];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) l2[c * 8 + k].x *= corr[2 * k], l2[c * 8 + k].y *= corr[2 * k + 1];
+#pragma unroll
+              for (int p = 0; p < PC; ++p) {
+                uint32_t u[16];
+                __syncwarp();
+                load16(to + p * R + c * 16, u);
+                wait_loads();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * corr[k]);
+                store16(to + p * R + c * 16, u);
+              }
+            }
+            wait_stores();
+          }
+        }
+        // ---- the weights, once the group's product before has read its own
+        if (n_own > 0) wait(&pvdone[g], (n_own - 1) & 1);
+#pragma unroll
+        for (int c = 0; c < R / 16; ++c) {
+          if (c >= chunks) break;
+          float x[16];
+          scores(c, x);
+          __half2 h[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float a = ex2(x[2 * k] - s_ref[c * 16 + 2 * k] + kHeadroom), b = ex2(x[2 * k + 1] - s_ref[c * 16 + 2 * k + 1] + kHeadroom);
+            l2[c * 8 + k] = fma2(float2{a, b}, float2{inv_v, inv_v}, l2[c * 8 + k]);
+            h[k] = __floats2half2_rn(a, b);
+          }
+#pragma unroll
+          for (int p = 0; p < PC; ++p) {
+            uint32_t out[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t b = half2_to_e4m3x2(h[k]);
+              out[k >> 1] |= b << ((k & 1) * 16);
+              if (p + 1 < PC) h[k] = __hmul2(__hsub2(h[k], from_e4m3x2(b)), __float2half2_rn(16.f));
+            }
+            *reinterpret_cast<uint4*>(pbuf + p * L::kPPiece + chunk_at<R>(j, c)) = make_uint4(out[0], out[1], out[2], out[3]);
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&sfree[g]);
+        fence_async_shared();
+        mbar_arrive(&pready[g]);
+        ++n_own;
+        first = false;
+      }
+      // ---- the segment's end. Every score of it has been read once both groups are here: q is the next one's.
+#pragma unroll
+      for (int c = 0; c < R / 16; ++c) {
+        if (c >= chunks) break;
+        float v[16];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[2 * k] = l2[c * 8 + k].x, v[2 * k + 1] = l2[c * 8 + k].y;
+        const float sum = reduce16(v);
+        if ((lane & 1) == 0) s_top[gw * R + c * 16 + (lane >> 1)] = sum;
+      }
+      if (!first) wait(&pvdone[g], (n_own - 1) & 1);
+      tc_fence_before();
+      named_bar_sync(1, NG * 128);
+      tc_fence_after();
+      const bool more = w.u < T1;
+      if (more) {
+        begin_segment(w);
+        put_q(w.at);
+      }
+      // the groups' states into one
+      if (tid < chunks * 16) {
+        float2 ml[NG];
+        float top = -INFINITY, den = 0.f;
+#pragma unroll
+        for (int k = 0; k < NG; ++k) {
+          const float* sums = reinterpret_cast<const float*>(smem + L::kTop) + k * 4 * R + tid;
+          const float ref = reinterpret_cast<const float*>(smem + L::kRef)[k * R + tid];
+          ml[k] = make_float2(ref == kNone ? -INFINITY : ref - kHeadroom, (sums[0] + sums[R]) + (sums[2 * R] + sums[3 * R]));
+          top = fmaxf(top, ml[k].x);
+        }
+#pragma unroll
+        for (int k = 0; k < NG; ++k) {
+          const float wk = weight_of(ml[k], top);
+          den += wk == 0.f ? 0.f : wk * ml[k].y;
+          reinterpret_cast<float*>(smem + L::kCorr)[k * R + tid] = wk;
+        }
+        s_ml[tid] = make_float2(top, den);
+      }
+      named_bar_sync(1, NG * 128);
+      if (j < R) s_ref[j] = kNone;
+      if (gw * 32 < D) {  // a dim a lane, 16 rows at a time, in turn by the groups
+        const int dim = gw * 32 + lane;
+        float* slot = P.part + (2 * static_cast<size_t>(cta) + (seg_no == 0 ? 0 : 1)) * static_cast<size_t>(P.slot_rows) * (D + 2);
+#pragma unroll 1
+        for (int c = g; c < chunks; c += NG) {
+          float o[16] = {};
+#pragma unroll
+          for (int k2 = 0; k2 < NG; ++k2) {
+            const float* wk = reinterpret_cast<const float*>(smem + L::kCorr) + k2 * R + c * 16;
+            float v[16] = {};
+#pragma unroll
+            for (int p = PC - 1; p >= 0; --p) {
+              uint32_t u[16];
+              __syncwarp();
+              load16(tmem + lanes + L::tO(k2) + p * R + c * 16, u);
+              wait_loads();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] = fmaf(v[k], 0.0625f, __uint_as_float(u[k]));
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (wk[k] != 0.f) o[k] = fmaf(wk[k], v[k], o[k]);  // (a group without a step: whatever its accumulator holds)
+          }
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int row = c * 16 + k;
+            if (row >= live) break;
+            if (whole) {
+              const float den = s_ml[row].y, x = o[k] * (den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den));
+              const int r = new_row(P, row);
+              const size_t at = ((static_cast<size_t>(s) * P.rows_per_seq + r) * P.nq + static_cast<size_t>(kvh) * grp + row - r * grp) * D + dim;
+              static_cast<uint16_t*>(P.out)[at] = static_cast<uint16_t>(pack2<BF16>(x, 0.f));
+            } else {
+              __stcg(slot + static_cast<size_t>(row) * D + dim, o[k]);
+            }
+          }
+        }
+      }
+      if (tid < live && !whole) {
+        float* slot = P.part + (2 * static_cast<size_t>(cta) + (seg_no == 0 ? 0 : 1)) * static_cast<size_t>(P.slot_rows) * (D + 2);
+        __stcg(reinterpret_cast<float2*>(slot + static_cast<size_t>(P.slot_rows) * D) + tid, s_ml[tid]);
+      }
+      tc_fence_before();
+      named_bar_sync(1, NG * 128);  // the buffers are the next segment's
+    }
+  }
+
+  // ---- every product has completed (the issuer waited for them) before the tensor memory goes
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kIssuer) {
+    tmem_relinquish();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, int R, bool BF16>
+int set_attr() {
+  using L = Layout8<D, R, BF16>;
+  static_assert(L::smem(kAttnMaxBatch) <= 232448, "shared memory of a CTA");
+  return static_cast<int>(cudaFuncSetAttribute(paged_attn8_kernel<D, R, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               L::smem(kAttnMaxBatch)));
+}
+template <int D, int R, bool BF16>
+int launch(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
+  using L = Layout8<D, R, BF16>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(n_ctas);
+  cfg.blockDim = dim3(L::kThreads);
+  cfg.dynamicSmemBytes = L::smem(p.batch);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, paged_attn8_kernel<D, R, BF16>, p));
+}
+template <int D, bool BF16>
+int launch_rows(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
+  if (p.rows <= 32) return launch<D, 32, BF16>(p, n_ctas, stream);
+  return p.rows <= 64 ? launch<D, 64, BF16>(p, n_ctas, stream) : launch<D, 128, BF16>(p, n_ctas, stream);
+}
+
+}  // namespace
+
+int paged_attn8_set_attributes() {
+  const int e[] = {set_attr<64, 32, false>(),  set_attr<64, 32, true>(),  set_attr<64, 64, false>(),  set_attr<64, 64, true>(),
+                   set_attr<64, 128, false>(), set_attr<64, 128, true>(), set_attr<128, 32, false>(), set_attr<128, 32, true>(),
+                   set_attr<128, 64, false>(), set_attr<128, 64, true>(), set_attr<128, 128, false>(), set_attr<128, 128, true>()};
+  for (int x : e)
+    if (x != 0) return x;
+  return 0;
+}
+
+int launch_paged_attn8(const PagedAttnParams& p, bool bf16, int n_ctas, cudaStream_t stream) {
+  if (p.batch < 1 || p.batch > kAttnMaxBatch || n_ctas < 1 || n_ctas > kPagedMaxCtas || p.rows > 128)
+    return static_cast<int>(cudaErrorInvalidValue);
+  int e;
+  if (p.d == 128) e = bf16 ? launch_rows<128, true>(p, n_ctas, stream) : launch_rows<128, false>(p, n_ctas, stream);
+  else e = bf16 ? launch_rows<64, true>(p, n_ctas, stream) : launch_rows<64, false>(p, n_ctas, stream);
+  return e != 0 ? e : launch_paged_attn_join(p, bf16, n_ctas, stream);
+}
+
+}  // namespace dfl

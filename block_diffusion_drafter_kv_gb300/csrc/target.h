@@ -91,11 +91,19 @@ struct PagedAttnParams {
   const uint8_t* k_pool;   // this layer's
   const uint8_t* v_pool;
   const uint8_t* scales;   // of an 8-bit cache
-  const int* prefix_len;   // a prefix that all sequences share, or null
+  // A prefix that all sequences share (null: none). The list of tiles then has batch entries for the
+  // sequences' own positions and n_pre for the prefix, pre_rows new rows of the batch each.
+  const int* prefix_len;
   const int* prefix_table; // its row of the page table
+  int n_pre, pre_rows;
+  int slot_rows;           // rows of a partial slot
+  float* state;            // [2: own, prefix][batch * rows_per_seq][nq] rows of d outputs, then of (max, sum)
 };
 // Attention over an 8-bit cache, and with a shared prefix.
 int launch_paged_attn_rows(const PagedAttnParams& p, int dtype, cudaStream_t stream);
+int paged_attn8_set_attributes();
+int launch_paged_attn8(const PagedAttnParams& p, bool bf16, int n_ctas, cudaStream_t stream);
+int launch_paged_attn_join(const PagedAttnParams& p, bool bf16, int n_ctas, cudaStream_t stream);
 int paged_attn_rows(int rows);  // rows of a partial slot: `rows` rounded up to what a kernel variant holds
 int paged_attn_set_attributes();
 int launch_paged_attn(const PagedAttnParams& p, bool bf16, int n_ctas, cudaStream_t stream);
