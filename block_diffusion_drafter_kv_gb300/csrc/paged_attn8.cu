@@ -20,9 +20,11 @@
 // the first row that may see the key. The weights' reference m' is a running maximum of s_j + ev_j, so that
 // w_j <= 256 whatever the scales; p_j is w_j 2^-ev_j (|ev_j| <= 40: no overflow).
 //
-// CTA: one per SM, two softmax groups of 128 threads (one for more than 64 rows) that take alternate steps, each
-// with its own S, P, O and references, a warp that issues the products, a producer warp. Every wait is
-// bounded, as in paged_attn_tc.cu.
+// CTA: one per SM, two softmax groups of 128 threads, a warp that issues the products, a producer warp. The
+// groups take alternate steps, each with its own S, P, O and references; of more than 64 rows both take
+// every step, half of the rows each. Every wait is bounded, as in paged_attn_tc.cu.
+#include <type_traits>
+
 #include "paged_attn.cuh"
 #include "quant.cuh"
 
@@ -32,7 +34,8 @@ namespace {
 
 constexpr int kStepKeys = 128;
 constexpr float kNone = -3e38f;     // a reference where no key has been seen
-constexpr float kHeadroom = 4.f;    // binary orders of the weights at their reference, and by which scores may pass it
+constexpr float kHeadroom = 4.f;    // a reference is set so many binary orders below the largest score,
+constexpr float kMost = 8.f;        // and moves where one passes it by more than this: weights are at most 256
 
 // ---------------------------------------------------------------- descriptors
 DEV void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
@@ -122,6 +125,22 @@ DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
                "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
+DEV bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+DEV float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(*reinterpret_cast<unsigned long long*>(&d))
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+  return d;
+}
 DEV bool has_nan8(uint32_t v) { return (((v & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0; }
 
 // Sums of 16 values over the warp: lane L gets that of value L / 2.
@@ -143,46 +162,48 @@ DEV float reduce16(float (&v)[16]) {
 template <int D, int R, bool BF16>
 struct Layout8 {
   static constexpr int kPieces = BF16 ? 2 : 3;              // of q, and of the weights
-  static constexpr int NG = R <= 64 ? 2 : 1;                // softmax groups
-  static constexpr int kThreads = NG * 128 + 64;
+  static constexpr int SG = R == 32 ? 2 : 1;                // accumulators: one of each softmax group's steps, or one of all
+  static constexpr int RT = R == 32 ? 32 : R / 2;           // rows of a softmax thread
+  static constexpr int NB = R == 128 && !BF16 ? 1 : 2;      // buffers of S and P, taken by the steps in turn
+  static constexpr int kThreads = 256 + 64;
   static constexpr int kOperand = kStepKeys * D;            // K, or V, of a step
-  static constexpr int STAGES = D == 64 ? 8 : R == 32 ? 5 : R == 64 || BF16 ? 4 : 3;
+  static constexpr int STAGES = D == 64 ? (R == 128 ? 6 : 8) : R == 32 ? 5 : R == 64 ? 4 : 3;
   static constexpr int kPPiece = kStepKeys * R;
   static constexpr int kQPiece = R * D;
   static constexpr int kK = 0;
   static constexpr int kV = kK + STAGES * kOperand;
   static constexpr int kP = kV + STAGES * kOperand;
-  static constexpr int kQ = kP + NG * kPieces * kPPiece;
+  static constexpr int kQ = kP + NB * kPieces * kPPiece;
   static constexpr int kSc = kQ + kPieces * kQPiece;        // scales of a step: two tiles' 128 bytes
-  static constexpr int kRef = kSc + STAGES * 256;           // [NG][R] references
-  static constexpr int kGain = kRef + NG * R * 4;           // [R] 1 / the power of two that q was scaled by
-  static constexpr int kCorr = kGain + R * 4;               // [NG][R] factors of a moved reference; weights of the groups at the end
-  static constexpr int kTop = kCorr + NG * R * 4;           // [NG][4][R] warps' maxima; sums at the end
-  static constexpr int kMl = kTop + NG * 4 * R * 4;         // [R] (max, sum)
+  static constexpr int kBase = kSc + STAGES * 256;          // [SG][R] references
+  static constexpr int kGain = kBase + SG * R * 4;          // [R] 1 / the power of two that q was scaled by
+  static constexpr int kCorr = kGain + R * 4;               // [SG][R] factors of a moved reference; weights of the states at the end
+  static constexpr int kTop = kCorr + SG * R * 4;           // [2 groups][4][RT] warps' maxima; sums at the end
+  static constexpr int kMl = kTop + 2 * 4 * RT * 4;         // [R] (max, sum)
   static constexpr int kBar = kMl + R * 8;
-  static constexpr int kBars = 2 * STAGES + 4 * NG + 2;     // full, empty; S ready, free, P ready, PV done [NG]; Q, done
-  static constexpr int kFlags = kBar + kBars * 8;           // [0] abort, [1] TMEM base, [4..19] valid tiles of steps
+  static constexpr int kBars = 2 * STAGES + 4 * NB + 2;     // full, empty; S ready, free, P ready, PV done [NB]; Q, done
+  static constexpr int kFlags = kBar + kBars * 8;           // [0] abort, [1] TMEM base, [2..3] groups' chunks that move, [4..19] valid tiles of steps
   static constexpr int kWarpSums = kFlags + 80;
   static constexpr int kPre = kWarpSums + 64;
   static constexpr int smem(int batch) { return 1024 + kPre + (3 * batch + 1) * 4; }
-  static constexpr uint32_t tS(int g) { return g * R; }     // TMEM columns
-  static constexpr uint32_t tO(int g) { return NG * R + g * kPieces * R; }
-  static_assert(NG * R * (1 + kPieces) <= 512, "tensor memory");
+  static constexpr uint32_t tS(int b) { return b * R; }     // TMEM columns
+  static constexpr uint32_t tO(int sg) { return NB * R + sg * kPieces * R; }
+  static_assert(NB * R + SG * R * kPieces <= 512, "tensor memory");
 };
 
 template <int D, int R, bool BF16>
 __global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_kernel(const __grid_constant__ PagedAttnParams P) {
   using L = Layout8<D, R, BF16>;
-  constexpr int NG = L::NG, STAGES = L::STAGES, PC = L::kPieces;
+  constexpr int SG = L::SG, NB = L::NB, STAGES = L::STAGES, PC = L::kPieces;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
   uint64_t* empty = full + STAGES;
   uint64_t* sready = empty + STAGES;
-  uint64_t* sfree = sready + NG;
-  uint64_t* pready = sfree + NG;
-  uint64_t* pvdone = pready + NG;
-  uint64_t* qready = pvdone + NG;
+  uint64_t* sfree = sready + NB;
+  uint64_t* pready = sfree + NB;
+  uint64_t* pvdone = pready + NB;
+  uint64_t* qready = pvdone + NB;
   uint64_t* mdone = qready + 1;
   volatile int* flag = reinterpret_cast<volatile int*>(smem + L::kFlags);
   volatile int* s_valid = flag + 4;  // bit h: tile h of the step is there; by step mod 16, more than the ring holds
@@ -198,15 +219,15 @@ __global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < NG; ++i) {
+    for (int i = 0; i < NB; ++i) {
       mbar_init(&sready[i], 1);
-      mbar_init(&sfree[i], 128);
-      mbar_init(&pready[i], 128);
+      mbar_init(&sfree[i], 256 / SG);
+      mbar_init(&pready[i], 256 / SG);
       mbar_init(&pvdone[i], 1);
     }
-    mbar_init(qready, NG * 128);
+    mbar_init(qready, 256);
     mbar_init(mdone, 1);
-    flag[0] = 0;
+    flag[0] = flag[2] = flag[3] = 0;
     fence_mbar_init();
     tma_prefetch_desc(&P.kmap);
     tma_prefetch_desc(&P.vmap);
@@ -219,7 +240,7 @@ __global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_
   const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), T));
   const int cta = blockIdx.x;
   if (cta >= G) return;  // the whole CTA, before it holds any tensor memory
-  constexpr int kIssuer = NG * 4, kProducer = NG * 4 + 1;
+  constexpr int kIssuer = 8, kProducer = 9;
   if (warp == kIssuer) tmem_alloc(reinterpret_cast<uint32_t*>(smem + L::kFlags + 4), 512);
   tc_fence_before();
   __syncthreads();
@@ -302,88 +323,100 @@ __global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_
     __syncwarp();
   } else if (warp == kIssuer) {
     // ------------------------------------------------------------------ issuer of the products
-    if (lane == 0) {
-      constexpr uint32_t kQk = idesc_f8(128, R, false, false);
-      auto qk = [&](int i) {  // S^T = K Q^T
-        const int st = i % STAGES, g = i % NG;
-        tc_fence_after();
-        const uint64_t k0 = desc_rows<D>(smem_u32(smem + L::kK + st * L::kOperand), 16);
-        const uint64_t q0 = desc_rows<D>(smem_u32(smem + L::kQ), 16);
-        const uint32_t d = tmem + L::tS(g);
+    // The whole warp walks, one lane issues: descriptors that are the same in every lane are built in
+    // uniform registers, which is where the products take them from.
+    const bool leader = elect_one();
+    auto ready = [](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, test_wait(bar, parity)) != 0; };
+    constexpr uint32_t kQk = idesc_f8(128, R, false, false);
+    const uint64_t k_base = desc_rows<D>(smem_u32(smem + L::kK), 16), q_base = desc_rows<D>(smem_u32(smem + L::kQ), 16);
+    // (with 64 dims the upper half of M is the same dims again, unused)
+    const uint64_t v_base = desc_rows<D>(smem_u32(smem + L::kV), 0), p_base = desc_rows<R>(smem_u32(smem + L::kP), L::kPPiece);
+    auto qk = [&](int st, int b) {  // S^T = K Q^T
+      tc_fence_after();
+      const uint64_t k0 = k_base + (st * L::kOperand >> 4);
+      const uint32_t d = tmem + L::tS(b);
+      if (leader) {
 #pragma unroll
         for (int p = 0; p < PC; ++p)
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk)
-            mma_f8(d, k0 + (kk * 32 >> 4), q0 + ((p * L::kQPiece + kk * 32) >> 4), kQk, p + kk > 0 ? 1u : 0u);
-        tc_commit(&sready[g]);
-      };
-      auto pv = [&](int i, bool first) {  // O^T (+)= V^T P^T. With 64 dims M's upper half are the same dims again, unused.
-        const int st = i % STAGES, g = i % NG;
-        tc_fence_after();
-        const uint64_t v0 = desc_rows<D>(smem_u32(smem + L::kV + st * L::kOperand), 0);
-        const uint64_t p0 = desc_rows<R>(smem_u32(smem + L::kP + g * PC * L::kPPiece), L::kPPiece);
-        constexpr int N1 = PC * R <= 256 ? PC * R : 256, N2 = PC * R - N1;
-        constexpr uint32_t kPv1 = idesc_f8(128, N1, true, true);
+            mma_f8(d, k0 + (kk * 32 >> 4), q_base + ((p * L::kQPiece + kk * 32) >> 4), kQk, p + kk > 0 ? 1u : 0u);
+        tc_commit(&sready[b]);
+      }
+      __syncwarp();
+    };
+    auto pv = [&](int st, int b, bool first) {  // O^T (+)= V^T P^T
+      tc_fence_after();
+      const uint64_t v0 = v_base + (st * L::kOperand >> 4), p0 = p_base + (b * PC * L::kPPiece >> 4);
+      const uint32_t d = tmem + L::tO(SG == 2 ? b : 0), keep = first ? 0u : 1u;
+      constexpr int N1 = PC * R <= 256 ? PC * R : 256, N2 = PC * R - N1;
+      constexpr uint32_t kPv1 = idesc_f8(128, N1, true, true);
+      if (leader) {
 #pragma unroll
         for (int kk = 0; kk < kStepKeys / 32; ++kk) {
-          const uint32_t acc = kk > 0 || !first ? 1u : 0u;
-          mma_f8(tmem + L::tO(g), v0 + (kk * 32 * D >> 4), p0 + (kk * 32 * R >> 4), kPv1, acc);
+          mma_f8(d, v0 + (kk * 32 * D >> 4), p0 + (kk * 32 * R >> 4), kPv1, kk > 0 ? 1u : keep);
           if constexpr (N2 > 0) {
             constexpr uint32_t kPv2 = idesc_f8(128, N2, true, true);
-            mma_f8(tmem + L::tO(g) + N1, v0 + (kk * 32 * D >> 4), p0 + ((N1 / R * L::kPPiece + kk * 32 * R) >> 4), kPv2, acc);
+            mma_f8(d + N1, v0 + (kk * 32 * D >> 4), p0 + ((N1 / R * L::kPPiece + kk * 32 * R) >> 4), kPv2, kk > 0 ? 1u : keep);
           }
         }
-        tc_commit(&pvdone[g]);
+        tc_commit(&pvdone[b]);
         tc_commit(&empty[st]);
-      };
-      // Whichever product's inputs are ready goes next, so that neither waits behind the other's.
-      Walk w{T0, 0, {}};
-      int nqk = 0, npv = 0, segs = 0;
-      int seg_of[8] = {}, last_seg[NG];  // segment of a step, and of the group's last product
-      for (int g = 0; g < NG; ++g) last_seg[g] = -1;
-      uint64_t idle_since = 0;
-      uint32_t spins = 0;
-      bool start = true;
-      while (w.u < T1 || npv < nqk) {
-        bool moved = false;
-        if (w.u < T1 && nqk < npv + 2 * NG) {
-          if (w.left == 0) {
-            begin_segment(w);
-            start = true;
-          }
-          if (test_wait(&full[nqk % STAGES], (nqk / STAGES) & 1) &&
-              (nqk < NG || test_wait(&sfree[nqk % NG], (nqk / NG - 1) & 1)) && (!start || test_wait(qready, segs & 1))) {
-            segs += start;
-            start = false;
-            qk(nqk);
-            seg_of[nqk & 7] = segs;
-            const int cnt = min(2, w.left);
-            w.u += cnt;
-            w.left -= cnt;
-            ++nqk;
-            moved = true;
-          }
+      }
+      __syncwarp();
+    };
+    // Whichever product's inputs are ready goes next, so that neither waits behind the other's.
+    Walk w{T0, 0, {}};
+    int nqk = 0, npv = 0, segs = 0;   // products issued; segments begun
+    int kst = 0, vst = 0;             // their stages
+    uint32_t kph = 0;                 // phase of the next K stage
+    uint32_t newer = 0;               // by step mod 8: whether it is one of its segment's first SG, whose O is new
+    int from_start = 0;
+    uint64_t idle_since = 0;
+    uint32_t spins = 0;
+    bool start = true;
+    while (w.u < T1 || npv < nqk) {
+      bool moved = false;
+      if (w.u < T1 && nqk < npv + 2 * NB) {
+        if (w.left == 0) {
+          begin_segment(w);
+          start = true;
         }
-        if (npv < nqk && test_wait(&pready[npv % NG], (npv / NG) & 1)) {
-          const int seg = seg_of[npv & 7];
-          pv(npv, last_seg[npv % NG] != seg);
-          last_seg[npv % NG] = seg;
-          ++npv;
+        const int b = nqk % NB;
+        if (ready(&full[kst], kph) && (nqk < NB || ready(&sfree[b], (nqk / NB - 1) & 1)) && (!start || ready(qready, segs & 1))) {
+          qk(kst, b);
+          if (start) ++segs, from_start = 0;
+          start = false;
+          newer = (newer & ~(1u << (nqk & 7))) | (from_start < SG ? 1u : 0u) << (nqk & 7);
+          ++from_start;
+          const int cnt = min(2, w.left);
+          w.u += cnt;
+          w.left -= cnt;
+          ++nqk;
+          if (++kst == STAGES) kst = 0, kph ^= 1;
           moved = true;
         }
-        // (reading the timer takes some 600 cycles: only where nothing has moved for a while)
-        if (moved) {
-          spins = 0;
-        } else if ((++spins & 1023u) == 0) {
-          const uint64_t now = globaltimer_ns();
-          if (spins == 1024) idle_since = now;
-          if (flag[0] || now - idle_since > WL) {
-            if (!flag[0]) raise_flag(P.err, kDevTimeout);
-            flag[0] = 1;
-            break;
-          }
+      }
+      if (npv < nqk && ready(&pready[npv % NB], (npv / NB) & 1)) {
+        pv(vst, npv % NB, newer >> (npv & 7) & 1);
+        ++npv;
+        if (++vst == STAGES) vst = 0;
+        moved = true;
+      }
+      // (reading the timer takes some 600 cycles: only where nothing has moved for a while)
+      if (moved) {
+        spins = 0;
+      } else if ((++spins & 1023u) == 0) {
+        const uint64_t now = __shfl_sync(0xffffffffu, globaltimer_ns(), 0);
+        if (spins == 1024) idle_since = now;
+        if (__any_sync(0xffffffffu, flag[0] != 0) || now - idle_since > WL) {
+          if (lane == 0 && !flag[0]) raise_flag(P.err, kDevTimeout);
+          flag[0] = 1;
+          break;
         }
       }
+    }
+    if (leader) {
       tc_commit(mdone);
       if (!mbar_wait(mdone, 0, WL)) raise_flag(P.err, kDevTimeout);
     }
@@ -391,14 +424,16 @@ __global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_
   } else {
     // ------------------------------------------------------------------ softmax and output
     const int g = tid >> 7, j = tid & 127, gw = warp & 3;  // group, key of the step, warp of the group
+    const int sg = SG == 2 ? g : 0, row0 = SG == 2 ? 0 : g * L::RT;  // the state that it works on, its first row
+    constexpr int RT = L::RT, CT = RT / 16, CH = 2;
     const uint32_t lanes = static_cast<uint32_t>(gw * 32) << 16;
-    const uint32_t ts = tmem + lanes + L::tS(g), to = tmem + lanes + L::tO(g);
-    float* s_ref = reinterpret_cast<float*>(smem + L::kRef) + g * R;
+    const uint32_t to = tmem + lanes + L::tO(sg) + row0;
+    float* s_base = reinterpret_cast<float*>(smem + L::kBase) + sg * R + row0;
     float* s_gain = reinterpret_cast<float*>(smem + L::kGain);
-    float* s_corr = reinterpret_cast<float*>(smem + L::kCorr) + g * R;
-    float* s_top = reinterpret_cast<float*>(smem + L::kTop) + g * 4 * R;
+    float* s_corr = reinterpret_cast<float*>(smem + L::kCorr) + sg * R + row0;
+    float* s_top = reinterpret_cast<float*>(smem + L::kTop) + g * 4 * RT;
     float2* s_ml = reinterpret_cast<float2*>(smem + L::kMl);
-    uint8_t* pbuf = smem + L::kP + g * PC * L::kPPiece;
+    int* s_moves = const_cast<int*>(flag) + 2 + g;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!mbar_try_wait(bar, parity)) wait_long(bar, parity, flag, P.err, WL);
       __syncwarp();
@@ -407,7 +442,7 @@ __global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_
     auto put_q = [&](const Place& p) {
       constexpr int kParts = D / 16;  // threads of a row
       const int live = s_new[p.s] * grp, rows = (live + 15) & ~15;
-      for (int item = tid; item < rows * kParts; item += NG * 128) {
+      for (int item = tid; item < rows * kParts; item += 256) {
         const int row = item / kParts, part = item % kParts;
         uint4 in[2] = {};
         if (row < live) {
@@ -451,28 +486,31 @@ __global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_
       mbar_arrive(qready);
     };
 
-    float2 l2[R / 2];  // the key's part of every row's sum
-    int i = 0, n_own = 0, seg_no = 0;  // step; steps of this group
+    float2 l2[RT / 2];  // the key's part of every row's sum
+    int i = 0, seg_no = 0;  // step
     Walk w{T0, 0, {}};
     begin_segment(w);
     put_q(w.at);
-    if (j < R) s_ref[j] = kNone;
-    named_bar_sync(1, NG * 128);
+    if (j < RT) s_base[j] = kNone;
+    named_bar_sync(1, 256);
     for (; w.u < T1; ++seg_no) {
       const int s = w.at.s, kvh = w.at.g, t0 = w.at.t;
       const bool whole = t0 == 0 && w.left == w.at.nt;
       const int len = s_len[s], n_new = s_new[s], nk = len + n_new;
-      const int live = n_new * grp, chunks = (live + 15) >> 4;
+      const int live = n_new * grp, all_chunks = (live + 15) >> 4;
+      const int chunks = max(0, min(CT, all_chunks - row0 / 16));  // of 16 rows, of this thread
 #pragma unroll
-      for (int k = 0; k < R / 2; ++k) l2[k] = {0.f, 0.f};
-      bool first = true;  // of the group's steps in the segment
+      for (int k = 0; k < RT / 2; ++k) l2[k] = {0.f, 0.f};
+      int before = -1;  // the step before of the same accumulator in the segment
       for (; w.left > 0; ++i) {
         const int cnt = min(2, w.left), t = w.at.t;
         w.u += cnt;
         w.left -= cnt;
         w.at.t += cnt;
-        if (NG == 2 && (i & 1) != g) continue;
-        const int st = i % STAGES;
+        if (SG == 2 && (i & 1) != g) continue;
+        const int st = i % STAGES, b = i % NB;
+        const uint32_t ts = tmem + lanes + L::tS(b) + row0;
+        uint8_t* pbuf = smem + L::kP + b * PC * L::kPPiece;
         wait(&full[st], (i / STAGES) & 1);
         // the thread's key: its scales, and the first row that sees it
         const int valid = s_valid[i & 15];
@@ -483,7 +521,7 @@ __global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_
         const float f = P.scale_log2 * scale_value(kb);
         float ev = vb == kScaleNan ? __uint_as_float(0x7fc00000u) : static_cast<float>(static_cast<int>(vb) - kScaleBias);
         const float inv_v = scale_value(254u - min(vb, 253u));
-        const int rmin = !alive ? R : key <= len ? 0 : (key - len) * grp;
+        const int rmin = (!alive ? R : key <= len ? 0 : (key - len) * grp) - row0;
         const bool edge = valid != 3 || (t + 2) * kKeys > len + 1;  // some row may not see some key of the step (the same for all threads)
         if (edge) {
           // Values that no row sees are cleared (0 * NaN is NaN); a key that some rows see and that has a NaN
@@ -500,167 +538,196 @@ __global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_
             if (nan) ev = __uint_as_float(0x7fc00000u);
             clear = nan;
           }
-          if (clear)
+          if (SG == 1) named_bar_sync(1, 256);  // (both groups have looked)
+          if (clear && (SG == 2 || g == 0))
 #pragma unroll
             for (int ch = 0; ch < D / 16; ++ch) vrow[ch] = make_uint4(0, 0, 0, 0);
         }
-        wait(&sready[g], n_own & 1);
+        wait(&sready[b], (i / NB) & 1);
         tc_fence_after();
-        // s_j + ev_j of 16 rows; what a row does not see is -inf
-        auto scores = [&](int c, float (&x)[16]) {
-          uint32_t u[16];
-          __syncwarp();
-          load16(ts + c * 16, u);
-          float gain[16];
+        auto part = [&](auto from) {
+          constexpr int c0 = decltype(from)::value;
+        // 32 rows at a time (registers): s_j + ev_j; what a row does not see is -inf
+        float2 x[CH * 8];
+        {
+          uint32_t u[CH * 16];
+#pragma unroll
+          for (int c = 0; c < CH; ++c)
+            if (c0 + c < chunks) load16(ts + (c0 + c) * 16, *reinterpret_cast<uint32_t(*)[16]>(u + c * 16));
+          wait_loads();
+          if (c0 + CH >= CT) {
+            tc_fence_before();
+            mbar_arrive(&sfree[b]);
+          }
+#pragma unroll
+          for (int k = 0; k < CH * 8; ++k) x[k] = {__uint_as_float(u[2 * k]), __uint_as_float(u[2 * k + 1])};
+        }
+        bool any = false;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          if (c0 + c >= chunks) break;
+          float past = -INFINITY;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float4 v = reinterpret_cast<const float4*>(s_gain)[c * 4 + k];
-            gain[4 * k] = v.x, gain[4 * k + 1] = v.y, gain[4 * k + 2] = v.z, gain[4 * k + 3] = v.w;
+            const float4 gain = reinterpret_cast<const float4*>(s_gain + row0)[(c0 + c) * 4 + k], base = reinterpret_cast<const float4*>(s_base)[(c0 + c) * 4 + k];
+            float2* y = x + c * 8 + 2 * k;
+            y[0] = fma2(y[0], mul2(float2{gain.x, gain.y}, float2{f, f}), float2{ev, ev});
+            y[1] = fma2(y[1], mul2(float2{gain.z, gain.w}, float2{f, f}), float2{ev, ev});
+            if (edge) {
+              const int r = (c0 + c) * 16 + 4 * k;
+              y[0].x = r < rmin ? -INFINITY : y[0].x, y[0].y = r + 1 < rmin ? -INFINITY : y[0].y;
+              y[1].x = r + 2 < rmin ? -INFINITY : y[1].x, y[1].y = r + 3 < rmin ? -INFINITY : y[1].y;
+            }
+            const float2 d0 = add2(y[0], float2{-base.x, -base.y}), d1 = add2(y[1], float2{-base.z, -base.w});
+            past = fmaxf(past, fmaxf(fmaxf(d0.x, d0.y), fmaxf(d1.x, d1.y)));
           }
-          wait_loads();
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float v = __fmaf_rn(__uint_as_float(u[k]), __fmul_rn(f, gain[k]), ev);
-            x[k] = edge && c * 16 + k < rmin ? -INFINITY : v;
+          if (__any_sync(0xffffffffu, past > kMost)) {
+            any = true;
+            if (lane == 0) atomicOr(s_moves, 1 << (c0 + c));
           }
-        };
-        float past = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-          float x[16];
-          scores(c, x);
-#pragma unroll
-          for (int k = 0; k < 16; ++k) past = fmaxf(past, x[k] - s_ref[c * 16 + k]);
         }
-        if (named_bar_any(2 + g, 128, past > kHeadroom)) {
-          // ---- references that move: the rows' maxima over the group, then O and the sums
-#pragma unroll 1
-          for (int c = 0; c < chunks; ++c) {
-            float x[16];
-            scores(c, x);
+        if (named_bar_any(2 + g, 128, any)) {
+          // ---- references that move, 16 rows at a time: the rows' maxima over the group, then O and the sums
+          const int moves = *const_cast<volatile int*>(s_moves);
+#pragma unroll
+          for (int c = 0; c < CH; ++c) {
+            if (!(moves >> (c0 + c) & 1)) continue;
             float mine = 0.f;
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-              const float top = warp_max(x[k]);
+              const float top = warp_max(k & 1 ? x[c * 8 + k / 2].y : x[c * 8 + k / 2].x);
               if (lane == k) mine = top;
             }
-            if (lane < 16) s_top[gw * R + c * 16 + lane] = mine;
+            if (lane < 16) s_top[gw * RT + (c0 + c) * 16 + lane] = mine;
           }
           named_bar_sync(2 + g, 128);
-          if (j < chunks * 16) {
-            const float top = fmaxf(fmaxf(s_top[j], s_top[R + j]), fmaxf(s_top[2 * R + j], s_top[3 * R + j]));
-            const float old = s_ref[j];
-            const bool moves = top > old + kHeadroom;
-            s_corr[j] = moves ? ex2(old - top) : 1.f;
-            if (moves) s_ref[j] = top;
+          if (j == 0) *s_moves = 0;
+          if (j < RT && (moves >> (j >> 4) & 1)) {
+            const float top = fmaxf(fmaxf(s_top[j], s_top[RT + j]), fmaxf(s_top[2 * RT + j], s_top[3 * RT + j]));
+            const float old = s_base[j], now = top - kHeadroom;
+            const bool up = top - old > kMost;
+            s_corr[j] = up ? ex2(old - now) : 1.f;
+            if (up) s_base[j] = now;
           }
           named_bar_sync(2 + g, 128);
-          if (!first) {
-            wait(&pvdone[g], (n_own - 1) & 1);
+          if (before >= 0) {
+            wait(&pvdone[before % NB], (before / NB) & 1);
             tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < R / 16; ++c) {
-              if (c >= chunks) break;
+            for (int c = 0; c < CH; ++c) {
+              if (!(moves >> (c0 + c) & 1)) continue;
               float corr[16];
 #pragma unroll
-              for (int k = 0; k < 16; ++k) corr[k] = s_corr[c * 16 + k];
+              for (int k = 0; k < 4; ++k) {
+                const float4 v = reinterpret_cast<const float4*>(s_corr)[(c0 + c) * 4 + k];
+                corr[4 * k] = v.x, corr[4 * k + 1] = v.y, corr[4 * k + 2] = v.z, corr[4 * k + 3] = v.w;
+              }
 #pragma unroll
-              for (int k = 0; k < 8; ++k) l2[c * 8 + k].x *= corr[2 * k], l2[c * 8 + k].y *= corr[2 * k + 1];
+              for (int k = 0; k < 8; ++k) l2[(c0 + c) * 8 + k].x *= corr[2 * k], l2[(c0 + c) * 8 + k].y *= corr[2 * k + 1];
 #pragma unroll
               for (int p = 0; p < PC; ++p) {
                 uint32_t u[16];
                 __syncwarp();
-                load16(to + p * R + c * 16, u);
+                load16(to + p * R + (c0 + c) * 16, u);
                 wait_loads();
 #pragma unroll
                 for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * corr[k]);
-                store16(to + p * R + c * 16, u);
+                store16(to + p * R + (c0 + c) * 16, u);
               }
             }
             wait_stores();
           }
         }
-        // ---- the weights, once the group's product before has read its own
-        if (n_own > 0) wait(&pvdone[g], (n_own - 1) & 1);
+        // ---- the weights, once the last product from the buffer has read its own
+        if (c0 == 0 && i >= NB) wait(&pvdone[b], (i / NB - 1) & 1);
 #pragma unroll
-        for (int c = 0; c < R / 16; ++c) {
-          if (c >= chunks) break;
-          float x[16];
-          scores(c, x);
+        for (int c = 0; c < CH; ++c) {
+          if (c0 + c >= chunks) break;
           __half2 h[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float a = ex2(x[2 * k] - s_ref[c * 16 + 2 * k] + kHeadroom), b = ex2(x[2 * k + 1] - s_ref[c * 16 + 2 * k + 1] + kHeadroom);
-            l2[c * 8 + k] = fma2(float2{a, b}, float2{inv_v, inv_v}, l2[c * 8 + k]);
-            h[k] = __floats2half2_rn(a, b);
+          for (int k = 0; k < 4; ++k) {
+            const float4 base = reinterpret_cast<const float4*>(s_base)[(c0 + c) * 4 + k];
+            const int at = c * 8 + 2 * k;
+            const float2 d0 = add2(x[at], float2{-base.x, -base.y}), d1 = add2(x[at + 1], float2{-base.z, -base.w});
+            const float2 w0 = {ex2(d0.x), ex2(d0.y)}, w1 = {ex2(d1.x), ex2(d1.y)};
+            l2[c0 * 8 + at] = fma2(w0, float2{inv_v, inv_v}, l2[c0 * 8 + at]);
+            l2[c0 * 8 + at + 1] = fma2(w1, float2{inv_v, inv_v}, l2[c0 * 8 + at + 1]);
+            h[2 * k] = __floats2half2_rn(w0.x, w0.y);
+            h[2 * k + 1] = __floats2half2_rn(w1.x, w1.y);
           }
 #pragma unroll
           for (int p = 0; p < PC; ++p) {
-            uint32_t out[4] = {0, 0, 0, 0};
+            uint32_t out[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint32_t b = half2_to_e4m3x2(h[k]);
-              out[k >> 1] |= b << ((k & 1) * 16);
-              if (p + 1 < PC) h[k] = __hmul2(__hsub2(h[k], from_e4m3x2(b)), __float2half2_rn(16.f));
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t b0 = half2_to_e4m3x2(h[2 * k]), b1 = half2_to_e4m3x2(h[2 * k + 1]);
+              out[k] = b0 | b1 << 16;
+              if (p + 1 < PC) {
+                h[2 * k] = __hmul2(__hsub2(h[2 * k], from_e4m3x2(b0)), __float2half2_rn(16.f));
+                h[2 * k + 1] = __hmul2(__hsub2(h[2 * k + 1], from_e4m3x2(b1)), __float2half2_rn(16.f));
+              }
             }
-            *reinterpret_cast<uint4*>(pbuf + p * L::kPPiece + chunk_at<R>(j, c)) = make_uint4(out[0], out[1], out[2], out[3]);
+            *reinterpret_cast<uint4*>(pbuf + p * L::kPPiece + chunk_at<R>(j, row0 / 16 + c0 + c)) = make_uint4(out[0], out[1], out[2], out[3]);
           }
         }
-        tc_fence_before();
-        mbar_arrive(&sfree[g]);
+        };
+        part(std::integral_constant<int, 0>());
+        if constexpr (CT > CH) {
+          if (chunks > CH) part(std::integral_constant<int, CH>());
+          else tc_fence_before(), mbar_arrive(&sfree[b]);
+        }
         fence_async_shared();
-        mbar_arrive(&pready[g]);
-        ++n_own;
-        first = false;
+        tc_fence_before();
+        mbar_arrive(&pready[b]);
+        before = i;
       }
       // ---- the segment's end. Every score of it has been read once both groups are here: q is the next one's.
 #pragma unroll
-      for (int c = 0; c < R / 16; ++c) {
+      for (int c = 0; c < CT; ++c) {
         if (c >= chunks) break;
         float v[16];
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[2 * k] = l2[c * 8 + k].x, v[2 * k + 1] = l2[c * 8 + k].y;
         const float sum = reduce16(v);
-        if ((lane & 1) == 0) s_top[gw * R + c * 16 + (lane >> 1)] = sum;
+        if ((lane & 1) == 0) s_top[gw * RT + c * 16 + (lane >> 1)] = sum;
       }
-      if (!first) wait(&pvdone[g], (n_own - 1) & 1);
+      if (before >= 0) wait(&pvdone[before % NB], (before / NB) & 1);
       tc_fence_before();
-      named_bar_sync(1, NG * 128);
+      named_bar_sync(1, 256);
       tc_fence_after();
-      const bool more = w.u < T1;
-      if (more) {
+      if (w.u < T1) {
         begin_segment(w);
         put_q(w.at);
       }
-      // the groups' states into one
-      if (tid < chunks * 16) {
-        float2 ml[NG];
+      // the states into one
+      if (tid < all_chunks * 16) {
+        float2 ml[SG];
         float top = -INFINITY, den = 0.f;
 #pragma unroll
-        for (int k = 0; k < NG; ++k) {
-          const float* sums = reinterpret_cast<const float*>(smem + L::kTop) + k * 4 * R + tid;
-          const float ref = reinterpret_cast<const float*>(smem + L::kRef)[k * R + tid];
-          ml[k] = make_float2(ref == kNone ? -INFINITY : ref - kHeadroom, (sums[0] + sums[R]) + (sums[2 * R] + sums[3 * R]));
+        for (int k = 0; k < SG; ++k) {
+          const float* sums = reinterpret_cast<const float*>(smem + L::kTop) + (SG == 2 ? k * 4 * RT + tid : tid / RT * 4 * RT + tid % RT);
+          const float base = reinterpret_cast<const float*>(smem + L::kBase)[k * R + tid];
+          ml[k] = make_float2(base == kNone ? -INFINITY : base, (sums[0] + sums[RT]) + (sums[2 * RT] + sums[3 * RT]));
           top = fmaxf(top, ml[k].x);
         }
 #pragma unroll
-        for (int k = 0; k < NG; ++k) {
+        for (int k = 0; k < SG; ++k) {
           const float wk = weight_of(ml[k], top);
           den += wk == 0.f ? 0.f : wk * ml[k].y;
           reinterpret_cast<float*>(smem + L::kCorr)[k * R + tid] = wk;
         }
         s_ml[tid] = make_float2(top, den);
       }
-      named_bar_sync(1, NG * 128);
-      if (j < R) s_ref[j] = kNone;
+      named_bar_sync(1, 256);
+      if (j < RT) s_base[j] = kNone;
+      float* slot = P.part + (2 * static_cast<size_t>(cta) + (seg_no == 0 ? 0 : 1)) * static_cast<size_t>(P.slot_rows) * (D + 2);
       if (gw * 32 < D) {  // a dim a lane, 16 rows at a time, in turn by the groups
         const int dim = gw * 32 + lane;
-        float* slot = P.part + (2 * static_cast<size_t>(cta) + (seg_no == 0 ? 0 : 1)) * static_cast<size_t>(P.slot_rows) * (D + 2);
 #pragma unroll 1
-        for (int c = g; c < chunks; c += NG) {
+        for (int c = g; c < all_chunks; c += 2) {
           float o[16] = {};
 #pragma unroll
-          for (int k2 = 0; k2 < NG; ++k2) {
+          for (int k2 = 0; k2 < SG; ++k2) {
             const float* wk = reinterpret_cast<const float*>(smem + L::kCorr) + k2 * R + c * 16;
             float v[16] = {};
 #pragma unroll
@@ -674,29 +741,26 @@ __global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_
             }
 #pragma unroll
             for (int k = 0; k < 16; ++k)
-              if (wk[k] != 0.f) o[k] = fmaf(wk[k], v[k], o[k]);  // (a group without a step: whatever its accumulator holds)
+              if (wk[k] != 0.f) o[k] = fmaf(wk[k], v[k], o[k]);  // (a state without a step: whatever its accumulator holds)
           }
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const int row = c * 16 + k;
             if (row >= live) break;
             if (whole) {
-              const float den = s_ml[row].y, x = o[k] * (den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den));
+              const float den = s_ml[row].y, y = o[k] * (den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den));
               const int r = new_row(P, row);
               const size_t at = ((static_cast<size_t>(s) * P.rows_per_seq + r) * P.nq + static_cast<size_t>(kvh) * grp + row - r * grp) * D + dim;
-              static_cast<uint16_t*>(P.out)[at] = static_cast<uint16_t>(pack2<BF16>(x, 0.f));
+              static_cast<uint16_t*>(P.out)[at] = static_cast<uint16_t>(pack2<BF16>(y, 0.f));
             } else {
               __stcg(slot + static_cast<size_t>(row) * D + dim, o[k]);
             }
           }
         }
       }
-      if (tid < live && !whole) {
-        float* slot = P.part + (2 * static_cast<size_t>(cta) + (seg_no == 0 ? 0 : 1)) * static_cast<size_t>(P.slot_rows) * (D + 2);
-        __stcg(reinterpret_cast<float2*>(slot + static_cast<size_t>(P.slot_rows) * D) + tid, s_ml[tid]);
-      }
+      if (tid < live && !whole) __stcg(reinterpret_cast<float2*>(slot + static_cast<size_t>(P.slot_rows) * D) + tid, s_ml[tid]);
       tc_fence_before();
-      named_bar_sync(1, NG * 128);  // the buffers are the next segment's
+      named_bar_sync(1, 256);  // the buffers are the next segment's
     }
   }
 
