@@ -20,9 +20,9 @@
 // the first row that may see the key. The weights' reference m' is a running maximum of s_j + ev_j, so that
 // w_j <= 256 whatever the scales; p_j is w_j 2^-ev_j (|ev_j| <= 40: no overflow).
 //
-// CTA: one per SM, two softmax groups of 128 threads, a warp that issues the products, a producer warp. The
-// groups take alternate steps, each with its own S, P, O and references; of more than 64 rows both take
-// every step, half of the rows each. Every wait is bounded, as in paged_attn_tc.cu.
+// CTA: one per SM, four softmax groups of 128 threads, a warp that issues the products, a producer warp. Of at
+// most 16 rows each group takes every fourth step, with an accumulator and references of its own; of more
+// the groups share a step, some of the rows each. Every wait is bounded, as in paged_attn_tc.cu.
 #include <type_traits>
 
 #include "paged_attn.cuh"
@@ -33,9 +33,9 @@ namespace dfl {
 namespace {
 
 constexpr int kStepKeys = 128;
-constexpr float kNone = -3e38f;     // a reference where no key has been seen
+constexpr float kNone = 3e38f;      // the negative of a reference where no key has been seen
 constexpr float kHeadroom = 4.f;    // a reference is set so many binary orders below the largest score,
-constexpr float kMost = 8.f;        // and moves where one passes it by more than this: weights are at most 256
+constexpr float kMost = 256.f;      // and moves where a weight passes this
 
 // ---------------------------------------------------------------- descriptors
 DEV void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
@@ -83,6 +83,12 @@ DEV void store16(uint32_t taddr, const uint32_t (&r)[16]) {
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+DEV void load4(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr)
+               : "memory");
 }
 DEV void wait_loads() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 DEV void wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -158,16 +164,16 @@ DEV float reduce16(float (&v)[16]) {
   return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
-// D: head dim; R: rows of a problem that fit (32, 64, 128).
-template <int D, int R, bool BF16>
+// D: head dim; R: rows of a problem that the buffers hold (32, 64, 128); PH: steps that the four softmax groups
+// work on at a time (4: at most 16 rows, a step a group; 2: at most 32 rows, two groups a step; 1: all of them).
+template <int D, int R, int PH, bool BF16>
 struct Layout8 {
   static constexpr int kPieces = BF16 ? 2 : 3;              // of q, and of the weights
-  static constexpr int SG = R == 32 ? 2 : 1;                // accumulators: one of each softmax group's steps, or one of all
-  static constexpr int RT = R == 32 ? 32 : R / 2;           // rows of a softmax thread
-  static constexpr int NB = R == 128 && !BF16 ? 1 : 2;      // buffers of S and P, taken by the steps in turn
-  static constexpr int kThreads = 256 + 64;
+  static constexpr int RT = PH == 1 ? R / 4 : 16;           // rows of a softmax thread
+  static constexpr int NB = PH > 1 ? PH : R == 128 && !BF16 ? 1 : 2;  // buffers of S and P, taken by the steps in turn
+  static constexpr int kThreads = 512 + 64;
   static constexpr int kOperand = kStepKeys * D;            // K, or V, of a step
-  static constexpr int STAGES = D == 64 ? (R == 128 ? 6 : 8) : R == 32 ? 5 : R == 64 ? 4 : 3;
+  static constexpr int STAGES = D == 64 ? (R == 128 ? 6 : 8) : R == 128 ? 3 : R == 64 || !BF16 ? 4 : 5;
   static constexpr int kPPiece = kStepKeys * R;
   static constexpr int kQPiece = R * D;
   static constexpr int kK = 0;
@@ -175,26 +181,27 @@ struct Layout8 {
   static constexpr int kP = kV + STAGES * kOperand;
   static constexpr int kQ = kP + NB * kPieces * kPPiece;
   static constexpr int kSc = kQ + kPieces * kQPiece;        // scales of a step: two tiles' 128 bytes
-  static constexpr int kBase = kSc + STAGES * 256;          // [SG][R] references
-  static constexpr int kGain = kBase + SG * R * 4;          // [R] 1 / the power of two that q was scaled by
-  static constexpr int kCorr = kGain + R * 4;               // [SG][R] factors of a moved reference; weights of the states at the end
-  static constexpr int kTop = kCorr + SG * R * 4;           // [2 groups][4][RT] warps' maxima; sums at the end
-  static constexpr int kMl = kTop + 2 * 4 * RT * 4;         // [R] (max, sum)
+  static constexpr int kBase = kSc + STAGES * 256;          // [PH][R] references, negative
+  static constexpr int kGain = kBase + PH * R * 4;          // [R] 1 / the power of two that q was scaled by
+  static constexpr int kCorr = kGain + R * 4;               // [PH][R] factors of a moved reference; weights of the states at the end
+  static constexpr int kTop = kCorr + PH * R * 4;           // [4 groups][4 warps][RT] warps' maxima; sums at the end
+  static constexpr int kMl = kTop + 4 * 4 * RT * 4;         // [R] (max, sum)
   static constexpr int kBar = kMl + R * 8;
   static constexpr int kBars = 2 * STAGES + 4 * NB + 2;     // full, empty; S ready, free, P ready, PV done [NB]; Q, done
-  static constexpr int kFlags = kBar + kBars * 8;           // [0] abort, [1] TMEM base, [2..3] groups' chunks that move, [4..19] valid tiles of steps
+  static constexpr int kFlags = kBar + kBars * 8;           // [0] abort, [1] TMEM base, [4..19] valid tiles of steps
   static constexpr int kWarpSums = kFlags + 80;
-  static constexpr int kPre = kWarpSums + 64;
+  static constexpr int kPre = kWarpSums + 128;
   static constexpr int smem(int batch) { return 1024 + kPre + (3 * batch + 1) * 4; }
   static constexpr uint32_t tS(int b) { return b * R; }     // TMEM columns
-  static constexpr uint32_t tO(int sg) { return NB * R + sg * kPieces * R; }
-  static_assert(NB * R + SG * R * kPieces <= 512, "tensor memory");
+  static constexpr uint32_t tO(int ph) { return NB * R + ph * kPieces * R; }
+  static_assert(NB * R + PH * R * kPieces <= 512, "tensor memory");
+  static_assert(kThreads <= 32 * 32 && 4 * RT / PH <= R, "groups");
 };
 
-template <int D, int R, bool BF16>
-__global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_kernel(const __grid_constant__ PagedAttnParams P) {
-  using L = Layout8<D, R, BF16>;
-  constexpr int SG = L::SG, NB = L::NB, STAGES = L::STAGES, PC = L::kPieces;
+template <int D, int R, int PH, bool BF16>
+__global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_attn8_kernel(const __grid_constant__ PagedAttnParams P) {
+  using L = Layout8<D, R, PH, BF16>;
+  constexpr int NB = L::NB, STAGES = L::STAGES, PC = L::kPieces;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
@@ -221,13 +228,13 @@ __global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_
     }
     for (int i = 0; i < NB; ++i) {
       mbar_init(&sready[i], 1);
-      mbar_init(&sfree[i], 256 / SG);
-      mbar_init(&pready[i], 256 / SG);
+      mbar_init(&sfree[i], 512 / PH);
+      mbar_init(&pready[i], 512 / PH);
       mbar_init(&pvdone[i], 1);
     }
-    mbar_init(qready, 256);
+    mbar_init(qready, 512);
     mbar_init(mdone, 1);
-    flag[0] = flag[2] = flag[3] = 0;
+    flag[0] = 0;
     fence_mbar_init();
     tma_prefetch_desc(&P.kmap);
     tma_prefetch_desc(&P.vmap);
@@ -240,7 +247,7 @@ __global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_
   const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), T));
   const int cta = blockIdx.x;
   if (cta >= G) return;  // the whole CTA, before it holds any tensor memory
-  constexpr int kIssuer = 8, kProducer = 9;
+  constexpr int kIssuer = 16, kProducer = 17;
   if (warp == kIssuer) tmem_alloc(reinterpret_cast<uint32_t*>(smem + L::kFlags + 4), 512);
   tc_fence_before();
   __syncthreads();
@@ -348,7 +355,7 @@ __global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_
     auto pv = [&](int st, int b, bool first) {  // O^T (+)= V^T P^T
       tc_fence_after();
       const uint64_t v0 = v_base + (st * L::kOperand >> 4), p0 = p_base + (b * PC * L::kPPiece >> 4);
-      const uint32_t d = tmem + L::tO(SG == 2 ? b : 0), keep = first ? 0u : 1u;
+      const uint32_t d = tmem + L::tO(PH > 1 ? b : 0), keep = first ? 0u : 1u;
       constexpr int N1 = PC * R <= 256 ? PC * R : 256, N2 = PC * R - N1;
       constexpr uint32_t kPv1 = idesc_f8(128, N1, true, true);
       if (leader) {
@@ -370,7 +377,7 @@ __global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_
     int nqk = 0, npv = 0, segs = 0;   // products issued; segments begun
     int kst = 0, vst = 0;             // their stages
     uint32_t kph = 0;                 // phase of the next K stage
-    uint32_t newer = 0;               // by step mod 8: whether it is one of its segment's first SG, whose O is new
+    uint32_t newer = 0;               // by step mod 8: whether it is one of its segment's first PH, whose O is new
     int from_start = 0;
     uint64_t idle_since = 0;
     uint32_t spins = 0;
@@ -387,7 +394,7 @@ __global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_
           qk(kst, b);
           if (start) ++segs, from_start = 0;
           start = false;
-          newer = (newer & ~(1u << (nqk & 7))) | (from_start < SG ? 1u : 0u) << (nqk & 7);
+          newer = (newer & ~(1u << (nqk & 7))) | (from_start < PH ? 1u : 0u) << (nqk & 7);
           ++from_start;
           const int cnt = min(2, w.left);
           w.u += cnt;
@@ -423,17 +430,15 @@ __global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_
     __syncwarp();
   } else {
     // ------------------------------------------------------------------ softmax and output
-    const int g = tid >> 7, j = tid & 127, gw = warp & 3;  // group, key of the step, warp of the group
-    const int sg = SG == 2 ? g : 0, row0 = SG == 2 ? 0 : g * L::RT;  // the state that it works on, its first row
-    constexpr int RT = L::RT, CT = RT / 16, CH = 2;
+    const int g = tid >> 7, j = tid & 127, gw = warp & 3;    // group, key of the step, warp of the group
+    const int ph = g & (PH - 1), row0 = g / PH * L::RT;      // the accumulator that it works on, its first row
+    constexpr int RT = L::RT;
     const uint32_t lanes = static_cast<uint32_t>(gw * 32) << 16;
-    const uint32_t to = tmem + lanes + L::tO(sg) + row0;
-    float* s_base = reinterpret_cast<float*>(smem + L::kBase) + sg * R + row0;
+    float* s_base = reinterpret_cast<float*>(smem + L::kBase) + ph * R + row0;
     float* s_gain = reinterpret_cast<float*>(smem + L::kGain);
-    float* s_corr = reinterpret_cast<float*>(smem + L::kCorr) + sg * R + row0;
+    float* s_corr = reinterpret_cast<float*>(smem + L::kCorr) + ph * R + row0;
     float* s_top = reinterpret_cast<float*>(smem + L::kTop) + g * 4 * RT;
     float2* s_ml = reinterpret_cast<float2*>(smem + L::kMl);
-    int* s_moves = const_cast<int*>(flag) + 2 + g;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!mbar_try_wait(bar, parity)) wait_long(bar, parity, flag, P.err, WL);
       __syncwarp();
@@ -442,7 +447,7 @@ __global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_
     auto put_q = [&](const Place& p) {
       constexpr int kParts = D / 16;  // threads of a row
       const int live = s_new[p.s] * grp, rows = (live + 15) & ~15;
-      for (int item = tid; item < rows * kParts; item += 256) {
+      for (int item = tid; item < rows * kParts; item += 512) {
         const int row = item / kParts, part = item % kParts;
         uint4 in[2] = {};
         if (row < live) {
@@ -492,13 +497,12 @@ __global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_
     begin_segment(w);
     put_q(w.at);
     if (j < RT) s_base[j] = kNone;
-    named_bar_sync(1, 256);
+    named_bar_sync(1, 512);
     for (; w.u < T1; ++seg_no) {
       const int s = w.at.s, kvh = w.at.g, t0 = w.at.t;
       const bool whole = t0 == 0 && w.left == w.at.nt;
       const int len = s_len[s], n_new = s_new[s], nk = len + n_new;
-      const int live = n_new * grp, all_chunks = (live + 15) >> 4;
-      const int chunks = max(0, min(CT, all_chunks - row0 / 16));  // of 16 rows, of this thread
+      const int live = n_new * grp;
 #pragma unroll
       for (int k = 0; k < RT / 2; ++k) l2[k] = {0.f, 0.f};
       int before = -1;  // the step before of the same accumulator in the segment
@@ -507,10 +511,8 @@ __global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_
         w.u += cnt;
         w.left -= cnt;
         w.at.t += cnt;
-        if (SG == 2 && (i & 1) != g) continue;
+        if ((i & (PH - 1)) != ph) continue;
         const int st = i % STAGES, b = i % NB;
-        const uint32_t ts = tmem + lanes + L::tS(b) + row0;
-        uint8_t* pbuf = smem + L::kP + b * PC * L::kPPiece;
         wait(&full[st], (i / STAGES) & 1);
         // the thread's key: its scales, and the first row that sees it
         const int valid = s_valid[i & 15];
@@ -530,7 +532,7 @@ __global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_
           bool clear = !alive;
           if (alive && key >= len && n_new > 1) {
             bool nan = false;
-#pragma unroll
+#pragma unroll 1
             for (int ch = 0; ch < D / 16; ++ch) {
               const uint4 v = vrow[ch];
               nan |= has_nan8(v.x) || has_nan8(v.y) || has_nan8(v.z) || has_nan8(v.w);
@@ -538,123 +540,98 @@ __global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_
             if (nan) ev = __uint_as_float(0x7fc00000u);
             clear = nan;
           }
-          if (SG == 1) named_bar_sync(1, 256);  // (both groups have looked)
-          if (clear && (SG == 2 || g == 0))
-#pragma unroll
+          if (PH < 4) named_bar_sync(6 + ph, 512 / PH);  // (all groups of the step have looked)
+          if (clear && g < PH)
+#pragma unroll 1
             for (int ch = 0; ch < D / 16; ++ch) vrow[ch] = make_uint4(0, 0, 0, 0);
         }
         wait(&sready[b], (i / NB) & 1);
         tc_fence_after();
-        auto part = [&](auto from) {
-          constexpr int c0 = decltype(from)::value;
-        // 32 rows at a time (registers): s_j + ev_j; what a row does not see is -inf
-        float2 x[CH * 8];
-        {
-          uint32_t u[CH * 16];
+        const float2 f2 = {f, f}, ev2 = {ev, ev}, inv2 = {inv_v, inv_v};
+        bool waited = i < NB;  // for the last product from the buffer of P
 #pragma unroll
-          for (int c = 0; c < CH; ++c)
-            if (c0 + c < chunks) load16(ts + (c0 + c) * 16, *reinterpret_cast<uint32_t(*)[16]>(u + c * 16));
-          wait_loads();
-          if (c0 + CH >= CT) {
-            tc_fence_before();
-            mbar_arrive(&sfree[b]);
-          }
+        for (int c = 0; c < RT / 16; ++c) {  // 16 rows at a time
+          if (row0 + c * 16 >= live) break;
+          const uint32_t ts = tmem + lanes + L::tS(b) + row0 + c * 16;
+          float2 x[8];
+          auto scores = [&] {  // s_j + ev_j; what a row does not see is -inf
+            uint32_t u[16];
+            load16(ts, u);
+            wait_loads();
 #pragma unroll
-          for (int k = 0; k < CH * 8; ++k) x[k] = {__uint_as_float(u[2 * k]), __uint_as_float(u[2 * k + 1])};
-        }
-        bool any = false;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          if (c0 + c >= chunks) break;
-          float past = -INFINITY;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float4 gain = reinterpret_cast<const float4*>(s_gain + row0)[(c0 + c) * 4 + k], base = reinterpret_cast<const float4*>(s_base)[(c0 + c) * 4 + k];
-            float2* y = x + c * 8 + 2 * k;
-            y[0] = fma2(y[0], mul2(float2{gain.x, gain.y}, float2{f, f}), float2{ev, ev});
-            y[1] = fma2(y[1], mul2(float2{gain.z, gain.w}, float2{f, f}), float2{ev, ev});
-            if (edge) {
-              const int r = (c0 + c) * 16 + 4 * k;
-              y[0].x = r < rmin ? -INFINITY : y[0].x, y[0].y = r + 1 < rmin ? -INFINITY : y[0].y;
-              y[1].x = r + 2 < rmin ? -INFINITY : y[1].x, y[1].y = r + 3 < rmin ? -INFINITY : y[1].y;
+            for (int k = 0; k < 4; ++k) {
+              const float4 gain = reinterpret_cast<const float4*>(s_gain + row0)[c * 4 + k];
+              x[2 * k] = fma2(float2{__uint_as_float(u[4 * k]), __uint_as_float(u[4 * k + 1])}, mul2(float2{gain.x, gain.y}, f2), ev2);
+              x[2 * k + 1] = fma2(float2{__uint_as_float(u[4 * k + 2]), __uint_as_float(u[4 * k + 3])}, mul2(float2{gain.z, gain.w}, f2), ev2);
             }
-            const float2 d0 = add2(y[0], float2{-base.x, -base.y}), d1 = add2(y[1], float2{-base.z, -base.w});
-            past = fmaxf(past, fmaxf(fmaxf(d0.x, d0.y), fmaxf(d1.x, d1.y)));
-          }
-          if (__any_sync(0xffffffffu, past > kMost)) {
-            any = true;
-            if (lane == 0) atomicOr(s_moves, 1 << (c0 + c));
-          }
-        }
-        if (named_bar_any(2 + g, 128, any)) {
-          // ---- references that move, 16 rows at a time: the rows' maxima over the group, then O and the sums
-          const int moves = *const_cast<volatile int*>(s_moves);
+            if (edge)
 #pragma unroll
-          for (int c = 0; c < CH; ++c) {
-            if (!(moves >> (c0 + c) & 1)) continue;
+              for (int k = 0; k < 8; ++k) {
+                if (c * 16 + 2 * k < rmin) x[k].x = -INFINITY;
+                if (c * 16 + 2 * k + 1 < rmin) x[k].y = -INFINITY;
+              }
+          };
+          __half2 h[8], top = __float2half2_rn(0.f);
+          auto weights = [&] {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float4 base = reinterpret_cast<const float4*>(s_base)[c * 4 + k];
+              const float2 d0 = add2(x[2 * k], float2{base.x, base.y}), d1 = add2(x[2 * k + 1], float2{base.z, base.w});
+              x[2 * k] = {ex2(d0.x), ex2(d0.y)};
+              x[2 * k + 1] = {ex2(d1.x), ex2(d1.y)};
+              h[2 * k] = __floats2half2_rn(x[2 * k].x, x[2 * k].y);
+              h[2 * k + 1] = __floats2half2_rn(x[2 * k + 1].x, x[2 * k + 1].y);
+              top = __hmax2(top, __hmax2(h[2 * k], h[2 * k + 1]));
+            }
+          };
+          scores();
+          weights();
+          if (named_bar_any(2 + g, 128, __hgt(__hmax(__low2half(top), __high2half(top)), __float2half_rn(kMost)))) {
+            // ---- references that move: the rows' maxima over the group, then O and the sums. (Few instructions: most
+            // steps do not come here, and those that do wait for each of them to be fetched.)
+            scores();
             float mine = 0.f;
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-              const float top = warp_max(k & 1 ? x[c * 8 + k / 2].y : x[c * 8 + k / 2].x);
-              if (lane == k) mine = top;
+              const float most = warp_max(k & 1 ? x[k / 2].y : x[k / 2].x);
+              if (lane == k) mine = most;
             }
-            if (lane < 16) s_top[gw * RT + (c0 + c) * 16 + lane] = mine;
-          }
-          named_bar_sync(2 + g, 128);
-          if (j == 0) *s_moves = 0;
-          if (j < RT && (moves >> (j >> 4) & 1)) {
-            const float top = fmaxf(fmaxf(s_top[j], s_top[RT + j]), fmaxf(s_top[2 * RT + j], s_top[3 * RT + j]));
-            const float old = s_base[j], now = top - kHeadroom;
-            const bool up = top - old > kMost;
-            s_corr[j] = up ? ex2(old - now) : 1.f;
-            if (up) s_base[j] = now;
-          }
-          named_bar_sync(2 + g, 128);
-          if (before >= 0) {
-            wait(&pvdone[before % NB], (before / NB) & 1);
-            tc_fence_after();
+            if (lane < 16) s_top[gw * RT + c * 16 + lane] = mine;
+            named_bar_sync(2 + g, 128);
+            if (j < 16) {
+              const float* tops = s_top + c * 16 + j;
+              const float most = fmaxf(fmaxf(tops[0], tops[RT]), fmaxf(tops[2 * RT], tops[3 * RT]));
+              const float old = s_base[c * 16 + j], now = kHeadroom - most;
+              const bool up = most + old > kHeadroom;
+              s_corr[c * 16 + j] = up ? ex2(now - old) : 1.f;
+              if (up) s_base[c * 16 + j] = now;
+            }
+            named_bar_sync(2 + g, 128);
 #pragma unroll
-            for (int c = 0; c < CH; ++c) {
-              if (!(moves >> (c0 + c) & 1)) continue;
-              float corr[16];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float4 v = reinterpret_cast<const float4*>(s_corr)[(c0 + c) * 4 + k];
-                corr[4 * k] = v.x, corr[4 * k + 1] = v.y, corr[4 * k + 2] = v.z, corr[4 * k + 3] = v.w;
-              }
-#pragma unroll
-              for (int k = 0; k < 8; ++k) l2[(c0 + c) * 8 + k].x *= corr[2 * k], l2[(c0 + c) * 8 + k].y *= corr[2 * k + 1];
-#pragma unroll
+            for (int k = 0; k < 8; ++k) l2[c * 8 + k].x *= s_corr[c * 16 + 2 * k], l2[c * 8 + k].y *= s_corr[c * 16 + 2 * k + 1];
+            if (before >= 0) {
+              wait(&pvdone[before % NB], (before / NB) & 1);
+              tc_fence_after();
+#pragma unroll 1
               for (int p = 0; p < PC; ++p) {
+                const uint32_t to = tmem + lanes + L::tO(0) + ph * PC * R + p * R + row0 + c * 16;
                 uint32_t u[16];
                 __syncwarp();
-                load16(to + p * R + (c0 + c) * 16, u);
+                load16(to, u);
                 wait_loads();
 #pragma unroll
-                for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * corr[k]);
-                store16(to + p * R + (c0 + c) * 16, u);
+                for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * s_corr[c * 16 + k]);
+                store16(to, u);
               }
+              wait_stores();
             }
-            wait_stores();
+            weights();
           }
-        }
-        // ---- the weights, once the last product from the buffer has read its own
-        if (c0 == 0 && i >= NB) wait(&pvdone[b], (i / NB - 1) & 1);
+          if (!waited) wait(&pvdone[b], (i / NB - 1) & 1);
+          waited = true;
+          uint8_t* to = smem + L::kP + b * PC * L::kPPiece + chunk_at<R>(j, row0 / 16 + c);
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          if (c0 + c >= chunks) break;
-          __half2 h[8];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float4 base = reinterpret_cast<const float4*>(s_base)[(c0 + c) * 4 + k];
-            const int at = c * 8 + 2 * k;
-            const float2 d0 = add2(x[at], float2{-base.x, -base.y}), d1 = add2(x[at + 1], float2{-base.z, -base.w});
-            const float2 w0 = {ex2(d0.x), ex2(d0.y)}, w1 = {ex2(d1.x), ex2(d1.y)};
-            l2[c0 * 8 + at] = fma2(w0, float2{inv_v, inv_v}, l2[c0 * 8 + at]);
-            l2[c0 * 8 + at + 1] = fma2(w1, float2{inv_v, inv_v}, l2[c0 * 8 + at + 1]);
-            h[2 * k] = __floats2half2_rn(w0.x, w0.y);
-            h[2 * k + 1] = __floats2half2_rn(w1.x, w1.y);
-          }
+          for (int k = 0; k < 8; ++k) l2[c * 8 + k] = fma2(x[k], inv2, l2[c * 8 + k]);
 #pragma unroll
           for (int p = 0; p < PC; ++p) {
             uint32_t out[4];
@@ -667,24 +644,19 @@ __global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_
                 h[2 * k + 1] = __hmul2(__hsub2(h[2 * k + 1], from_e4m3x2(b1)), __float2half2_rn(16.f));
               }
             }
-            *reinterpret_cast<uint4*>(pbuf + p * L::kPPiece + chunk_at<R>(j, row0 / 16 + c0 + c)) = make_uint4(out[0], out[1], out[2], out[3]);
+            *reinterpret_cast<uint4*>(to + p * L::kPPiece) = make_uint4(out[0], out[1], out[2], out[3]);
           }
-        }
-        };
-        part(std::integral_constant<int, 0>());
-        if constexpr (CT > CH) {
-          if (chunks > CH) part(std::integral_constant<int, CH>());
-          else tc_fence_before(), mbar_arrive(&sfree[b]);
         }
         fence_async_shared();
         tc_fence_before();
         mbar_arrive(&pready[b]);
+        mbar_arrive(&sfree[b]);
         before = i;
       }
-      // ---- the segment's end. Every score of it has been read once both groups are here: q is the next one's.
+      // ---- the segment's end. Every score of it has been read once all groups are here: q is the next one's.
 #pragma unroll
-      for (int c = 0; c < CT; ++c) {
-        if (c >= chunks) break;
+      for (int c = 0; c < RT / 16; ++c) {
+        if (row0 + c * 16 >= live) break;
         float v[16];
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[2 * k] = l2[c * 8 + k].x, v[2 * k + 1] = l2[c * 8 + k].y;
@@ -693,74 +665,72 @@ __global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_
       }
       if (before >= 0) wait(&pvdone[before % NB], (before / NB) & 1);
       tc_fence_before();
-      named_bar_sync(1, 256);
+      named_bar_sync(1, 512);
       tc_fence_after();
       if (w.u < T1) {
         begin_segment(w);
         put_q(w.at);
       }
       // the states into one
-      if (tid < all_chunks * 16) {
-        float2 ml[SG];
+      if (tid < live) {
+        float2 ml[PH];
         float top = -INFINITY, den = 0.f;
 #pragma unroll
-        for (int k = 0; k < SG; ++k) {
-          const float* sums = reinterpret_cast<const float*>(smem + L::kTop) + (SG == 2 ? k * 4 * RT + tid : tid / RT * 4 * RT + tid % RT);
+        for (int k = 0; k < PH; ++k) {
+          const float* sums = reinterpret_cast<const float*>(smem + L::kTop) + (tid / RT * PH + k) * 4 * RT + tid % RT;
           const float base = reinterpret_cast<const float*>(smem + L::kBase)[k * R + tid];
-          ml[k] = make_float2(base == kNone ? -INFINITY : base, (sums[0] + sums[RT]) + (sums[2 * RT] + sums[3 * RT]));
+          ml[k] = make_float2(base == kNone ? -INFINITY : -base, (sums[0] + sums[RT]) + (sums[2 * RT] + sums[3 * RT]));
           top = fmaxf(top, ml[k].x);
         }
 #pragma unroll
-        for (int k = 0; k < SG; ++k) {
+        for (int k = 0; k < PH; ++k) {
           const float wk = weight_of(ml[k], top);
           den += wk == 0.f ? 0.f : wk * ml[k].y;
           reinterpret_cast<float*>(smem + L::kCorr)[k * R + tid] = wk;
         }
         s_ml[tid] = make_float2(top, den);
       }
-      named_bar_sync(1, 256);
+      named_bar_sync(1, 512);
       if (j < RT) s_base[j] = kNone;
       float* slot = P.part + (2 * static_cast<size_t>(cta) + (seg_no == 0 ? 0 : 1)) * static_cast<size_t>(P.slot_rows) * (D + 2);
-      if (gw * 32 < D) {  // a dim a lane, 16 rows at a time, in turn by the groups
+      if (gw * 32 < D) {  // a dim a lane, four rows at a time, in turn by the groups
         const int dim = gw * 32 + lane;
 #pragma unroll 1
-        for (int c = g; c < all_chunks; c += 2) {
-          float o[16] = {};
+        for (int r4 = 4 * g; r4 < live; r4 += 16) {
+          uint32_t u[PH][PC][4];
+          __syncwarp();
 #pragma unroll
-          for (int k2 = 0; k2 < SG; ++k2) {
-            const float* wk = reinterpret_cast<const float*>(smem + L::kCorr) + k2 * R + c * 16;
-            float v[16] = {};
+          for (int k = 0; k < PH; ++k)
 #pragma unroll
-            for (int p = PC - 1; p >= 0; --p) {
-              uint32_t u[16];
-              __syncwarp();
-              load16(tmem + lanes + L::tO(k2) + p * R + c * 16, u);
-              wait_loads();
+            for (int p = 0; p < PC; ++p) load4(tmem + lanes + L::tO(k) + p * R + r4, u[k][p]);
+          wait_loads();
 #pragma unroll
-              for (int k = 0; k < 16; ++k) v[k] = fmaf(v[k], 0.0625f, __uint_as_float(u[k]));
-            }
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if (wk[k] != 0.f) o[k] = fmaf(wk[k], v[k], o[k]);  // (a state without a step: whatever its accumulator holds)
-          }
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int row = c * 16 + k;
+          for (int q = 0; q < 4; ++q) {
+            const int row = r4 + q;
             if (row >= live) break;
+            float o = 0.f;
+#pragma unroll
+            for (int k = 0; k < PH; ++k) {
+              float v = 0.f;
+#pragma unroll
+              for (int p = PC - 1; p >= 0; --p) v = fmaf(v, 0.0625f, __uint_as_float(u[k][p][q]));
+              const float wk = reinterpret_cast<const float*>(smem + L::kCorr)[k * R + row];
+              if (wk != 0.f) o = fmaf(wk, v, o);  // (a state without a step: whatever its accumulator holds)
+            }
             if (whole) {
-              const float den = s_ml[row].y, y = o[k] * (den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den));
+              const float den = s_ml[row].y, y = o * (den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den));
               const int r = new_row(P, row);
               const size_t at = ((static_cast<size_t>(s) * P.rows_per_seq + r) * P.nq + static_cast<size_t>(kvh) * grp + row - r * grp) * D + dim;
               static_cast<uint16_t*>(P.out)[at] = static_cast<uint16_t>(pack2<BF16>(y, 0.f));
             } else {
-              __stcg(slot + static_cast<size_t>(row) * D + dim, o[k]);
+              __stcg(slot + static_cast<size_t>(row) * D + dim, o);
             }
           }
         }
       }
       if (tid < live && !whole) __stcg(reinterpret_cast<float2*>(slot + static_cast<size_t>(P.slot_rows) * D) + tid, s_ml[tid]);
       tc_fence_before();
-      named_bar_sync(1, 256);  // the buffers are the next segment's
+      named_bar_sync(1, 512);  // the buffers are the next segment's
     }
   }
 
@@ -774,16 +744,23 @@ __global__ void __launch_bounds__(Layout8<D, R, BF16>::kThreads, 1) paged_attn8_
   }
 }
 
-template <int D, int R, bool BF16>
+template <int D, int R, int PH, bool BF16>
 int set_attr() {
-  using L = Layout8<D, R, BF16>;
+  using L = Layout8<D, R, PH, BF16>;
   static_assert(L::smem(kAttnMaxBatch) <= 232448, "shared memory of a CTA");
-  return static_cast<int>(cudaFuncSetAttribute(paged_attn8_kernel<D, R, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return static_cast<int>(cudaFuncSetAttribute(paged_attn8_kernel<D, R, PH, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                L::smem(kAttnMaxBatch)));
 }
-template <int D, int R, bool BF16>
+template <int D, bool BF16>
+int set_attrs() {
+  const int e[] = {set_attr<D, 32, 4, BF16>(), set_attr<D, 32, 2, BF16>(), set_attr<D, 64, 1, BF16>(), set_attr<D, 128, 1, BF16>()};
+  for (int x : e)
+    if (x != 0) return x;
+  return 0;
+}
+template <int D, int R, int PH, bool BF16>
 int launch(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
-  using L = Layout8<D, R, BF16>;
+  using L = Layout8<D, R, PH, BF16>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(n_ctas);
   cfg.blockDim = dim3(L::kThreads);
@@ -794,20 +771,19 @@ int launch(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return static_cast<int>(cudaLaunchKernelEx(&cfg, paged_attn8_kernel<D, R, BF16>, p));
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, paged_attn8_kernel<D, R, PH, BF16>, p));
 }
 template <int D, bool BF16>
 int launch_rows(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
-  if (p.rows <= 32) return launch<D, 32, BF16>(p, n_ctas, stream);
-  return p.rows <= 64 ? launch<D, 64, BF16>(p, n_ctas, stream) : launch<D, 128, BF16>(p, n_ctas, stream);
+  if (p.rows <= 16) return launch<D, 32, 4, BF16>(p, n_ctas, stream);
+  if (p.rows <= 32) return launch<D, 32, 2, BF16>(p, n_ctas, stream);
+  return p.rows <= 64 ? launch<D, 64, 1, BF16>(p, n_ctas, stream) : launch<D, 128, 1, BF16>(p, n_ctas, stream);
 }
 
 }  // namespace
 
 int paged_attn8_set_attributes() {
-  const int e[] = {set_attr<64, 32, false>(),  set_attr<64, 32, true>(),  set_attr<64, 64, false>(),  set_attr<64, 64, true>(),
-                   set_attr<64, 128, false>(), set_attr<64, 128, true>(), set_attr<128, 32, false>(), set_attr<128, 32, true>(),
-                   set_attr<128, 64, false>(), set_attr<128, 64, true>(), set_attr<128, 128, false>(), set_attr<128, 128, true>()};
+  const int e[] = {set_attrs<64, false>(), set_attrs<64, true>(), set_attrs<128, false>(), set_attrs<128, true>()};
   for (int x : e)
     if (x != 0) return x;
   return 0;
