@@ -51,7 +51,8 @@ bool encode(PFN_cuTensorMapEncodeTiled_v12000 fn, CUtensorMap* m, void* base, co
   const CUtensorMapDataType type = bits8(c) ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                    : c.dtype == DFLASH_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   return fn(m, type, 3, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            bits8(c) && d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            bits8(c) && d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            !bits8(c) ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : d == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

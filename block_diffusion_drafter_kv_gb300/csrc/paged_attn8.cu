@@ -164,22 +164,28 @@ DEV float reduce16(float (&v)[16]) {
   return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
-// D: head dim; R: rows of a problem that the buffers hold (32, 64, 128); PH: steps that the four softmax groups
+// D: head dim; R: rows of a problem that the buffers hold (16, 32, 64, 128); PH: steps that the four softmax groups
 // work on at a time (4: at most 16 rows, a step a group; 2: at most 32 rows, two groups a step; 1: all of them).
 template <int D, int R, int PH, bool BF16>
 struct Layout8 {
   static constexpr int kPieces = BF16 ? 2 : 3;              // of q, and of the weights
   static constexpr int RT = PH == 1 ? R / 4 : 16;           // rows of a softmax thread
+  // A product's time hardly goes with N up to a hundred: pieces of q side by side, in columns of their own, as far as
+  // tensor memory holds them (the rest add up in the last of them).
+  static constexpr int ST = R <= 32 ? kPieces : R == 64 ? 2 : 1;
+  static constexpr int kPW = R > 16 ? R : BF16 ? 32 : 64;   // bytes of a key's row of weights: a piece, or with 16 rows all pieces
+  static constexpr int kPiece = R > 16 ? kStepKeys * R : 16;     // from a weight's piece to the next
+  static constexpr int kPBuf = R > 16 ? kPieces * kPiece : kStepKeys * kPW;
+  static constexpr int kOCols = R > 16 ? kPieces * R : kPW;
   static constexpr int NB = PH > 1 ? PH : R == 128 && !BF16 ? 1 : 2;  // buffers of S and P, taken by the steps in turn
   static constexpr int kThreads = 512 + 64;
   static constexpr int kOperand = kStepKeys * D;            // K, or V, of a step
-  static constexpr int STAGES = D == 64 ? (R == 128 ? 6 : 8) : R == 128 ? 3 : R == 64 || !BF16 ? 4 : 5;
-  static constexpr int kPPiece = kStepKeys * R;
+  static constexpr int STAGES = D == 64 ? (R == 128 ? 6 : 8) : R == 128 ? 3 : R == 64 ? 4 : 5;
   static constexpr int kQPiece = R * D;
   static constexpr int kK = 0;
   static constexpr int kV = kK + STAGES * kOperand;
   static constexpr int kP = kV + STAGES * kOperand;
-  static constexpr int kQ = kP + NB * kPieces * kPPiece;
+  static constexpr int kQ = kP + NB * kPBuf;
   static constexpr int kSc = kQ + kPieces * kQPiece;        // scales of a step: two tiles' 128 bytes
   static constexpr int kBase = kSc + STAGES * 256;          // [PH][R] references, negative
   static constexpr int kGain = kBase + PH * R * 4;          // [R] 1 / the power of two that q was scaled by
@@ -192,9 +198,9 @@ struct Layout8 {
   static constexpr int kWarpSums = kFlags + 80;
   static constexpr int kPre = kWarpSums + 128;
   static constexpr int smem(int batch) { return 1024 + kPre + (3 * batch + 1) * 4; }
-  static constexpr uint32_t tS(int b) { return b * R; }     // TMEM columns
-  static constexpr uint32_t tO(int ph) { return NB * R + ph * kPieces * R; }
-  static_assert(NB * R + PH * R * kPieces <= 512, "tensor memory");
+  static constexpr uint32_t tS(int b) { return b * ST * R; }     // TMEM columns
+  static constexpr uint32_t tO(int ph) { return NB * ST * R + ph * kOCols; }
+  static_assert(NB * ST * R + PH * kOCols <= 512, "tensor memory");
   static_assert(kThreads <= 32 * 32 && 4 * RT / PH <= R, "groups");
 };
 
@@ -334,37 +340,39 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
     // uniform registers, which is where the products take them from.
     const bool leader = elect_one();
     auto ready = [](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, test_wait(bar, parity)) != 0; };
-    constexpr uint32_t kQk = idesc_f8(128, R, false, false);
+    constexpr uint32_t kQkAll = idesc_f8(128, L::ST * R, false, false), kQkOne = idesc_f8(128, R, false, false);
     const uint64_t k_base = desc_rows<D>(smem_u32(smem + L::kK), 16), q_base = desc_rows<D>(smem_u32(smem + L::kQ), 16);
     // (with 64 dims the upper half of M is the same dims again, unused)
-    const uint64_t v_base = desc_rows<D>(smem_u32(smem + L::kV), 0), p_base = desc_rows<R>(smem_u32(smem + L::kP), L::kPPiece);
+    const uint64_t v_base = desc_rows<D>(smem_u32(smem + L::kV), 0), p_base = desc_rows<L::kPW>(smem_u32(smem + L::kP), L::kPiece);
     auto qk = [&](int st, int b) {  // S^T = K Q^T
       tc_fence_after();
       const uint64_t k0 = k_base + (st * L::kOperand >> 4);
       const uint32_t d = tmem + L::tS(b);
       if (leader) {
 #pragma unroll
-        for (int p = 0; p < PC; ++p)
+        for (int kk = 0; kk < D / 32; ++kk) mma_f8(d, k0 + (kk * 32 >> 4), q_base + (kk * 32 >> 4), kQkAll, kk > 0 ? 1u : 0u);
+#pragma unroll
+        for (int p = L::ST; p < PC; ++p)
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk)
-            mma_f8(d, k0 + (kk * 32 >> 4), q_base + ((p * L::kQPiece + kk * 32) >> 4), kQk, p + kk > 0 ? 1u : 0u);
+            mma_f8(d + (L::ST - 1) * R, k0 + (kk * 32 >> 4), q_base + ((p * L::kQPiece + kk * 32) >> 4), kQkOne, 1u);
         tc_commit(&sready[b]);
       }
       __syncwarp();
     };
     auto pv = [&](int st, int b, bool first) {  // O^T (+)= V^T P^T
       tc_fence_after();
-      const uint64_t v0 = v_base + (st * L::kOperand >> 4), p0 = p_base + (b * PC * L::kPPiece >> 4);
+      const uint64_t v0 = v_base + (st * L::kOperand >> 4), p0 = p_base + (b * L::kPBuf >> 4);
       const uint32_t d = tmem + L::tO(PH > 1 ? b : 0), keep = first ? 0u : 1u;
-      constexpr int N1 = PC * R <= 256 ? PC * R : 256, N2 = PC * R - N1;
+      constexpr int N1 = L::kOCols <= 256 ? L::kOCols : 256, N2 = L::kOCols - N1;
       constexpr uint32_t kPv1 = idesc_f8(128, N1, true, true);
       if (leader) {
 #pragma unroll
         for (int kk = 0; kk < kStepKeys / 32; ++kk) {
-          mma_f8(d, v0 + (kk * 32 * D >> 4), p0 + (kk * 32 * R >> 4), kPv1, kk > 0 ? 1u : keep);
+          mma_f8(d, v0 + (kk * 32 * D >> 4), p0 + (kk * 32 * L::kPW >> 4), kPv1, kk > 0 ? 1u : keep);
           if constexpr (N2 > 0) {
             constexpr uint32_t kPv2 = idesc_f8(128, N2, true, true);
-            mma_f8(d + N1, v0 + (kk * 32 * D >> 4), p0 + ((N1 / R * L::kPPiece + kk * 32 * R) >> 4), kPv2, kk > 0 ? 1u : keep);
+            mma_f8(d + N1, v0 + (kk * 32 * D >> 4), p0 + ((N1 / R * L::kPiece + kk * 32 * R) >> 4), kPv2, kk > 0 ? 1u : keep);
           }
         }
         tc_commit(&pvdone[b]);
@@ -555,14 +563,21 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
           const uint32_t ts = tmem + lanes + L::tS(b) + row0 + c * 16;
           float2 x[8];
           auto scores = [&] {  // s_j + ev_j; what a row does not see is -inf
-            uint32_t u[16];
-            load16(ts, u);
+            uint32_t u[L::ST][16];
+#pragma unroll
+            for (int p = 0; p < L::ST; ++p) load16(ts + p * R, u[p]);
             wait_loads();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              x[k] = {__uint_as_float(u[0][2 * k]), __uint_as_float(u[0][2 * k + 1])};
+#pragma unroll
+              for (int p = 1; p < L::ST; ++p) x[k] = add2(x[k], float2{__uint_as_float(u[p][2 * k]), __uint_as_float(u[p][2 * k + 1])});
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const float4 gain = reinterpret_cast<const float4*>(s_gain + row0)[c * 4 + k];
-              x[2 * k] = fma2(float2{__uint_as_float(u[4 * k]), __uint_as_float(u[4 * k + 1])}, mul2(float2{gain.x, gain.y}, f2), ev2);
-              x[2 * k + 1] = fma2(float2{__uint_as_float(u[4 * k + 2]), __uint_as_float(u[4 * k + 3])}, mul2(float2{gain.z, gain.w}, f2), ev2);
+              x[2 * k] = fma2(x[2 * k], mul2(float2{gain.x, gain.y}, f2), ev2);
+              x[2 * k + 1] = fma2(x[2 * k + 1], mul2(float2{gain.z, gain.w}, f2), ev2);
             }
             if (edge)
 #pragma unroll
@@ -614,7 +629,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
               tc_fence_after();
 #pragma unroll 1
               for (int p = 0; p < PC; ++p) {
-                const uint32_t to = tmem + lanes + L::tO(0) + ph * PC * R + p * R + row0 + c * 16;
+                const uint32_t to = tmem + lanes + L::tO(0) + ph * L::kOCols + p * R + row0 + c * 16;
                 uint32_t u[16];
                 __syncwarp();
                 load16(to, u);
@@ -629,7 +644,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
           }
           if (!waited) wait(&pvdone[b], (i / NB - 1) & 1);
           waited = true;
-          uint8_t* to = smem + L::kP + b * PC * L::kPPiece + chunk_at<R>(j, row0 / 16 + c);
+          uint8_t* to = smem + L::kP + b * L::kPBuf;
 #pragma unroll
           for (int k = 0; k < 8; ++k) l2[c * 8 + k] = fma2(x[k], inv2, l2[c * 8 + k]);
 #pragma unroll
@@ -644,7 +659,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
                 h[2 * k + 1] = __hmul2(__hsub2(h[2 * k + 1], from_e4m3x2(b1)), __float2half2_rn(16.f));
               }
             }
-            *reinterpret_cast<uint4*>(to + p * L::kPPiece) = make_uint4(out[0], out[1], out[2], out[3]);
+            *reinterpret_cast<uint4*>(to + (R > 16 ? p * L::kPiece + chunk_at<R>(j, row0 / 16 + c) : chunk_at<L::kPW>(j, p))) = make_uint4(out[0], out[1], out[2], out[3]);
           }
         }
         fence_async_shared();
@@ -753,7 +768,7 @@ int set_attr() {
 }
 template <int D, bool BF16>
 int set_attrs() {
-  const int e[] = {set_attr<D, 32, 4, BF16>(), set_attr<D, 32, 2, BF16>(), set_attr<D, 64, 1, BF16>(), set_attr<D, 128, 1, BF16>()};
+  const int e[] = {set_attr<D, 16, 4, BF16>(), set_attr<D, 32, 2, BF16>(), set_attr<D, 64, 1, BF16>(), set_attr<D, 128, 1, BF16>()};
   for (int x : e)
     if (x != 0) return x;
   return 0;
@@ -775,7 +790,7 @@ int launch(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
 }
 template <int D, bool BF16>
 int launch_rows(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
-  if (p.rows <= 16) return launch<D, 32, 4, BF16>(p, n_ctas, stream);
+  if (p.rows <= 16) return launch<D, 16, 4, BF16>(p, n_ctas, stream);
   if (p.rows <= 32) return launch<D, 32, 2, BF16>(p, n_ctas, stream);
   return p.rows <= 64 ? launch<D, 64, 1, BF16>(p, n_ctas, stream) : launch<D, 128, 1, BF16>(p, n_ctas, stream);
 }
