@@ -18,6 +18,9 @@ namespace {
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+bool bits8(const dflash_cache_config& c) { return c.dtype == DFLASH_E4M3_F16 || c.dtype == DFLASH_E4M3_BF16; }
+bool io_bf16(const dflash_cache_config& c) { return c.dtype == DFLASH_BF16 || c.dtype == DFLASH_E4M3_BF16; }
+
 struct CacheLayout {
   size_t err, prefix, part, total;
 };
@@ -27,13 +30,12 @@ CacheLayout layout_of(const dflash_cache_config& c) {
   L.err = 0;
   L.prefix = 256;
   L.part = L.prefix + up256((std::min<size_t>(c.max_batch, kAttnMaxBatch) + 1) * 4);
-  const size_t rows = paged_attn_rows(c.n_heads / c.n_kv_heads * c.max_block);
+  // (in 8 bits calls of fewer rows than these take more slots of fewer rows: 4 of 16, 2 of 32)
+  const int most = c.n_heads / c.n_kv_heads * c.max_block;
+  const size_t rows = bits8(c) ? std::max(64, paged_attn8_rows(most)) : paged_attn_rows(most);
   L.total = L.part + up256(2 * kPagedMaxCtas * rows * (c.head_dim + 2) * 4);
   return L;
 }
-
-bool bits8(const dflash_cache_config& c) { return c.dtype == DFLASH_E4M3_F16 || c.dtype == DFLASH_E4M3_BF16; }
-bool io_bf16(const dflash_cache_config& c) { return c.dtype == DFLASH_BF16 || c.dtype == DFLASH_E4M3_BF16; }
 
 // Of a call with a shared prefix: the fp32 outputs and (max, sum) of each row's two parts.
 size_t shared_bytes(const dflash_cache_config& c, long long rows) {
@@ -278,7 +280,8 @@ static int attend(dflash_cache* c, int32_t layer, const void* q, const int32_t* 
   P.scales = c->layer_scales(layer);
   P.prefix_len = prefix >= 0 ? c->len + prefix : nullptr;
   P.prefix_table = prefix >= 0 ? c->page_table + static_cast<size_t>(prefix) * f.pages_per_seq : nullptr;
-  P.slot_rows = paged_attn_rows(P.rows);
+  P.slot_rows = bits8(f) ? paged_attn8_rows(P.rows) : paged_attn_rows(P.rows);
+  P.strands = bits8(f) ? paged_attn8_strands(P.rows) : 1;
   const size_t seq_bytes = static_cast<size_t>(rows_per_seq) * f.n_heads * f.head_dim * 2;
   for (int s = 0; s < batch; s += kAttnMaxBatch) {
     P.q = static_cast<const uint8_t*>(q) + s * seq_bytes;

@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(256) paged_attn_join_kernel(const __grid_const
   const long long T = static_cast<long long>(P.nkv) * all;
   const int nt = p1 - p0;
   if (nt == 0 || row >= n_new * grp) return;
-  const int G = static_cast<int>(min(static_cast<long long>(n_ctas), T));
+  const int G = n_ranges(T, n_ctas, P.strands);
   const long long base = static_cast<long long>(P.nkv) * p0 + static_cast<long long>(g) * nt;
   const int c0 = cta_of(base, T, G), c1 = cta_of(base + nt - 1, T, G);
   if (c0 == c1) return;
@@ -630,7 +630,7 @@ int launch_join(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return static_cast<int>(cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<D, BF16>, p, n_ctas, paged_attn_rows(p.rows)));
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<D, BF16>, p, n_ctas, p.slot_rows));
 }
 
 }  // namespace

@@ -119,6 +119,13 @@ DEV void count_tiles(const PagedAttnParams& P, int* s_pre, int* s_len, int* s_ne
     for (int s = tid; s <= P.batch; s += THREADS) P.prefix[s] = s_pre[s];
 }
 
+// How many ranges the list of T tiles is cut into, for n_ctas CTAs of `strands` ranges each: no empty one, and
+// no more than one a CTA where they would be shorter than two tiles.
+DEV int n_ranges(long long T, int n_ctas, int strands) {
+  const long long n = n_ctas;
+  return static_cast<int>(min(T, strands == 1 ? n : min(n * strands, max(n, (T + 1) >> 1))));
+}
+
 // The new row that row x < 256 of a problem belongs to, x / group: (x + 1/2) / group is 1 / 512 or more
 // from the next integers, far more than a product of floats is off.
 DEV int new_row(const PagedAttnParams& P, int x) { return static_cast<int>((static_cast<float>(x) + 0.5f) * P.group_inv); }

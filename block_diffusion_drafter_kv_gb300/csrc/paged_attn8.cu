@@ -21,8 +21,9 @@
 // w_j <= 256 whatever the scales; p_j is w_j 2^-ev_j (|ev_j| <= 40: no overflow).
 //
 // CTA: one per SM, four softmax groups of 128 threads, a warp that issues the products, a producer warp. Of at
-// most 16 rows each group takes every fourth step, with an accumulator and references of its own; of more
-// the groups share a step, some of the rows each. Every wait is bounded, as in paged_attn_tc.cu.
+// most 16 rows each group is a strand of its own, with its range of the list, so that one's start and end of a
+// segment run under the others' steps; of more rows two or four groups share a strand's steps, some of the rows
+// each. Every wait is bounded, as in paged_attn_tc.cu.
 #include <type_traits>
 
 #include "paged_attn.cuh"
@@ -164,8 +165,8 @@ DEV float reduce16(float (&v)[16]) {
   return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
-// D: head dim; R: rows of a problem that the buffers hold (16, 32, 64, 128); PH: steps that the four softmax groups
-// work on at a time (4: at most 16 rows, a step a group; 2: at most 32 rows, two groups a step; 1: all of them).
+// D: head dim; R: rows of a problem that the buffers hold (16, 32, 64, 128); PH: strands of a CTA, each with a range of
+// the list, accumulators and 4 / PH of the softmax groups (4: at most 16 rows; 2: at most 32 rows; 1).
 template <int D, int R, int PH, bool BF16>
 struct Layout8 {
   static constexpr int kPieces = BF16 ? 2 : 3;              // of q, and of the weights
@@ -180,21 +181,21 @@ struct Layout8 {
   static constexpr int NB = PH > 1 ? PH : R == 128 && !BF16 ? 1 : 2;  // buffers of S and P, taken by the steps in turn
   static constexpr int kThreads = 512 + 64;
   static constexpr int kOperand = kStepKeys * D;            // K, or V, of a step
-  static constexpr int STAGES = D == 64 ? (R == 128 ? 6 : 8) : R == 128 ? 3 : R == 64 ? 4 : 5;
+  static constexpr int STAGES = D == 64 ? (R == 128 ? 6 : 8) : R == 128 ? 3 : R == 64 || !BF16 ? 4 : 5;
   static constexpr int kQPiece = R * D;
   static constexpr int kK = 0;
   static constexpr int kV = kK + STAGES * kOperand;
   static constexpr int kP = kV + STAGES * kOperand;
   static constexpr int kQ = kP + NB * kPBuf;
-  static constexpr int kSc = kQ + kPieces * kQPiece;        // scales of a step: two tiles' 128 bytes
+  static constexpr int kSc = kQ + PH * kPieces * kQPiece;   // scales of a step: two tiles' 128 bytes
   static constexpr int kBase = kSc + STAGES * 256;          // [PH][R] references, negative
-  static constexpr int kGain = kBase + PH * R * 4;          // [R] 1 / the power of two that q was scaled by
-  static constexpr int kCorr = kGain + R * 4;               // [PH][R] factors of a moved reference; weights of the states at the end
+  static constexpr int kGain = kBase + PH * R * 4;          // [PH][R] 1 / the power of two that q was scaled by
+  static constexpr int kCorr = kGain + PH * R * 4;          // [PH][R] factors of a moved reference
   static constexpr int kTop = kCorr + PH * R * 4;           // [4 groups][4 warps][RT] warps' maxima; sums at the end
-  static constexpr int kMl = kTop + 4 * 4 * RT * 4;         // [R] (max, sum)
-  static constexpr int kBar = kMl + R * 8;
-  static constexpr int kBars = 2 * STAGES + 4 * NB + 2;     // full, empty; S ready, free, P ready, PV done [NB]; Q, done
-  static constexpr int kFlags = kBar + kBars * 8;           // [0] abort, [1] TMEM base, [4..19] valid tiles of steps
+  static constexpr int kMl = kTop + 4 * 4 * RT * 4;         // [PH][R] (max, sum)
+  static constexpr int kBar = kMl + PH * R * 8;
+  static constexpr int kBars = 2 * STAGES + 4 * NB + PH + 1;  // full, empty; S ready, free, P ready, PV done [NB]; Q [PH]; done
+  static constexpr int kFlags = kBar + kBars * 8;           // [0] abort, [1] TMEM base, [4..19] steps: 1, 2: tiles that are there, 4: begins a segment, 8: none (its strand is done), 16: of the last round
   static constexpr int kWarpSums = kFlags + 80;
   static constexpr int kPre = kWarpSums + 128;
   static constexpr int smem(int batch) { return 1024 + kPre + (3 * batch + 1) * 4; }
@@ -217,9 +218,9 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
   uint64_t* pready = sfree + NB;
   uint64_t* pvdone = pready + NB;
   uint64_t* qready = pvdone + NB;
-  uint64_t* mdone = qready + 1;
+  uint64_t* mdone = qready + PH;
   volatile int* flag = reinterpret_cast<volatile int*>(smem + L::kFlags);
-  volatile int* s_valid = flag + 4;  // bit h: tile h of the step is there; by step mod 16, more than the ring holds
+  volatile int* s_step = flag + 4;  // by step mod 16, more than the ring holds
   int* s_warp = reinterpret_cast<int*>(smem + L::kWarpSums);
   int* s_pre = reinterpret_cast<int*>(smem + L::kPre);
   int* s_len = s_pre + P.batch + 1;
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
       mbar_init(&pready[i], 512 / PH);
       mbar_init(&pvdone[i], 1);
     }
-    mbar_init(qready, 512);
+    for (int i = 0; i < PH; ++i) mbar_init(&qready[i], 512 / PH);
     mbar_init(mdone, 1);
     flag[0] = 0;
     fence_mbar_init();
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
   count_tiles<L::kThreads>(P, s_pre, s_len, s_new, s_warp);
   const int batch = P.batch, nkv = P.nkv, grp = P.group;
   const long long T = static_cast<long long>(nkv) * s_pre[batch];
-  const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), T));
+  const int G = n_ranges(T, gridDim.x, PH);
   const int cta = blockIdx.x;
   if (cta >= G) return;  // the whole CTA, before it holds any tensor memory
   constexpr int kIssuer = 16, kProducer = 17;
@@ -259,38 +260,53 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(flag[1]);
-  const long long T0 = range_begin(cta, T, G), T1 = range_begin(cta + 1, T, G);
 
-  // The walk of every role: steps of up to two tiles of the segments of [T0, T1).
+  // A strand's walk: steps of up to two tiles of the segments of its range. Step n of strand v is the CTA's step
+  // n * PH + v; strands that are done have empty steps until the last one is.
   struct Walk {
-    long long u;
+    long long u, end;
     int left;  // tiles of the segment that are left
     Place at;  // of the next tile
   };
+  auto range_of = [&](int v) { return v * static_cast<int>(gridDim.x) + cta; };
+  auto begin_walk = [&](int v) {
+    const int r = range_of(v);
+    return r < G ? Walk{range_begin(r, T, G), range_begin(r + 1, T, G), 0, {}} : Walk{0, 0, 0, {}};
+  };
   auto begin_segment = [&](Walk& w) {
     w.at = locate(s_pre, batch, nkv, w.u);
-    w.left = static_cast<int>(min(T1 - w.u, static_cast<long long>(w.at.nt - w.at.t)));
+    w.left = static_cast<int>(min(w.end - w.u, static_cast<long long>(w.at.nt - w.at.t)));
   };
 
   if (warp == kProducer) {
-    // ------------------------------------------------------------------ producer
+    // ------------------------------------------------------------------ producer: 32 / PH lanes a strand
+    constexpr int LS = 32 / PH;
     const uint64_t pol = T * (2 * kKeys * D) > (16ll << 20) ? policy_evict_first() : policy_evict_last();
-    int i = 0;       // step
-    bool go = true;  // the same in every lane
-    Walk w{T0, 0, {}};
-    int ids = -1, id0 = 0;  // page ids of the segment's next tiles, one a lane; the lane that has the next one
-    while (w.u < T1 && go) {
-      if (w.left == 0) {
-        begin_segment(w);
-        id0 = 32;
+    int i0 = 0;       // the round's first step
+    bool go = true;   // the same in every lane
+    Walk w = begin_walk(lane / LS);
+    int ids = -1, id0 = LS;  // page ids of the segment's next tiles, one a lane; the lane that has the next one
+    while (go && __any_sync(0xffffffffu, w.u < w.end)) {
+      // every strand's next step
+      int info = 8, page[2] = {-1, -1}, head = 0;
+      const bool some = w.u < w.end;
+      if (some) {
+        info = 0;
+        if (w.left == 0) {
+          begin_segment(w);
+          id0 = LS;
+          info = 4;
+        }
+        head = w.at.g;
       }
-      int page[2] = {-1, -1};
-      const int cnt = min(2, w.left);
-      for (int h = 0; h < cnt; ++h) {
-        if (id0 == 32) {
+      const int cnt = some ? min(2, w.left) : 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h < cnt && id0 == LS) {
           ids = -1;
-          if (lane < w.left - h) {
-            ids = __ldcg(P.page_table + static_cast<size_t>(w.at.s) * P.pages_per_seq + w.at.t + h + lane);
+          const int k = lane % LS;
+          if (k < w.left - h) {
+            ids = __ldcg(P.page_table + static_cast<size_t>(w.at.s) * P.pages_per_seq + w.at.t + h + k);
             if (ids < 0 || ids >= P.n_pages) {
               raise_flag(P.err, kDevCapacity);
               ids = -1;
@@ -298,41 +314,53 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
           }
           id0 = 0;
         }
-        page[h] = __shfl_sync(0xffffffffu, ids, id0++);
-      }
-      const int st = i % STAGES;
-      if (i >= STAGES) {
-        bool ok = !flag[0];
-        if (ok && lane == 0 && !mbar_wait(&empty[st], (i / STAGES - 1) & 1, WL)) {
-          raise_flag(P.err, kDevTimeout);
-          flag[0] = 1;
-          ok = false;
+        __syncwarp();
+        const int id = __shfl_sync(0xffffffffu, ids, (lane & ~(LS - 1)) + (id0 & (LS - 1)));
+        if (h < cnt) {
+          page[h] = id;
+          info |= (id >= 0) << h;
+          ++id0;
         }
-        go = __all_sync(0xffffffffu, ok);
-        if (!go) break;
       }
-      if (lane == 0) {
-        const int valid = (page[0] >= 0) | (page[1] >= 0) << 1;
-        s_valid[i & 15] = valid;
-        if (valid) mbar_arrive_expect_tx(&full[st], (valid == 3 ? 2 : 1) * (2 * kKeys * D + 2 * kKeys));
-        else mbar_arrive(&full[st]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (page[h] >= 0) {
-            tma_load_3d(smem + L::kK + st * L::kOperand + h * kKeys * D, &P.kmap, &full[st], 0, w.at.g, page[h] * kKeys, pol);
-            tma_load_3d(smem + L::kV + st * L::kOperand + h * kKeys * D, &P.vmap, &full[st], 0, w.at.g, page[h] * kKeys, pol);
-            bulk_load(smem + L::kSc + st * 256 + h * 128, P.scales + (static_cast<size_t>(page[h]) * nkv + w.at.g) * 128, 128, &full[st]);
-          }
-      }
-      __syncwarp();
-      ++i;
       w.u += cnt;
       w.left -= cnt;
       w.at.t += cnt;
+      if (!__any_sync(0xffffffffu, w.u < w.end)) info |= 16;
+#pragma unroll 1
+      for (int v = 0; v < PH; ++v) {
+        const int i = i0 + v, st = i % STAGES;
+        bool ok = !flag[0];
+        if (lane == v * LS) {
+          if (ok && i >= STAGES && !mbar_wait(&empty[st], (i / STAGES - 1) & 1, WL)) {
+            raise_flag(P.err, kDevTimeout);
+            flag[0] = 1;
+            ok = false;
+          }
+          if (ok) {
+            s_step[i & 15] = info;
+            const int tiles = (info & 1) + (info >> 1 & 1);
+            if (tiles) mbar_arrive_expect_tx(&full[st], tiles * (2 * kKeys * D + 2 * kKeys));
+            else mbar_arrive(&full[st]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (info >> h & 1) {
+                tma_load_3d(smem + L::kK + st * L::kOperand + h * kKeys * D, &P.kmap, &full[st], 0, head, page[h] * kKeys, pol);
+                tma_load_3d(smem + L::kV + st * L::kOperand + h * kKeys * D, &P.vmap, &full[st], 0, head, page[h] * kKeys, pol);
+                bulk_load(smem + L::kSc + st * 256 + h * 128, P.scales + (static_cast<size_t>(page[h]) * nkv + head) * 128, 128, &full[st]);
+              }
+          }
+        }
+        go = __all_sync(0xffffffffu, ok);
+        if (!go) {
+          i0 += v;  // steps issued
+          break;
+        }
+      }
+      if (go) i0 += PH;
     }
     // every copy issued has landed before the CTA leaves
     if (lane == 0)
-      for (int k = max(0, i - STAGES); k < i; ++k) mbar_wait(&full[k % STAGES], (k / STAGES) & 1, WL);
+      for (int k = max(0, i0 - STAGES); k < i0; ++k) mbar_wait(&full[k % STAGES], (k / STAGES) & 1, WL);
     __syncwarp();
   } else if (warp == kIssuer) {
     // ------------------------------------------------------------------ issuer of the products
@@ -344,26 +372,26 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
     const uint64_t k_base = desc_rows<D>(smem_u32(smem + L::kK), 16), q_base = desc_rows<D>(smem_u32(smem + L::kQ), 16);
     // (with 64 dims the upper half of M is the same dims again, unused)
     const uint64_t v_base = desc_rows<D>(smem_u32(smem + L::kV), 0), p_base = desc_rows<L::kPW>(smem_u32(smem + L::kP), L::kPiece);
-    auto qk = [&](int st, int b) {  // S^T = K Q^T
+    auto qk = [&](int st, int v, int b) {  // S^T = K Q^T
       tc_fence_after();
-      const uint64_t k0 = k_base + (st * L::kOperand >> 4);
+      const uint64_t k0 = k_base + (st * L::kOperand >> 4), q0 = q_base + (v * PC * L::kQPiece >> 4);
       const uint32_t d = tmem + L::tS(b);
       if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < D / 32; ++kk) mma_f8(d, k0 + (kk * 32 >> 4), q_base + (kk * 32 >> 4), kQkAll, kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < D / 32; ++kk) mma_f8(d, k0 + (kk * 32 >> 4), q0 + (kk * 32 >> 4), kQkAll, kk > 0 ? 1u : 0u);
 #pragma unroll
         for (int p = L::ST; p < PC; ++p)
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk)
-            mma_f8(d + (L::ST - 1) * R, k0 + (kk * 32 >> 4), q_base + ((p * L::kQPiece + kk * 32) >> 4), kQkOne, 1u);
+            mma_f8(d + (L::ST - 1) * R, k0 + (kk * 32 >> 4), q0 + ((p * L::kQPiece + kk * 32) >> 4), kQkOne, 1u);
         tc_commit(&sready[b]);
       }
       __syncwarp();
     };
-    auto pv = [&](int st, int b, bool first) {  // O^T (+)= V^T P^T
+    auto pv = [&](int st, int v, int b, bool first) {  // O^T (+)= V^T P^T
       tc_fence_after();
       const uint64_t v0 = v_base + (st * L::kOperand >> 4), p0 = p_base + (b * L::kPBuf >> 4);
-      const uint32_t d = tmem + L::tO(PH > 1 ? b : 0), keep = first ? 0u : 1u;
+      const uint32_t d = tmem + L::tO(v), keep = first ? 0u : 1u;
       constexpr int N1 = L::kOCols <= 256 ? L::kOCols : 256, N2 = L::kOCols - N1;
       constexpr uint32_t kPv1 = idesc_f8(128, N1, true, true);
       if (leader) {
@@ -380,43 +408,54 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
       }
       __syncwarp();
     };
-    // Whichever product's inputs are ready goes next, so that neither waits behind the other's.
-    Walk w{T0, 0, {}};
-    int nqk = 0, npv = 0, segs = 0;   // products issued; segments begun
-    int kst = 0, vst = 0;             // their stages
-    uint32_t kph = 0;                 // phase of the next K stage
-    uint32_t newer = 0;               // by step mod 8: whether it is one of its segment's first PH, whose O is new
-    int from_start = 0;
+    // Whichever product's inputs are ready goes next, so that no strand waits for another.
+    int nqk[PH], npv[PH], segs[PH];  // of each strand: products issued, segments begun
+    uint32_t starts[PH];             // by step mod 32: whether it begins a segment, whose O is new
+    uint32_t open = (1u << PH) - 1;  // strands with further steps
+    uint64_t taken = 0;              // how often each stage has been read, mod 256
+#pragma unroll
+    for (int v = 0; v < PH; ++v) nqk[v] = npv[v] = segs[v] = 0, starts[v] = 0;
     uint64_t idle_since = 0;
     uint32_t spins = 0;
-    bool start = true;
-    while (w.u < T1 || npv < nqk) {
+    bool busy = true;  // products to come
+    while (busy) {
       bool moved = false;
-      if (w.u < T1 && nqk < npv + 2 * NB) {
-        if (w.left == 0) {
-          begin_segment(w);
-          start = true;
+      busy = open != 0;
+#pragma unroll
+      for (int v = 0; v < PH; ++v) {
+        if ((open >> v & 1) && nqk[v] < npv[v] + NB / PH) {
+          const int n = nqk[v], i = n * PH + v, st = i % STAGES, use = i / STAGES, b = i % NB;
+          // (a barrier tells phases apart by parity: only the stage's next one may be asked for)
+          if ((static_cast<uint32_t>(taken >> (8 * st)) & 255u) == (static_cast<uint32_t>(use) & 255u) && ready(&full[st], use & 1)) {
+            const int info = s_step[i & 15];
+            bool took = false;
+            if (info & 8) {
+              if (leader) mbar_arrive(&empty[st]);
+              ++npv[v];
+              took = true;
+            } else if ((n < NB / PH || ready(&sfree[b], (i / NB - 1) & 1)) && (!(info & 4) || ready(&qready[v], segs[v] & 1))) {
+              qk(st, v, b);
+              starts[v] = (starts[v] & ~(1u << (n & 31))) | static_cast<uint32_t>(info >> 2 & 1) << (n & 31);
+              segs[v] += info >> 2 & 1;
+              took = true;
+            }
+            if (took) {
+              ++nqk[v];
+              taken = (taken & ~(255ull << (8 * st))) | static_cast<uint64_t>((use + 1) & 255) << (8 * st);
+              if (info & 16) open &= ~(1u << v);
+              moved = true;
+            }
+          }
         }
-        const int b = nqk % NB;
-        if (ready(&full[kst], kph) && (nqk < NB || ready(&sfree[b], (nqk / NB - 1) & 1)) && (!start || ready(qready, segs & 1))) {
-          qk(kst, b);
-          if (start) ++segs, from_start = 0;
-          start = false;
-          newer = (newer & ~(1u << (nqk & 7))) | (from_start < PH ? 1u : 0u) << (nqk & 7);
-          ++from_start;
-          const int cnt = min(2, w.left);
-          w.u += cnt;
-          w.left -= cnt;
-          ++nqk;
-          if (++kst == STAGES) kst = 0, kph ^= 1;
-          moved = true;
+        if (npv[v] < nqk[v]) {
+          busy = true;
+          const int i = npv[v] * PH + v, b = i % NB;
+          if (ready(&pready[b], (i / NB) & 1)) {
+            pv(i % STAGES, v, b, starts[v] >> (npv[v] & 31) & 1);
+            ++npv[v];
+            moved = true;
+          }
         }
-      }
-      if (npv < nqk && ready(&pready[npv % NB], (npv / NB) & 1)) {
-        pv(vst, npv % NB, newer >> (npv & 7) & 1);
-        ++npv;
-        if (++vst == STAGES) vst = 0;
-        moved = true;
       }
       // (reading the timer takes some 600 cycles: only where nothing has moved for a while)
       if (moved) {
@@ -439,14 +478,16 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
   } else {
     // ------------------------------------------------------------------ softmax and output
     const int g = tid >> 7, j = tid & 127, gw = warp & 3;    // group, key of the step, warp of the group
-    const int ph = g & (PH - 1), row0 = g / PH * L::RT;      // the accumulator that it works on, its first row
+    const int ph = g & (PH - 1), row0 = g / PH * L::RT;      // its strand, its first row
+    const int sid = g / PH * 128 + j;                        // thread of the strand
+    constexpr int kStrand = 512 / PH;
     constexpr int RT = L::RT;
     const uint32_t lanes = static_cast<uint32_t>(gw * 32) << 16;
     float* s_base = reinterpret_cast<float*>(smem + L::kBase) + ph * R + row0;
-    float* s_gain = reinterpret_cast<float*>(smem + L::kGain);
+    float* s_gain = reinterpret_cast<float*>(smem + L::kGain) + ph * R;
     float* s_corr = reinterpret_cast<float*>(smem + L::kCorr) + ph * R + row0;
     float* s_top = reinterpret_cast<float*>(smem + L::kTop) + g * 4 * RT;
-    float2* s_ml = reinterpret_cast<float2*>(smem + L::kMl);
+    float2* s_ml = reinterpret_cast<float2*>(smem + L::kMl) + ph * R;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!mbar_try_wait(bar, parity)) wait_long(bar, parity, flag, P.err, WL);
       __syncwarp();
@@ -455,7 +496,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
     auto put_q = [&](const Place& p) {
       constexpr int kParts = D / 16;  // threads of a row
       const int live = s_new[p.s] * grp, rows = (live + 15) & ~15;
-      for (int item = tid; item < rows * kParts; item += 512) {
+      for (int item = sid; item < rows * kParts; item += kStrand) {
         const int row = item / kParts, part = item % kParts;
         uint4 in[2] = {};
         if (row < live) {
@@ -492,38 +533,39 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
             const float2 v = __half22float2(from_e4m3x2(b));
             x[2 * k] -= v.x, x[2 * k + 1] -= v.y;
           }
-          *reinterpret_cast<uint4*>(smem + L::kQ + p2 * L::kQPiece + chunk_at<D>(row, part)) = make_uint4(out[0], out[1], out[2], out[3]);
+          *reinterpret_cast<uint4*>(smem + L::kQ + (ph * PC + p2) * L::kQPiece + chunk_at<D>(row, part)) = make_uint4(out[0], out[1], out[2], out[3]);
         }
       }
       fence_async_shared();
-      mbar_arrive(qready);
+      mbar_arrive(&qready[ph]);
     };
 
     float2 l2[RT / 2];  // the key's part of every row's sum
-    int i = 0, seg_no = 0;  // step
-    Walk w{T0, 0, {}};
-    begin_segment(w);
-    put_q(w.at);
-    if (j < RT) s_base[j] = kNone;
-    named_bar_sync(1, 512);
-    for (; w.u < T1; ++seg_no) {
+    int i = ph, seg_no = 0;  // step
+    Walk w = begin_walk(ph);
+    if (w.u < w.end) {
+      begin_segment(w);
+      put_q(w.at);
+      if (j < RT) s_base[j] = kNone;
+      named_bar_sync(6 + ph, kStrand);
+    }
+    for (; w.u < w.end; ++seg_no) {
       const int s = w.at.s, kvh = w.at.g, t0 = w.at.t;
       const bool whole = t0 == 0 && w.left == w.at.nt;
       const int len = s_len[s], n_new = s_new[s], nk = len + n_new;
       const int live = n_new * grp;
 #pragma unroll
       for (int k = 0; k < RT / 2; ++k) l2[k] = {0.f, 0.f};
-      int before = -1;  // the step before of the same accumulator in the segment
-      for (; w.left > 0; ++i) {
+      int before = -1;  // the step before in the segment
+      for (; w.left > 0; i += PH) {
         const int cnt = min(2, w.left), t = w.at.t;
         w.u += cnt;
         w.left -= cnt;
         w.at.t += cnt;
-        if ((i & (PH - 1)) != ph) continue;
         const int st = i % STAGES, b = i % NB;
         wait(&full[st], (i / STAGES) & 1);
         // the thread's key: its scales, and the first row that sees it
-        const int valid = s_valid[i & 15];
+        const int valid = s_step[i & 15] & 3;
         const int key = t * kKeys + j;
         const bool alive = (valid >> (j >> 6) & 1) && key < nk;
         const uint8_t* sc = smem + L::kSc + st * 256 + (j >> 6) * 128 + (j & 63);
@@ -548,7 +590,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
             if (nan) ev = __uint_as_float(0x7fc00000u);
             clear = nan;
           }
-          if (PH < 4) named_bar_sync(6 + ph, 512 / PH);  // (all groups of the step have looked)
+          if (PH < 4) named_bar_sync(6 + ph, kStrand);  // (all groups of the step have looked)
           if (clear && g < PH)
 #pragma unroll 1
             for (int ch = 0; ch < D / 16; ++ch) vrow[ch] = make_uint4(0, 0, 0, 0);
@@ -600,11 +642,15 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
             }
           };
           scores();
-          weights();
-          if (named_bar_any(2 + g, 128, __hgt(__hmax(__low2half(top), __high2half(top)), __float2half_rn(kMost)))) {
+          bool move = before < 0;
+          if (!move) {
+            weights();
+            move = named_bar_any(2 + g, 128, __hgt(__hmax(__low2half(top), __high2half(top)), __float2half_rn(kMost)));
+            if (move) scores();
+          }
+          if (move) {
             // ---- references that move: the rows' maxima over the group, then O and the sums. (Few instructions: most
             // steps do not come here, and those that do wait for each of them to be fetched.)
-            scores();
             float mine = 0.f;
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
@@ -629,7 +675,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
               tc_fence_after();
 #pragma unroll 1
               for (int p = 0; p < PC; ++p) {
-                const uint32_t to = tmem + lanes + L::tO(0) + ph * L::kOCols + p * R + row0 + c * 16;
+                const uint32_t to = tmem + lanes + L::tO(ph) + p * R + row0 + c * 16;
                 uint32_t u[16];
                 __syncwarp();
                 load16(to, u);
@@ -668,7 +714,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
         mbar_arrive(&sfree[b]);
         before = i;
       }
-      // ---- the segment's end. Every score of it has been read once all groups are here: q is the next one's.
+      // ---- the segment's end. Every score of it has been read once the strand's groups are here: q is the next one's.
 #pragma unroll
       for (int c = 0; c < RT / 16; ++c) {
         if (row0 + c * 16 >= live) break;
@@ -678,46 +724,28 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
         const float sum = reduce16(v);
         if ((lane & 1) == 0) s_top[gw * RT + c * 16 + (lane >> 1)] = sum;
       }
-      if (before >= 0) wait(&pvdone[before % NB], (before / NB) & 1);
-      tc_fence_before();
-      named_bar_sync(1, 512);
-      tc_fence_after();
-      if (w.u < T1) {
+      named_bar_sync(6 + ph, kStrand);
+      if (w.u < w.end) {
         begin_segment(w);
         put_q(w.at);
       }
-      // the states into one
-      if (tid < live) {
-        float2 ml[PH];
-        float top = -INFINITY, den = 0.f;
-#pragma unroll
-        for (int k = 0; k < PH; ++k) {
-          const float* sums = reinterpret_cast<const float*>(smem + L::kTop) + (tid / RT * PH + k) * 4 * RT + tid % RT;
-          const float base = reinterpret_cast<const float*>(smem + L::kBase)[k * R + tid];
-          ml[k] = make_float2(base == kNone ? -INFINITY : -base, (sums[0] + sums[RT]) + (sums[2 * RT] + sums[3 * RT]));
-          top = fmaxf(top, ml[k].x);
-        }
-#pragma unroll
-        for (int k = 0; k < PH; ++k) {
-          const float wk = weight_of(ml[k], top);
-          den += wk == 0.f ? 0.f : wk * ml[k].y;
-          reinterpret_cast<float*>(smem + L::kCorr)[k * R + tid] = wk;
-        }
-        s_ml[tid] = make_float2(top, den);
+      if (j < RT) {
+        const float base = s_base[j];
+        s_ml[row0 + j] = make_float2(base == kNone ? -INFINITY : -base, (s_top[j] + s_top[RT + j]) + (s_top[2 * RT + j] + s_top[3 * RT + j]));
+        s_base[j] = kNone;
       }
-      named_bar_sync(1, 512);
-      if (j < RT) s_base[j] = kNone;
-      float* slot = P.part + (2 * static_cast<size_t>(cta) + (seg_no == 0 ? 0 : 1)) * static_cast<size_t>(P.slot_rows) * (D + 2);
+      wait(&pvdone[before % NB], (before / NB) & 1);
+      named_bar_sync(6 + ph, kStrand);
+      tc_fence_after();
+      float* slot = P.part + (2 * static_cast<size_t>(range_of(ph)) + (seg_no == 0 ? 0 : 1)) * static_cast<size_t>(P.slot_rows) * (D + 2);
       if (gw * 32 < D) {  // a dim a lane, four rows at a time, in turn by the groups
         const int dim = gw * 32 + lane;
 #pragma unroll 1
-        for (int r4 = 4 * g; r4 < live; r4 += 16) {
-          uint32_t u[PH][PC][4];
+        for (int r4 = g / PH * 4; r4 < live; r4 += 16 / PH) {
+          uint32_t u[PC][4];
           __syncwarp();
 #pragma unroll
-          for (int k = 0; k < PH; ++k)
-#pragma unroll
-            for (int p = 0; p < PC; ++p) load4(tmem + lanes + L::tO(k) + p * R + r4, u[k][p]);
+          for (int p = 0; p < PC; ++p) load4(tmem + lanes + L::tO(ph) + p * R + r4, u[p]);
           wait_loads();
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -725,13 +753,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
             if (row >= live) break;
             float o = 0.f;
 #pragma unroll
-            for (int k = 0; k < PH; ++k) {
-              float v = 0.f;
-#pragma unroll
-              for (int p = PC - 1; p >= 0; --p) v = fmaf(v, 0.0625f, __uint_as_float(u[k][p][q]));
-              const float wk = reinterpret_cast<const float*>(smem + L::kCorr)[k * R + row];
-              if (wk != 0.f) o = fmaf(wk, v, o);  // (a state without a step: whatever its accumulator holds)
-            }
+            for (int p = PC - 1; p >= 0; --p) o = fmaf(o, 0.0625f, __uint_as_float(u[p][q]));
             if (whole) {
               const float den = s_ml[row].y, y = o * (den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den));
               const int r = new_row(P, row);
@@ -743,9 +765,9 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
           }
         }
       }
-      if (tid < live && !whole) __stcg(reinterpret_cast<float2*>(slot + static_cast<size_t>(P.slot_rows) * D) + tid, s_ml[tid]);
+      if (sid < live && !whole) __stcg(reinterpret_cast<float2*>(slot + static_cast<size_t>(P.slot_rows) * D) + sid, s_ml[sid]);
       tc_fence_before();
-      named_bar_sync(1, 512);  // the buffers are the next segment's
+      named_bar_sync(6 + ph, kStrand);  // the accumulators and sums are the next segment's
     }
   }
 
@@ -796,6 +818,9 @@ int launch_rows(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
 }
 
 }  // namespace
+
+int paged_attn8_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+int paged_attn8_strands(int rows) { return rows <= 16 ? 4 : rows <= 32 ? 2 : 1; }
 
 int paged_attn8_set_attributes() {
   const int e[] = {set_attrs<64, false>(), set_attrs<64, true>(), set_attrs<128, false>(), set_attrs<128, true>()};

@@ -97,10 +97,13 @@ struct PagedAttnParams {
   const int* prefix_table; // its row of the page table
   int n_pre, pre_rows;
   int slot_rows;           // rows of a partial slot
+  int strands;             // ranges of the list that a CTA takes
   float* state;            // [2: own, prefix][batch * rows_per_seq][nq] rows of d outputs, then of (max, sum)
 };
 // Attention over an 8-bit cache, and with a shared prefix.
 int launch_paged_attn_rows(const PagedAttnParams& p, int dtype, cudaStream_t stream);
+int paged_attn8_rows(int rows);     // as paged_attn_rows, of the kernel for 8-bit caches
+int paged_attn8_strands(int rows);  // and its ranges a CTA
 int paged_attn8_set_attributes();
 int launch_paged_attn8(const PagedAttnParams& p, bool bf16, int n_ctas, cudaStream_t stream);
 int launch_paged_attn_join(const PagedAttnParams& p, bool bf16, int n_ctas, cudaStream_t stream);
