@@ -20,12 +20,13 @@
 // the first row that may see the key. The weights' reference m' is a running maximum of s_j + ev_j, so that
 // w_j <= 256 whatever the scales; p_j is w_j 2^-ev_j (|ev_j| <= 40: no overflow).
 //
-// CTA: one per SM, four softmax groups of 128 threads, a warp that issues the products, a producer warp. Of at
-// most 16 rows each group is a strand of its own, with its range of the list, so that one's start and end of a
-// segment run under the others' steps; of more rows two or four groups share a strand's steps, some of the rows
-// each. Every wait is bounded, as in paged_attn_tc.cu.
-#include <type_traits>
-
+// CTA: one per SM; four softmax groups of 128 threads, a key of the step each. Of at most 16 rows each group is a
+// strand of its own: a range of the list, a producer warp, stages, accumulators, so that one's start and end
+// of a segment run under the others' steps. Of more rows two or four groups make a strand, some of its rows
+// each. Of a strand that is one group the first warp issues the products: the next S as soon as the scores of
+// this one are in registers, O once the weights are written. (One warp that issued for four strands noticed what
+// was ready some 1200 cycles late.) Larger strands have a warp for that. Every wait is bounded; past the limit
+// the later ones pass at once and the CTA walks to its end without results.
 #include "paged_attn.cuh"
 #include "quant.cuh"
 
@@ -117,6 +118,7 @@ DEV bool named_bar_any(int id, int n, bool v) {
       : "memory");
   return any != 0;
 }
+DEV void named_bar_arrive(int id, int n) { asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 DEV float warp_max(float x) {  // NaN left out
   float y;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
@@ -179,24 +181,27 @@ struct Layout8 {
   static constexpr int kPBuf = R > 16 ? kPieces * kPiece : kStepKeys * kPW;
   static constexpr int kOCols = R > 16 ? kPieces * R : kPW;
   static constexpr int NB = PH > 1 ? PH : R == 128 && !BF16 ? 1 : 2;  // buffers of S and P, taken by the steps in turn
-  static constexpr int kThreads = 512 + 64;
+  static constexpr int NS = NB / PH;                        // of a strand
+  static constexpr bool kIssuer = PH < 4;                   // a warp for the products
+  static constexpr int kThreads = 512 + 32 * PH * (kIssuer ? 2 : 1);
   static constexpr int kOperand = kStepKeys * D;            // K, or V, of a step
-  static constexpr int STAGES = D == 64 ? (R == 128 ? 6 : 8) : R == 128 ? 3 : R == 64 || !BF16 ? 4 : 5;
+  static constexpr int STAGES = D == 64 ? (R == 128 ? 6 : 8) : R == 128 ? 3 : 4;
+  static constexpr int SP = STAGES / PH;                    // of a strand
   static constexpr int kQPiece = R * D;
   static constexpr int kK = 0;
   static constexpr int kV = kK + STAGES * kOperand;
   static constexpr int kP = kV + STAGES * kOperand;
   static constexpr int kQ = kP + NB * kPBuf;
-  static constexpr int kSc = kQ + PH * kPieces * kQPiece;   // scales of a step: two tiles' 128 bytes
-  static constexpr int kBase = kSc + STAGES * 256;          // [PH][R] references, negative
+  static constexpr int kSc = kQ + PH * kPieces * kQPiece;   // [PH][2 SP] scales of a step: two tiles' 128 bytes
+  static constexpr int kBase = kSc + 2 * STAGES * 256;      // [PH][R] references, negative
   static constexpr int kGain = kBase + PH * R * 4;          // [PH][R] 1 / the power of two that q was scaled by
   static constexpr int kCorr = kGain + PH * R * 4;          // [PH][R] factors of a moved reference
   static constexpr int kTop = kCorr + PH * R * 4;           // [4 groups][4 warps][RT] warps' maxima; sums at the end
   static constexpr int kMl = kTop + 4 * 4 * RT * 4;         // [PH][R] (max, sum)
   static constexpr int kBar = kMl + PH * R * 8;
-  static constexpr int kBars = 2 * STAGES + 4 * NB + PH + 1;  // full, empty; S ready, free, P ready, PV done [NB]; Q [PH]; done
-  static constexpr int kFlags = kBar + kBars * 8;           // [0] abort, [1] TMEM base, [4..19] steps: 1, 2: tiles that are there, 4: begins a segment, 8: none (its strand is done), 16: of the last round
-  static constexpr int kWarpSums = kFlags + 80;
+  static constexpr int kBars = 6 * SP + 4 * NS + 2;         // of a strand: K full, empty, V full, empty [SP]; scales full [2 SP]; S ready, PV done, S free, P ready [NS]; Q; all done
+  static constexpr int kFlags = kBar + PH * kBars * 8;      // [0] abort, [1] TMEM base, then [PH][16] steps: 1, 2: tiles that are there, 4: a segment's first, 8: the last
+  static constexpr int kWarpSums = kFlags + 16 + PH * 64;
   static constexpr int kPre = kWarpSums + 128;
   static constexpr int smem(int batch) { return 1024 + kPre + (3 * batch + 1) * 4; }
   static constexpr uint32_t tS(int b) { return b * ST * R; }     // TMEM columns
@@ -208,19 +213,10 @@ struct Layout8 {
 template <int D, int R, int PH, bool BF16>
 __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_attn8_kernel(const __grid_constant__ PagedAttnParams P) {
   using L = Layout8<D, R, PH, BF16>;
-  constexpr int NB = L::NB, STAGES = L::STAGES, PC = L::kPieces;
+  constexpr int NS = L::NS, SP = L::SP, PC = L::kPieces;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
-  uint64_t* empty = full + STAGES;
-  uint64_t* sready = empty + STAGES;
-  uint64_t* sfree = sready + NB;
-  uint64_t* pready = sfree + NB;
-  uint64_t* pvdone = pready + NB;
-  uint64_t* qready = pvdone + NB;
-  uint64_t* mdone = qready + PH;
   volatile int* flag = reinterpret_cast<volatile int*>(smem + L::kFlags);
-  volatile int* s_step = flag + 4;  // by step mod 16, more than the ring holds
   int* s_warp = reinterpret_cast<int*>(smem + L::kWarpSums);
   int* s_pre = reinterpret_cast<int*>(smem + L::kPre);
   int* s_len = s_pre + P.batch + 1;
@@ -229,18 +225,11 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
   const uint64_t WL = P.wait_ns;
 
   if (tid == 0) {
-    for (int i = 0; i < STAGES; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
+    for (int i = 0; i < PH * L::kBars; ++i) {
+      const int k = i % L::kBars - 6 * SP - 2 * NS;  // from S free on
+      mbar_init(&bars[i], k >= 0 && k <= 2 * NS ? 512 / PH : 1);
     }
-    for (int i = 0; i < NB; ++i) {
-      mbar_init(&sready[i], 1);
-      mbar_init(&sfree[i], 512 / PH);
-      mbar_init(&pready[i], 512 / PH);
-      mbar_init(&pvdone[i], 1);
-    }
-    for (int i = 0; i < PH; ++i) mbar_init(&qready[i], 512 / PH);
-    mbar_init(mdone, 1);
     flag[0] = 0;
     fence_mbar_init();
     tma_prefetch_desc(&P.kmap);
@@ -254,59 +243,109 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
   const int G = n_ranges(T, gridDim.x, PH);
   const int cta = blockIdx.x;
   if (cta >= G) return;  // the whole CTA, before it holds any tensor memory
-  constexpr int kIssuer = 16, kProducer = 17;
-  if (warp == kIssuer) tmem_alloc(reinterpret_cast<uint32_t*>(smem + L::kFlags + 4), 512);
+  if (warp == 16) tmem_alloc(reinterpret_cast<uint32_t*>(smem + L::kFlags + 4), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(flag[1]);
 
-  // A strand's walk: steps of up to two tiles of the segments of its range. Step n of strand v is the CTA's step
-  // n * PH + v; strands that are done have empty steps until the last one is.
-  struct Walk {
-    long long u, end;
-    int left;  // tiles of the segment that are left
-    Place at;  // of the next tile
+  // The thread's strand, and its walk: steps of up to two tiles of the segments of its range.
+  const int g = tid >> 7;                                     // softmax group
+  const int ph = warp < 16 ? g & (PH - 1) : (warp - 16) % PH;
+  const int range = ph * static_cast<int>(gridDim.x) + cta;
+  const long long end = range < G ? range_begin(range + 1, T, G) : 0;
+  long long u = range < G ? range_begin(range, T, G) : 0;     // the next tile
+  Place at{};
+  int left = 0;                                               // tiles of the segment that are left
+  auto begin_segment = [&] {
+    at = locate(s_pre, batch, nkv, u);
+    left = static_cast<int>(min(end - u, static_cast<long long>(at.nt - at.t)));
   };
-  auto range_of = [&](int v) { return v * static_cast<int>(gridDim.x) + cta; };
-  auto begin_walk = [&](int v) {
-    const int r = range_of(v);
-    return r < G ? Walk{range_begin(r, T, G), range_begin(r + 1, T, G), 0, {}} : Walk{0, 0, 0, {}};
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + L::kBar) + ph * L::kBars;
+  uint64_t* kempty = kfull + SP;
+  uint64_t* vfull = kempty + SP;
+  uint64_t* vempty = vfull + SP;
+  uint64_t* scfull = vempty + SP;
+  uint64_t* sready = scfull + 2 * SP;
+  uint64_t* pvdone = sready + NS;
+  uint64_t* sfree = pvdone + NS;
+  uint64_t* pready = sfree + NS;
+  uint64_t* qready = pready + NS;
+  uint64_t* mdone = qready + 1;
+  volatile int* s_step = flag + 4 + ph * 16;  // by step mod 16, more than a ring holds
+  uint8_t* kring = smem + L::kK + ph * SP * L::kOperand;
+  uint8_t* vring = smem + L::kV + ph * SP * L::kOperand;
+  uint8_t* scring = smem + L::kSc + ph * 2 * SP * 256;  // twice as long: a step's scales are read after K's stage may go on
+
+  // The products of step n, by one lane; the whole warp is here, so that descriptors are built in uniform registers.
+  constexpr uint32_t kQkAll = idesc_f8(128, L::ST * R, false, false), kQkOne = idesc_f8(128, R, false, false);
+  auto qk = [&](int n) {  // S^T = K Q^T
+    const uint64_t k0 = desc_rows<D>(smem_u32(kring) + n % SP * L::kOperand, 16), q0 = desc_rows<D>(smem_u32(smem + L::kQ) + ph * PC * L::kQPiece, 16);
+    const uint32_t d = tmem + L::tS(ph * NS + n % NS);
+    tc_fence_after();
+    if (elect_one()) {
+#pragma unroll
+      for (int kk = 0; kk < D / 32; ++kk) mma_f8(d, k0 + (kk * 32 >> 4), q0 + (kk * 32 >> 4), kQkAll, kk > 0 ? 1u : 0u);
+#pragma unroll
+      for (int p = L::ST; p < PC; ++p)
+#pragma unroll
+        for (int kk = 0; kk < D / 32; ++kk)
+          mma_f8(d + (L::ST - 1) * R, k0 + (kk * 32 >> 4), q0 + ((p * L::kQPiece + kk * 32) >> 4), kQkOne, 1u);
+      tc_commit(&sready[n % NS]);
+      tc_commit(&kempty[n % SP]);
+    }
+    __syncwarp();
   };
-  auto begin_segment = [&](Walk& w) {
-    w.at = locate(s_pre, batch, nkv, w.u);
-    w.left = static_cast<int>(min(w.end - w.u, static_cast<long long>(w.at.nt - w.at.t)));
+  auto pv = [&](int n, bool first) {  // O^T (+)= V^T P^T. With 64 dims the upper half of M is the same dims again, unused.
+    const uint64_t v0 = desc_rows<D>(smem_u32(vring) + n % SP * L::kOperand, 0);
+    const uint64_t p0 = desc_rows<L::kPW>(smem_u32(smem + L::kP) + (ph * NS + n % NS) * L::kPBuf, L::kPiece);
+    const uint32_t d = tmem + L::tO(ph), keep = first ? 0u : 1u;
+    constexpr int N1 = L::kOCols <= 256 ? L::kOCols : 256, N2 = L::kOCols - N1;
+    constexpr uint32_t kPv1 = idesc_f8(128, N1, true, true);
+    tc_fence_after();
+    if (elect_one()) {
+#pragma unroll
+      for (int kk = 0; kk < kStepKeys / 32; ++kk) {
+        mma_f8(d, v0 + (kk * 32 * D >> 4), p0 + (kk * 32 * L::kPW >> 4), kPv1, kk > 0 ? 1u : keep);
+        if constexpr (N2 > 0) {
+          constexpr uint32_t kPv2 = idesc_f8(128, N2, true, true);
+          mma_f8(d + N1, v0 + (kk * 32 * D >> 4), p0 + ((N1 / R * L::kPiece + kk * 32 * R) >> 4), kPv2, kk > 0 ? 1u : keep);
+        }
+      }
+      tc_commit(&pvdone[n % NS]);
+      tc_commit(&vempty[n % SP]);
+    }
+    __syncwarp();
   };
 
-  if (warp == kProducer) {
-    // ------------------------------------------------------------------ producer: 32 / PH lanes a strand
-    constexpr int LS = 32 / PH;
+  if (warp >= 16 && warp < 16 + PH) {
+    // ------------------------------------------------------------------ producer
     const uint64_t pol = T * (2 * kKeys * D) > (16ll << 20) ? policy_evict_first() : policy_evict_last();
-    int i0 = 0;       // the round's first step
-    bool go = true;   // the same in every lane
-    Walk w = begin_walk(lane / LS);
-    int ids = -1, id0 = LS;  // page ids of the segment's next tiles, one a lane; the lane that has the next one
-    while (go && __any_sync(0xffffffffu, w.u < w.end)) {
-      // every strand's next step
-      int info = 8, page[2] = {-1, -1}, head = 0;
-      const bool some = w.u < w.end;
-      if (some) {
-        info = 0;
-        if (w.left == 0) {
-          begin_segment(w);
-          id0 = LS;
-          info = 4;
-        }
-        head = w.at.g;
+    int n = 0, kn = 0, vn = 0;  // step; copies of K and of V issued
+    bool go = true;             // the same in every lane
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      bool ok = !flag[0];
+      if (ok && lane == 0 && !mbar_wait(bar, parity, WL)) {
+        raise_flag(P.err, kDevTimeout);
+        flag[0] = 1;
+        ok = false;
       }
-      const int cnt = some ? min(2, w.left) : 0;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (h < cnt && id0 == LS) {
+      go = __all_sync(0xffffffffu, ok);
+    };
+    int ids = -1, id0 = 32;  // page ids of the segment's next tiles, one a lane; the lane that has the next one
+    while (u < end && go) {
+      const bool start = left == 0;
+      if (start) {
+        begin_segment();
+        id0 = 32;
+      }
+      int page[2] = {-1, -1};
+      const int cnt = min(2, left);
+      for (int h = 0; h < cnt; ++h) {
+        if (id0 == 32) {
           ids = -1;
-          const int k = lane % LS;
-          if (k < w.left - h) {
-            ids = __ldcg(P.page_table + static_cast<size_t>(w.at.s) * P.pages_per_seq + w.at.t + h + k);
+          if (lane < left - h) {
+            ids = __ldcg(P.page_table + static_cast<size_t>(at.s) * P.pages_per_seq + at.t + h + lane);
             if (ids < 0 || ids >= P.n_pages) {
               raise_flag(P.err, kDevCapacity);
               ids = -1;
@@ -314,148 +353,76 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
           }
           id0 = 0;
         }
-        __syncwarp();
-        const int id = __shfl_sync(0xffffffffu, ids, (lane & ~(LS - 1)) + (id0 & (LS - 1)));
-        if (h < cnt) {
-          page[h] = id;
-          info |= (id >= 0) << h;
-          ++id0;
-        }
+        page[h] = __shfl_sync(0xffffffffu, ids, id0++);
       }
-      w.u += cnt;
-      w.left -= cnt;
-      w.at.t += cnt;
-      if (!__any_sync(0xffffffffu, w.u < w.end)) info |= 16;
-#pragma unroll 1
-      for (int v = 0; v < PH; ++v) {
-        const int i = i0 + v, st = i % STAGES;
-        bool ok = !flag[0];
-        if (lane == v * LS) {
-          if (ok && i >= STAGES && !mbar_wait(&empty[st], (i / STAGES - 1) & 1, WL)) {
-            raise_flag(P.err, kDevTimeout);
-            flag[0] = 1;
-            ok = false;
-          }
-          if (ok) {
-            s_step[i & 15] = info;
-            const int tiles = (info & 1) + (info >> 1 & 1);
-            if (tiles) mbar_arrive_expect_tx(&full[st], tiles * (2 * kKeys * D + 2 * kKeys));
-            else mbar_arrive(&full[st]);
+      const int st = n % SP, sc = n % (2 * SP), valid = (page[0] >= 0) | (page[1] >= 0) << 1, tiles = (valid & 1) + (valid >> 1);
+      if (n >= SP) wait(&kempty[st], (n / SP - 1) & 1);
+      if (!go) break;
+      if (lane == 0) {
+        s_step[n & 15] = valid | (start ? 4 : 0) | (u + cnt >= end ? 8 : 0);
+        if (tiles) {
+          mbar_arrive_expect_tx(&scfull[sc], tiles * 2 * kKeys);
+          mbar_arrive_expect_tx(&kfull[st], tiles * kKeys * D);
+        } else {
+          mbar_arrive(&scfull[sc]);
+          mbar_arrive(&kfull[st]);
+        }
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              if (info >> h & 1) {
-                tma_load_3d(smem + L::kK + st * L::kOperand + h * kKeys * D, &P.kmap, &full[st], 0, head, page[h] * kKeys, pol);
-                tma_load_3d(smem + L::kV + st * L::kOperand + h * kKeys * D, &P.vmap, &full[st], 0, head, page[h] * kKeys, pol);
-                bulk_load(smem + L::kSc + st * 256 + h * 128, P.scales + (static_cast<size_t>(page[h]) * nkv + head) * 128, 128, &full[st]);
-              }
+        for (int h = 0; h < 2; ++h)
+          if (page[h] >= 0) {
+            tma_load_3d(kring + st * L::kOperand + h * kKeys * D, &P.kmap, &kfull[st], 0, at.g, page[h] * kKeys, pol);
+            bulk_load(scring + sc * 256 + h * 128, P.scales + (static_cast<size_t>(page[h]) * nkv + at.g) * 128, 128, &scfull[sc]);
           }
-        }
-        go = __all_sync(0xffffffffu, ok);
-        if (!go) {
-          i0 += v;  // steps issued
-          break;
-        }
       }
-      if (go) i0 += PH;
+      __syncwarp();
+      kn = n + 1;
+      if (n >= SP) wait(&vempty[st], (n / SP - 1) & 1);
+      if (!go) break;
+      if (lane == 0) {
+        if (tiles) mbar_arrive_expect_tx(&vfull[st], tiles * kKeys * D);
+        else mbar_arrive(&vfull[st]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (page[h] >= 0) tma_load_3d(vring + st * L::kOperand + h * kKeys * D, &P.vmap, &vfull[st], 0, at.g, page[h] * kKeys, pol);
+      }
+      __syncwarp();
+      vn = ++n;
+      u += cnt;
+      left -= cnt;
+      at.t += cnt;
     }
     // every copy issued has landed before the CTA leaves
-    if (lane == 0)
-      for (int k = max(0, i0 - STAGES); k < i0; ++k) mbar_wait(&full[k % STAGES], (k / STAGES) & 1, WL);
+    if (lane == 0) {
+      for (int k = max(0, kn - SP); k < kn; ++k) mbar_wait(&kfull[k % SP], (k / SP) & 1, WL);
+      for (int k = max(0, kn - 2 * SP); k < kn; ++k) mbar_wait(&scfull[k % (2 * SP)], (k / (2 * SP)) & 1, WL);
+      for (int k = max(0, vn - SP); k < vn; ++k) mbar_wait(&vfull[k % SP], (k / SP) & 1, WL);
+    }
     __syncwarp();
-  } else if (warp == kIssuer) {
-    // ------------------------------------------------------------------ issuer of the products
-    // The whole warp walks, one lane issues: descriptors that are the same in every lane are built in
-    // uniform registers, which is where the products take them from.
-    const bool leader = elect_one();
+  } else if (warp >= 16) {
+    // ------------------------------------------------------------------ issuer: whichever product's inputs are ready goes next
     auto ready = [](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, test_wait(bar, parity)) != 0; };
-    constexpr uint32_t kQkAll = idesc_f8(128, L::ST * R, false, false), kQkOne = idesc_f8(128, R, false, false);
-    const uint64_t k_base = desc_rows<D>(smem_u32(smem + L::kK), 16), q_base = desc_rows<D>(smem_u32(smem + L::kQ), 16);
-    // (with 64 dims the upper half of M is the same dims again, unused)
-    const uint64_t v_base = desc_rows<D>(smem_u32(smem + L::kV), 0), p_base = desc_rows<L::kPW>(smem_u32(smem + L::kP), L::kPiece);
-    auto qk = [&](int st, int v, int b) {  // S^T = K Q^T
-      tc_fence_after();
-      const uint64_t k0 = k_base + (st * L::kOperand >> 4), q0 = q_base + (v * PC * L::kQPiece >> 4);
-      const uint32_t d = tmem + L::tS(b);
-      if (leader) {
-#pragma unroll
-        for (int kk = 0; kk < D / 32; ++kk) mma_f8(d, k0 + (kk * 32 >> 4), q0 + (kk * 32 >> 4), kQkAll, kk > 0 ? 1u : 0u);
-#pragma unroll
-        for (int p = L::ST; p < PC; ++p)
-#pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk)
-            mma_f8(d + (L::ST - 1) * R, k0 + (kk * 32 >> 4), q0 + ((p * L::kQPiece + kk * 32) >> 4), kQkOne, 1u);
-        tc_commit(&sready[b]);
-      }
-      __syncwarp();
-    };
-    auto pv = [&](int st, int v, int b, bool first) {  // O^T (+)= V^T P^T
-      tc_fence_after();
-      const uint64_t v0 = v_base + (st * L::kOperand >> 4), p0 = p_base + (b * L::kPBuf >> 4);
-      const uint32_t d = tmem + L::tO(v), keep = first ? 0u : 1u;
-      constexpr int N1 = L::kOCols <= 256 ? L::kOCols : 256, N2 = L::kOCols - N1;
-      constexpr uint32_t kPv1 = idesc_f8(128, N1, true, true);
-      if (leader) {
-#pragma unroll
-        for (int kk = 0; kk < kStepKeys / 32; ++kk) {
-          mma_f8(d, v0 + (kk * 32 * D >> 4), p0 + (kk * 32 * L::kPW >> 4), kPv1, kk > 0 ? 1u : keep);
-          if constexpr (N2 > 0) {
-            constexpr uint32_t kPv2 = idesc_f8(128, N2, true, true);
-            mma_f8(d + N1, v0 + (kk * 32 * D >> 4), p0 + ((N1 / R * L::kPiece + kk * 32 * R) >> 4), kPv2, kk > 0 ? 1u : keep);
-          }
-        }
-        tc_commit(&pvdone[b]);
-        tc_commit(&empty[st]);
-      }
-      __syncwarp();
-    };
-    // Whichever product's inputs are ready goes next, so that no strand waits for another.
-    int nqk[PH], npv[PH], segs[PH];  // of each strand: products issued, segments begun
-    uint32_t starts[PH];             // by step mod 32: whether it begins a segment, whose O is new
-    uint32_t open = (1u << PH) - 1;  // strands with further steps
-    uint64_t taken = 0;              // how often each stage has been read, mod 256
-#pragma unroll
-    for (int v = 0; v < PH; ++v) nqk[v] = npv[v] = segs[v] = 0, starts[v] = 0;
+    int nqk = 0, npv = 0, segs = 0;  // products issued, segments begun
+    uint32_t starts = 0;             // by step mod 32: whether it begins a segment, whose O is new
+    bool open = u < end;             // steps to come
     uint64_t idle_since = 0;
     uint32_t spins = 0;
-    bool busy = true;  // products to come
-    while (busy) {
+    while (open || npv < nqk) {
       bool moved = false;
-      busy = open != 0;
-#pragma unroll
-      for (int v = 0; v < PH; ++v) {
-        if ((open >> v & 1) && nqk[v] < npv[v] + NB / PH) {
-          const int n = nqk[v], i = n * PH + v, st = i % STAGES, use = i / STAGES, b = i % NB;
-          // (a barrier tells phases apart by parity: only the stage's next one may be asked for)
-          if ((static_cast<uint32_t>(taken >> (8 * st)) & 255u) == (static_cast<uint32_t>(use) & 255u) && ready(&full[st], use & 1)) {
-            const int info = s_step[i & 15];
-            bool took = false;
-            if (info & 8) {
-              if (leader) mbar_arrive(&empty[st]);
-              ++npv[v];
-              took = true;
-            } else if ((n < NB / PH || ready(&sfree[b], (i / NB - 1) & 1)) && (!(info & 4) || ready(&qready[v], segs[v] & 1))) {
-              qk(st, v, b);
-              starts[v] = (starts[v] & ~(1u << (n & 31))) | static_cast<uint32_t>(info >> 2 & 1) << (n & 31);
-              segs[v] += info >> 2 & 1;
-              took = true;
-            }
-            if (took) {
-              ++nqk[v];
-              taken = (taken & ~(255ull << (8 * st))) | static_cast<uint64_t>((use + 1) & 255) << (8 * st);
-              if (info & 16) open &= ~(1u << v);
-              moved = true;
-            }
-          }
+      if (open && nqk < npv + 2 * NS && ready(&kfull[nqk % SP], (nqk / SP) & 1)) {
+        const int info = s_step[nqk & 15];
+        if ((nqk < NS || ready(&sfree[nqk % NS], (nqk / NS - 1) & 1)) && (!(info & 4) || ready(qready, segs & 1))) {
+          qk(nqk);
+          starts = (starts & ~(1u << (nqk & 31))) | static_cast<uint32_t>(info >> 2 & 1) << (nqk & 31);
+          segs += info >> 2 & 1;
+          ++nqk;
+          if (info & 8) open = false;
+          moved = true;
         }
-        if (npv[v] < nqk[v]) {
-          busy = true;
-          const int i = npv[v] * PH + v, b = i % NB;
-          if (ready(&pready[b], (i / NB) & 1)) {
-            pv(i % STAGES, v, b, starts[v] >> (npv[v] & 31) & 1);
-            ++npv[v];
-            moved = true;
-          }
-        }
+      }
+      if (npv < nqk && ready(&pready[npv % NS], (npv / NS) & 1) && ready(&vfull[npv % SP], (npv / SP) & 1)) {
+        pv(npv, starts >> (npv & 31) & 1);
+        ++npv;
+        moved = true;
       }
       // (reading the timer takes some 600 cycles: only where nothing has moved for a while)
       if (moved) {
@@ -470,18 +437,17 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
         }
       }
     }
-    if (leader) {
+    if (elect_one()) {
       tc_commit(mdone);
       if (!mbar_wait(mdone, 0, WL)) raise_flag(P.err, kDevTimeout);
     }
     __syncwarp();
   } else {
-    // ------------------------------------------------------------------ softmax and output
-    const int g = tid >> 7, j = tid & 127, gw = warp & 3;    // group, key of the step, warp of the group
-    const int ph = g & (PH - 1), row0 = g / PH * L::RT;      // its strand, its first row
+    // ------------------------------------------------------------------ softmax, products and output
+    const int j = tid & 127, gw = warp & 3, row0 = g / PH * L::RT;  // key of the step, warp of the group, first row
     const int sid = g / PH * 128 + j;                        // thread of the strand
-    constexpr int kStrand = 512 / PH;
-    constexpr int RT = L::RT;
+    const bool issues = !L::kIssuer && gw == 0;              // the products
+    constexpr int RT = L::RT, kStrand = 512 / PH;
     const uint32_t lanes = static_cast<uint32_t>(gw * 32) << 16;
     float* s_base = reinterpret_cast<float*>(smem + L::kBase) + ph * R + row0;
     float* s_gain = reinterpret_cast<float*>(smem + L::kGain) + ph * R;
@@ -493,9 +459,9 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
       __syncwarp();
     };
     // a segment's q, taken apart; rows up to the next multiple of 16 that are not there are zero
-    auto put_q = [&](const Place& p) {
+    auto put_q = [&] {
       constexpr int kParts = D / 16;  // threads of a row
-      const int live = s_new[p.s] * grp, rows = (live + 15) & ~15;
+      const int live = s_new[at.s] * grp, rows = (live + 15) & ~15;
       for (int item = sid; item < rows * kParts; item += kStrand) {
         const int row = item / kParts, part = item % kParts;
         uint4 in[2] = {};
@@ -503,7 +469,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
           const int r = new_row(P, row);
           const uint4* src = reinterpret_cast<const uint4*>(
               static_cast<const uint16_t*>(P.q) +
-              ((static_cast<size_t>(p.s) * P.rows_per_seq + r) * P.nq + static_cast<size_t>(p.g) * grp + row - r * grp) * D + part * 16);
+              ((static_cast<size_t>(at.s) * P.rows_per_seq + r) * P.nq + static_cast<size_t>(at.g) * grp + row - r * grp) * D + part * 16);
           in[0] = __ldcg(src), in[1] = __ldcg(src + 1);
         }
         const uint32_t* u = reinterpret_cast<const uint32_t*>(in);
@@ -537,38 +503,43 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
         }
       }
       fence_async_shared();
-      mbar_arrive(&qready[ph]);
+      if (L::kIssuer) mbar_arrive(qready);
     };
 
     float2 l2[RT / 2];  // the key's part of every row's sum
-    int i = ph, seg_no = 0;  // step
-    Walk w = begin_walk(ph);
-    if (w.u < w.end) {
-      begin_segment(w);
-      put_q(w.at);
+    int n = 0, seg_no = 0;  // step
+    if (u < end) {
+      begin_segment();
+      put_q();
       if (j < RT) s_base[j] = kNone;
       named_bar_sync(6 + ph, kStrand);
     }
-    for (; w.u < w.end; ++seg_no) {
-      const int s = w.at.s, kvh = w.at.g, t0 = w.at.t;
-      const bool whole = t0 == 0 && w.left == w.at.nt;
+    for (; u < end; ++seg_no) {
+      const int s = at.s, kvh = at.g;
+      const bool whole = at.t == 0 && left == at.nt;
       const int len = s_len[s], n_new = s_new[s], nk = len + n_new;
       const int live = n_new * grp;
+      const int last = live > row0 ? min(RT / 16, (live - row0 + 15) / 16) - 1 : -1;  // of the group's 16 rows at a time
 #pragma unroll
       for (int k = 0; k < RT / 2; ++k) l2[k] = {0.f, 0.f};
-      int before = -1;  // the step before in the segment
-      for (; w.left > 0; i += PH) {
-        const int cnt = min(2, w.left), t = w.at.t;
-        w.u += cnt;
-        w.left -= cnt;
-        w.at.t += cnt;
-        const int st = i % STAGES, b = i % NB;
-        wait(&full[st], (i / STAGES) & 1);
+      const int n0 = n, n1 = n + ((left + 1) >> 1);  // the segment's steps
+      if (issues)
+        for (int k = n0; k < min(n1, n0 + NS); ++k) {
+          wait(&kfull[k % SP], (k / SP) & 1);
+          qk(k);
+        }
+      for (; n < n1; ++n) {
+        const int cnt = min(2, left), t = at.t;
+        u += cnt;
+        left -= cnt;
+        at.t += cnt;
+        const int st = n % SP, b = n % NS;
+        wait(&scfull[n % (2 * SP)], (n / (2 * SP)) & 1);
         // the thread's key: its scales, and the first row that sees it
-        const int valid = s_step[i & 15] & 3;
+        const int valid = s_step[n & 15] & 3;
         const int key = t * kKeys + j;
         const bool alive = (valid >> (j >> 6) & 1) && key < nk;
-        const uint8_t* sc = smem + L::kSc + st * 256 + (j >> 6) * 128 + (j & 63);
+        const uint8_t* sc = scring + n % (2 * SP) * 256 + (j >> 6) * 128 + (j & 63);
         const uint32_t kb = sc[0], vb = sc[64];
         const float f = P.scale_log2 * scale_value(kb);
         float ev = vb == kScaleNan ? __uint_as_float(0x7fc00000u) : static_cast<float>(static_cast<int>(vb) - kScaleBias);
@@ -578,7 +549,10 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
         if (edge) {
           // Values that no row sees are cleared (0 * NaN is NaN); a key that some rows see and that has a NaN
           // among its values becomes one of zeros whose scale is NaN.
-          uint4* vrow = reinterpret_cast<uint4*>(smem + L::kV + st * L::kOperand + j * D);
+          uint4* vrow = reinterpret_cast<uint4*>(vring + st * L::kOperand + j * D);
+          // (a barrier tells phases apart by parity: only after the stage's last values are spent may the next be asked for)
+          if (n >= NS) wait(&pvdone[b], (n / NS - 1) & 1);
+          wait(&vfull[st], (n / SP) & 1);
           bool clear = !alive;
           if (alive && key >= len && n_new > 1) {
             bool nan = false;
@@ -595,20 +569,30 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
 #pragma unroll 1
             for (int ch = 0; ch < D / 16; ++ch) vrow[ch] = make_uint4(0, 0, 0, 0);
         }
-        wait(&sready[b], (i / NB) & 1);
+        wait(&sready[b], (n / NS) & 1);
         tc_fence_after();
         const float2 f2 = {f, f}, ev2 = {ev, ev}, inv2 = {inv_v, inv_v};
-        bool waited = i < NB;  // for the last product from the buffer of P
+        bool later = false;  // the next S, where its K is not there yet
+        auto scores_read = [&] {  // by the group: the next S may come into their place
+          if (L::kIssuer) {
+            mbar_arrive(&sfree[b]);
+          } else if (issues && n + NS < n1) {
+            later = !__all_sync(0xffffffffu, test_wait(&kfull[(n + NS) % SP], ((n + NS) / SP) & 1));
+            if (!later) qk(n + NS);
+          }
+        };
+        if (last < 0) scores_read();
 #pragma unroll
         for (int c = 0; c < RT / 16; ++c) {  // 16 rows at a time
-          if (row0 + c * 16 >= live) break;
-          const uint32_t ts = tmem + lanes + L::tS(b) + row0 + c * 16;
+          if (c > last) break;
+          const uint32_t ts = tmem + lanes + L::tS(ph * NS + b) + row0 + c * 16;
           float2 x[8];
           auto scores = [&] {  // s_j + ev_j; what a row does not see is -inf
             uint32_t u[L::ST][16];
 #pragma unroll
             for (int p = 0; p < L::ST; ++p) load16(ts + p * R, u[p]);
             wait_loads();
+            tc_fence_before();
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               x[k] = {__uint_as_float(u[0][2 * k]), __uint_as_float(u[0][2 * k + 1])};
@@ -642,11 +626,12 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
             }
           };
           scores();
-          bool move = before < 0;
+          bool move = n == n0;
           if (!move) {
             weights();
             move = named_bar_any(2 + g, 128, __hgt(__hmax(__low2half(top), __high2half(top)), __float2half_rn(kMost)));
             if (move) scores();
+            else if (c == last) scores_read();
           }
           if (move) {
             // ---- references that move: the rows' maxima over the group, then O and the sums. (Few instructions: most
@@ -659,6 +644,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
             }
             if (lane < 16) s_top[gw * RT + c * 16 + lane] = mine;
             named_bar_sync(2 + g, 128);
+            if (c == last) scores_read();
             if (j < 16) {
               const float* tops = s_top + c * 16 + j;
               const float most = fmaxf(fmaxf(tops[0], tops[RT]), fmaxf(tops[2 * RT], tops[3 * RT]));
@@ -670,8 +656,8 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
             named_bar_sync(2 + g, 128);
 #pragma unroll
             for (int k = 0; k < 8; ++k) l2[c * 8 + k].x *= s_corr[c * 16 + 2 * k], l2[c * 8 + k].y *= s_corr[c * 16 + 2 * k + 1];
-            if (before >= 0) {
-              wait(&pvdone[before % NB], (before / NB) & 1);
+            if (n > n0) {
+              wait(&pvdone[(n - 1) % NS], ((n - 1) / NS) & 1);
               tc_fence_after();
 #pragma unroll 1
               for (int p = 0; p < PC; ++p) {
@@ -688,9 +674,8 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
             }
             weights();
           }
-          if (!waited) wait(&pvdone[b], (i / NB - 1) & 1);
-          waited = true;
-          uint8_t* to = smem + L::kP + b * L::kPBuf;
+          if (c == 0 && n >= NS) wait(&pvdone[b], (n / NS - 1) & 1);  // the last product from the buffer
+          uint8_t* to = smem + L::kP + (ph * NS + b) * L::kPBuf;
 #pragma unroll
           for (int k = 0; k < 8; ++k) l2[c * 8 + k] = fma2(x[k], inv2, l2[c * 8 + k]);
 #pragma unroll
@@ -708,11 +693,23 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
             *reinterpret_cast<uint4*>(to + (R > 16 ? p * L::kPiece + chunk_at<R>(j, row0 / 16 + c) : chunk_at<L::kPW>(j, p))) = make_uint4(out[0], out[1], out[2], out[3]);
           }
         }
+        // (a group without rows must not be a step ahead of the others at P's barrier either)
+        if (last < 0 && n >= NS) wait(&pvdone[b], (n / NS - 1) & 1);
         fence_async_shared();
         tc_fence_before();
-        mbar_arrive(&pready[b]);
-        mbar_arrive(&sfree[b]);
-        before = i;
+        if (L::kIssuer) {
+          mbar_arrive(&pready[b]);
+        } else if (issues) {
+          named_bar_sync(10 + ph, kStrand);
+          wait(&vfull[st], (n / SP) & 1);
+          pv(n, n == n0);
+          if (later) {
+            wait(&kfull[(n + NS) % SP], ((n + NS) / SP) & 1);
+            qk(n + NS);
+          }
+        } else {
+          named_bar_arrive(10 + ph, kStrand);
+        }
       }
       // ---- the segment's end. Every score of it has been read once the strand's groups are here: q is the next one's.
 #pragma unroll
@@ -725,19 +722,19 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
         if ((lane & 1) == 0) s_top[gw * RT + c * 16 + (lane >> 1)] = sum;
       }
       named_bar_sync(6 + ph, kStrand);
-      if (w.u < w.end) {
-        begin_segment(w);
-        put_q(w.at);
+      if (u < end) {
+        begin_segment();
+        put_q();
       }
       if (j < RT) {
         const float base = s_base[j];
         s_ml[row0 + j] = make_float2(base == kNone ? -INFINITY : -base, (s_top[j] + s_top[RT + j]) + (s_top[2 * RT + j] + s_top[3 * RT + j]));
         s_base[j] = kNone;
       }
-      wait(&pvdone[before % NB], (before / NB) & 1);
+      wait(&pvdone[(n - 1) % NS], ((n - 1) / NS) & 1);
       named_bar_sync(6 + ph, kStrand);
       tc_fence_after();
-      float* slot = P.part + (2 * static_cast<size_t>(range_of(ph)) + (seg_no == 0 ? 0 : 1)) * static_cast<size_t>(P.slot_rows) * (D + 2);
+      float* slot = P.part + (2 * static_cast<size_t>(range) + (seg_no == 0 ? 0 : 1)) * static_cast<size_t>(P.slot_rows) * (D + 2);
       if (gw * 32 < D) {  // a dim a lane, four rows at a time, in turn by the groups
         const int dim = gw * 32 + lane;
 #pragma unroll 1
@@ -769,13 +766,18 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
       tc_fence_before();
       named_bar_sync(6 + ph, kStrand);  // the accumulators and sums are the next segment's
     }
+    if (issues && elect_one()) {  // every product has completed before the CTA leaves
+      tc_commit(mdone);
+      if (!mbar_wait(mdone, 0, WL)) raise_flag(P.err, kDevTimeout);
+    }
+    __syncwarp();
   }
 
-  // ---- every product has completed (the issuer waited for them) before the tensor memory goes
+  // ---- every product has completed (the issuing warps waited for them) before the tensor memory goes
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kIssuer) {
+  if (warp == 16) {
     tmem_relinquish();
     tmem_dealloc(tmem, 512);
   }

@@ -233,6 +233,23 @@ def test_captured_replayed_and_on_two_streams(B, nq, rows):
     c.check()
 
 
+@pytest.mark.parametrize("nq,nkv,rows", [(8, 2, 1), (8, 2, 5), (32, 8, 16), (16, 2, 16)])
+def test_again_and_again(B, nq, nkv, rows):
+    """Sequences with fewer new rows than others (softmax groups without rows beside groups with some), many
+    calls in a row: the same bits every time."""
+    lens = [n * 997 % 6000 for n in range(24)]
+    news = [1 + n * 7 % rows for n in range(24)]
+    c = Case(B, nq, nkv, 128, torch.bfloat16, lens, news, rows, seed=rows)
+    c.attend()
+    c.check(seqs=range(0, 24, 5))
+    want = c.out.clone()
+    for _ in range(100):
+        c.out.fill_(3.0)
+        c.attend()
+        assert torch.equal(c.out, want)
+    assert c.cache.device_error() == 0
+
+
 @pytest.mark.parametrize("nq,nkv,rows", [(2, 1, 2), (4, 1, 8)])
 def test_as_many_sequences_as_a_handle_takes(B, nq, nkv, rows):
     lens = [(n * 37) % 200 for n in range(8192)]
