@@ -20,7 +20,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libdflash.so")
 SOURCES = ["gemv.cu", "attention.cu", "attn_tc.cu", "small.cu", "capi.cu", "verify_noalloc.cu", "pages.cu", "append.cu",
-           "paged_attn.cu", "paged_attn_tc.cu", "paged_attn8.cu", "attn_rows.cu", "cache_read.cu", "logprobs.cu", "cache.cu"]
+           "paged_attn.cu", "paged_attn_tc.cu", "paged_attn8.cu", "attn_shared.cu", "cache_read.cu", "logprobs.cu", "cache.cu"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

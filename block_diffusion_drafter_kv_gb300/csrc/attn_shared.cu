@@ -1,0 +1,141 @@
+// Attention with a prefix that all sequences of a batch share: the list of tiles of paged_attn.cu with the
+// prefix's tiles behind the sequences' own, once for every pre_rows of the batch's new rows. Of those rows one
+// product takes all query heads of a KV head, so that the prefix is read once for 64 or 128 rows
+// instead of once a sequence. Own positions and prefix run in the same launch of the kernels for blocks
+// (paged_attn_tc.cu, paged_attn8.cu), whose list is cut evenly whatever the two take; this file has the
+// join of a row's parts, of both.
+//
+// Bound: the prefix's products (4 d operations a key and query row) once there are some hundred rows, else bytes.
+#include "paged_attn.cuh"
+
+namespace dfl {
+
+namespace {
+
+constexpr int kJoinWarps = 8;
+
+// One warp a row and query head: weights 2^(m - M) / sum 2^(m - M) l over the parts of its own positions, then
+// of the prefix, each in the order of the ranges.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __grid_constant__ PagedAttnParams P, int n_ctas) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int row = blockIdx.x, head = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+  if (head >= P.nq) return;
+  const int s = row / P.rows_per_seq, r = row - s * P.rows_per_seq, g = head / P.group;
+  const int before = __ldcg(P.prefix_len);
+  int len;
+  bool bad;
+  const int n = rows_of(P, s, len, bad);
+  if (r >= n || before < 0 || before > static_cast<long long>(P.pages_per_seq) * kPagePos) return;
+  const int entries = P.batch + P.n_pre;
+  const long long T = static_cast<long long>(P.nkv) * __ldcg(P.prefix + entries);
+  const int G = n_ranges(T, n_ctas, P.strands);
+  const size_t slot_floats = static_cast<size_t>(P.slot_rows) * (D + 2);
+  constexpr int E = D / 32, kAhead = 8;
+  float acc[E] = {}, M = -INFINITY, den = 0.f;
+  for (int which = 0; which < 2; ++which) {
+    const int e = which == 0 ? s : P.batch + row / P.pre_rows;
+    const int p0 = __ldcg(P.prefix + e), nt = __ldcg(P.prefix + e + 1) - p0;
+    if (nt == 0) continue;
+    const int at = ((which == 0 ? r : row % P.pre_rows)) * P.group + head - g * P.group;  // the row in its entry
+    const long long base = static_cast<long long>(P.nkv) * p0 + static_cast<long long>(g) * nt;
+    const int c0 = cta_of(base, T, G), c1 = cta_of(base + nt - 1, T, G);
+    const int c0_second = range_begin(c0, T, G) < base;
+    const bool whole = c0 == c1;
+    const size_t state = state_row(P, e, row, head);
+    auto slot_of = [&](int c) { return P.part + (2 * static_cast<size_t>(c) + (c == c0 ? c0_second : 0)) * slot_floats; };
+    for (int b = c0; b <= c1; b += 32) {
+      const int cnt = min(32, c1 - b + 1);
+      float v[kAhead][E];
+      auto load = [&](int k0) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          if (k0 + k >= cnt) break;
+          const float* src = (whole ? P.state + state * D : slot_of(b + k0 + k) + static_cast<size_t>(at) * D) + lane * E;
+          if (E == 4) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+            v[k][0] = x.x, v[k][1] = x.y, v[k][E - 2] = x.z, v[k][E - 1] = x.w;
+          } else {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+            v[k][0] = x.x, v[k][1] = x.y;
+          }
+        }
+      };
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (lane < cnt)
+        ml = __ldcg(whole ? state_sums(P) + state
+                          : reinterpret_cast<const float2*>(slot_of(b + lane) + static_cast<size_t>(P.slot_rows) * D) + at);
+      load(0);
+      float top = ml.x;
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      top = fmaxf(top, M);
+      // what the parts so far weigh now: nothing where they have seen no key, as they are where all was NaN
+      const float was = weight_of(make_float2(M, den), top);
+      M = top;
+      den = was == 0.f ? 0.f : den * was;
+#pragma unroll
+      for (int x = 0; x < E; ++x) acc[x] = was == 0.f ? 0.f : acc[x] * was;
+      const float w = weight_of(ml, M), wl = w == 0.f ? 0.f : w * ml.y;
+      for (int k0 = 0; k0 < cnt; k0 += kAhead) {
+        if (k0 > 0) load(k0);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          if (k0 + k >= cnt) break;
+          const float wk = __shfl_sync(0xffffffffu, w, k0 + k);
+          den += __shfl_sync(0xffffffffu, wl, k0 + k);
+#pragma unroll
+          for (int x = 0; x < E; ++x) acc[x] = wk == 0.f ? acc[x] : fmaf(wk, v[k][x], acc[x]);
+        }
+      }
+    }
+  }
+  const float inv = den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den);
+  uint16_t* dst = static_cast<uint16_t*>(P.out) + (static_cast<size_t>(row) * P.nq + head) * D + lane * E;
+#pragma unroll
+  for (int x = 0; x < E; x += 2) *reinterpret_cast<uint32_t*>(dst + x) = pack2<BF16>(acc[x] * inv, acc[x + 1] * inv);
+}
+
+template <int D, bool BF16>
+int launch_join(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.batch * p.rows_per_seq, (p.nq + kJoinWarps - 1) / kJoinWarps);
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, shared_join_kernel<D, BF16>, p, n_ctas));
+}
+
+}  // namespace
+
+int launch_shared_join(const PagedAttnParams& p, bool bf16, int n_ctas, cudaStream_t stream) {
+  if (p.d == 128) return bf16 ? launch_join<128, true>(p, n_ctas, stream) : launch_join<128, false>(p, n_ctas, stream);
+  return bf16 ? launch_join<64, true>(p, n_ctas, stream) : launch_join<64, false>(p, n_ctas, stream);
+}
+
+// Sequences of a launch: their own entries and the prefix's, no more than these, are kAttnMaxBatch.
+int shared_batch() { return kAttnMaxBatch / 2; }
+
+int launch_paged_attn_shared(PagedAttnParams p, int dtype, int n_ctas, cudaStream_t stream) {
+  const bool bits8 = dtype == DFLASH_E4M3_F16 || dtype == DFLASH_E4M3_BF16, bf16 = dtype == DFLASH_BF16 || dtype == DFLASH_E4M3_BF16;
+  // Rows of an entry: all of the batch where they are few, else as many as a product takes, and at least a sequence's own
+  // (group * rows_per_seq <= 128: there are no more entries of the prefix than sequences).
+  const long long all = static_cast<long long>(p.batch) * p.rows_per_seq * p.group;
+  const int most = bits8 ? (p.rows <= 64 ? 64 : 128) : 128;
+  const int rows = static_cast<int>(all < most ? all : most);
+  p.slot_rows = bits8 ? paged_attn8_rows(rows) : rows <= 64 ? 64 : 128;
+  p.strands = bits8 ? paged_attn8_strands(rows) : 1;
+  p.pre_rows = p.slot_rows / p.group;
+  p.n_pre = (p.batch * p.rows_per_seq + p.pre_rows - 1) / p.pre_rows;
+  if (bits8) return launch_paged_attn8(p, bf16, n_ctas, stream);
+  const int e = launch_paged_attn_tc(p, bf16, n_ctas, stream);
+  return e != 0 ? e : launch_shared_join(p, bf16, n_ctas, stream);
+}
+
+}  // namespace dfl

@@ -37,9 +37,17 @@ CacheLayout layout_of(const dflash_cache_config& c) {
   return L;
 }
 
-// Of a call with a shared prefix: the fp32 outputs and (max, sum) of each row's two parts.
-size_t shared_bytes(const dflash_cache_config& c, long long rows) {
-  return 2 * static_cast<size_t>(rows) * c.n_heads * (c.head_dim + 2) * 4;
+// Of a call with a shared prefix: the tiles before each entry of the list, the ranges' parts, and the fp32 outputs
+// with (max, sum) of each row's own positions and prefix.
+struct SharedLayout {
+  size_t prefix, part, state, total;
+};
+SharedLayout shared_layout(const dflash_cache_config& c, long long rows) {
+  SharedLayout L{};
+  L.part = up256((kAttnMaxBatch + 1) * 4);
+  L.state = L.part + up256(2 * kPagedMaxCtas * 128 * static_cast<size_t>(c.head_dim + 2) * 4);
+  L.total = L.state + up256(2 * static_cast<size_t>(rows) * c.n_heads * (c.head_dim + 2) * 4);
+  return L;
 }
 
 // One layer's pool [rows][nkv][d]: boxes of 64 positions x 1 head x 64 dims (128 bytes), or in 8 bits
@@ -248,7 +256,7 @@ int dflash_cache_append_shared(dflash_cache* c, int32_t layer, const void* q, co
 }
 
 static int attend(dflash_cache* c, int32_t layer, const void* q, const int32_t* n_new, int32_t batch, int32_t rows_per_seq,
-                  int32_t prefix, void* out, void* stream) {
+                  int32_t prefix, uint8_t* shared, void* out, void* stream) {
   if (!c) return DFLASH_E_INVAL;
   if (!c->bound) return DFLASH_E_STATE;
   const auto& f = c->cfg;
@@ -282,17 +290,25 @@ static int attend(dflash_cache* c, int32_t layer, const void* q, const int32_t* 
   P.prefix_table = prefix >= 0 ? c->page_table + static_cast<size_t>(prefix) * f.pages_per_seq : nullptr;
   P.slot_rows = bits8(f) ? paged_attn8_rows(P.rows) : paged_attn_rows(P.rows);
   P.strands = bits8(f) ? paged_attn8_strands(P.rows) : 1;
+  int step = kAttnMaxBatch;
+  if (prefix >= 0) {
+    const SharedLayout S = shared_layout(f, static_cast<long long>(batch) * rows_per_seq);
+    P.prefix = reinterpret_cast<int*>(shared + S.prefix);
+    P.part = reinterpret_cast<float*>(shared + S.part);
+    P.state = reinterpret_cast<float*>(shared + S.state);
+    step = shared_batch();
+  }
   const size_t seq_bytes = static_cast<size_t>(rows_per_seq) * f.n_heads * f.head_dim * 2;
-  for (int s = 0; s < batch; s += kAttnMaxBatch) {
+  for (int s = 0; s < batch; s += step) {
     P.q = static_cast<const uint8_t*>(q) + s * seq_bytes;
     P.out = static_cast<uint8_t*>(out) + s * seq_bytes;
     P.len = c->len + s;
     P.n_new = n_new + s;
     P.page_table = c->page_table + static_cast<size_t>(s) * f.pages_per_seq;
-    P.batch = std::min(batch - s, kAttnMaxBatch);
+    P.batch = std::min(batch - s, step);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int ctas = std::min(c->n_sms, kPagedMaxCtas);
-    if ((prefix >= 0 ? launch_paged_attn_rows(P, f.dtype, st)
+    if ((prefix >= 0 ? launch_paged_attn_shared(P, f.dtype, ctas, st)
          : bits8(f) ? launch_paged_attn8(P, io_bf16(f), ctas, st)
                     : launch_paged_attn(P, io_bf16(f), ctas, st)) != 0)
       return DFLASH_E_CUDA;
@@ -302,12 +318,12 @@ static int attend(dflash_cache* c, int32_t layer, const void* q, const int32_t* 
 
 int dflash_cache_attend(dflash_cache* c, int32_t layer, const void* q, const int32_t* n_new, int32_t batch, int32_t rows_per_seq,
                         void* out, void* stream) {
-  return attend(c, layer, q, n_new, batch, rows_per_seq, -1, out, stream);
+  return attend(c, layer, q, n_new, batch, rows_per_seq, -1, nullptr, out, stream);
 }
 
 size_t dflash_cache_shared_workspace_size(const dflash_cache_config* c, int32_t rows) {
   if (rows < 1 || dflash_cache_config_check(c) != DFLASH_OK) return 0;
-  return shared_bytes(*c, rows);
+  return shared_layout(*c, rows).total;
 }
 
 int dflash_cache_attend_shared(dflash_cache* c, int32_t layer, const void* q, const int32_t* n_new, int32_t batch,
@@ -316,8 +332,8 @@ int dflash_cache_attend_shared(dflash_cache* c, int32_t layer, const void* q, co
   if (!c || prefix < 0 || !workspace || !aligned(workspace, 256)) return DFLASH_E_INVAL;
   if (!c->bound) return DFLASH_E_STATE;
   if (batch < 1 || rows_per_seq < 1) return DFLASH_E_INVAL;
-  if (workspace_bytes < shared_bytes(c->cfg, static_cast<long long>(batch) * rows_per_seq)) return DFLASH_E_CAPACITY;
-  return attend(c, layer, q, n_new, batch, rows_per_seq, prefix, out, stream);
+  if (workspace_bytes < shared_layout(c->cfg, static_cast<long long>(batch) * rows_per_seq).total) return DFLASH_E_CAPACITY;
+  return attend(c, layer, q, n_new, batch, rows_per_seq, prefix, static_cast<uint8_t*>(workspace), out, stream);
 }
 
 int dflash_cache_read(dflash_cache* c, int32_t layer, const int32_t* first, const int32_t* count, int32_t batch,

@@ -119,6 +119,67 @@ DEV void count_tiles(const PagedAttnParams& P, int* s_pre, int* s_len, int* s_ne
     for (int s = tid; s <= P.batch; s += THREADS) P.prefix[s] = s_pre[s];
 }
 
+// With a shared prefix the list has the sequences' own positions first (entries 0 .. batch - 1), then the
+// prefix once for every pre_rows new rows of the batch. An entry of the prefix is as one whose rows all stand at its
+// last position: s_len is that, s_new its new rows (of several sequences).
+template <int THREADS>
+DEV void count_entries(const PagedAttnParams& P, int* s_pre, int* s_len, int* s_new, int* s_warp) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int entries = P.batch + P.n_pre, before = __ldcg(P.prefix_len);
+  const bool none = before < 0 || before > static_cast<long long>(P.pages_per_seq) * kPagePos;
+  if (none && blockIdx.x == 0 && tid == 0) raise_flag(P.err, kDevCapacity);
+  const int per = (entries + THREADS - 1) / THREADS;
+  const int e0 = min(tid * per, entries), e1 = min(e0 + per, entries);
+  int mine = 0;
+  for (int e = e0; e < e1; ++e) {
+    int len = before - 1, n, keys = before;
+    if (e < P.batch) {
+      bool bad;
+      n = rows_of(P, e, len, bad);
+      if (bad && blockIdx.x == 0) raise_flag(P.err, kDevCapacity);
+      keys = len + n;
+    } else {
+      n = min(P.pre_rows, P.batch * P.rows_per_seq - (e - P.batch) * P.pre_rows);
+    }
+    if (none) n = 0;
+    s_len[e] = len;
+    s_new[e] = n;
+    s_pre[e + 1] = n > 0 ? (keys + kKeys - 1) / kKeys : 0;
+    mine += s_pre[e + 1];
+  }
+  int v = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  if (lane == 31) s_warp[warp] = v;
+  __syncthreads();
+  int sum = v - mine;
+  for (int w = 0; w < warp; ++w) sum += s_warp[w];
+  for (int e = e0; e < e1; ++e) {
+    sum += s_pre[e + 1];
+    s_pre[e + 1] = sum;
+  }
+  if (tid == 0) s_pre[0] = 0;
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int e = tid; e <= entries; e += THREADS) P.prefix[e] = s_pre[e];
+}
+// Of an entry: its first row among the batch's new rows, its pages, and where a row of its outputs goes in `state`.
+template <bool SHARED>
+DEV int first_row(const PagedAttnParams& P, int e) { return !SHARED || e < P.batch ? e * P.rows_per_seq : (e - P.batch) * P.pre_rows; }
+template <bool SHARED>
+DEV const int* pages_of(const PagedAttnParams& P, int e) {
+  return !SHARED || e < P.batch ? P.page_table + static_cast<size_t>(e) * P.pages_per_seq : P.prefix_table;
+}
+DEV size_t state_row(const PagedAttnParams& P, int e, int row, int head) {
+  return (static_cast<size_t>(e < P.batch ? 0 : P.batch * P.rows_per_seq) + row) * P.nq + head;
+}
+DEV float2* state_sums(const PagedAttnParams& P) {
+  return reinterpret_cast<float2*>(P.state + 2 * static_cast<size_t>(P.batch) * P.rows_per_seq * P.nq * P.d);
+}
+
 // How many ranges the list of T tiles is cut into, for n_ctas CTAs of `strands` ranges each: no empty one, and
 // no more than one a CTA where they would be shorter than two tiles.
 DEV int n_ranges(long long T, int n_ctas, int strands) {

@@ -210,7 +210,7 @@ struct Layout8 {
   static_assert(kThreads <= 32 * 32 && 4 * RT / PH <= R, "groups");
 };
 
-template <int D, int R, int PH, bool BF16>
+template <int D, int R, int PH, bool BF16, bool SHARED>
 __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_attn8_kernel(const __grid_constant__ PagedAttnParams P) {
   using L = Layout8<D, R, PH, BF16>;
   constexpr int NS = L::NS, SP = L::SP, PC = L::kPieces;
@@ -219,8 +219,9 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
   volatile int* flag = reinterpret_cast<volatile int*>(smem + L::kFlags);
   int* s_warp = reinterpret_cast<int*>(smem + L::kWarpSums);
   int* s_pre = reinterpret_cast<int*>(smem + L::kPre);
-  int* s_len = s_pre + P.batch + 1;
-  int* s_new = s_len + P.batch;
+  const int entries = SHARED ? P.batch + P.n_pre : P.batch;
+  int* s_len = s_pre + entries + 1;
+  int* s_new = s_len + entries;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint64_t WL = P.wait_ns;
 
@@ -237,9 +238,10 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
   }
   pdl_wait();
   pdl_launch_dependents();
-  count_tiles<L::kThreads>(P, s_pre, s_len, s_new, s_warp);
-  const int batch = P.batch, nkv = P.nkv, grp = P.group;
-  const long long T = static_cast<long long>(nkv) * s_pre[batch];
+  if constexpr (SHARED) count_entries<L::kThreads>(P, s_pre, s_len, s_new, s_warp);
+  else count_tiles<L::kThreads>(P, s_pre, s_len, s_new, s_warp);
+  const int nkv = P.nkv, grp = P.group;
+  const long long T = static_cast<long long>(nkv) * s_pre[entries];
   const int G = n_ranges(T, gridDim.x, PH);
   const int cta = blockIdx.x;
   if (cta >= G) return;  // the whole CTA, before it holds any tensor memory
@@ -258,7 +260,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
   Place at{};
   int left = 0;                                               // tiles of the segment that are left
   auto begin_segment = [&] {
-    at = locate(s_pre, batch, nkv, u);
+    at = locate(s_pre, entries, nkv, u);
     left = static_cast<int>(min(end - u, static_cast<long long>(at.nt - at.t)));
   };
   uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + L::kBar) + ph * L::kBars;
@@ -345,7 +347,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
         if (id0 == 32) {
           ids = -1;
           if (lane < left - h) {
-            ids = __ldcg(P.page_table + static_cast<size_t>(at.s) * P.pages_per_seq + at.t + h + lane);
+            ids = __ldcg(pages_of<SHARED>(P, at.s) + at.t + h + lane);
             if (ids < 0 || ids >= P.n_pages) {
               raise_flag(P.err, kDevCapacity);
               ids = -1;
@@ -469,7 +471,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
           const int r = new_row(P, row);
           const uint4* src = reinterpret_cast<const uint4*>(
               static_cast<const uint16_t*>(P.q) +
-              ((static_cast<size_t>(at.s) * P.rows_per_seq + r) * P.nq + static_cast<size_t>(at.g) * grp + row - r * grp) * D + part * 16);
+              ((static_cast<size_t>(first_row<SHARED>(P, at.s)) + r) * P.nq + static_cast<size_t>(at.g) * grp + row - r * grp) * D + part * 16);
           in[0] = __ldcg(src), in[1] = __ldcg(src + 1);
         }
         const uint32_t* u = reinterpret_cast<const uint32_t*>(in);
@@ -517,8 +519,9 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
     for (; u < end; ++seg_no) {
       const int s = at.s, kvh = at.g;
       const bool whole = at.t == 0 && left == at.nt;
-      const int len = s_len[s], n_new = s_new[s], nk = len + n_new;
-      const int live = n_new * grp;
+      const bool pre = SHARED && s >= P.batch;
+      const int len = s_len[s], n_new = pre ? 1 : s_new[s], nk = len + n_new;
+      const int live = s_new[s] * grp;
       const int last = live > row0 ? min(RT / 16, (live - row0 + 15) / 16) - 1 : -1;  // of the group's 16 rows at a time
 #pragma unroll
       for (int k = 0; k < RT / 2; ++k) l2[k] = {0.f, 0.f};
@@ -751,16 +754,23 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
             float o = 0.f;
 #pragma unroll
             for (int p = PC - 1; p >= 0; --p) o = fmaf(o, 0.0625f, __uint_as_float(u[p][q]));
-            if (whole) {
+            if (!SHARED && whole) {
               const float den = s_ml[row].y, y = o * (den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den));
               const int r = new_row(P, row);
               const size_t at = ((static_cast<size_t>(s) * P.rows_per_seq + r) * P.nq + static_cast<size_t>(kvh) * grp + row - r * grp) * D + dim;
               static_cast<uint16_t*>(P.out)[at] = static_cast<uint16_t>(pack2<BF16>(y, 0.f));
+            } else if (SHARED && whole) {
+              const int r = new_row(P, row);
+              __stcg(P.state + state_row(P, s, first_row<SHARED>(P, s) + r, kvh * grp + row - r * grp) * D + dim, o);
             } else {
               __stcg(slot + static_cast<size_t>(row) * D + dim, o);
             }
           }
         }
+      }
+      if (SHARED && sid < live && whole) {
+        const int r = new_row(P, sid);
+        __stcg(state_sums(P) + state_row(P, s, first_row<SHARED>(P, s) + r, kvh * grp + sid - r * grp), s_ml[sid]);
       }
       if (sid < live && !whole) __stcg(reinterpret_cast<float2*>(slot + static_cast<size_t>(P.slot_rows) * D) + sid, s_ml[sid]);
       tc_fence_before();
@@ -783,40 +793,45 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
   }
 }
 
-template <int D, int R, int PH, bool BF16>
+template <int D, int R, int PH, bool BF16, bool SHARED>
 int set_attr() {
   using L = Layout8<D, R, PH, BF16>;
   static_assert(L::smem(kAttnMaxBatch) <= 232448, "shared memory of a CTA");
-  return static_cast<int>(cudaFuncSetAttribute(paged_attn8_kernel<D, R, PH, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return static_cast<int>(cudaFuncSetAttribute(paged_attn8_kernel<D, R, PH, BF16, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                L::smem(kAttnMaxBatch)));
 }
-template <int D, bool BF16>
+template <int D, bool BF16, bool SHARED>
 int set_attrs() {
-  const int e[] = {set_attr<D, 16, 4, BF16>(), set_attr<D, 32, 2, BF16>(), set_attr<D, 64, 1, BF16>(), set_attr<D, 128, 1, BF16>()};
+  const int e[] = {set_attr<D, 16, 4, BF16, SHARED>(), set_attr<D, 32, 2, BF16, SHARED>(), set_attr<D, 64, 1, BF16, SHARED>(),
+                   set_attr<D, 128, 1, BF16, SHARED>()};
   for (int x : e)
     if (x != 0) return x;
   return 0;
 }
-template <int D, int R, int PH, bool BF16>
+template <int D, int R, int PH, bool BF16, bool SHARED>
 int launch(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
   using L = Layout8<D, R, PH, BF16>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(n_ctas);
   cfg.blockDim = dim3(L::kThreads);
-  cfg.dynamicSmemBytes = L::smem(p.batch);
+  cfg.dynamicSmemBytes = L::smem(p.batch + p.n_pre);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return static_cast<int>(cudaLaunchKernelEx(&cfg, paged_attn8_kernel<D, R, PH, BF16>, p));
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, paged_attn8_kernel<D, R, PH, BF16, SHARED>, p));
+}
+template <int D, bool BF16, bool SHARED>
+int launch_slots(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
+  if (p.slot_rows <= 16) return launch<D, 16, 4, BF16, SHARED>(p, n_ctas, stream);
+  if (p.slot_rows <= 32) return launch<D, 32, 2, BF16, SHARED>(p, n_ctas, stream);
+  return p.slot_rows <= 64 ? launch<D, 64, 1, BF16, SHARED>(p, n_ctas, stream) : launch<D, 128, 1, BF16, SHARED>(p, n_ctas, stream);
 }
 template <int D, bool BF16>
 int launch_rows(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
-  if (p.rows <= 16) return launch<D, 16, 4, BF16>(p, n_ctas, stream);
-  if (p.rows <= 32) return launch<D, 32, 2, BF16>(p, n_ctas, stream);
-  return p.rows <= 64 ? launch<D, 64, 1, BF16>(p, n_ctas, stream) : launch<D, 128, 1, BF16>(p, n_ctas, stream);
+  return p.prefix_len ? launch_slots<D, BF16, true>(p, n_ctas, stream) : launch_slots<D, BF16, false>(p, n_ctas, stream);
 }
 
 }  // namespace
@@ -825,19 +840,21 @@ int paged_attn8_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows
 int paged_attn8_strands(int rows) { return rows <= 16 ? 4 : rows <= 32 ? 2 : 1; }
 
 int paged_attn8_set_attributes() {
-  const int e[] = {set_attrs<64, false>(), set_attrs<64, true>(), set_attrs<128, false>(), set_attrs<128, true>()};
+  const int e[] = {set_attrs<64, false, false>(), set_attrs<64, true, false>(), set_attrs<128, false, false>(), set_attrs<128, true, false>(),
+                   set_attrs<64, false, true>(),  set_attrs<64, true, true>(),  set_attrs<128, false, true>(),  set_attrs<128, true, true>()};
   for (int x : e)
     if (x != 0) return x;
   return 0;
 }
 
 int launch_paged_attn8(const PagedAttnParams& p, bool bf16, int n_ctas, cudaStream_t stream) {
-  if (p.batch < 1 || p.batch > kAttnMaxBatch || n_ctas < 1 || n_ctas > kPagedMaxCtas || p.rows > 128)
+  if (p.batch < 1 || p.batch + p.n_pre > kAttnMaxBatch || n_ctas < 1 || n_ctas > kPagedMaxCtas || p.rows > 128)
     return static_cast<int>(cudaErrorInvalidValue);
   int e;
   if (p.d == 128) e = bf16 ? launch_rows<128, true>(p, n_ctas, stream) : launch_rows<128, false>(p, n_ctas, stream);
   else e = bf16 ? launch_rows<64, true>(p, n_ctas, stream) : launch_rows<64, false>(p, n_ctas, stream);
-  return e != 0 ? e : launch_paged_attn_join(p, bf16, n_ctas, stream);
+  if (e != 0) return e;
+  return p.prefix_len ? launch_shared_join(p, bf16, n_ctas, stream) : launch_paged_attn_join(p, bf16, n_ctas, stream);
 }
 
 }  // namespace dfl

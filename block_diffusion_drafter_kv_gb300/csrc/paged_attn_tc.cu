@@ -128,7 +128,7 @@ struct TcLayout {
   static constexpr uint32_t kS = 0, kO = 256, kQ = 384, kP = 448;  // TMEM columns: S buffers at 0 and kN
 };
 
-template <int D, bool BF16, int H>
+template <int D, bool BF16, int H, bool SHARED>
 __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __grid_constant__ PagedAttnParams P) {
   using L = TcLayout<D, H>;
   extern __shared__ uint8_t smem_raw[];
@@ -148,8 +148,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
   volatile int* s_valid = flag + 4;  // bit h: tile h of the step is there; by step mod 16, more than the rings hold
   int* s_warp = reinterpret_cast<int*>(smem + L::kWarpSums);
   int* s_pre = reinterpret_cast<int*>(smem + L::kPre);
-  int* s_len = s_pre + P.batch + 1;
-  int* s_new = s_len + P.batch;
+  const int entries = SHARED ? P.batch + P.n_pre : P.batch;
+  int* s_len = s_pre + entries + 1;
+  int* s_new = s_len + entries;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint64_t WL = P.wait_ns;
 
@@ -175,9 +176,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
   }
   pdl_wait();
   pdl_launch_dependents();
-  count_tiles<kTcThreads>(P, s_pre, s_len, s_new, s_warp);
-  const int batch = P.batch, nkv = P.nkv, grp = P.group;
-  const long long T = static_cast<long long>(nkv) * s_pre[batch];
+  if constexpr (SHARED) count_entries<kTcThreads>(P, s_pre, s_len, s_new, s_warp);
+  else count_tiles<kTcThreads>(P, s_pre, s_len, s_new, s_warp);
+  const int nkv = P.nkv, grp = P.group;
+  const long long T = static_cast<long long>(nkv) * s_pre[entries];
   const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), T));
   const int cta = blockIdx.x;
   if (cta >= G) return;  // the whole CTA, before it holds any tensor memory
@@ -195,7 +197,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
     Place at;    // of the next tile
   };
   auto begin_segment = [&](Walk& w) {
-    w.at = locate(s_pre, batch, nkv, w.u);
+    w.at = locate(s_pre, entries, nkv, w.u);
     w.left = static_cast<int>(min(T1 - w.u, static_cast<long long>(w.at.nt - w.at.t)));
   };
 
@@ -220,9 +222,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
       if (w.left == 0) {
         begin_segment(w);
         id0 = 32;
-        if (lane < s_new[w.at.s])  // the segment's q, a new row a lane
+        for (int r = lane; r < s_new[w.at.s]; r += 32)  // the segment's q, a new row a lane
           bulk_prefetch_l2(static_cast<const uint16_t*>(P.q) +
-                               ((static_cast<size_t>(w.at.s) * P.rows_per_seq + lane) * P.nq + static_cast<size_t>(w.at.g) * grp) * D,
+                               ((static_cast<size_t>(first_row<SHARED>(P, w.at.s)) + r) * P.nq + static_cast<size_t>(w.at.g) * grp) * D,
                            grp * D * 2);
       }
       int page[2] = {-1, -1};
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
         if (id0 == 32) {
           ids = -1;
           if (lane < w.left - h) {
-            ids = __ldcg(P.page_table + static_cast<size_t>(w.at.s) * P.pages_per_seq + w.at.t + h + lane);
+            ids = __ldcg(pages_of<SHARED>(P, w.at.s) + w.at.t + h + lane);
             if (ids < 0 || ids >= P.n_pages) {
               raise_flag(P.err, kDevCapacity);
               ids = -1;
@@ -390,7 +392,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
       const int r = new_row(P, row);
       const uint4* src = reinterpret_cast<const uint4*>(
           static_cast<const uint16_t*>(P.q) +
-          ((static_cast<size_t>(p.s) * P.rows_per_seq + r) * P.nq + p.g * grp + row - r * grp) * D);
+          ((static_cast<size_t>(first_row<SHARED>(P, p.s)) + r) * P.nq + p.g * grp + row - r * grp) * D);
       const bool there = row < s_new[p.s] * grp;
 #pragma unroll
       for (int ch = 0; ch < D / 8; ++ch) qrow[ch] = there ? __ldcg(src + ch) : make_uint4(0, 0, 0, 0);
@@ -424,10 +426,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
     for (; w.u < T1; ++seg_no) {
       const int s = w.at.s, g = w.at.g, t0 = w.at.t;
       const bool whole = t0 == 0 && w.left == w.at.nt;
-      const int len = s_len[s], n_new = s_new[s], nk = len + n_new;
+      const bool pre = SHARED && s >= P.batch;
+      const int len = s_len[s], n_new = pre ? 1 : s_new[s], nk = len + n_new;
       const int r = new_row(P, row), head = g * grp + row - r * grp;
-      const bool there = row < n_new * grp;
-      const int lim = len + r;  // last key the row may see
+      const bool there = row < s_new[s] * grp;
+      const int lim = pre ? len : len + r;  // last key the row may see
       float m = -INFINITY, l = 0.f;
       uint32_t kept = 0;  // new keys whose values are added at the end
       bool first = true, huge = false;
@@ -610,10 +613,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
       };
       const float inv = den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den);
       float* slot = P.part + (2 * static_cast<size_t>(cta) + (seg_no == 0 ? 0 : 1)) * static_cast<size_t>(L::kRows) * (D + 2);
-      uint16_t* dst = static_cast<uint16_t*>(P.out) + ((static_cast<size_t>(s) * P.rows_per_seq + r) * P.nq + head) * D;
+      uint16_t* dst = SHARED ? nullptr : static_cast<uint16_t*>(P.out) + ((static_cast<size_t>(s) * P.rows_per_seq + r) * P.nq + head) * D;
+      const size_t state = SHARED ? state_row(P, s, first_row<SHARED>(P, s) + r, head) : 0;
       auto put = [&](int c, const float (&o)[16]) {
         if (!there) return;
-        if (whole) {
+        if (!SHARED && whole) {
           uint4 v[2];
           uint32_t* b = reinterpret_cast<uint32_t*>(v);
 #pragma unroll
@@ -621,10 +625,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
           *reinterpret_cast<uint4*>(dst + c * 16) = v[0];
           *reinterpret_cast<uint4*>(dst + c * 16 + 8) = v[1];
         } else {
+          float* to = SHARED && whole ? P.state + state * D : slot + static_cast<size_t>(row) * D;
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            __stcg(reinterpret_cast<float4*>(slot + static_cast<size_t>(row) * D + c * 16 + 4 * q),
-                   make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]));
+            __stcg(reinterpret_cast<float4*>(to + c * 16 + 4 * q), make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]));
         }
       };
       if (H == 2) {
@@ -659,6 +663,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
           put(c, o);
         }
       }
+      if (SHARED && hh == 0 && there && whole) __stcg(state_sums(P) + state, make_float2(M, den));
       if (hh == 0 && there && !whole)
         __stcg(reinterpret_cast<float2*>(slot + static_cast<size_t>(L::kRows) * D) + row, make_float2(M, den));
       tc_fence_before();
@@ -676,45 +681,51 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
   }
 }
 
-template <int D, bool BF16, int H>
+template <int D, bool BF16, int H, bool SHARED>
 int set_tc_attr() {
   static_assert(TcLayout<D, H>::smem(kAttnMaxBatch) <= 232448, "shared memory of a CTA");
-  return static_cast<int>(cudaFuncSetAttribute(paged_attn_tc_kernel<D, BF16, H>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return static_cast<int>(cudaFuncSetAttribute(paged_attn_tc_kernel<D, BF16, H, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                TcLayout<D, H>::smem(kAttnMaxBatch)));
 }
-template <int D, bool BF16, int H>
+template <int D, bool BF16, int H, bool SHARED>
 int launch_tc(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(n_ctas);
   cfg.blockDim = dim3(kTcThreads);
-  cfg.dynamicSmemBytes = TcLayout<D, H>::smem(p.batch);
+  cfg.dynamicSmemBytes = TcLayout<D, H>::smem(p.batch + p.n_pre);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return static_cast<int>(cudaLaunchKernelEx(&cfg, paged_attn_tc_kernel<D, BF16, H>, p));
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, paged_attn_tc_kernel<D, BF16, H, SHARED>, p));
+}
+template <int D, bool BF16>
+int set_tc_attrs() {
+  const int e[] = {set_tc_attr<D, BF16, 1, false>(), set_tc_attr<D, BF16, 2, false>(), set_tc_attr<D, BF16, 1, true>(), set_tc_attr<D, BF16, 2, true>()};
+  for (int x : e)
+    if (x != 0) return x;
+  return 0;
+}
+template <int D, bool BF16>
+int launch_tc_rows(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
+  if (p.prefix_len) return p.slot_rows <= 64 ? launch_tc<D, BF16, 2, true>(p, n_ctas, stream) : launch_tc<D, BF16, 1, true>(p, n_ctas, stream);
+  return p.rows <= 64 ? launch_tc<D, BF16, 2, false>(p, n_ctas, stream) : launch_tc<D, BF16, 1, false>(p, n_ctas, stream);
 }
 
 }  // namespace
 
 int paged_attn_tc_set_attributes() {
-  const int e[] = {set_tc_attr<64, false, 1>(),  set_tc_attr<64, false, 2>(),  set_tc_attr<64, true, 1>(),  set_tc_attr<64, true, 2>(),
-                   set_tc_attr<128, false, 1>(), set_tc_attr<128, false, 2>(), set_tc_attr<128, true, 1>(), set_tc_attr<128, true, 2>()};
+  const int e[] = {set_tc_attrs<64, false>(), set_tc_attrs<64, true>(), set_tc_attrs<128, false>(), set_tc_attrs<128, true>()};
   for (int x : e)
     if (x != 0) return x;
   return 0;
 }
 
 int launch_paged_attn_tc(const PagedAttnParams& p, bool bf16, int n_ctas, cudaStream_t stream) {
-  const bool two = p.rows <= 64;
-  if (p.d == 128) {
-    if (bf16) return two ? launch_tc<128, true, 2>(p, n_ctas, stream) : launch_tc<128, true, 1>(p, n_ctas, stream);
-    return two ? launch_tc<128, false, 2>(p, n_ctas, stream) : launch_tc<128, false, 1>(p, n_ctas, stream);
-  }
-  if (bf16) return two ? launch_tc<64, true, 2>(p, n_ctas, stream) : launch_tc<64, true, 1>(p, n_ctas, stream);
-  return two ? launch_tc<64, false, 2>(p, n_ctas, stream) : launch_tc<64, false, 1>(p, n_ctas, stream);
+  if (p.d == 128) return bf16 ? launch_tc_rows<128, true>(p, n_ctas, stream) : launch_tc_rows<128, false>(p, n_ctas, stream);
+  return bf16 ? launch_tc_rows<64, true>(p, n_ctas, stream) : launch_tc_rows<64, false>(p, n_ctas, stream);
 }
 
 }  // namespace dfl

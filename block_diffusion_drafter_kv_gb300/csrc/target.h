@@ -100,8 +100,10 @@ struct PagedAttnParams {
   int strands;             // ranges of the list that a CTA takes
   float* state;            // [2: own, prefix][batch * rows_per_seq][nq] rows of d outputs, then of (max, sum)
 };
-// Attention over an 8-bit cache, and with a shared prefix.
-int launch_paged_attn_rows(const PagedAttnParams& p, int dtype, cudaStream_t stream);
+// With a shared prefix: chooses pre_rows, n_pre, slot_rows and strands; at most shared_batch() sequences.
+int launch_paged_attn_shared(PagedAttnParams p, int dtype, int n_ctas, cudaStream_t stream);
+int launch_shared_join(const PagedAttnParams& p, bool bf16, int n_ctas, cudaStream_t stream);
+int shared_batch();
 int paged_attn8_rows(int rows);     // as paged_attn_rows, of the kernel for 8-bit caches
 int paged_attn8_strands(int rows);  // and its ranges a CTA
 int paged_attn8_set_attributes();
