@@ -37,10 +37,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
   float acc[E] = {}, M = -INFINITY, den = 0.f;
   for (int which = 0; which < 2; ++which) {
     const int e = which == 0 ? s : P.batch + row / P.pre_rows;
-    const int p0 = __ldcg(P.prefix + e), nt = __ldcg(P.prefix + e + 1) - p0;
-    if (nt == 0) continue;
+    const int p0 = __ldcg(P.prefix + e), all = __ldcg(P.prefix + e + 1) - p0, nt = all - P.extra;
+    if (nt <= 0) continue;
     const int at = ((which == 0 ? r : row % P.pre_rows)) * P.group + head - g * P.group;  // the row in its entry
-    const long long base = static_cast<long long>(P.nkv) * p0 + static_cast<long long>(g) * nt;
+    const long long base = static_cast<long long>(P.nkv) * p0 + static_cast<long long>(g) * all;
     const int c0 = cta_of(base, T, G), c1 = cta_of(base + nt - 1, T, G);
     const int c0_second = range_begin(c0, T, G) < base;
     const bool whole = c0 == c1;
@@ -119,8 +119,8 @@ int launch_shared_join(const PagedAttnParams& p, bool bf16, int n_ctas, cudaStre
   return bf16 ? launch_join<64, true>(p, n_ctas, stream) : launch_join<64, false>(p, n_ctas, stream);
 }
 
-// Sequences of a launch: their own entries and the prefix's, no more than these, are kAttnMaxBatch.
-int shared_batch() { return kAttnMaxBatch / 2; }
+// Sequences of a launch: their own entries and the prefix's, no more than these, leave room for two CTAs a SM.
+int shared_batch() { return kAttnMaxBatch / 4; }
 
 int launch_paged_attn_shared(PagedAttnParams p, int dtype, int n_ctas, cudaStream_t stream) {
   const bool bits8 = dtype == DFLASH_E4M3_F16 || dtype == DFLASH_E4M3_BF16, bf16 = dtype == DFLASH_BF16 || dtype == DFLASH_E4M3_BF16;
@@ -134,6 +134,8 @@ int launch_paged_attn_shared(PagedAttnParams p, int dtype, int n_ctas, cudaStrea
   p.pre_rows = p.slot_rows / p.group;
   p.n_pre = (p.batch * p.rows_per_seq + p.pre_rows - 1) / p.pre_rows;
   if (bits8) return launch_paged_attn8(p, bf16, n_ctas, stream);
+  if (p.slot_rows == 128) n_ctas = 2 * n_ctas < kSharedMaxCtas ? 2 * n_ctas : kSharedMaxCtas;  // two CTAs a SM
+  p.extra = 4;
   const int e = launch_paged_attn_tc(p, bf16, n_ctas, stream);
   return e != 0 ? e : launch_shared_join(p, bf16, n_ctas, stream);
 }

@@ -45,7 +45,7 @@ struct SharedLayout {
 SharedLayout shared_layout(const dflash_cache_config& c, long long rows) {
   SharedLayout L{};
   L.part = up256((kAttnMaxBatch + 1) * 4);
-  L.state = L.part + up256(2 * kPagedMaxCtas * 128 * static_cast<size_t>(c.head_dim + 2) * 4);
+  L.state = L.part + up256(2 * kSharedMaxCtas * 128 * static_cast<size_t>(c.head_dim + 2) * 4);
   L.total = L.state + up256(2 * static_cast<size_t>(rows) * c.n_heads * (c.head_dim + 2) * 4);
   return L;
 }

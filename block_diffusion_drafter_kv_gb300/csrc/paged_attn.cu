@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(256) paged_attn_join_kernel(const __grid_const
     int len = 0, upto;
     bool bad;
     const int n = lane < P.batch ? rows_of(P, lane, len, bad) : 0;
-    const int before = scan_tiles(n, len, lane, upto);
+    const int before = scan_tiles(n, len, P.extra, lane, upto);
     n_new = __shfl_sync(0xffffffffu, n, s);
     p0 = __shfl_sync(0xffffffffu, before, s);
     p1 = __shfl_sync(0xffffffffu, upto, s);
@@ -522,10 +522,10 @@ __global__ void __launch_bounds__(256) paged_attn_join_kernel(const __grid_const
   }
   pdl_launch_dependents();
   const long long T = static_cast<long long>(P.nkv) * all;
-  const int nt = p1 - p0;
-  if (nt == 0 || row >= n_new * grp) return;
+  const int nt = p1 - p0 - P.extra;
+  if (nt <= 0 || row >= n_new * grp) return;
   const int G = n_ranges(T, n_ctas, P.strands);
-  const long long base = static_cast<long long>(P.nkv) * p0 + static_cast<long long>(g) * nt;
+  const long long base = static_cast<long long>(P.nkv) * p0 + static_cast<long long>(g) * (p1 - p0);
   const int c0 = cta_of(base, T, G), c1 = cta_of(base + nt - 1, T, G);
   if (c0 == c1) return;
   const size_t slot_floats = static_cast<size_t>(slot_rows) * (D + 2);

@@ -54,8 +54,8 @@ DEV int rows_of(const PagedAttnParams& P, int s, int& len, bool& bad) {
 }
 
 // With up to 32 sequences, one a lane: the tiles per head of those before the lane's, and with its own.
-DEV int scan_tiles(int n, int len, int lane, int& upto) {
-  const int mine = n > 0 ? (len + n + kKeys - 1) / kKeys : 0;
+DEV int scan_tiles(int n, int len, int extra, int lane, int& upto) {
+  const int mine = n > 0 ? (len + n + kKeys - 1) / kKeys + extra : 0;
   upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -76,7 +76,7 @@ DEV void count_tiles(const PagedAttnParams& P, int* s_pre, int* s_len, int* s_ne
     bool bad = false;
     const int n = lane < P.batch ? rows_of(P, lane, len, bad) : 0;
     if (bad && blockIdx.x == 0 && warp == 0) raise_flag(P.err, kDevCapacity);
-    const int before = scan_tiles(n, len, lane, upto);
+    const int before = scan_tiles(n, len, P.extra, lane, upto);
     if (lane < P.batch) {
       s_len[lane] = len;
       s_new[lane] = n;
@@ -96,7 +96,7 @@ DEV void count_tiles(const PagedAttnParams& P, int* s_pre, int* s_len, int* s_ne
     if (bad && blockIdx.x == 0) raise_flag(P.err, kDevCapacity);
     s_len[s] = len;
     s_new[s] = n;
-    s_pre[s + 1] = n > 0 ? (len + n + kKeys - 1) / kKeys : 0;
+    s_pre[s + 1] = n > 0 ? (len + n + kKeys - 1) / kKeys + P.extra : 0;
     mine += s_pre[s + 1];
   }
   int v = mine;
@@ -144,7 +144,7 @@ DEV void count_entries(const PagedAttnParams& P, int* s_pre, int* s_len, int* s_
     if (none) n = 0;
     s_len[e] = len;
     s_new[e] = n;
-    s_pre[e + 1] = n > 0 ? (keys + kKeys - 1) / kKeys : 0;
+    s_pre[e + 1] = n > 0 && keys > 0 ? (keys + kKeys - 1) / kKeys + P.extra : 0;
     mine += s_pre[e + 1];
   }
   int v = mine;
@@ -191,11 +191,11 @@ DEV int n_ranges(long long T, int n_ctas, int strands) {
 // from the next integers, far more than a product of floats is off.
 DEV int new_row(const PagedAttnParams& P, int x) { return static_cast<int>((static_cast<float>(x) + 0.5f) * P.group_inv); }
 
-// List position u: sequence s, KV head g, tile t of the pair's nt.
+// List position u: sequence s, KV head g, tile t of the pair's nt (or behind them, where a list counts more).
 struct Place {
   int s, g, t, nt;
 };
-DEV Place locate(const int* s_pre, int batch, int nkv, long long u) {
+DEV Place locate(const int* s_pre, int batch, int nkv, long long u, int extra = 0) {
   int lo = 0, hi = batch - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -208,6 +208,7 @@ DEV Place locate(const int* s_pre, int batch, int nkv, long long u) {
   const long long rest = u - static_cast<long long>(nkv) * s_pre[lo];
   p.g = static_cast<int>(quotient(rest, p.nt));
   p.t = static_cast<int>(rest - static_cast<long long>(p.g) * p.nt);
+  p.nt -= extra;
   return p;
 }
 

@@ -258,11 +258,21 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
   const long long end = range < G ? range_begin(range + 1, T, G) : 0;
   long long u = range < G ? range_begin(range, T, G) : 0;     // the next tile
   Place at{};
-  int left = 0;                                               // tiles of the segment that are left
+  int left = 0, began = 0;                                    // tiles of the segment that are left; whether the range begins behind a pair's tiles
   auto begin_segment = [&] {
-    at = locate(s_pre, entries, nkv, u);
+    at = locate(s_pre, entries, nkv, u, P.extra);
     left = static_cast<int>(min(end - u, static_cast<long long>(at.nt - at.t)));
   };
+  auto advance = [&](int cnt) {
+    u += cnt;
+    left -= cnt;
+    at.t += cnt;
+    if (at.t == at.nt) u = min(end, u + P.extra);
+  };
+  if (P.extra > 0 && u < end) {
+    const Place p = locate(s_pre, entries, nkv, u, P.extra);
+    if (p.t >= p.nt) u = min(end, u + p.nt + P.extra - p.t), began = 1;
+  }
   uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + L::kBar) + ph * L::kBars;
   uint64_t* kempty = kfull + SP;
   uint64_t* vfull = kempty + SP;
@@ -361,7 +371,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
       if (n >= SP) wait(&kempty[st], (n / SP - 1) & 1);
       if (!go) break;
       if (lane == 0) {
-        s_step[n & 15] = valid | (start ? 4 : 0) | (u + cnt >= end ? 8 : 0);
+        s_step[n & 15] = valid | (start ? 4 : 0) | (u + cnt + (at.t + cnt == at.nt ? P.extra : 0) >= end ? 8 : 0);
         if (tiles) {
           mbar_arrive_expect_tx(&scfull[sc], tiles * 2 * kKeys);
           mbar_arrive_expect_tx(&kfull[st], tiles * kKeys * D);
@@ -389,9 +399,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
       }
       __syncwarp();
       vn = ++n;
-      u += cnt;
-      left -= cnt;
-      at.t += cnt;
+      advance(cnt);
     }
     // every copy issued has landed before the CTA leaves
     if (lane == 0) {
@@ -509,7 +517,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
     };
 
     float2 l2[RT / 2];  // the key's part of every row's sum
-    int n = 0, seg_no = 0;  // step
+    int n = 0, seg_no = began;  // step
     if (u < end) {
       begin_segment();
       put_q();
@@ -532,10 +540,8 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
           qk(k);
         }
       for (; n < n1; ++n) {
-        const int cnt = min(2, left), t = at.t;
-        u += cnt;
-        left -= cnt;
-        at.t += cnt;
+        const int t = at.t;
+        advance(min(2, left));
         const int st = n % SP, b = n % NS;
         wait(&scfull[n % (2 * SP)], (n / (2 * SP)) & 1);
         // the thread's key: its scales, and the first row that sees it

@@ -104,20 +104,23 @@ constexpr int kTcThreads = 192;
 constexpr float kMove = 8.f;         // log2 growth of a row's maximum that moves its reference
 constexpr int kNewKeys = 16;         // new rows' keys at most
 
-// D: head dim; H: tiles a step takes (2: at most 64 rows; 1: at most 128).
-template <int D, int H>
+// D: head dim; H: tiles a step takes (2: at most 64 rows; 1: at most 128); PAIR: half of a SM, for two CTAs: one
+// buffer of S, Q in shared memory, rings half as long.
+template <int D, int H, bool PAIR = false>
 struct TcLayout {
   static constexpr int kRows = kLanes / H;                 // rows of a problem
   static constexpr int kN = 64 * H;                        // keys of a step
   static constexpr int kTile = kKeys * 128;                // one 64-dim box of one tile
   static constexpr int kBox = H * kTile;                   // of a step's tiles
   static constexpr int kOperand = D / 64 * kBox;           // K, or V, of a step
-  static constexpr int kSlots = D == 128 ? (H == 2 ? 3 : 6) : (H == 2 ? 6 : 8);  // of each ring
+  static constexpr int kSlots = PAIR ? (D == 128 ? 2 : 4) : D == 128 ? (H == 2 ? 3 : 6) : (H == 2 ? 6 : 8);  // of each ring
+  static constexpr int NS = PAIR ? 1 : 2;                  // buffers of S
   static constexpr int kK = 0;
   static constexpr int kV = kK + kSlots * kOperand;
-  static constexpr int kZ = kV + kSlots * kOperand;        // values of new keys that left the products
+  static constexpr int kQs = kV + kSlots * kOperand;       // q, as the ring's boxes of 128 rows
+  static constexpr int kZ = kQs + (PAIR ? kLanes * D * 2 : 0);  // values of new keys that left the products
   static constexpr int kZs = kZ + kNewKeys * D * 2;        // their scores [128][16]
-  static constexpr int kX = kZs + kLanes * kNewKeys * 4;   // outputs that meet at a segment's end: two rounds of 16 columns
+  static constexpr int kX = kZs + kLanes * kNewKeys * (PAIR ? 0 : 4);   // outputs that meet at a segment's end: two rounds of 16 columns
   static constexpr int kMl = kX + (H == 2 ? 8192 : 0);     // and their (max, sum)
   static constexpr int kBar = kMl + kLanes * 8;
   static constexpr int kBars = 4 * kSlots + 2 + 2 + 4;     // K full, empty; V full, empty; S ready, free [2]; P, PV, Q, done
@@ -125,12 +128,15 @@ struct TcLayout {
   static constexpr int kWarpSums = kFlags + 80;
   static constexpr int kPre = kWarpSums + 32;
   static constexpr int smem(int batch) { return 1024 + kPre + (3 * batch + 1) * 4; }
-  static constexpr uint32_t kS = 0, kO = 256, kQ = 384, kP = 448;  // TMEM columns: S buffers at 0 and kN
+  static constexpr uint32_t kS = 0, kO = PAIR ? 64 : 256, kQ = 384, kP = PAIR ? 192 : 448;  // TMEM columns: S buffers at 0 and kN
+  static constexpr uint32_t kColumns = PAIR ? 256 : 512;
 };
 
 template <int D, bool BF16, int H, bool SHARED>
-__global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __grid_constant__ PagedAttnParams P) {
-  using L = TcLayout<D, H>;
+__global__ void __launch_bounds__(kTcThreads, SHARED && H == 1 ? 2 : 1) paged_attn_tc_kernel(const __grid_constant__ PagedAttnParams P) {
+  constexpr bool PAIR = SHARED && H == 1;
+  using L = TcLayout<D, H, PAIR>;
+  constexpr int NS = L::NS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + L::kBar);
@@ -183,12 +189,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
   const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), T));
   const int cta = blockIdx.x;
   if (cta >= G) return;  // the whole CTA, before it holds any tensor memory
-  if (warp == 4) tmem_alloc(reinterpret_cast<uint32_t*>(smem + L::kFlags + 4), 512);
+  if (warp == 4) tmem_alloc(reinterpret_cast<uint32_t*>(smem + L::kFlags + 4), L::kColumns);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(flag[1]);
-  const long long T0 = range_begin(cta, T, G), T1 = range_begin(cta + 1, T, G);
+  const int extra = SHARED ? P.extra : 0;
+  const long long T1 = range_begin(cta + 1, T, G);
+  long long T0 = range_begin(cta, T, G);
+  int began = 0;  // whether the range begins behind a pair's tiles
+  if (SHARED) {
+    const Place p = locate(s_pre, entries, nkv, T0, extra);
+    if (p.t >= p.nt) T0 = min(T1, T0 + p.nt + extra - p.t), began = 1;
+  }
 
   // The walk of every role: steps of up to H tiles of the segments of [T0, T1).
   struct Walk {
@@ -197,8 +210,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
     Place at;    // of the next tile
   };
   auto begin_segment = [&](Walk& w) {
-    w.at = locate(s_pre, entries, nkv, w.u);
+    w.at = locate(s_pre, entries, nkv, w.u, extra);
     w.left = static_cast<int>(min(T1 - w.u, static_cast<long long>(w.at.nt - w.at.t)));
+  };
+  auto advance = [&](Walk& w, int cnt) {
+    w.u += cnt;
+    w.left -= cnt;
+    w.at.t += cnt;
+    if (SHARED && w.at.t == w.at.nt) w.u = min(T1, w.u + extra);
   };
 
   if (warp == 5) {
@@ -287,9 +306,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
       }
       __syncwarp();
       ++i;
-      w.u += cnt;
-      w.left -= cnt;
-      w.at.t += cnt;
+      advance(w, cnt);
     }
     // every copy issued has landed before the CTA leaves
     if (lane == 0)
@@ -308,11 +325,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
         // one descriptor and constant steps of its address field: building each one took longer
         // than the product it describes
         const uint64_t k0 = smem_desc_k_sw128(smem_u32(smem + L::kK + st * L::kOperand));
-        const uint32_t d = tmem + L::kS + (i & 1) * L::kN;
+        const uint32_t d = tmem + L::kS + (i % NS) * L::kN;
+        const uint64_t q0 = smem_desc_k_sw128(smem_u32(smem + L::kQs));
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ts(d, tmem + L::kQ + kk * 8, k0 + (((kk >> 2) * L::kBox + (kk & 3) * 32) >> 4), kQk, kk > 0 ? 1u : 0u);
-        tc_commit(&sready[i & 1]);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t k = k0 + (((kk >> 2) * L::kBox + (kk & 3) * 32) >> 4);
+          if (PAIR) tc_mma_bf16(d, q0 + (((kk >> 2) * kLanes * 128 + (kk & 3) * 32) >> 4), k, kQk, kk > 0 ? 1u : 0u);
+          else mma_ts(d, tmem + L::kQ + kk * 8, k, kQk, kk > 0 ? 1u : 0u);
+        }
+        tc_commit(&sready[i % NS]);
         tc_commit(&kempty[st]);
       };
       auto pv = [&](int i, bool first) {  // O (+)= P V
@@ -340,14 +361,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
             start = true;
           }
           if (mbar_test(&kfull[nqk % L::kSlots], (nqk / L::kSlots) & 1) &&
-              (nqk < 2 || mbar_test(&sfree[nqk & 1], ((nqk >> 1) - 1) & 1)) && (!start || mbar_test(qready, segs & 1))) {
+              (nqk < NS || mbar_test(&sfree[nqk % NS], (nqk / NS - 1) & 1)) && (!start || mbar_test(qready, segs & 1))) {
             qk(nqk);
             first_of[nqk & 3] = start;
             segs += start;
             start = false;
-            const int cnt = min(H, w.left);
-            w.u += cnt;
-            w.left -= cnt;
+            advance(w, min(H, w.left));
             ++nqk;
             moved = true;
           }
@@ -380,7 +399,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
     const int row = H == 2 ? tid & 63 : tid;     // row of the problem
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t orow = tmem + lanes + L::kO;
-    float* s_z = reinterpret_cast<float*>(smem + L::kZs) + tid * kNewKeys;
+    float z_local[PAIR ? kNewKeys : 1];  // (two CTAs a SM have no shared memory for what is hardly ever used)
+    float* s_z = PAIR ? z_local : reinterpret_cast<float*>(smem + L::kZs) + tid * kNewKeys;
     float2* s_ml = reinterpret_cast<float2*>(smem + L::kMl);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!mbar_try_wait(bar, parity)) wait_long(bar, parity, flag, P.err, WL);
@@ -398,6 +418,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
       for (int ch = 0; ch < D / 8; ++ch) qrow[ch] = there ? __ldcg(src + ch) : make_uint4(0, 0, 0, 0);
     };
     auto store_q = [&]() {  // once the products with the q before it are done
+      if (PAIR) {
+#pragma unroll
+        for (int ch = 0; ch < D / 8; ++ch)
+          *reinterpret_cast<uint4*>(smem + L::kQs + (ch >> 3) * kLanes * 128 + sw128(tid, ch & 7)) = qrow[ch];
+        fence_async_shared();
+        mbar_arrive(qready);
+        return;
+      }
       __syncwarp();
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
@@ -418,11 +446,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
       tmem_store16(tmem + lanes + L::kP + (1 - hh) * 32, zero);
       tmem_store16(tmem + lanes + L::kP + (1 - hh) * 32 + 16, zero);
     }
-    int i = 0, seg_no = 0;
+    int i = 0, seg_no = began;
     Walk w{T0, 0, {}};
-    begin_segment(w);
-    load_q(w.at);
-    store_q();
+    if (w.u < T1) {
+      begin_segment(w);
+      load_q(w.at);
+      store_q();
+    }
     for (; w.u < T1; ++seg_no) {
       const int s = w.at.s, g = w.at.g, t0 = w.at.t;
       const bool whole = t0 == 0 && w.left == w.at.nt;
@@ -436,22 +466,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
       bool first = true, huge = false;
       for (; w.left > 0; ++i, first = false) {
         const int cnt = min(H, w.left), t = w.at.t + hh;
-        w.u += cnt;
-        w.left -= cnt;
-        w.at.t += cnt;
-        wait(&sready[i & 1], (i >> 1) & 1);
+        advance(w, cnt);
+        wait(&sready[i % NS], (i / NS) & 1);
         tc_fence_after();
         float sc[64];
         {
           uint32_t u[4][16];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_load16(tmem + lanes + L::kS + (i & 1) * L::kN + hh * 64 + c * 16, u[c]);
+          for (int c = 0; c < 4; ++c) tmem_load16(tmem + lanes + L::kS + (i % NS) * L::kN + hh * 64 + c * 16, u[c]);
           tmem_wait_loads();
 #pragma unroll
           for (int k = 0; k < 64; ++k) sc[k] = __uint_as_float(u[k >> 4][k & 15]);
         }
         tc_fence_before();
-        mbar_arrive(&sfree[i & 1]);
+        mbar_arrive(&sfree[i % NS]);
         const bool valid = s_valid[i & 15] >> hh & 1;
         const int key0 = t * kKeys;
         const bool edge = (w.at.t * kKeys) > len + 1;  // some row may not see some key of the step (the same for all threads)
@@ -677,22 +705,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
   tc_fence_after();
   if (warp == 4) {
     tmem_relinquish();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, L::kColumns);
   }
 }
 
 template <int D, bool BF16, int H, bool SHARED>
 int set_tc_attr() {
-  static_assert(TcLayout<D, H>::smem(kAttnMaxBatch) <= 232448, "shared memory of a CTA");
+  static_assert(SHARED && H == 1 ? TcLayout<D, H, SHARED && H == 1>::smem(kAttnMaxBatch / 2) <= 115712 : TcLayout<D, H, SHARED && H == 1>::smem(kAttnMaxBatch) <= 232448,
+                "shared memory of a CTA");
   return static_cast<int>(cudaFuncSetAttribute(paged_attn_tc_kernel<D, BF16, H, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               TcLayout<D, H>::smem(kAttnMaxBatch)));
+                                               TcLayout<D, H, SHARED && H == 1>::smem(kAttnMaxBatch)));
 }
 template <int D, bool BF16, int H, bool SHARED>
 int launch_tc(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(n_ctas);
   cfg.blockDim = dim3(kTcThreads);
-  cfg.dynamicSmemBytes = TcLayout<D, H>::smem(p.batch + p.n_pre);
+  cfg.dynamicSmemBytes = TcLayout<D, H, SHARED && H == 1>::smem(p.batch + p.n_pre);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -14,6 +14,7 @@ constexpr int kPagePos = 64;          // positions per page, and keys per attent
 constexpr int kMaxBatch = 8192;       // sequences of a pool and of a cache (a pool call keeps five integers each in shared memory)
 constexpr int kAttnMaxBatch = 1024;   // sequences of an attention launch (three integers each beside its rings)
 constexpr int kPagedMaxCtas = 256;    // attention partial slots are sized for this many CTAs
+constexpr int kSharedMaxCtas = 320;   // with a shared prefix, of up to two a SM
 
 // Makes a handle's device current for a call, and the caller's again afterwards.
 class DeviceGuard {
@@ -98,6 +99,7 @@ struct PagedAttnParams {
   int n_pre, pre_rows;
   int slot_rows;           // rows of a partial slot
   int strands;             // ranges of the list that a CTA takes
+  int extra;               // tiles that the list counts behind each pair for a segment's start and end
   float* state;            // [2: own, prefix][batch * rows_per_seq][nq] rows of d outputs, then of (max, sum)
 };
 // With a shared prefix: chooses pre_rows, n_pre, slot_rows and strands; at most shared_batch() sequences.

@@ -553,7 +553,7 @@ int dflash_cache_attend(dflash_cache* c, int32_t layer, const void* q, const int
  * filled as any other sequence's: dflash_pages_reserve, dflash_cache_append). Every new row of the
  * batch sees all of them, then the positions 0 .. len[s] + r of its own sequence:
  *   out[s][r][h] = sum_j softmax_j(scale * q[s][r][h] . K_j) V_j, j over both
- * The prefix is read once for all sequences (of every 512), and its products are taken for many
+ * The prefix is read once for all sequences (of every 256), and its products are taken for many
  * sequences at once. q, n_new, out and the rest as for dflash_cache_attend; where len[prefix] is out of
  * range the whole batch is left out.
  *   prefix     batch <= prefix < max_batch

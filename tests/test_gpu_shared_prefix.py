@@ -57,7 +57,7 @@ def test_more_sequences_than_a_launch_takes(B, bits, rows):
     news = [rows if n % 5 else n % (rows + 1) for n in range(1300)]
     c = Case(B, 4, 2, 64, torch.float16, lens, news, rows, bits=bits, prefix=200, seed=rows)
     c.attend()
-    c.check(seqs=sorted({min(1299, max(0, 512 * k + i)) for k in range(4) for i in (-2, -1, 0, 1)} | set(range(5, 1300, 150))))
+    c.check(seqs=sorted({min(1299, max(0, 256 * k + i)) for k in range(6) for i in (-2, -1, 0, 1)} | set(range(5, 1300, 150))))
     assert c.cache.device_error() == 0
 
 
