@@ -133,7 +133,10 @@ int launch_paged_attn_shared(PagedAttnParams p, int dtype, int n_ctas, cudaStrea
   p.strands = bits8 ? paged_attn8_strands(rows) : 1;
   p.pre_rows = p.slot_rows / p.group;
   p.n_pre = (p.batch * p.rows_per_seq + p.pre_rows - 1) / p.pre_rows;
-  if (bits8) return launch_paged_attn8(p, bf16, n_ctas, stream);
+  if (bits8) {
+    p.extra = paged_attn8_extra(p.rows);
+    return launch_paged_attn8(p, bf16, n_ctas, stream);
+  }
   if (p.slot_rows == 128) n_ctas = 2 * n_ctas < kSharedMaxCtas ? 2 * n_ctas : kSharedMaxCtas;  // two CTAs a SM
   p.extra = 4;
   const int e = launch_paged_attn_tc(p, bf16, n_ctas, stream);

@@ -30,7 +30,7 @@ CacheLayout layout_of(const dflash_cache_config& c) {
   L.err = 0;
   L.prefix = 256;
   L.part = L.prefix + up256((std::min<size_t>(c.max_batch, kAttnMaxBatch) + 1) * 4);
-  // (in 8 bits calls of fewer rows than these take more slots of fewer rows: 4 of 16, 2 of 32)
+  // (in 8 bits calls of fewer rows take more slots of fewer rows: 4 of 16, 2 of 32)
   const int most = c.n_heads / c.n_kv_heads * c.max_block;
   const size_t rows = bits8(c) ? std::max(64, paged_attn8_rows(most)) : paged_attn_rows(most);
   L.total = L.part + up256(2 * kPagedMaxCtas * rows * (c.head_dim + 2) * 4);
@@ -290,6 +290,7 @@ static int attend(dflash_cache* c, int32_t layer, const void* q, const int32_t* 
   P.prefix_table = prefix >= 0 ? c->page_table + static_cast<size_t>(prefix) * f.pages_per_seq : nullptr;
   P.slot_rows = bits8(f) ? paged_attn8_rows(P.rows) : paged_attn_rows(P.rows);
   P.strands = bits8(f) ? paged_attn8_strands(P.rows) : 1;
+  P.extra = bits8(f) ? paged_attn8_extra(P.rows) : 0;
   int step = kAttnMaxBatch;
   if (prefix >= 0) {
     const SharedLayout S = shared_layout(f, static_cast<long long>(batch) * rows_per_seq);

@@ -172,7 +172,7 @@ DEV float reduce16(float (&v)[16]) {
 template <int D, int R, int PH, bool BF16>
 struct Layout8 {
   static constexpr int kPieces = BF16 ? 2 : 3;              // of q, and of the weights
-  static constexpr int RT = PH == 1 ? R / 4 : 16;           // rows of a softmax thread
+  static constexpr int RT = R == 16 ? 16 : R * PH / 4;      // rows of a softmax thread
   // A product's time hardly goes with N up to a hundred: pieces of q side by side, in columns of their own, as far as
   // tensor memory holds them (the rest add up in the last of them).
   static constexpr int ST = R <= 32 ? kPieces : R == 64 ? 2 : 1;
@@ -844,6 +844,8 @@ int launch_rows(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
 
 int paged_attn8_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 int paged_attn8_strands(int rows) { return rows <= 16 ? 4 : rows <= 32 ? 2 : 1; }
+// A segment's start and end cost about as much as so many tiles.
+int paged_attn8_extra(int rows) { return 6 + rows / 8; }
 
 int paged_attn8_set_attributes() {
   const int e[] = {set_attrs<64, false, false>(), set_attrs<64, true, false>(), set_attrs<128, false, false>(), set_attrs<128, true, false>(),

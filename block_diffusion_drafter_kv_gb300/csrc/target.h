@@ -108,6 +108,7 @@ int launch_shared_join(const PagedAttnParams& p, bool bf16, int n_ctas, cudaStre
 int shared_batch();
 int paged_attn8_rows(int rows);     // as paged_attn_rows, of the kernel for 8-bit caches
 int paged_attn8_strands(int rows);  // and its ranges a CTA
+int paged_attn8_extra(int rows);    // and what a list counts behind each pair
 int paged_attn8_set_attributes();
 int launch_paged_attn8(const PagedAttnParams& p, bool bf16, int n_ctas, cudaStream_t stream);
 int launch_paged_attn_join(const PagedAttnParams& p, bool bf16, int n_ctas, cudaStream_t stream);
