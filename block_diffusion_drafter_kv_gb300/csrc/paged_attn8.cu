@@ -198,7 +198,8 @@ struct Layout8 {
   static constexpr int kCorr = kGain + PH * R * 4;          // [PH][R] factors of a moved reference
   static constexpr int kTop = kCorr + PH * R * 4;           // [4 groups][4 warps][RT] warps' maxima; sums at the end
   static constexpr int kMl = kTop + 4 * 4 * RT * 4;         // [PH][R] (max, sum)
-  static constexpr int kBar = kMl + PH * R * 8;
+  static constexpr int kRow = kMl + PH * R * 8;             // [PH][R] where a row's output goes, in rows of D
+  static constexpr int kBar = kRow + PH * R * 4;
   static constexpr int kBars = 6 * SP + 4 * NS + 2;         // of a strand: K full, empty, V full, empty [SP]; scales full [2 SP]; S ready, PV done, S free, P ready [NS]; Q; all done
   static constexpr int kFlags = kBar + PH * kBars * 8;      // [0] abort, [1] TMEM base, then [PH][16] steps: 1, 2: tiles that are there, 4: a segment's first, 8: the last
   static constexpr int kWarpSums = kFlags + 16 + PH * 64;
@@ -350,6 +351,10 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
       if (start) {
         begin_segment();
         id0 = 32;
+        for (int r = lane; r < s_new[at.s]; r += 32)  // the segment's q, a new row a lane
+          bulk_prefetch_l2(static_cast<const uint16_t*>(P.q) +
+                               ((static_cast<size_t>(first_row<SHARED>(P, at.s)) + r) * P.nq + static_cast<size_t>(at.g) * grp) * D,
+                           grp * D * 2);
       }
       int page[2] = {-1, -1};
       const int cnt = min(2, left);
@@ -464,6 +469,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
     float* s_corr = reinterpret_cast<float*>(smem + L::kCorr) + ph * R + row0;
     float* s_top = reinterpret_cast<float*>(smem + L::kTop) + g * 4 * RT;
     float2* s_ml = reinterpret_cast<float2*>(smem + L::kMl) + ph * R;
+    uint32_t* s_row = reinterpret_cast<uint32_t*>(smem + L::kRow) + ph * R;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!mbar_try_wait(bar, parity)) wait_long(bar, parity, flag, P.err, WL);
       __syncwarp();
@@ -544,17 +550,13 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
         advance(min(2, left));
         const int st = n % SP, b = n % NS;
         wait(&scfull[n % (2 * SP)], (n / (2 * SP)) & 1);
-        // the thread's key: its scales, and the first row that sees it
-        const int valid = s_step[n & 15] & 3;
-        const int key = t * kKeys + j;
-        const bool alive = (valid >> (j >> 6) & 1) && key < nk;
         const uint8_t* sc = scring + n % (2 * SP) * 256 + (j >> 6) * 128 + (j & 63);
         const uint32_t kb = sc[0], vb = sc[64];
-        const float f = P.scale_log2 * scale_value(kb);
-        float ev = vb == kScaleNan ? __uint_as_float(0x7fc00000u) : static_cast<float>(static_cast<int>(vb) - kScaleBias);
-        const float inv_v = scale_value(254u - min(vb, 253u));
-        const int rmin = (!alive ? R : key <= len ? 0 : (key - len) * grp) - row0;
-        const bool edge = valid != 3 || (t + 2) * kKeys > len + 1;  // some row may not see some key of the step (the same for all threads)
+        const int valid = s_step[n & 15] & 3;
+        // some row may not see some key of the step (the same for all threads)
+        const bool edge = valid != 3 || (t + 2) * kKeys > len + 1;
+        int rmin = 0;  // the first row that sees the thread's key
+        bool nan = false;
         if (edge) {
           // Values that no row sees are cleared (0 * NaN is NaN); a key that some rows see and that has a NaN
           // among its values becomes one of zeros whose scale is NaN.
@@ -562,22 +564,27 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
           // (a barrier tells phases apart by parity: only after the stage's last values are spent may the next be asked for)
           if (n >= NS) wait(&pvdone[b], (n / NS - 1) & 1);
           wait(&vfull[st], (n / SP) & 1);
+          const int key = t * kKeys + j;
+          const bool alive = (valid >> (j >> 6) & 1) && key < nk;
+          rmin = (!alive ? R : key <= len ? 0 : (key - len) * grp) - row0;
           bool clear = !alive;
           if (alive && key >= len && n_new > 1) {
-            bool nan = false;
-#pragma unroll 1
+#pragma unroll 4
             for (int ch = 0; ch < D / 16; ++ch) {
               const uint4 v = vrow[ch];
               nan |= has_nan8(v.x) || has_nan8(v.y) || has_nan8(v.z) || has_nan8(v.w);
             }
-            if (nan) ev = __uint_as_float(0x7fc00000u);
             clear = nan;
           }
           if (PH < 4) named_bar_sync(6 + ph, kStrand);  // (all groups of the step have looked)
           if (clear && g < PH)
-#pragma unroll 1
+#pragma unroll
             for (int ch = 0; ch < D / 16; ++ch) vrow[ch] = make_uint4(0, 0, 0, 0);
         }
+        // the scales of the thread's key
+        const float f = P.scale_log2 * scale_value(kb);
+        const float ev = vb == kScaleNan || nan ? __uint_as_float(0x7fc00000u) : static_cast<float>(static_cast<int>(vb) - kScaleBias);
+        const float inv_v = scale_value(254u - min(vb, 253u));
         wait(&sready[b], (n / NS) & 1);
         tc_fence_after();
         const float2 f2 = {f, f}, ev2 = {ev, ev}, inv2 = {inv_v, inv_v};
@@ -594,19 +601,18 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
 #pragma unroll
         for (int c = 0; c < RT / 16; ++c) {  // 16 rows at a time
           if (c > last) break;
-          const uint32_t ts = tmem + lanes + L::tS(ph * NS + b) + row0 + c * 16;
           float2 x[8];
           auto scores = [&] {  // s_j + ev_j; what a row does not see is -inf
-            uint32_t u[L::ST][16];
+            uint32_t sraw[L::ST][16];
 #pragma unroll
-            for (int p = 0; p < L::ST; ++p) load16(ts + p * R, u[p]);
+            for (int p = 0; p < L::ST; ++p) load16(tmem + lanes + L::tS(ph * NS + b) + row0 + c * 16 + p * R, sraw[p]);
             wait_loads();
             tc_fence_before();
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              x[k] = {__uint_as_float(u[0][2 * k]), __uint_as_float(u[0][2 * k + 1])};
+              x[k] = {__uint_as_float(sraw[0][2 * k]), __uint_as_float(sraw[0][2 * k + 1])};
 #pragma unroll
-              for (int p = 1; p < L::ST; ++p) x[k] = add2(x[k], float2{__uint_as_float(u[p][2 * k]), __uint_as_float(u[p][2 * k + 1])});
+              for (int p = 1; p < L::ST; ++p) x[k] = add2(x[k], float2{__uint_as_float(sraw[p][2 * k]), __uint_as_float(sraw[p][2 * k + 1])});
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -735,9 +741,16 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
         begin_segment();
         put_q();
       }
+      // its rows' (max, sum), or for finished outputs (max, 1 / sum), and where they go: among the outputs, in `state`, in a slot
       if (j < RT) {
-        const float base = s_base[j];
-        s_ml[row0 + j] = make_float2(base == kNone ? -INFINITY : -base, (s_top[j] + s_top[RT + j]) + (s_top[2 * RT + j] + s_top[3 * RT + j]));
+        const float base = s_base[j], den = (s_top[j] + s_top[RT + j]) + (s_top[2 * RT + j] + s_top[3 * RT + j]);
+        const int row = row0 + j, r = new_row(P, row), head = kvh * grp + row - r * grp;
+        float2 ml = make_float2(base == kNone ? -INFINITY : -base, den);
+        s_row[row] = !whole ? row : static_cast<uint32_t>(SHARED ? state_row(P, s, first_row<SHARED>(P, s) + r, head)
+                                                                   : (static_cast<size_t>(s) * P.rows_per_seq + r) * P.nq + head);
+        if (SHARED && whole && row < live) __stcg(state_sums(P) + s_row[row], ml);
+        if (!SHARED && whole) ml.y = den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den);
+        s_ml[row] = ml;
         s_base[j] = kNone;
       }
       wait(&pvdone[(n - 1) % NS], ((n - 1) / NS) & 1);
@@ -746,6 +759,8 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
       float* slot = P.part + (2 * static_cast<size_t>(range) + (seg_no == 0 ? 0 : 1)) * static_cast<size_t>(P.slot_rows) * (D + 2);
       if (gw * 32 < D) {  // a dim a lane, four rows at a time, in turn by the groups
         const int dim = gw * 32 + lane;
+        float* to = (SHARED && whole ? P.state : slot) + dim;
+        uint16_t* out = static_cast<uint16_t*>(P.out) + dim;
 #pragma unroll 1
         for (int r4 = g / PH * 4; r4 < live; r4 += 16 / PH) {
           uint32_t u[PC][4];
@@ -755,28 +770,15 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
           wait_loads();
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int row = r4 + q;
-            if (row >= live) break;
             float o = 0.f;
 #pragma unroll
             for (int p = PC - 1; p >= 0; --p) o = fmaf(o, 0.0625f, __uint_as_float(u[p][q]));
-            if (!SHARED && whole) {
-              const float den = s_ml[row].y, y = o * (den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den));
-              const int r = new_row(P, row);
-              const size_t at = ((static_cast<size_t>(s) * P.rows_per_seq + r) * P.nq + static_cast<size_t>(kvh) * grp + row - r * grp) * D + dim;
-              static_cast<uint16_t*>(P.out)[at] = static_cast<uint16_t>(pack2<BF16>(y, 0.f));
-            } else if (SHARED && whole) {
-              const int r = new_row(P, row);
-              __stcg(P.state + state_row(P, s, first_row<SHARED>(P, s) + r, kvh * grp + row - r * grp) * D + dim, o);
-            } else {
-              __stcg(slot + static_cast<size_t>(row) * D + dim, o);
-            }
+            const size_t at_row = static_cast<size_t>(s_row[r4 + q]) * D;
+            if (r4 + q >= live) break;
+            if (!SHARED && whole) out[at_row] = static_cast<uint16_t>(pack2<BF16>(o * s_ml[r4 + q].y, 0.f));
+            else __stcg(to + at_row, o);
           }
         }
-      }
-      if (SHARED && sid < live && whole) {
-        const int r = new_row(P, sid);
-        __stcg(state_sums(P) + state_row(P, s, first_row<SHARED>(P, s) + r, kvh * grp + sid - r * grp), s_ml[sid]);
       }
       if (sid < live && !whole) __stcg(reinterpret_cast<float2*>(slot + static_cast<size_t>(P.slot_rows) * D) + sid, s_ml[sid]);
       tc_fence_before();
