@@ -12,42 +12,58 @@ namespace dfl {
 
 namespace {
 
-constexpr int kJoinWarps = 8;
+constexpr int kJoinHeads = 32;  // query heads of a CTA, a warp each
 
-// One warp a row and query head: weights 2^(m - M) / sum 2^(m - M) l over the parts of its own positions, then
-// of the prefix, each in the order of the ranges.
+// One CTA a row and 32 query heads: which ranges the row's own positions and its prefix lie in, a lane for each KV
+// head and both (the divisions took most of the time when every warp made its own), then a warp a head: weights
+// 2^(m - M) / sum 2^(m - M) l over the parts of its own positions, then of the prefix, each in the order of the ranges.
 template <int D, bool BF16>
-__global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __grid_constant__ PagedAttnParams P, int n_ctas) {
+__global__ void __launch_bounds__(32 * kJoinHeads) shared_join_kernel(const __grid_constant__ PagedAttnParams P, int n_ctas) {
+  __shared__ int s_c0[2][kJoinHeads], s_c1[2][kJoinHeads], s_slot0[2][kJoinHeads];
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x, head = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
-  if (head >= P.nq) return;
-  const int s = row / P.rows_per_seq, r = row - s * P.rows_per_seq, g = head / P.group;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = blockIdx.x, head0 = blockIdx.y * kJoinHeads, head = head0 + warp;
+  const int s = row / P.rows_per_seq, r = row - s * P.rows_per_seq, g0 = head0 / P.group, tile = row / P.pre_rows;
   const int before = __ldcg(P.prefix_len);
   int len;
   bool bad;
   const int n = rows_of(P, s, len, bad);
-  if (r >= n || before < 0 || before > static_cast<long long>(P.pages_per_seq) * kPagePos) return;
-  const int entries = P.batch + P.n_pre;
-  const long long T = static_cast<long long>(P.nkv) * __ldcg(P.prefix + entries);
-  const int G = n_ranges(T, n_ctas, P.strands);
-  const size_t slot_floats = static_cast<size_t>(P.slot_rows) * (D + 2);
-  constexpr int E = D / 32, kAhead = 8;
-  float acc[E] = {}, M = -INFINITY, den = 0.f;
-  for (int which = 0; which < 2; ++which) {
-    const int e = which == 0 ? s : P.batch + row / P.pre_rows;
+  if (r >= n || before < 0 || before > static_cast<long long>(P.pages_per_seq) * kPagePos) return;  // (the whole CTA)
+  if (warp < 2) {
+    const int e = warp == 0 ? s : P.batch + tile, g = g0 + lane;
     const int p0 = __ldcg(P.prefix + e), all = __ldcg(P.prefix + e + 1) - p0, nt = all - P.extra;
-    if (nt <= 0) continue;
-    const int at = ((which == 0 ? r : row % P.pre_rows)) * P.group + head - g * P.group;  // the row in its entry
-    const long long base = static_cast<long long>(P.nkv) * p0 + static_cast<long long>(g) * all;
-    const int c0 = cta_of(base, T, G), c1 = cta_of(base + nt - 1, T, G);
-    const int c0_second = range_begin(c0, T, G) < base;
+    int c0 = 0, c1 = -1, slot0 = 0;
+    if (nt > 0 && g < P.nkv) {
+      const long long T = static_cast<long long>(P.nkv) * __ldcg(P.prefix + P.batch + P.n_pre);
+      const int G = n_ranges(T, n_ctas, P.strands);
+      const long long base = static_cast<long long>(P.nkv) * p0 + static_cast<long long>(g) * all;
+      c0 = cta_of(base, T, G), c1 = cta_of(base + nt - 1, T, G);
+      slot0 = 2 * c0 + (range_begin(c0, T, G) < base);  // c0's, of the others it is the first
+    }
+    s_c0[warp][lane] = c0, s_c1[warp][lane] = c1, s_slot0[warp][lane] = slot0;
+  }
+  __syncthreads();
+  if (head >= P.nq) return;
+  const int g = head / P.group;
+  const size_t slot_floats = static_cast<size_t>(P.slot_rows) * (D + 2);
+  constexpr int E = D / 32, kAhead = 4;
+  float acc[E] = {}, M = -INFINITY, den = 0.f;
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    const int c0 = s_c0[which][g - g0], c1 = s_c1[which][g - g0], slot0 = s_slot0[which][g - g0];
+    if (c1 < c0) continue;
+    const int at = (which == 0 ? r : row - tile * P.pre_rows) * P.group + head - g * P.group;  // the row in its entry
     const bool whole = c0 == c1;
-    const size_t state = state_row(P, e, row, head);
-    auto slot_of = [&](int c) { return P.part + (2 * static_cast<size_t>(c) + (c == c0 ? c0_second : 0)) * slot_floats; };
+    const size_t state = state_row(P, which == 0 ? s : P.batch, row, head);
+    auto slot_of = [&](int c) { return P.part + static_cast<size_t>(c == c0 ? slot0 : 2 * c) * slot_floats; };
+#pragma unroll 1
     for (int b = c0; b <= c1; b += 32) {
       const int cnt = min(32, c1 - b + 1);
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (lane < cnt)
+        ml = __ldcg(whole ? state_sums(P) + state
+                          : reinterpret_cast<const float2*>(slot_of(b + lane) + static_cast<size_t>(P.slot_rows) * D) + at);
       float v[kAhead][E];
       auto load = [&](int k0) {
 #pragma unroll
@@ -63,10 +79,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
           }
         }
       };
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (lane < cnt)
-        ml = __ldcg(whole ? state_sums(P) + state
-                          : reinterpret_cast<const float2*>(slot_of(b + lane) + static_cast<size_t>(P.slot_rows) * D) + at);
       load(0);
       float top = ml.x;
 #pragma unroll
@@ -79,6 +91,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
 #pragma unroll
       for (int x = 0; x < E; ++x) acc[x] = was == 0.f ? 0.f : acc[x] * was;
       const float w = weight_of(ml, M), wl = w == 0.f ? 0.f : w * ml.y;
+#pragma unroll 1
       for (int k0 = 0; k0 < cnt; k0 += kAhead) {
         if (k0 > 0) load(k0);
 #pragma unroll
@@ -94,15 +107,17 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
   }
   const float inv = den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den);
   uint16_t* dst = static_cast<uint16_t*>(P.out) + (static_cast<size_t>(row) * P.nq + head) * D + lane * E;
-#pragma unroll
-  for (int x = 0; x < E; x += 2) *reinterpret_cast<uint32_t*>(dst + x) = pack2<BF16>(acc[x] * inv, acc[x + 1] * inv);
+  if constexpr (E == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<BF16>(acc[0] * inv, acc[1] * inv), pack2<BF16>(acc[E - 2] * inv, acc[E - 1] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = pack2<BF16>(acc[0] * inv, acc[1] * inv);
 }
 
 template <int D, bool BF16>
 int launch_join(const PagedAttnParams& p, int n_ctas, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.batch * p.rows_per_seq, (p.nq + kJoinWarps - 1) / kJoinWarps);
-  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.gridDim = dim3(p.batch * p.rows_per_seq, (p.nq + kJoinHeads - 1) / kJoinHeads);
+  cfg.blockDim = dim3(32 * (p.nq < kJoinHeads ? (p.nq > 1 ? p.nq : 2) : kJoinHeads));
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -189,7 +189,10 @@ __global__ void __launch_bounds__(kTcThreads, SHARED && H == 1 ? 2 : 1) paged_at
   const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), T));
   const int cta = blockIdx.x;
   if (cta >= G) return;  // the whole CTA, before it holds any tensor memory
-  if (warp == 4) tmem_alloc(reinterpret_cast<uint32_t*>(smem + L::kFlags + 4), L::kColumns);
+  if (warp == 4) {
+    tmem_alloc(reinterpret_cast<uint32_t*>(smem + L::kFlags + 4), L::kColumns);
+    if (PAIR) tmem_relinquish();  // the SM's other CTA allocates its half
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -704,7 +707,7 @@ __global__ void __launch_bounds__(kTcThreads, SHARED && H == 1 ? 2 : 1) paged_at
   __syncthreads();
   tc_fence_after();
   if (warp == 4) {
-    tmem_relinquish();
+    if (!PAIR) tmem_relinquish();
     tmem_dealloc(tmem, L::kColumns);
   }
 }
@@ -713,6 +716,10 @@ template <int D, bool BF16, int H, bool SHARED>
 int set_tc_attr() {
   static_assert(SHARED && H == 1 ? TcLayout<D, H, SHARED && H == 1>::smem(kAttnMaxBatch / 2) <= 115712 : TcLayout<D, H, SHARED && H == 1>::smem(kAttnMaxBatch) <= 232448,
                 "shared memory of a CTA");
+  if (SHARED && H == 1) {
+    const cudaError_t e = cudaFuncSetAttribute(paged_attn_tc_kernel<D, BF16, H, SHARED>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return static_cast<int>(e);
+  }
   return static_cast<int>(cudaFuncSetAttribute(paged_attn_tc_kernel<D, BF16, H, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                TcLayout<D, H, SHARED && H == 1>::smem(kAttnMaxBatch)));
 }
