@@ -153,7 +153,7 @@ int launch_paged_attn_shared(PagedAttnParams p, int dtype, int n_ctas, cudaStrea
     return launch_paged_attn8(p, bf16, n_ctas, stream);
   }
   if (p.slot_rows == 128) n_ctas = 2 * n_ctas < kSharedMaxCtas ? 2 * n_ctas : kSharedMaxCtas;  // two CTAs a SM
-  p.extra = 4;
+  p.extra = 6;
   const int e = launch_paged_attn_tc(p, bf16, n_ctas, stream);
   return e != 0 ? e : launch_shared_join(p, bf16, n_ctas, stream);
 }

@@ -1,7 +1,11 @@
 // Rows of a paged cache, dense: positions first[s] .. first[s] + count[s] of every sequence, from 16
 // or 8 bits, to fp16 or bf16. Bound: memory, each row read once and written once.
 //
-// A thread takes 16 values of a row's K and the same of its V: 16 or 32 bytes in, 32 out.
+// A warp takes a row of positions x heads (or several, where they are short): the length and page are looked up
+// once for it, then each lane has 8 values of K and of V at a time, 8 or 16 bytes in and 16 out each, with four such
+// pairs under way.
+#include <type_traits>
+
 #include "quant.cuh"
 
 namespace dfl {
@@ -9,6 +13,7 @@ namespace dfl {
 namespace {
 
 constexpr int kReadThreads = 256;
+constexpr int kAhead = 4;
 
 template <typename Y>
 DEV uint32_t pack(float lo, float hi);
@@ -31,63 +36,81 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadPara
   pdl_wait();
   pdl_launch_dependents();
   constexpr bool kBits8 = sizeof(X) == 1;
-  const int per_row = P.nkv * (P.d / 16);
-  const long long items = static_cast<long long>(P.batch) * P.rows_per_seq * per_row;
-  for (long long i = blockIdx.x * static_cast<long long>(kReadThreads) + threadIdx.x; i < items; i += static_cast<long long>(gridDim.x) * kReadThreads) {
-    const long long row = i / per_row;
-    const int part = static_cast<int>(i - row * per_row);
-    const int s = static_cast<int>(row / P.rows_per_seq), r = static_cast<int>(row - static_cast<long long>(s) * P.rows_per_seq);
-    const int first = __ldcg(P.first + s), count = __ldcg(P.count + s);
+  using Word = std::conditional_t<kBits8, uint2, uint4>;  // a lane's 8 values
+  const int lane = threadIdx.x & 31;
+  const int width = P.nkv * P.d / 8, heads_step = P.d / 8;  // lanes' worth of a row, of a head
+  const int per_warp = width < 32 ? 32 / width : 1;         // rows of a warp
+  const int sub = width < 32 ? lane / width : 0, at0 = width < 32 ? lane - sub * width : lane;
+  const int rows = P.batch * P.rows_per_seq;  // (less than 2^31)
+  const int warps = gridDim.x * (kReadThreads / 32), warp = blockIdx.x * (kReadThreads / 32) + (threadIdx.x >> 5);
+  if (sub >= per_warp) return;
+  for (long long row0 = static_cast<long long>(warp) * per_warp + sub; row0 < rows; row0 += static_cast<long long>(warps) * per_warp) {
+    const int row = static_cast<int>(row0), s = row / P.rows_per_seq, r = row - s * P.rows_per_seq;
+    const int first = __ldg(P.first + s), count = __ldg(P.count + s);
     if (first < 0 || count < 0 || count > P.rows_per_seq ||
         static_cast<long long>(first) + count > static_cast<long long>(P.pages_per_seq) * kPagePos) {
-      if (r == 0 && part == 0) raise_flag(P.err, kDevCapacity);
+      if (r == 0 && at0 == 0) raise_flag(P.err, kDevCapacity);
       continue;
     }
     if (r >= count) continue;
     const int pos = first + r;
-    const int page = __ldcg(P.page_table + static_cast<size_t>(s) * P.pages_per_seq + pos / kPagePos);
+    const int page = __ldg(P.page_table + static_cast<size_t>(s) * P.pages_per_seq + pos / kPagePos);
     if (page < 0 || page >= P.n_pages) {
-      if (part == 0) raise_flag(P.err, kDevCapacity);
+      if (at0 == 0) raise_flag(P.err, kDevCapacity);
       continue;
     }
     const int slot = page * kPagePos + pos % kPagePos;
-    const size_t at = static_cast<size_t>(slot) * P.nkv * P.d + part * 16, to = static_cast<size_t>(row) * P.nkv * P.d + part * 16;
-    const int head = part / (P.d / 16);
+    const size_t from = static_cast<size_t>(slot) * P.nkv * P.d, to = static_cast<size_t>(row) * P.nkv * P.d;
+    for (int at = at0; at < width; at += 32 * kAhead) {
+      Word in[kAhead][2];
+      uint32_t scale[kAhead][2];
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      const X* src = reinterpret_cast<const X*>(which == 0 ? P.k_pool : P.v_pool) + at;
-      uint32_t out[8];
-      if constexpr (kBits8) {
-        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(src));
-        const float f = scale_value(__ldg(P.scales + scale_index(slot, P.nkv, head, which)));
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+      for (int k = 0; k < kAhead; ++k)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float2 x = __half22float2(from_e4m3x2(u[k >> 1] >> ((k & 1) * 16)));
-          out[k] = pack<Y>(x.x * f, x.y * f);
+        for (int which = 0; which < 2; ++which) {
+          const int x = at + 32 * k;
+          if (x >= width) break;
+          in[k][which] = __ldcs(reinterpret_cast<const Word*>(reinterpret_cast<const X*>(which == 0 ? P.k_pool : P.v_pool) + from + x * 8));
+          if (kBits8) scale[k][which] = __ldg(P.scales + scale_index(slot, P.nkv, x / heads_step, which));
         }
-      } else {
-        const uint4 v[2] = {__ldcs(reinterpret_cast<const uint4*>(src)), __ldcs(reinterpret_cast<const uint4*>(src) + 1)};
-        const uint32_t u[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float2 x = widen(X{}, u[k]);
-          out[k] = pack<Y>(x.x, x.y);
+      for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+          const int x = at + 32 * k;
+          if (x >= width) break;
+          uint32_t out[4];
+          const uint32_t* u = reinterpret_cast<const uint32_t*>(&in[k][which]);
+          if constexpr (kBits8) {
+            const float f = scale_value(scale[k][which]);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const float2 v = __half22float2(from_e4m3x2(u[y >> 1] >> ((y & 1) * 16)));
+              out[y] = pack<Y>(v.x * f, v.y * f);
+            }
+          } else {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const float2 v = widen(X{}, u[y]);
+              out[y] = pack<Y>(v.x, v.y);
+            }
+          }
+          *reinterpret_cast<uint4*>(static_cast<Y*>(which == 0 ? P.k_out : P.v_out) + to + x * 8) = make_uint4(out[0], out[1], out[2], out[3]);
         }
-      }
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<Y*>(which == 0 ? P.k_out : P.v_out) + to);
-      dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-      dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+      if (width < 32) break;  // (a row that shares its warp is done)
     }
   }
 }
 
 template <typename X, typename Y>
 int launch(const ReadParams& p, int n_sms, cudaStream_t stream) {
-  const long long items = static_cast<long long>(p.batch) * p.rows_per_seq * p.nkv * (p.d / 16);
-  const long long blocks = (items + kReadThreads - 1) / kReadThreads;
+  const int width = p.nkv * p.d / 8, per_cta = kReadThreads / 32 * (width < 32 ? 32 / width : 1);
+  const long long blocks = (static_cast<long long>(p.batch) * p.rows_per_seq + per_cta - 1) / per_cta;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks < 8ll * n_sms ? blocks : 8ll * n_sms));
+  // Wide rows: as good as one a warp, so that new warps' loads run under the others' stores; short ones, whose look-ups
+  // count, several. 8 x 8192 rows of 1024 values in 8 bits: 54 us against 57; 64 x 1024 of 512 values: 31.6 against 29.5.
+  const long long most = (width > 64 ? 64ll : 8ll) * n_sms;
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks < most ? blocks : most));
   cfg.blockDim = dim3(kReadThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
