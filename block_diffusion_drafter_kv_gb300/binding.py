@@ -77,6 +77,7 @@ SIGNATURES = {
     "dflash_pages_reserve": (c_int32, [POINTER(DflashPagePool), c_void_p, c_void_p, c_int32, c_int32, c_void_p,
                                        c_void_p]),
     "dflash_pages_release": (c_int32, [POINTER(DflashPagePool), c_void_p, c_int32, c_void_p]),
+    "dflash_pages_move": (c_int32, [POINTER(DflashPagePool), c_int32, c_int32, c_void_p, c_void_p]),
     "dflash_cache_config_check": (c_int32, [POINTER(DflashCacheConfig)]),
     "dflash_cache_workspace_size": (c_size_t, [POINTER(DflashCacheConfig)]),
     "dflash_cache_create": (c_int32, [POINTER(DflashCacheConfig), POINTER(c_void_p)]),
@@ -439,6 +440,13 @@ class PagePool:
         _require_min(length, _torch_calls()[2], batch, "length", self.device)
         self._call(self.L.dflash_pages_release, "dflash_pages_release", stream, length.data_ptr(), batch)
 
+    def move(self, src: int, dst: int, length=None, stream=None):
+        """The pages of sequence src, and with `length` (int32 [max_batch]) its length, become those of sequence
+        dst, which holds none: a prompt read as sequence 0 becomes a prefix that others share."""
+        if length is not None:
+            _require_min(length, _torch_calls()[2], max(src, dst) + 1, "length", self.device)
+        self._call(self.L.dflash_pages_move, "dflash_pages_move", stream, src, dst, _ptr(length))
+
     def device_error(self, clear: bool = True) -> int:
         """The device error flags of the calls so far (waits for the current stream)."""
         v = int(self.state[2])
@@ -469,7 +477,7 @@ class PagedCache:
 
     Sequences that share a prefix: append and attend take `prefix`, the number of the sequence whose
     positions come before those of every sequence of the call (one of the page table's that is not in the
-    batch, filled like any other). shared_rows: the most rows (batch * rows_per_seq) of such an attend;
+    batch: read as sequence 0, then PagePool.move). shared_rows: the most rows (batch * rows_per_seq) of such an attend;
     its workspace is kept here."""
 
     def __init__(self, n_layers: int, n_heads: int, n_kv_heads: int, head_dim: int, pages: PagePool, length, dtype=None,

@@ -254,6 +254,39 @@ __global__ void __launch_bounds__(kThreads) pages_init_kernel(const dflash_page_
   if (me < 4) p.state[me] = me == 0 ? p.n_pages : 0;
 }
 
+struct MoveParams {
+  dflash_page_pool p;
+  int from, to;
+  int* len;
+};
+// One CTA: a row of the table, its count, its length.
+__global__ void __launch_bounds__(kThreads) pages_move_kernel(const MoveParams P) {
+  pdl_wait();
+  pdl_launch_dependents();
+  __shared__ int s_held[2];
+  if (threadIdx.x < 2) s_held[threadIdx.x] = __ldcg(P.p.held + (threadIdx.x == 0 ? P.from : P.to));
+  __syncthreads();
+  const int held = s_held[0];
+  if (s_held[1] != 0 || held < 0 || held > P.p.pages_per_seq) {
+    if (threadIdx.x == 0) raise_flag(P.p.state + 2, kDevCapacity);
+    return;
+  }
+  int* from = P.p.page_table + static_cast<size_t>(P.from) * P.p.pages_per_seq;
+  int* to = P.p.page_table + static_cast<size_t>(P.to) * P.p.pages_per_seq;
+  for (int i = threadIdx.x; i < held; i += kThreads) {
+    to[i] = __ldcg(from + i);
+    from[i] = -1;
+  }
+  if (threadIdx.x == 0) {
+    P.p.held[P.to] = held;
+    P.p.held[P.from] = 0;
+    if (P.len) {
+      P.len[P.to] = __ldcg(P.len + P.from);
+      P.len[P.from] = 0;
+    }
+  }
+}
+
 bool pool_ok(const dflash_page_pool* p) {
   auto at4 = [](const void* q) { return q && (reinterpret_cast<uintptr_t>(q) & 3) == 0; };
   return p && p->n_pages >= 1 && static_cast<long long>(p->n_pages) * kPagePos < (1LL << 31) && p->pages_per_seq >= 1 &&
@@ -328,4 +361,15 @@ extern "C" int dflash_pages_release(const dflash_page_pool* p, const int32_t* le
   const long long most = static_cast<long long>(batch) * p->pages_per_seq;
   return dfl::launch(dfl::pages_release_kernel, (most < p->n_pages ? most : p->n_pages) / 2, 3, batch, P,
                      stream);
+}
+
+extern "C" int dflash_pages_move(const dflash_page_pool* p, int32_t from, int32_t to, int32_t* len, void* stream) {
+  if (!dfl::pool_ok(p) || !dfl::at4(len) || from < 0 || to < 0 || from == to) return DFLASH_E_INVAL;
+  if (from >= p->max_batch || to >= p->max_batch) return DFLASH_E_CAPACITY;
+  dfl::MoveParams P{};
+  P.p = *p;
+  P.from = from;
+  P.to = to;
+  P.len = len;
+  return dfl::launch(dfl::pages_move_kernel, 1, 0, 0, P, stream);
 }

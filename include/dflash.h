@@ -442,6 +442,11 @@ int dflash_pages_reserve(const dflash_page_pool* p, const int32_t* len, const in
  * releases nothing. */
 int dflash_pages_release(const dflash_page_pool* p, const int32_t* len, int32_t batch, void* stream);
 
+/* Sequence `from`'s pages become those of sequence `to`, which holds none (else nothing changes and
+ * DFLASH_DEV_CAPACITY is set), and with `len` (int32 [max_batch], or NULL) its length moves along: a
+ * prompt that is read as sequence 0 of a batch of one becomes the prefix that later batches share. */
+int dflash_pages_move(const dflash_page_pool* p, int32_t from, int32_t to, int32_t* len, void* stream);
+
 /* ---- the target's paged cache ------------------------------------------------------
  * K/V of a causal target model whose attention runs in this library: rotary positions
  * and append of a step's new rows, and their attention. One handle serves all layers.
@@ -549,8 +554,8 @@ int dflash_cache_attend(dflash_cache* c, int32_t layer, const void* q, const int
                         int32_t rows_per_seq, void* out, void* stream);
 
 /* Attention of sequences that share a prefix (a system prompt, one document's questions): the
- * len[prefix] positions of sequence `prefix`, whose pages the page table's row `prefix` lists (it is
- * filled as any other sequence's: dflash_pages_reserve, dflash_cache_append). Every new row of the
+ * len[prefix] positions of sequence `prefix`, whose pages the page table's row `prefix` lists (read as
+ * a sequence of its own, then dflash_pages_move). Every new row of the
  * batch sees all of them, then the positions 0 .. len[s] + r of its own sequence:
  *   out[s][r][h] = sum_j softmax_j(scale * q[s][r][h] . K_j) V_j, j over both
  * The prefix is read once for all sequences (of every 256), and its products are taken for many

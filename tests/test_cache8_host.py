@@ -43,6 +43,7 @@ def test_calls_need_a_handle(L):
     assert L.dflash_cache_append_shared(None, 0, P16, P16, P16, B.F16, 8, 8, 8, P4, 1, 1, 2, P16, None) == -1
     assert L.dflash_cache_attend_shared(None, 0, P16, P4, 1, 1, 2, P16, P16, 1 << 30, None) == -1
     assert L.dflash_cache_read(None, 0, P4, P4, 1, 1, B.F16, P16, P16, None) == -1
+    assert L.dflash_pages_move(None, 0, 1, None, None) == -1
 
 
 def test_wrappers_refuse_what_the_library_would_misread():
