@@ -3,7 +3,9 @@
 //
 // A warp takes a row of positions x heads (or several, where they are short): the length and page are looked up
 // once for it, then each lane has 8 values of K and of V at a time, 8 or 16 bytes in and 16 out each, with four such
-// pairs under way.
+// pairs under way. Measured: 8 sequences of up to 8192 positions, 8 heads of 128 in 8 bits 54 us (91% of the copy rate), in 16 bits
+// 67 us (97%); 64 of 1024, 8 heads of 64 in 8 bits 29 us (72%). (A thread for every 16 values, which looks its row up by
+// itself: 75, 91 and 35 us.)
 #include <type_traits>
 
 #include "quant.cuh"
