@@ -124,8 +124,8 @@ struct TcLayout {
   static constexpr int kQs = kV + kSlots * kOperand;       // q, as the ring's boxes of 128 rows
   static constexpr int kZ = kQs + (PAIR ? kLanes * D * 2 : 0);  // values of new keys that left the products
   static constexpr int kZs = kZ + kNewKeys * D * 2;        // their scores [128][16]
-  static constexpr int kX = kZs + kLanes * kNewKeys * (PAIR ? 0 : 4);   // outputs that meet at a segment's end: two rounds of 16 columns
-  static constexpr int kMl = kX + (H == 2 ? 8192 : 0);     // and their (max, sum)
+  static constexpr int kX = kZs + kLanes * kNewKeys * (PAIR ? 0 : 4);   // outputs that meet at a segment's end: two rounds of 16 columns; PAIR: on their way out
+  static constexpr int kMl = kX + (PAIR ? 4096 : H == 2 ? 8192 : 0);  // and their (max, sum)
   static constexpr int kBar = kMl + kLanes * 8;
   static constexpr int kBars = 4 * kSlots + 2 + 2 + 4;     // K full, empty; V full, empty; S ready, free [2]; P, PV, Q, done
   static constexpr int kFlags = kBar + kBars * 8;          // [0] abort, [1] TMEM base, [2..3] odd values, [4..19] valid tiles of steps
@@ -230,8 +230,10 @@ __global__ void __launch_bounds__(kTcThreads, SHARED && H == 1 ? 2 : 1) paged_at
   if (warp == 5) {
     // ------------------------------------------------------------------ producer
     const uint64_t pol = T * (D * 256) > (16ll << 20) ? policy_evict_first() : policy_evict_last();
-    int i = 0;       // step
-    bool go = true;  // the same in every lane
+    // Steps whose K, whose V is on its way. With rings of two stages (PAIR) K goes a step ahead, so that it does not wait for
+    // a V stage: 64 sequences' blocks of 16 behind 8192 positions 216 us, 229 without; longer rings gain nothing by it (100 and 98 us).
+    int ik = 0, iv = 0;
+    bool go = true;      // the same in every lane
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       bool ok = go && !flag[0];
       if (ok && lane == 0 && !mbar_wait(bar, parity, WL)) {
@@ -244,83 +246,92 @@ __global__ void __launch_bounds__(kTcThreads, SHARED && H == 1 ? 2 : 1) paged_at
     Walk w{T0, 0, {}};
     int ids = -1;           // page ids of the segment's next tiles, one a lane
     int id0 = 0;            // lane that has the next one
-    while (w.u < T1 && go) {
-      if (w.left == 0) {
-        begin_segment(w);
-        id0 = 32;
-        for (int r = lane; r < s_new[w.at.s]; r += 32)  // the segment's q, a new row a lane
-          bulk_prefetch_l2(static_cast<const uint16_t*>(P.q) +
-                               ((static_cast<size_t>(first_row<SHARED>(P, w.at.s)) + r) * P.nq + static_cast<size_t>(w.at.g) * grp) * D,
-                           grp * D * 2);
-      }
-      int page[2] = {-1, -1};
-      const int cnt = min(H, w.left);
-      for (int h = 0; h < cnt; ++h) {
-        if (id0 == 32) {
-          ids = -1;
-          if (lane < w.left - h) {
-            ids = __ldcg(pages_of<SHARED>(P, w.at.s) + w.at.t + h + lane);
-            if (ids < 0 || ids >= P.n_pages) {
-              raise_flag(P.err, kDevCapacity);
-              ids = -1;
+    int vpage[2] = {-1, -1}, vg = 0;  // of the step whose V is next
+    while (go && (w.u < T1 || iv < ik)) {
+      int page[2] = {-1, -1}, g = 0;
+      const bool more = w.u < T1;
+      if (more) {
+        if (w.left == 0) {
+          begin_segment(w);
+          id0 = 32;
+          for (int r = lane; r < s_new[w.at.s]; r += 32)  // the segment's q, a new row a lane
+            bulk_prefetch_l2(static_cast<const uint16_t*>(P.q) +
+                                 ((static_cast<size_t>(first_row<SHARED>(P, w.at.s)) + r) * P.nq + static_cast<size_t>(w.at.g) * grp) * D,
+                             grp * D * 2);
+        }
+        const int cnt = min(H, w.left);
+        g = w.at.g;
+        for (int h = 0; h < cnt; ++h) {
+          if (id0 == 32) {
+            ids = -1;
+            if (lane < w.left - h) {
+              ids = __ldcg(pages_of<SHARED>(P, w.at.s) + w.at.t + h + lane);
+              if (ids < 0 || ids >= P.n_pages) {
+                raise_flag(P.err, kDevCapacity);
+                ids = -1;
+              }
             }
+            id0 = 0;
           }
-          id0 = 0;
+          page[h] = __shfl_sync(0xffffffffu, ids, id0++);
         }
-        page[h] = __shfl_sync(0xffffffffu, ids, id0++);
-      }
-      const int st = i % L::kSlots;
-      const uint32_t bytes = ((page[0] >= 0) + (page[1] >= 0)) * D * 128;  // of K, and of V
-      uint8_t* kd = smem + L::kK + st * L::kOperand;
-      uint8_t* vd = smem + L::kV + st * L::kOperand;
-      if (i >= L::kSlots) wait(&kempty[st], (i / L::kSlots - 1) & 1);
-      if (!go) break;
-      if (lane == 0) {
-        s_valid[i & 15] = (page[0] >= 0) | (page[1] >= 0) << 1;
-        if (bytes) mbar_arrive_expect_tx(&kfull[st], bytes);
-        else mbar_arrive(&kfull[st]);
+        const int st = ik % L::kSlots;
+        uint8_t* kd = smem + L::kK + st * L::kOperand;
+        if (ik >= L::kSlots) wait(&kempty[st], (ik / L::kSlots - 1) & 1);
+        if (!go) break;
+        if (lane == 0) {
+          const uint32_t bytes = ((page[0] >= 0) + (page[1] >= 0)) * D * 128;
+          s_valid[ik & 15] = (page[0] >= 0) | (page[1] >= 0) << 1;
+          if (bytes) mbar_arrive_expect_tx(&kfull[st], bytes);
+          else mbar_arrive(&kfull[st]);
 #pragma unroll
-        for (int h = 0; h < H; ++h)
-          if (page[h] >= 0)
+          for (int h = 0; h < H; ++h)
+            if (page[h] >= 0)
 #pragma unroll
-            for (int b = 0; b < D / 64; ++b)
-              tma_load_3d(kd + b * L::kBox + h * L::kTile, &P.kmap, &kfull[st], b * 64, w.at.g, page[h] * kKeys, pol);
-      }
-      __syncwarp();
-      if (i >= L::kSlots) wait(&vempty[st], (i / L::kSlots - 1) & 1);
-      if (!go) {
-        // K's copy of this step is in flight and V's is not: its slot's barrier never completes
-        if (lane == 0) mbar_wait(&kfull[st], (i / L::kSlots) & 1, WL);
-        break;
-      }
-#pragma unroll
-      for (int h = 0; h < H; ++h)
-        if (page[h] < 0) {  // no such tile: its values are cleared
-          for (int k = lane; k < D / 64 * kKeys * 8; k += 32)
-            *reinterpret_cast<uint4*>(vd + k / (kKeys * 8) * L::kBox + h * L::kTile + k % (kKeys * 8) * 16) = uint4{0, 0, 0, 0};
+              for (int b = 0; b < D / 64; ++b)
+                tma_load_3d(kd + b * L::kBox + h * L::kTile, &P.kmap, &kfull[st], b * 64, g, page[h] * kKeys, pol);
         }
-      fence_async_shared();
-      __syncwarp();
-      if (lane == 0) {
-        if (bytes) mbar_arrive_expect_tx(&vfull[st], bytes);
-        else mbar_arrive(&vfull[st]);
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-          if (page[h] >= 0)
-#pragma unroll
-            for (int b = 0; b < D / 64; ++b)
-              tma_load_3d(vd + b * L::kBox + h * L::kTile, &P.vmap, &vfull[st], b * 64, w.at.g, page[h] * kKeys, pol);
+        __syncwarp();
+        ++ik;
+        advance(w, cnt);
       }
-      __syncwarp();
-      ++i;
-      advance(w, cnt);
+      if (!PAIR) vpage[0] = page[0], vpage[1] = page[1], vg = g;
+      if (!PAIR || iv + more < ik) {
+        const int st = iv % L::kSlots;
+        uint8_t* vd = smem + L::kV + st * L::kOperand;
+        if (iv >= L::kSlots) wait(&vempty[st], (iv / L::kSlots - 1) & 1);
+        if (!go) break;
+        if (vpage[0] < 0 || (H == 2 && vpage[1] < 0)) {
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+            if (vpage[h] < 0) {  // no such tile: its values are cleared
+              for (int k = lane; k < D / 64 * kKeys * 8; k += 32)
+                *reinterpret_cast<uint4*>(vd + k / (kKeys * 8) * L::kBox + h * L::kTile + k % (kKeys * 8) * 16) = uint4{0, 0, 0, 0};
+            }
+          fence_async_shared();
+          __syncwarp();
+        }
+        if (lane == 0) {
+          const uint32_t bytes = ((vpage[0] >= 0) + (vpage[1] >= 0)) * D * 128;
+          if (bytes) mbar_arrive_expect_tx(&vfull[st], bytes);
+          else mbar_arrive(&vfull[st]);
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+            if (vpage[h] >= 0)
+#pragma unroll
+              for (int b = 0; b < D / 64; ++b)
+                tma_load_3d(vd + b * L::kBox + h * L::kTile, &P.vmap, &vfull[st], b * 64, vg, vpage[h] * kKeys, pol);
+        }
+        __syncwarp();
+        ++iv;
+      }
+      if (PAIR) vpage[0] = page[0], vpage[1] = page[1], vg = g;
     }
     // every copy issued has landed before the CTA leaves
-    if (lane == 0)
-      for (int k = max(0, i - L::kSlots); k < i; ++k) {
-        mbar_wait(&kfull[k % L::kSlots], (k / L::kSlots) & 1, WL);
-        mbar_wait(&vfull[k % L::kSlots], (k / L::kSlots) & 1, WL);
-      }
+    if (lane == 0) {
+      for (int k = max(0, ik - L::kSlots); k < ik; ++k) mbar_wait(&kfull[k % L::kSlots], (k / L::kSlots) & 1, WL);
+      for (int k = max(0, iv - L::kSlots); k < iv; ++k) mbar_wait(&vfull[k % L::kSlots], (k / L::kSlots) & 1, WL);
+    }
     __syncwarp();
   } else if (warp == 4) {
     // ------------------------------------------------------------------ MMA issuer
@@ -416,6 +427,21 @@ __global__ void __launch_bounds__(kTcThreads, SHARED && H == 1 ? 2 : 1) paged_at
     // a segment's row of q; rows that are not there are zero
     uint4 qrow[D / 8];
     auto load_q = [&](const Place& p) {
+      if (PAIR) {  // into shared memory, a row by D / 8 threads
+        constexpr int kAt = 256 / D;  // rows at a time
+        const int ch = lane % (D / 8), n = s_new[p.s] * grp;
+#pragma unroll
+        for (int k = 0; k < 32 / kAt; ++k) {
+          const int y = warp * 32 + k * kAt + lane / (D / 8), r = new_row(P, y);
+          const uint4* src = reinterpret_cast<const uint4*>(
+              static_cast<const uint16_t*>(P.q) + ((static_cast<size_t>(first_row<SHARED>(P, p.s)) + r) * P.nq + p.g * grp + y - r * grp) * D);
+          qrow[k] = y < n ? __ldcg(src + ch) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int k = 0; k < 32 / kAt; ++k)
+          *reinterpret_cast<uint4*>(smem + L::kQs + (ch >> 3) * kLanes * 128 + sw128(warp * 32 + k * kAt + lane / (D / 8), ch & 7)) = qrow[k];
+        return;
+      }
       const int r = new_row(P, row);
       const uint4* src = reinterpret_cast<const uint4*>(
           static_cast<const uint16_t*>(P.q) +
@@ -426,9 +452,6 @@ __global__ void __launch_bounds__(kTcThreads, SHARED && H == 1 ? 2 : 1) paged_at
     };
     auto store_q = [&]() {  // once the products with the q before it are done
       if (PAIR) {
-#pragma unroll
-        for (int ch = 0; ch < D / 8; ++ch)
-          *reinterpret_cast<uint4*>(smem + L::kQs + (ch >> 3) * kLanes * 128 + sw128(tid, ch & 7)) = qrow[ch];
         fence_async_shared();
         mbar_arrive(qready);
         return;
@@ -526,34 +549,34 @@ __global__ void __launch_bounds__(kTcThreads, SHARED && H == 1 ? 2 : 1) paged_at
           huge = __any_sync(0xffffffffu, fabsf(m) > 1048576.f && fabsf(m) < INFINITY);
         }
         if (edge) {
-          // The step's V rows behind the last key are cleared; new keys are looked through, a key
-          // a thread (with two tiles every thread has one, with one the first 64).
-          const int vk = H == 2 ? tid & 63 : tid;  // key in the thread's tile
-          const int vkey = key0 + vk;
-          const bool mine = vk < kKeys && valid;
-          uint8_t* vrow = smem + L::kV + (i % L::kSlots) * L::kOperand + hh * L::kTile;
+          // The step's V rows behind the last key are cleared; new keys are looked through.
+          // Both by the 16-byte chunk, neighbours along a row: with a row a thread each of the two loops took 3000 cycles (128
+          // sequences of 500, blocks of 16: 117 us, 106 now).
+          constexpr int kChunks = D / 8, kTeam = kLanes / H;
+          const int member = H == 2 ? tid & 63 : tid;
+          const int from = min(max(len - key0, 0), kKeys), upto = min(max(nk - key0, 0), kKeys);  // new keys of the tile
+          uint8_t* vtile = smem + L::kV + (i % L::kSlots) * L::kOperand + hh * L::kTile;
+          auto chunk = [&](int x) { return vtile + (x % kChunks >> 3) * L::kBox + sw128(x / kChunks, x & 7); };
           wait(&vfull[i % L::kSlots], (i / L::kSlots) & 1);
           if (tid == 0) s_odd[i & 1] = 0;
           named_bar_sync(2, kLanes);
-          if (mine && vkey >= len && vkey < nk && n_new > 1) {
+          if (valid && n_new > 1) {
             bool odd = false;
-#pragma unroll 4
-            for (int ch = 0; ch < D / 8; ++ch) {
-              const uint4 v = *reinterpret_cast<const uint4*>(vrow + (ch >> 3) * L::kBox + sw128(vk, ch & 7));
+            for (int x = from * kChunks + member; x < upto * kChunks; x += kTeam) {
+              const uint4 v = *reinterpret_cast<const uint4*>(chunk(x));
               odd |= non_finite2<BF16>(v.x) || non_finite2<BF16>(v.y) || non_finite2<BF16>(v.z) || non_finite2<BF16>(v.w);
             }
             if (odd) s_odd[i & 1] = 1;
           }
           named_bar_sync(2, kLanes);
           const bool odd = s_odd[i & 1] != 0;
-          if (mine && (vkey >= nk || (odd && vkey >= len))) {
-#pragma unroll 4
-            for (int ch = 0; ch < D / 8; ++ch) {
-              uint4* at = reinterpret_cast<uint4*>(vrow + (ch >> 3) * L::kBox + sw128(vk, ch & 7));
-              if (vkey < nk) *reinterpret_cast<uint4*>(smem + L::kZ + (vkey - len) * (D * 2) + ch * 16) = *at;
+          if (valid)
+            for (int x = (odd ? from : upto) * kChunks + member; x < kKeys * kChunks; x += kTeam) {
+              uint4* at = reinterpret_cast<uint4*>(chunk(x));
+              const int key = x / kChunks;
+              if (key < upto) *reinterpret_cast<uint4*>(smem + L::kZ + (key0 + key - len) * (D * 2) + x % kChunks * 16) = *at;
               *at = make_uint4(0, 0, 0, 0);
             }
-          }
           if (odd && valid) {  // (a tile of another CTA's has its new keys looked after there)
             const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
@@ -651,6 +674,30 @@ __global__ void __launch_bounds__(kTcThreads, SHARED && H == 1 ? 2 : 1) paged_at
       uint16_t* dst = SHARED ? nullptr : static_cast<uint16_t*>(P.out) + ((static_cast<size_t>(s) * P.rows_per_seq + r) * P.nq + head) * D;
       const size_t state = SHARED ? state_row(P, s, first_row<SHARED>(P, s) + r, head) : 0;
       auto put = [&](int c, const float (&o)[16]) {
+        if constexpr (PAIR) {
+          // 16 columns of the warp's rows, 16 rows at a time, through shared memory: four threads write a row's 64 bytes, for 8
+          // lines a store, not 32.
+          float4* x = reinterpret_cast<float4*>(smem + L::kX) + warp * 64;  // [4][16 rows]
+          const int q = lane & 3, n = s_new[s] * grp;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            __syncwarp();
+            if (lane >> 4 == h)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) x[k * 16 + (lane & 15 ^ 2 * k)] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int at = 8 * k + (lane >> 2), y = warp * 32 + h * 16 + at;
+              if (y < n) {
+                const int yr = new_row(P, y);
+                float* to = whole ? P.state + state_row(P, s, first_row<SHARED>(P, s) + yr, g * grp + y - yr * grp) * D : slot + static_cast<size_t>(y) * D;
+                __stcg(reinterpret_cast<float4*>(to + c * 16) + q, x[q * 16 + (at ^ 2 * q)]);
+              }
+            }
+          }
+          return;
+        }
         if (!there) return;
         if (!SHARED && whole) {
           uint4 v[2];
