@@ -157,8 +157,9 @@ int launch_paged_attn_shared(PagedAttnParams p, int dtype, int n_ctas, cudaStrea
     return launch_paged_attn8(p, bf16, n_ctas, stream);
   }
   if (p.slot_rows == 128) n_ctas = 2 * n_ctas < kSharedMaxCtas ? 2 * n_ctas : kSharedMaxCtas;  // two CTAs a SM
-  // 4, 6 and 8 tiles: 34.4, 34.3 and 35.9 us (32 x 4096), 77.5, 74.2 and 75.6 us (16 x 8190, blocks of 16); none: 51 and 141 (one CTA a SM)
-  p.extra = 6;
+  // With 4, 5, 6 and 8 tiles: one token of 32 sequences behind 4096 positions 32.0, 32.2, 33.3 and 34.3 us, blocks of 16 of 64
+  // behind 8192 244, 224, 213 and 198 us, of 16 behind 8190 75, 69, 65 and 66 us (10: 68).
+  p.extra = p.rows <= 16 ? 5 : 8;
   const int e = launch_paged_attn_tc(p, bf16, n_ctas, stream);
   return e != 0 ? e : launch_shared_join(p, bf16, n_ctas, stream);
 }

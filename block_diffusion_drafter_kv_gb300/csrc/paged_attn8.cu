@@ -569,6 +569,9 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
           // Values that no row sees are cleared (0 * NaN is NaN); a key that some rows see and that has a NaN
           // among its values becomes one of zeros whose scale is NaN.
           uint4* vrow = reinterpret_cast<uint4*>(vring + st * L::kOperand + j * D);
+          // Eight neighbours at eight places of 128 bytes (128 sequences of 500, blocks of 16: 126 us, 132 without); with 128 rows a
+          // thread has no registers left for it (180 us against 165 at 4 sequences of 32768).
+          auto bank = [&](int ch) { return R == 128 ? ch : (ch + (j >> (D == 64))) & (D / 16 - 1); };
           // (a barrier tells phases apart by parity: only after the stage's last values are spent may the next be asked for)
           if (n >= NS) wait(&pvdone[b], (n / NS - 1) & 1);
           wait(&vfull[st], (n / SP) & 1);
@@ -579,7 +582,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
           if (alive && key >= len && n_new > 1) {
 #pragma unroll 4
             for (int ch = 0; ch < D / 16; ++ch) {
-              const uint4 v = vrow[ch];
+              const uint4 v = vrow[bank(ch)];
               nan |= has_nan8(v.x) || has_nan8(v.y) || has_nan8(v.z) || has_nan8(v.w);
             }
             clear = nan;
@@ -587,7 +590,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
           if (PH < 4) named_bar_sync(6 + ph, kStrand);  // (all groups of the step have looked)
           if (clear && g < PH)
 #pragma unroll
-            for (int ch = 0; ch < D / 16; ++ch) vrow[ch] = make_uint4(0, 0, 0, 0);
+            for (int ch = 0; ch < D / 16; ++ch) vrow[bank(ch)] = make_uint4(0, 0, 0, 0);
         }
         // the scales of the thread's key
         const float f = P.scale_log2 * scale_value(kb);
