@@ -16,9 +16,9 @@ namespace dfl {
 
 namespace {
 
-constexpr int kJoinHeads = 32;  // query heads of a CTA, a warp each
+constexpr int kJoinHeads = 8;  // query heads of a CTA, a warp each (16 x 8190, blocks of 16: 63.6 us; with 32 heads 65.7, half a wave of the CTAs idle)
 
-// One CTA a row and 32 query heads: which ranges the row's own positions and its prefix lie in, a lane for each KV
+// One CTA a row and 8 query heads: which ranges the row's own positions and its prefix lie in, a lane for each KV
 // head and both (the divisions took most of the time when every warp made its own), then a warp a head: weights
 // 2^(m - M) / sum 2^(m - M) l over the parts of its own positions, then of the prefix, each in the order of the ranges.
 template <int D, bool BF16>
@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(32 * kJoinHeads) shared_join_kernel(const __gr
       c0 = cta_of(base, T, G), c1 = cta_of(base + nt - 1, T, G);
       slot0 = 2 * c0 + (range_begin(c0, T, G) < base);  // c0's, of the others it is the first
     }
-    s_c0[warp][lane] = c0, s_c1[warp][lane] = c1, s_slot0[warp][lane] = slot0;
+    if (lane < kJoinHeads) s_c0[warp][lane] = c0, s_c1[warp][lane] = c1, s_slot0[warp][lane] = slot0;
   }
   __syncthreads();
   if (head >= P.nq) return;
