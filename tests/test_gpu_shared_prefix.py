@@ -124,6 +124,31 @@ def test_what_lies_behind_the_prefix_is_never_used(B, bits):
 
 
 @pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nq,nkv,rows,seqs", [(8, 1, 16, 3), (8, 2, 16, 5), (4, 1, 5, 40)])
+@pytest.mark.parametrize("odd", [7, 1, 0])
+def test_new_keys_that_are_not_finite(B, bits, d, nq, nkv, rows, seqs, odd):
+    """A new key whose values are NaN, before and behind a page's end: the rows before it are as they were, in the other
+    sequences too, those from it on are NaN."""
+    odd = min(odd, rows - 1)
+    lens = [60 if n % 2 else 64 * (n % 7) + 63 for n in range(seqs)]
+    c = Case(B, nq, nkv, d, torch.bfloat16, lens, [rows] * seqs, rows, bits=bits, prefix=130, seed=odd)
+    for s in (0, seqs - 2):
+        at = c.at(s)[lens[s] + odd: lens[s] + odd + 1]
+        if bits == 8:
+            c.set_scales("v", at, 255)
+        else:
+            c.cache.v_pool[0, at] = NAN
+    c.attend()
+    got = c.out.reshape(seqs, rows, nq, d).float()
+    for s in (0, seqs - 2):
+        assert bool(torch.isnan(got[s, odd:]).all())
+        c.check(seqs=[s], rows=range(odd))
+    c.check(seqs=[s for s in range(0, seqs, 1 + seqs // 8) if s not in (0, seqs - 2)])
+    assert c.cache.device_error() == 0
+
+
+@pytest.mark.parametrize("bits", [16, 8])
 @pytest.mark.parametrize("rows", [1, 16])
 def test_captured_replayed_and_on_two_streams(B, bits, rows):
     sets = []
