@@ -21,8 +21,8 @@
 // w_j <= 256 whatever the scales; p_j is w_j 2^-ev_j (|ev_j| <= 40: no overflow).
 //
 // Measured (32 query heads on 8 KV heads, d 128; in brackets the 16-bit cache): 32 ragged sequences of 512 to 8192
-// keys, one token, 57 us, 75% of the copy rate (94); 4 sequences of 32768, one token, 52 us, 76% (86; with d 64 36 us, 56%),
-// with blocks of 16 (64 rows) 83 us, 48% (98), with 128 rows 165 us (119). Few rows are bound by memory, one row of 128 bytes
+// keys, one token, 56 us, 75% of the copy rate (94); 4 sequences of 32768, one token, 51 us, 78% (89; with d 64 35 us, 57%),
+// with blocks of 16 (64 rows) 83 us, 48% (96), with 128 rows 165 us (117). Few rows are bound by memory, one row of 128 bytes
 // a position and head, and by the starts and ends of the ranges. From 64 rows on it is the softmax: a step of
 // 128 keys is 6200 warp instructions (100 to a warp's key and row, in 16 warps of 96 registers, and the issuer's
 // polling), 56% of what the SM can issue, in a chain of some 2600 cycles, against 1400 cycles of HBM time.

@@ -8,11 +8,11 @@
 // 128 lanes of the softmax have a row of 64 scores; P keeps zeros where a row's other tile is, and
 // O += P V (M = 128, K = 128 keys) adds up two states per row, which meet at the segment's
 // end. With 65 to 128 rows a step is one tile. Measured (bf16, 32 query heads on 8 KV heads, 4
-// sequences of 32768, d 128): 90 us with 20 rows, 97 with 64 (81% of the copy rate), 119 with 128;
+// sequences of 32768, d 128): 90 us with 20 rows, 96 with 64 (83% of the copy rate), 117 with 128;
 // against a two-tile step's 2750 cycles of HBM time (64 KB) issuing its products takes 1250 and its
 // softmax 1100, overlapped between steps, so that it waits for copies; a one-tile step (1400 cycles of
 // HBM time) waits for the chain of its products and softmax (1700), d 64 likewise (75 us with 64 rows, 53%).
-// Short caches (128 sequences of 500: 117 us with 64 rows, 38%, 168 us with 128 rows, 29%) are bound by the
+// Short caches (128 sequences of 500: 107 us with 64 rows, 41%, 158 us with 128 rows, 31%) are bound by the
 // segments' ends: q, output.
 //
 //   S   two TMEM buffers of N columns: the next step's Q K^T runs under this one's softmax
@@ -29,8 +29,9 @@
 // the end without results, so that none of their barriers and collective steps is missed.
 //
 // With a prefix that all sequences share (SHARED; attn_shared.cu) the list has entries of the prefix too, and every
-// pair's outputs stay in fp32 for the join. Two CTAs share a SM there where rows are up to 128 (PAIR): 72 us against
-// 106 for one, at 16 sequences' blocks of 16 behind 8190 positions.
+// pair's outputs stay in fp32 for the join. Two CTAs share a SM there where rows are up to 128 (PAIR), each with half
+// of the tensor memory: 106 us with one, 72 with both at 16 sequences' blocks of 16 behind 8190 positions (62 now). A step of
+// both takes 2050 cycles, 64 KB from L2 and 1000 cycles of the tensor cores.
 //
 // Keys that are hidden: weights 0. What lies behind a sequence's last key is cleared in the V
 // stage before the product, and so is a dropped page (0 * NaN is NaN). The new rows' own keys, of
