@@ -25,22 +25,37 @@ constexpr int kJoinHeads = 8;  // query heads of a CTA, a warp each (16 x 8190, 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(32 * kJoinHeads) shared_join_kernel(const __grid_constant__ PagedAttnParams P, int n_ctas) {
   __shared__ int s_c0[2][kJoinHeads], s_c1[2][kJoinHeads], s_slot0[2][kJoinHeads];
-  pdl_wait();
-  pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = blockIdx.x, head0 = blockIdx.y * kJoinHeads, head = head0 + warp;
   const int s = row / P.rows_per_seq, r = row - s * P.rows_per_seq, g0 = head0 / P.group, tile = row / P.pre_rows;
+  // With an entry a lane the list is known before the first kernel ends (it let this one start once all before it had
+  // finished), and the ranges are worked out meanwhile.
+  const int entries = P.batch + P.n_pre;
+  if (entries > 32) pdl_wait();
   const int before = __ldcg(P.prefix_len);
   int len;
   bool bad;
-  const int n = rows_of(P, s, len, bad);
-  if (r >= n || before < 0 || before > static_cast<long long>(P.pages_per_seq) * kPagePos) return;  // (the whole CTA)
-  if (warp < 2) {
+  const bool there = r < rows_of(P, s, len, bad) && !no_prefix(P, before);  // the same for the whole CTA
+  if (there && warp < 2) {
     const int e = warp == 0 ? s : P.batch + tile, g = g0 + lane;
-    const int p0 = __ldcg(P.prefix + e), all = __ldcg(P.prefix + e + 1) - p0, nt = all - P.extra;
+    int p0, all, list;
+    if (entries <= 32) {
+      int l, n;
+      const int mine = lane < entries ? entry_tiles(P, lane, before, false, l, n, bad) : 0;
+      int upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      p0 = __shfl_sync(0xffffffffu, upto - mine, e), all = __shfl_sync(0xffffffffu, mine, e), list = __shfl_sync(0xffffffffu, upto, 31);
+    } else {
+      p0 = __ldcg(P.prefix + e), all = __ldcg(P.prefix + e + 1) - p0, list = __ldcg(P.prefix + entries);
+    }
+    const int nt = all - P.extra;
     int c0 = 0, c1 = -1, slot0 = 0;
     if (nt > 0 && g < P.nkv) {
-      const long long T = static_cast<long long>(P.nkv) * __ldcg(P.prefix + P.batch + P.n_pre);
+      const long long T = static_cast<long long>(P.nkv) * list;
       const int G = n_ranges(T, n_ctas, P.strands);
       const long long base = static_cast<long long>(P.nkv) * p0 + static_cast<long long>(g) * all;
       c0 = cta_of(base, T, G), c1 = cta_of(base + nt - 1, T, G);
@@ -48,6 +63,9 @@ __global__ void __launch_bounds__(32 * kJoinHeads) shared_join_kernel(const __gr
     }
     if (lane < kJoinHeads) s_c0[warp][lane] = c0, s_c1[warp][lane] = c1, s_slot0[warp][lane] = slot0;
   }
+  if (entries <= 32) pdl_wait();
+  pdl_launch_dependents();
+  if (!there) return;
   __syncthreads();
   if (head >= P.nq) return;
   const int g = head / P.group;

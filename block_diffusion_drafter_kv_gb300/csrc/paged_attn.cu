@@ -514,24 +514,28 @@ __global__ void __launch_bounds__(256) paged_attn_join_kernel(const __grid_const
     p0 = __shfl_sync(0xffffffffu, before, s);
     p1 = __shfl_sync(0xffffffffu, upto, s);
     all = __shfl_sync(0xffffffffu, upto, 31);
-    pdl_wait();
   } else {
     pdl_wait();
     p0 = __ldcg(P.prefix + s), p1 = __ldcg(P.prefix + s + 1), all = __ldcg(P.prefix + P.batch);
     n_new = __ldcg(P.n_new + s);
   }
-  pdl_launch_dependents();
   const long long T = static_cast<long long>(P.nkv) * all;
   const int nt = p1 - p0 - P.extra;
-  if (nt <= 0 || row >= n_new * grp) return;
-  const int G = n_ranges(T, n_ctas, P.strands);
-  const long long base = static_cast<long long>(P.nkv) * p0 + static_cast<long long>(g) * (p1 - p0);
-  const int c0 = cta_of(base, T, G), c1 = cta_of(base + nt - 1, T, G);
+  const bool cut = nt > 0 && row < n_new * grp;
+  long long base = 0;
+  int G = 1, c0 = 0, c1 = 0, c0_second = 0;
+  if (cut) {
+    G = n_ranges(T, n_ctas, P.strands);
+    base = static_cast<long long>(P.nkv) * p0 + static_cast<long long>(g) * (p1 - p0);
+    c0 = cta_of(base, T, G), c1 = cta_of(base + nt - 1, T, G);
+    // The pair is the first segment of every CTA whose range starts with it or inside it: of all but
+    // perhaps c0. (Asking each range's start, a 64-bit division, took most of this kernel's time.)
+    c0_second = range_begin(c0, T, G) < base;
+  }
+  if (P.batch <= 32) pdl_wait();
+  pdl_launch_dependents();
   if (c0 == c1) return;
   const size_t slot_floats = static_cast<size_t>(slot_rows) * (D + 2);
-  // The pair is the first segment of every CTA whose range starts with it or inside it: of all but
-  // perhaps c0. (Asking each range's start, a 64-bit division, took most of this kernel's time.)
-  const int c0_second = range_begin(c0, T, G) < base;
   auto slot_of = [&](int c) { return P.part + (2 * static_cast<size_t>(c) + (c == c0 ? c0_second : 0)) * slot_floats; };
   constexpr int E = D / 32;  // columns of a lane
   constexpr int kAhead = 8;  // parts whose loads are in flight together

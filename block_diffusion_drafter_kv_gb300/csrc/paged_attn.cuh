@@ -122,29 +122,39 @@ DEV void count_tiles(const PagedAttnParams& P, int* s_pre, int* s_len, int* s_ne
 // With a shared prefix the list has the sequences' own positions first (entries 0 .. batch - 1), then the
 // prefix once for every pre_rows new rows of the batch. An entry of the prefix is as one whose rows all stand at its
 // last position: s_len is that, s_new its new rows (of several sequences).
+// entry_tiles: what the list counts of entry e for each head.
+DEV int entry_tiles(const PagedAttnParams& P, int e, int before, bool none, int& len, int& n, bool& bad) {
+  len = before - 1;
+  int keys = before;
+  bad = false;
+  if (e < P.batch) {
+    n = rows_of(P, e, len, bad);
+    keys = len + n;
+  } else {
+    n = min(P.pre_rows, P.batch * P.rows_per_seq - (e - P.batch) * P.pre_rows);
+  }
+  if (none) n = 0;
+  return n > 0 && keys > 0 ? (keys + kKeys - 1) / kKeys + P.extra : 0;
+}
+DEV bool no_prefix(const PagedAttnParams& P, int before) {
+  return before < 0 || before > static_cast<long long>(P.pages_per_seq) * kPagePos;
+}
 template <int THREADS>
 DEV void count_entries(const PagedAttnParams& P, int* s_pre, int* s_len, int* s_new, int* s_warp) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int entries = P.batch + P.n_pre, before = __ldcg(P.prefix_len);
-  const bool none = before < 0 || before > static_cast<long long>(P.pages_per_seq) * kPagePos;
+  const bool none = no_prefix(P, before);
   if (none && blockIdx.x == 0 && tid == 0) raise_flag(P.err, kDevCapacity);
   const int per = (entries + THREADS - 1) / THREADS;
   const int e0 = min(tid * per, entries), e1 = min(e0 + per, entries);
   int mine = 0;
   for (int e = e0; e < e1; ++e) {
-    int len = before - 1, n, keys = before;
-    if (e < P.batch) {
-      bool bad;
-      n = rows_of(P, e, len, bad);
-      if (bad && blockIdx.x == 0) raise_flag(P.err, kDevCapacity);
-      keys = len + n;
-    } else {
-      n = min(P.pre_rows, P.batch * P.rows_per_seq - (e - P.batch) * P.pre_rows);
-    }
-    if (none) n = 0;
+    int len, n;
+    bool bad;
+    s_pre[e + 1] = entry_tiles(P, e, before, none, len, n, bad);
+    if (bad && blockIdx.x == 0) raise_flag(P.err, kDevCapacity);
     s_len[e] = len;
     s_new[e] = n;
-    s_pre[e + 1] = n > 0 && keys > 0 ? (keys + kKeys - 1) / kKeys + P.extra : 0;
     mine += s_pre[e + 1];
   }
   int v = mine;
