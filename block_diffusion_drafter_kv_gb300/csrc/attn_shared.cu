@@ -8,8 +8,8 @@
 // Bound: the prefix's products (4 d operations a key and query row) once there are some hundred rows, else bytes.
 // In 16 bits a product of 128 rows and 64 keys is 512 cycles of the tensor cores in a chain of 1900 (S, softmax, P by one
 // warpgroup), so two CTAs share a SM: 1030 cycles a tile. Measured (32 query heads on 8 KV heads, d 128): 32 sequences behind 4096
-// positions, one token 31 us (every sequence reading the prefix itself: 93 us); 16 behind 8190, blocks of 16 62 us (98 us);
-// 64 behind 8192, blocks of 16 196 us (368 us), 690 TFLOP/s. In 8 bits 40 us (32 behind 8192, one token) and 102 us (16
+// positions, one token 31 us (every sequence reading the prefix itself: 93 us); 16 behind 8190, blocks of 16 60 us (98 us);
+// 64 behind 8192, blocks of 16 194 us (368 us), 697 TFLOP/s. In 8 bits 40 us (32 behind 8192, one token) and 100 us (16
 // behind 8190, blocks of 16): from 64 rows on no faster than each for itself.
 #include "paged_attn.cuh"
 

@@ -30,7 +30,7 @@
 //
 // With a prefix that all sequences share (SHARED; attn_shared.cu) the list has entries of the prefix too, and every
 // pair's outputs stay in fp32 for the join. Two CTAs share a SM there where rows are up to 128 (PAIR), each with half
-// of the tensor memory: 106 us with one, 72 with both at 16 sequences' blocks of 16 behind 8190 positions (62 now). A step of
+// of the tensor memory: 106 us with one, 72 with both at 16 sequences' blocks of 16 behind 8190 positions (60 now). A step of
 // both takes 2050 cycles, 64 KB from L2 and 1000 cycles of the tensor cores.
 //
 // Keys that are hidden: weights 0. What lies behind a sequence's last key is cleared in the V
