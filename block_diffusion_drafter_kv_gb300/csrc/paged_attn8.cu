@@ -24,7 +24,7 @@
 // keys, one token, 56 us, 75% of the copy rate (94); 4 sequences of 32768, one token, 51 us, 78% (89; with d 64 35 us, 57%),
 // with blocks of 16 (64 rows) 83 us, 48% (96), with 128 rows 165 us (117). Few rows are bound by memory, one row of 128 bytes
 // a position and head, and by the starts and ends of the ranges. From 64 rows on it is the softmax: a step of
-// 128 keys is 6200 warp instructions (100 to a warp's key and row, in 16 warps of 96 registers, and the issuer's
+// 128 keys is 6200 warp instructions (some 300 in each of 16 warps, half of them whatever its rows, the rest the issuer's
 // polling), 56% of what the SM can issue, in a chain of some 2600 cycles, against 1400 cycles of HBM time.
 //
 // CTA: one per SM; four softmax groups of 128 threads, a key of the step each. Of at most 16 rows each group is a
