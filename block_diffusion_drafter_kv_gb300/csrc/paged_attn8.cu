@@ -554,15 +554,17 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
           qk(k);
         }
       for (; n < n1; ++n) {
-        const int t = at.t;
-        advance(min(2, left));
+        const int t = at.t, cnt = min(2, left);
+        advance(cnt);
         const int st = n % SP, b = n % NS;
         wait(&scfull[n % (2 * SP)], (n / (2 * SP)) & 1);
         const uint8_t* sc = scring + n % (2 * SP) * 256 + (j >> 6) * 128 + (j & 63);
         const uint32_t kb = sc[0], vb = sc[64];
         const int valid = s_step[n & 15] & 3;
-        // some row may not see some key of the step (the same for all threads)
-        const bool edge = valid != 3 || (t + 2) * kKeys > len + 1;
+        // Some row may not see some key of the step: by the walk alone, and so the same for all threads whatever a wait that
+        // ran out has left in s_step. Barriers go by this.
+        const bool ends = cnt < 2 || (t + 2) * kKeys > len + 1;
+        const bool edge = ends || valid != 3;
         int rmin = 0;  // the first row that sees the thread's key
         bool nan = false;
         if (edge) {
@@ -579,7 +581,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
           const bool alive = (valid >> (j >> 6) & 1) && key < nk;
           rmin = (!alive ? R : key <= len ? 0 : (key - len) * grp) - row0;
           bool clear = !alive;
-          if (alive && key >= len && n_new > 1) {
+          if (ends && alive && key >= len && n_new > 1) {
 #pragma unroll 4
             for (int ch = 0; ch < D / 16; ++ch) {
               const uint4 v = vrow[bank(ch)];
@@ -587,7 +589,8 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
             }
             clear = nan;
           }
-          if (PH < 4) named_bar_sync(6 + ph, kStrand);  // (all groups of the step have looked)
+          // (all groups of the step have looked; where only a page is missing none looks, and each thread clears what is its own)
+          if (PH < 4 && ends) named_bar_sync(6 + ph, kStrand);
           if (clear && g < PH)
 #pragma unroll
             for (int ch = 0; ch < D / 16; ++ch) vrow[bank(ch)] = make_uint4(0, 0, 0, 0);
