@@ -14,11 +14,18 @@
 //   q   a row is scaled by a power of two to a largest magnitude in [128, 256) and taken apart into
 //       2 (bf16) or 3 (fp16) numbers of 4 significant bits: exact, but for what lies below 2^-10
 //       of e4m3's scale there, 2^-17 of the row's largest value. Their products add up in one accumulator.
-//   w   as fp16, then 2 (bf16) or 3 (fp16) e4m3 numbers, each the sixteenfold rest of the one before, so
-//       that it reaches 2^-18 (2^-22) below the row's largest w_j; an accumulator each, N = pieces x rows.
+//   w   as fp16, then 2 (bf16) or 3 (fp16) e4m3 numbers, each 32 times the rest of the one before; an
+//       accumulator each, N = pieces x rows.
 // A thread of the softmax has one key and all rows: the key's scales are its own two numbers, and so is
-// the first row that may see the key. The weights' reference m' is a running maximum of s_j + ev_j, so that
-// w_j <= 256 whatever the scales; p_j is w_j 2^-ev_j (|ev_j| <= 40: no overflow).
+// the first row that may see the key. The weights' reference m' is set to the maximum of s_j + ev_j over a step less 4, and
+// moved up where a w_j passes 256; p_j is w_j 2^-ev_j (|ev_j| <= 40: no overflow).
+//   small w  The last piece ends at 2^-15 (2^-20), whatever the largest weight is. One key far above thousands of others, as a
+//       context's first often is, would leave their sum out: 9% of an output at 18 binary orders and 28000 keys, when
+//       references only rose. So one step in 8 is looked at, and a row that had too few weights of 8 or more gets a lower
+//       reference: O and the sums grow, up to 40 orders. Where a reference is set the sum is 16 at least, a step with a weight of
+//       8 adds 8, and a look stands for 8 x 128 weights of 2^-15 each at most: of a row's weights at most 3/8 x 1024 x 2^-15 (2^-20)
+//       of the sum of its steps' largest is lost, however long the range. Of 4 x 32768 keys, 64 rows: 82 us without the looks, 85
+//       with them (89 and 95 where scores spread twice as far); 128 rows 161 and 186, whose threads have no registers left for it.
 //
 // Measured (32 query heads on 8 KV heads, d 128; in brackets the 16-bit cache): 32 ragged sequences of 512 to 8192
 // keys, one token, 56 us, 75% of the copy rate (94); 4 sequences of 32768, one token, 51 us, 78% (89; with d 64 35 us, 57%),
@@ -44,7 +51,12 @@ namespace {
 constexpr int kStepKeys = 128;
 constexpr float kNone = 3e38f;      // the negative of a reference where no key has been seen
 constexpr float kHeadroom = 4.f;    // a reference is set so many binary orders below the largest score,
-constexpr float kMost = 256.f;      // and moves where a weight passes this
+constexpr float kMost = 256.f;      // moves up where a weight passes this,
+constexpr int kLook = 8;            // and down where, of one step in so many, too many had no weight of 8:
+constexpr int kCredit = 4;          // more than so many,
+constexpr int kGain = 2;            // and so many for each that had one
+constexpr float kDeepest = 40.f;    // no further than this below its highest in a segment (what is lost then is nothing)
+constexpr float kRest = 32.f;       // a weight's pieces: the rest of one, at most 8, goes into the next times this
 
 // ---------------------------------------------------------------- descriptors
 DEV void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
@@ -205,7 +217,9 @@ struct Layout8 {
   static constexpr int kGain = kBase + PH * R * 4;          // [PH][R] 1 / the power of two that q was scaled by
   static constexpr int kCorr = kGain + PH * R * 4;          // [PH][R] factors of a moved reference
   static constexpr int kTop = kCorr + PH * R * 4;           // [4 groups][4 warps][RT] warps' maxima; sums at the end
-  static constexpr int kMl = kTop + 4 * 4 * RT * 4;         // [PH][R] (max, sum)
+  static constexpr int kHigh = kTop + 4 * 4 * RT * 4;       // [PH][R] references, negative, where they were highest
+  static constexpr int kLeft = kHigh + PH * R * 4;          // [PH][R] what is left of kCredit
+  static constexpr int kMl = kLeft + PH * R * 4;            // [PH][R] (max, sum)
   static constexpr int kRow = kMl + PH * R * 8;             // [PH][R] where a row's output goes, in rows of D
   static constexpr int kBar = kRow + PH * R * 4;
   static constexpr int kBars = 6 * SP + 4 * NS + 2;         // of a strand: K full, empty, V full, empty [SP]; scales full [2 SP]; S ready, PV done, S free, P ready [NS]; Q; all done
@@ -476,6 +490,8 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
     float* s_gain = reinterpret_cast<float*>(smem + L::kGain) + ph * R;
     float* s_corr = reinterpret_cast<float*>(smem + L::kCorr) + ph * R + row0;
     float* s_top = reinterpret_cast<float*>(smem + L::kTop) + g * 4 * RT;
+    float* s_high = reinterpret_cast<float*>(smem + L::kHigh) + ph * R + row0;
+    int* s_left = reinterpret_cast<int*>(smem + L::kLeft) + ph * R + row0;
     float2* s_ml = reinterpret_cast<float2*>(smem + L::kMl) + ph * R;
     uint32_t* s_row = reinterpret_cast<uint32_t*>(smem + L::kRow) + ph * R;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -535,7 +551,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
     if (u < end) {
       begin_segment();
       put_q();
-      if (j < RT) s_base[j] = kNone;
+      if (j < RT) s_base[j] = s_high[j] = kNone, s_left[j] = kCredit;
       named_bar_sync(6 + ph, kStrand);
     }
     for (; u < end; ++seg_no) {
@@ -655,7 +671,8 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
             }
           };
           scores();
-          bool move = n == n0;
+          const bool look = n > n0 && (n - n0) % kLook == 0 && !ends;  // (by the walk alone)
+          bool move = n == n0 || look;
           if (!move) {
             weights();
             move = named_bar_any(2 + g, 128, __hgt(__hmax(__low2half(top), __high2half(top)), __float2half_rn(kMost)));
@@ -663,7 +680,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
             else if (c == last) scores_read();
           }
           if (move) {
-            // ---- references that move: the rows' maxima over the group, then O and the sums. (Few instructions: most
+            // ---- references that may move: the rows' maxima over the group, then O and the sums. (Few instructions: most
             // steps do not come here, and those that do wait for each of them to be fetched.)
             float mine = 0.f;
 #pragma unroll
@@ -674,18 +691,35 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
             if (lane < 16) s_top[gw * RT + c * 16 + lane] = mine;
             named_bar_sync(2 + g, 128);
             if (c == last) scores_read();
+            bool moved = false;
             if (j < 16) {
               const float* tops = s_top + c * 16 + j;
               const float most = fmaxf(fmaxf(tops[0], tops[RT]), fmaxf(tops[2 * RT], tops[3 * RT]));
-              const float old = s_base[c * 16 + j], now = kHeadroom - most;
-              const bool up = most + old > kHeadroom;
-              s_corr[c * 16 + j] = up ? ex2(now - old) : 1.f;
-              if (up) s_base[c * 16 + j] = now;
+              const float old = s_base[c * 16 + j], high = s_high[c * 16 + j], over = most + old;  // log2 of the largest weight
+              const bool up = over > (look ? 8.f : kHeadroom);  // (a look alone moves none that kMost lets be)
+              bool down = false;
+              if (look) {
+                const int rest = s_left[c * 16 + j] + (over >= 3.f ? kGain : -1);
+                s_left[c * 16 + j] = rest;
+                // (not where no key has been seen, nor where there is no such row)
+                down = rest < 0 && over < 3.f && most > -INFINITY && old < high + kDeepest && row0 + c * 16 + j < live;
+              }
+              moved = up || down;
+              s_corr[c * 16 + j] = 1.f;
+              if (moved) {
+                const float now = up ? kHeadroom - most : fminf(kHeadroom - most, high + kDeepest);
+                s_corr[c * 16 + j] = ex2(now - old);
+                s_base[c * 16 + j] = now;
+                s_high[c * 16 + j] = fminf(high, now);
+                s_left[c * 16 + j] = kCredit;
+              }
             }
-            named_bar_sync(2 + g, 128);
+            moved = named_bar_any(2 + g, 128, moved);
+            if (moved) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) l2[c * 8 + k].x *= s_corr[c * 16 + 2 * k], l2[c * 8 + k].y *= s_corr[c * 16 + 2 * k + 1];
-            if (n > n0) {
+              for (int k = 0; k < 8; ++k) l2[c * 8 + k].x *= s_corr[c * 16 + 2 * k], l2[c * 8 + k].y *= s_corr[c * 16 + 2 * k + 1];
+            }
+            if (moved && n > n0) {
               wait(&pvdone[(n - 1) % NS], ((n - 1) / NS) & 1);
               tc_fence_after();
 #pragma unroll 1
@@ -715,8 +749,8 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
               const uint32_t b0 = half2_to_e4m3x2(h[2 * k]), b1 = half2_to_e4m3x2(h[2 * k + 1]);
               out[k] = b0 | b1 << 16;
               if (p + 1 < PC) {
-                h[2 * k] = __hmul2(__hsub2(h[2 * k], from_e4m3x2(b0)), __float2half2_rn(16.f));
-                h[2 * k + 1] = __hmul2(__hsub2(h[2 * k + 1], from_e4m3x2(b1)), __float2half2_rn(16.f));
+                h[2 * k] = __hmul2(__hsub2(h[2 * k], from_e4m3x2(b0)), __float2half2_rn(kRest));
+                h[2 * k + 1] = __hmul2(__hsub2(h[2 * k + 1], from_e4m3x2(b1)), __float2half2_rn(kRest));
               }
             }
             *reinterpret_cast<uint4*>(to + (R > 16 ? p * L::kPiece + chunk_at<R>(j, row0 / 16 + c) : chunk_at<L::kPW>(j, p))) = make_uint4(out[0], out[1], out[2], out[3]);
@@ -765,7 +799,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
         if (SHARED && whole && row < live) __stcg(state_sums(P) + s_row[row], ml);
         if (!SHARED && whole) ml.y = den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den);
         s_ml[row] = ml;
-        s_base[j] = kNone;
+        s_base[j] = s_high[j] = kNone, s_left[j] = kCredit;
       }
       wait(&pvdone[(n - 1) % NS], ((n - 1) / NS) & 1);
       named_bar_sync(6 + ph, kStrand);
@@ -786,7 +820,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
           for (int q = 0; q < 4; ++q) {
             float o = 0.f;
 #pragma unroll
-            for (int p = PC - 1; p >= 0; --p) o = fmaf(o, 0.0625f, __uint_as_float(u[p][q]));
+            for (int p = PC - 1; p >= 0; --p) o = fmaf(o, 1.f / kRest, __uint_as_float(u[p][q]));
             const size_t at_row = static_cast<size_t>(s_row[r4 + q]) * D;
             if (r4 + q >= live) break;
             if (!SHARED && whole) out[at_row] = static_cast<uint16_t>(pack2<BF16>(o * s_ml[r4 + q].y, 0.f));
