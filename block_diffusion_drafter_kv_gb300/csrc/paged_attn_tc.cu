@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(kTcThreads, SHARED && H == 1 ? 2 : 1) paged_at
             l *= corr;
             m = mx;
           }
-          huge = __any_sync(0xffffffffu, fabsf(m) > 1048576.f && fabsf(m) < INFINITY);
+          huge = fabsf(m) > 1048576.f && fabsf(m) < INFINITY;  // (the row's own: no other's scores change its rounding)
         }
         if (edge) {
           // The step's V rows behind the last key are cleared; new keys are looked through.
