@@ -179,6 +179,11 @@ DEV void count_entries(const PagedAttnParams& P, int* s_pre, int* s_len, int* s_
 // Of an entry: its first row among the batch's new rows, its pages, and where a row of its outputs goes in `state`.
 template <bool SHARED>
 DEV int first_row(const PagedAttnParams& P, int e) { return !SHARED || e < P.batch ? e * P.rows_per_seq : (e - P.batch) * P.pre_rows; }
+// Whether row `row` of the batch's buffers is one of this call's new rows.
+DEV bool row_is_new(const PagedAttnParams& P, const int* s_new, int row) {
+  const int s = row / P.rows_per_seq;
+  return row - s * P.rows_per_seq < s_new[s];
+}
 template <bool SHARED>
 DEV const int* pages_of(const PagedAttnParams& P, int e) {
   return !SHARED || e < P.batch ? P.page_table + static_cast<size_t>(e) * P.pages_per_seq : P.prefix_table;

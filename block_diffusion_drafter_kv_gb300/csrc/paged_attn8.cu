@@ -498,15 +498,16 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
       if (!mbar_try_wait(bar, parity)) wait_long(bar, parity, flag, P.err, WL);
       __syncwarp();
     };
-    // a segment's q, taken apart; rows up to the next multiple of 16 that are not there are zero
+    // a segment's q, taken apart; rows up to the next multiple of 16 that are not there are zero, and so are those of a
+    // prefix's entry that are not of this call: what lies there must not move the references of the rows beside them
     auto put_q = [&] {
       constexpr int kParts = D / 16;  // threads of a row
       const int live = s_new[at.s] * grp, rows = (live + 15) & ~15;
       for (int item = sid; item < rows * kParts; item += kStrand) {
         const int row = item / kParts, part = item % kParts;
         uint4 in[2] = {};
-        if (row < live) {
-          const int r = new_row(P, row);
+        const int r = new_row(P, row);
+        if (row < live && (!SHARED || at.s < P.batch || row_is_new(P, s_new, first_row<SHARED>(P, at.s) + r))) {
           const uint4* src = reinterpret_cast<const uint4*>(
               static_cast<const uint16_t*>(P.q) +
               ((static_cast<size_t>(first_row<SHARED>(P, at.s)) + r) * P.nq + static_cast<size_t>(at.g) * grp + row - r * grp) * D + part * 16);

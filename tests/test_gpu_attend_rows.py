@@ -32,7 +32,7 @@ def test_other_rows_change_no_bit_in_16_bits(B, dtype, nq, rows):
             assert torch.equal(c.out.view(-1, 128)[keep], want[keep]), (change, keep)
 
 
-@pytest.mark.parametrize("bits", [16])
+@pytest.mark.parametrize("bits", [16, 8])
 @pytest.mark.parametrize("nq,nkv,rows", [(4, 1, 1), (8, 2, 5), (4, 1, 16), (8, 1, 16), (8, 1, 3)])
 def test_rows_of_other_sequences_behind_a_prefix(B, bits, nq, nkv, rows):
     """Behind a prefix products take rows of several sequences together. What lies in rows that are none of this call's changes
