@@ -32,7 +32,8 @@ DEV uint32_t pack<__nv_bfloat16>(float lo, float hi) {
 DEV float2 widen(__half, uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
 DEV float2 widen(__nv_bfloat16, uint32_t u) { return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u)); }
 
-// X: uint8_t for an 8-bit cache.
+// X: uint8_t for an 8-bit cache. Lengths, page ids and scales by ordinary loads: the kernel before may still write them when
+// this one starts, so they are not read-only for as long as it runs.
 template <typename X, typename Y>
 __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadParams P) {
   pdl_wait();
@@ -48,7 +49,7 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadPara
   if (sub >= per_warp) return;
   for (long long row0 = static_cast<long long>(warp) * per_warp + sub; row0 < rows; row0 += static_cast<long long>(warps) * per_warp) {
     const int row = static_cast<int>(row0), s = row / P.rows_per_seq, r = row - s * P.rows_per_seq;
-    const int first = __ldg(P.first + s), count = __ldg(P.count + s);
+    const int first = P.first[s], count = P.count[s];
     if (first < 0 || count < 0 || count > P.rows_per_seq ||
         static_cast<long long>(first) + count > static_cast<long long>(P.pages_per_seq) * kPagePos) {
       if (r == 0 && at0 == 0) raise_flag(P.err, kDevCapacity);
@@ -56,7 +57,7 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadPara
     }
     if (r >= count) continue;
     const int pos = first + r;
-    const int page = __ldg(P.page_table + static_cast<size_t>(s) * P.pages_per_seq + pos / kPagePos);
+    const int page = P.page_table[static_cast<size_t>(s) * P.pages_per_seq + pos / kPagePos];
     if (page < 0 || page >= P.n_pages) {
       if (at0 == 0) raise_flag(P.err, kDevCapacity);
       continue;
@@ -73,7 +74,7 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadPara
           const int x = at + 32 * k;
           if (x >= width) break;
           in[k][which] = __ldcs(reinterpret_cast<const Word*>(reinterpret_cast<const X*>(which == 0 ? P.k_pool : P.v_pool) + from + x * 8));
-          if (kBits8) scale[k][which] = __ldg(P.scales + scale_index(slot, P.nkv, x / heads_step, which));
+          if (kBits8) scale[k][which] = P.scales[scale_index(slot, P.nkv, x / heads_step, which)];
         }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k)
