@@ -387,12 +387,12 @@ _calls = None
 
 
 def _torch_calls():
-    """(raw handle of a device's current stream, index of the current device, int32), looked up once:
+    """(raw handle of a device's current stream, index of the current device, int32, uint8), looked up once:
     the small calls below take a few microseconds in all."""
     global _calls
     if _calls is None:
         import torch
-        _calls = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, torch.int32
+        _calls = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, torch.int32, torch.uint8
     return _calls
 
 
@@ -478,7 +478,11 @@ class PagedCache:
     Sequences that share a prefix: append and attend take `prefix`, the number of the sequence whose
     positions come before those of every sequence of the call (one of the page table's that is not in the
     batch: read as sequence 0, then PagePool.move). shared_rows: the most rows (batch * rows_per_seq) of such an attend;
-    its workspace is kept here."""
+    its workspace is kept here.
+
+    Calls on one cache are ordered on one stream, and so are replays of graphs that hold them: attend leaves its parts in a
+    workspace of the cache's. An attend with a prefix may run beside others where it is given a workspace of its own
+    (shared_workspace)."""
 
     def __init__(self, n_layers: int, n_heads: int, n_kv_heads: int, head_dim: int, pages: PagePool, length, dtype=None,
                  max_block: int = 0, rope_cos=None, rope_sin=None, rope_interleaved: bool = False, scale: float = 0.0,
@@ -534,9 +538,18 @@ class PagedCache:
                 check(self.L.dflash_cache_bind(h, self.k_pool.data_ptr(), self.v_pool.data_ptr(), *args), "dflash_cache_bind")
             self._shared = None
             if shared_rows:
-                self._shared_bytes = self.L.dflash_cache_shared_workspace_size(ctypes.byref(self.cfg), shared_rows)
-                self._shared = torch.empty(self._shared_bytes + 256, dtype=torch.uint8, device="cuda")
+                self._shared = self.shared_workspace(shared_rows)
+                self._shared_bytes = self._shared.numel() - 256
         self._q_row, self._kv_row = n_heads * head_dim, n_kv_heads * head_dim
+
+    def shared_workspace(self, rows: int):
+        """A workspace for attend with a prefix, of up to `rows` rows (batch * rows_per_seq), on the cache's device."""
+        import torch
+        _require_31_bits(rows, "rows")
+        nbytes = self.L.dflash_cache_shared_workspace_size(ctypes.byref(self.cfg), rows)
+        if not nbytes:
+            raise DFlashError(DFLASH_E_INVAL, "rows: 1 or more")
+        return torch.empty(nbytes + 256, dtype=torch.uint8, device=self.device)
 
     def append(self, layer: int, q, k, v, slots, batch: int, rows_per_seq: int, q_out, stream=None, prefix: Optional[int] = None):
         """Rotary positions on q and k, k and v into the cache at `slots` (from
@@ -557,23 +570,32 @@ class PagedCache:
         else:
             check(self.L.dflash_cache_append_shared(*args, prefix, _ptr(q_out), _stream_on(stream, dev)), "dflash_cache_append_shared")
 
-    def attend(self, layer: int, q, n_new, batch: int, rows_per_seq: int, out, stream=None, prefix: Optional[int] = None):
+    def attend(self, layer: int, q, n_new, batch: int, rows_per_seq: int, out, stream=None, prefix: Optional[int] = None,
+               workspace=None):
         """Causal attention of row r of every sequence (position length[s] + r, r < n_new[s]) over
         the cache; q and out: contiguous [batch * rows_per_seq][n_heads][head_dim] of the
         cache's dtype. Rows past n_new[s] of out are left as they were. With `prefix`, every row sees
-        all length[prefix] positions of that sequence first; they are read once for the batch."""
+        all length[prefix] positions of that sequence first; they are read once for the batch. `workspace`: one from
+        shared_workspace in place of the cache's own, for a call that others may overlap; it is the call's until that has run."""
         numel = batch * rows_per_seq * self._q_row
         _require_on(q, self.dtype, numel, "q", self.device)
         _require_on(out, self.dtype, numel, "out", self.device)
         _require_min(n_new, _torch_calls()[2], batch, "n_new", self.device)
         if prefix is None:
+            if workspace is not None:
+                raise DFlashError(DFLASH_E_INVAL, "workspace: of an attend with a prefix")
             check(self.L.dflash_cache_attend(self.c, layer, q.data_ptr(), n_new.data_ptr(), batch, rows_per_seq, out.data_ptr(),
                                              _stream_on(stream, self.device)), "dflash_cache_attend")
             return
-        if self._shared is None:
-            raise DFlashError(DFLASH_E_INVAL, "attention with a prefix needs a cache with shared_rows")
+        if workspace is None:
+            if self._shared is None:
+                raise DFlashError(DFLASH_E_INVAL, "attention with a prefix needs a cache with shared_rows, or a workspace")
+            workspace, nbytes = self._shared, self._shared_bytes
+        else:
+            _require_on(workspace, _torch_calls()[3], workspace.numel(), "workspace", self.device)
+            nbytes = max(0, workspace.numel() - 256)
         check(self.L.dflash_cache_attend_shared(self.c, layer, q.data_ptr(), n_new.data_ptr(), batch, rows_per_seq, prefix,
-                                                out.data_ptr(), (self._shared.data_ptr() + 255) // 256 * 256, self._shared_bytes,
+                                                out.data_ptr(), (workspace.data_ptr() + 255) // 256 * 256, nbytes,
                                                 _stream_on(stream, self.device)), "dflash_cache_attend_shared")
 
     def read(self, layer: int, first, count, batch: int, rows_per_seq: int, k_out, v_out, stream=None):
