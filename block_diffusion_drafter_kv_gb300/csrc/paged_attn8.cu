@@ -24,15 +24,17 @@
 //       references only rose. So one step in 8 is looked at, and a row that had too few weights of 8 or more gets a lower
 //       reference: O and the sums grow, up to 40 orders. Where a reference is set the sum is 16 at least, a step with a weight of
 //       8 adds 8, and a look stands for 8 x 128 weights of 2^-15 each at most: of a row's weights at most 3/8 x 1024 x 2^-15 (2^-20)
-//       of the sum of its steps' largest is lost, however long the range. Of 4 x 32768 keys, 64 rows: 82 us without the looks, 85
-//       with them (89 and 95 where scores spread twice as far); 128 rows 161 and 186, whose threads have no registers left for it.
+//       of the sum of its steps' largest is lost, however long the range, and a sixth of that behind one key far above all.
+//       Of 4 x 32768 keys, 64 rows: 82 us without the looks, 87 with them (89 and 99 where scores spread twice as far); 128
+//       rows 161 and 198, whose threads have no registers left for it.
 //
 // Measured (32 query heads on 8 KV heads, d 128; in brackets the 16-bit cache): 32 ragged sequences of 512 to 8192
-// keys, one token, 56 us, 75% of the copy rate (94); 4 sequences of 32768, one token, 51 us, 78% (89; with d 64 35 us, 57%),
-// with blocks of 16 (64 rows) 83 us, 48% (96), with 128 rows 165 us (117). Few rows are bound by memory, one row of 128 bytes
+// keys, one token, 52 to 56 us, 75 to 81% of the copy rate (94); 4 sequences of 32768, one token, 51 us, 79% (89; with d 64 36 us,
+// 55%), with blocks of 16 (64 rows) 87 us, 46% (97), with 128 rows 198 us (119). Few rows are bound by memory, one row of 128 bytes
 // a position and head, and by the starts and ends of the ranges. From 64 rows on it is the softmax: a step of
-// 128 keys is 6200 warp instructions (some 300 in each of 16 warps, half of them whatever its rows, the rest the issuer's
-// polling), 56% of what the SM can issue, in a chain of some 2600 cycles, against 1400 cycles of HBM time.
+// 128 keys is 6500 warp instructions (some 300 in each of 16 warps, half of them whatever its rows, the rest the issuer's
+// polling), 58% of what the SM can issue, in a chain of some 2700 cycles, against 1400 cycles of HBM time. (Choices below that name 83
+// and 126 us were measured while references only rose.)
 //
 // CTA: one per SM; four softmax groups of 128 threads, a key of the step each. Of at most 16 rows each group is a
 // strand of its own: a range of the list, a producer warp, stages, accumulators, so that one's start and end
@@ -52,9 +54,9 @@ constexpr int kStepKeys = 128;
 constexpr float kNone = 3e38f;      // the negative of a reference where no key has been seen
 constexpr float kHeadroom = 4.f;    // a reference is set so many binary orders below the largest score,
 constexpr float kMost = 256.f;      // moves up where a weight passes this,
-constexpr int kLook = 8;            // and down where, of one step in so many, too many had no weight of 8:
-constexpr int kCredit = 4;          // more than so many,
-constexpr int kGain = 2;            // and so many for each that had one
+constexpr int kLook = 8;            // and down where, of one step in so many, more had no weight of 8
+constexpr int kGain = 2;            // than so many times those that had one,
+constexpr int kCredit = 4;          // and this more behind a move up by less than 2^12 (where scores spread, the next steps are lower again)
 constexpr float kDeepest = 40.f;    // no further than this below its highest in a segment (what is lost then is nothing)
 constexpr float kRest = 32.f;       // a weight's pieces: the rest of one, at most 8, goes into the next times this
 
@@ -552,7 +554,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
     if (u < end) {
       begin_segment();
       put_q();
-      if (j < RT) s_base[j] = s_high[j] = kNone, s_left[j] = kCredit;
+      if (j < RT) s_base[j] = s_high[j] = kNone, s_left[j] = 0;
       named_bar_sync(6 + ph, kStrand);
     }
     for (; u < end; ++seg_no) {
@@ -672,7 +674,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
             }
           };
           scores();
-          const bool look = n > n0 && (n - n0) % kLook == 0 && !ends;  // (by the walk alone)
+          const bool look = (n - n0) % kLook == kLook / 2 && !ends;  // (by the walk alone)
           bool move = n == n0 || look;
           if (!move) {
             weights();
@@ -712,7 +714,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
                 s_corr[c * 16 + j] = ex2(now - old);
                 s_base[c * 16 + j] = now;
                 s_high[c * 16 + j] = fminf(high, now);
-                s_left[c * 16 + j] = kCredit;
+                s_left[c * 16 + j] = up && over <= 16.f ? kCredit : 0;
               }
             }
             moved = named_bar_any(2 + g, 128, moved);
@@ -800,7 +802,7 @@ __global__ void __launch_bounds__(Layout8<D, R, PH, BF16>::kThreads, 1) paged_at
         if (SHARED && whole && row < live) __stcg(state_sums(P) + s_row[row], ml);
         if (!SHARED && whole) ml.y = den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den);
         s_ml[row] = ml;
-        s_base[j] = s_high[j] = kNone, s_left[j] = kCredit;
+        s_base[j] = s_high[j] = kNone, s_left[j] = 0;
       }
       wait(&pvdone[(n - 1) % NS], ((n - 1) / NS) & 1);
       named_bar_sync(6 + ph, kStrand);
