@@ -575,7 +575,8 @@ class PagedCache:
         """Causal attention of row r of every sequence (position length[s] + r, r < n_new[s]) over
         the cache; q and out: contiguous [batch * rows_per_seq][n_heads][head_dim] of the
         cache's dtype. Rows past n_new[s] of out are left as they were. With `prefix`, every row sees
-        all length[prefix] positions of that sequence first; they are read once for the batch. `workspace`: one from
+        all length[prefix] positions of that sequence first; they are read once for the sequences that fill 128 rows of
+        q for a KV head (64 in 8 bits where a sequence has no more), not once a sequence. `workspace`: one from
         shared_workspace in place of the cache's own, for a call that others may overlap; it is the call's until that has run."""
         numel = batch * rows_per_seq * self._q_row
         _require_on(q, self.dtype, numel, "q", self.device)

@@ -9,8 +9,9 @@
 // In 16 bits a product of 128 rows and 64 keys is 512 cycles of the tensor cores in a chain of 1900 (S, softmax, P by one
 // warpgroup), so two CTAs share a SM: 1030 cycles a tile. Measured (32 query heads on 8 KV heads, d 128): 32 sequences behind 4096
 // positions, one token 31 us (every sequence reading the prefix itself: 93 us); 16 behind 8190, blocks of 16 60 us (98 us);
-// 64 behind 8192, blocks of 16 194 us (368 us), 697 TFLOP/s. In 8 bits 40 us (32 behind 8192, one token) and 100 us (16
-// behind 8190, blocks of 16): from 64 rows on no faster than each for itself.
+// 64 behind 8192, blocks of 16 194 us (368 us), 697 TFLOP/s; 8 behind 131072, blocks of 16 293 us (626 us). In 8 bits 42 us (32 behind
+// 8192, one token) and 107 us (16 behind 8190, blocks of 16). A sequence with more than half of an entry's rows has the entry for
+// itself: in 8 bits (64 rows, or 128 for sequences of more than 64) one of more than 32 is no faster than without a prefix to share.
 #include "paged_attn.cuh"
 
 namespace dfl {
