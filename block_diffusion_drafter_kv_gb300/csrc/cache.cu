@@ -299,6 +299,9 @@ static int attend(dflash_cache* c, int32_t layer, const void* q, const int32_t* 
     P.state = reinterpret_cast<float*>(shared + S.state);
     step = shared_batch();
   }
+  // A launch counts its tiles per head in 31 bits: of every sequence, and of a prefix for at most every sequence.
+  const long long tiles = (prefix >= 0 ? 2 : 1) * (static_cast<long long>(f.pages_per_seq) + kMaxExtra);
+  step = static_cast<int>(std::max(1LL, std::min<long long>(step, ((1LL << 31) - 1) / tiles)));
   const size_t seq_bytes = static_cast<size_t>(rows_per_seq) * f.n_heads * f.head_dim * 2;
   for (int s = 0; s < batch; s += step) {
     P.q = static_cast<const uint8_t*>(q) + s * seq_bytes;

@@ -903,6 +903,7 @@ int paged_attn8_strands(int rows) { return rows <= 16 ? 4 : rows <= 32 ? 2 : 1; 
 // cycles). With and without: 32 ragged sequences, one token 57 and 60 us, blocks of 16 111 and 154 us; a prefix of 8190 shared by
 // 16 sequences' blocks 105 and 292 us. (8 + rows / 4: 58, 111 and 108.)
 int paged_attn8_extra(int rows) { return 6 + rows / 8; }
+static_assert(6 + 128 / 8 <= kMaxExtra, "tiles that a list counts behind a pair");
 
 int paged_attn8_set_attributes() {
   const int e[] = {set_attrs<64, false, false>(), set_attrs<64, true, false>(), set_attrs<128, false, false>(), set_attrs<128, true, false>(),

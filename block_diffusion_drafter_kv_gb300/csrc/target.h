@@ -13,6 +13,7 @@ namespace dfl {
 constexpr int kPagePos = 64;          // positions per page, and keys per attention tile
 constexpr int kMaxBatch = 8192;       // sequences of a pool and of a cache (a pool call keeps five integers each in shared memory)
 constexpr int kAttnMaxBatch = 1024;   // sequences of an attention launch (three integers each beside its rings)
+constexpr int kMaxExtra = 32;         // PagedAttnParams::extra at most
 constexpr int kPagedMaxCtas = 256;    // attention partial slots are sized for this many CTAs
 constexpr int kSharedMaxCtas = 320;   // with a shared prefix, of up to two a SM
 
