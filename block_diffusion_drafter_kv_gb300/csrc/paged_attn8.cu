@@ -26,7 +26,7 @@
 //       8 adds 8, and a look stands for 8 x 128 weights of 2^-15 each at most: of a row's weights at most 3/8 x 1024 x 2^-15 (2^-20)
 //       of the sum of its steps' largest is lost, however long the range, and a sixth of that behind one key far above all.
 //       Of 4 x 32768 keys, 64 rows: 82 us without the looks, 87 with them (89 and 99 where scores spread twice as far); 128
-//       rows 161 and 198, whose threads have no registers left for it.
+//       rows 164 and 198, whose threads have no registers left for it.
 //
 // Measured (32 query heads on 8 KV heads, d 128; in brackets the 16-bit cache): 32 ragged sequences of 512 to 8192
 // keys, one token, 52 to 56 us, 75 to 81% of the copy rate (94); 4 sequences of 32768, one token, 51 us, 79% (89; with d 64 36 us,

@@ -554,10 +554,11 @@ int dflash_cache_append_shared(dflash_cache* c, int32_t layer, const void* q, co
  * in fp16), of which the result's own rounding is 1.7e-3 (2.1e-4).
  * In 8 bits the cache's values go to the products as they are, and q and the weights as sums of e4m3
  * numbers: q exactly but for what lies 2^-17 below its row's largest magnitude, each weight to
- * 2^-8 (bf16) or 2^-11 + 2^-12 (fp16). What is lost besides of many small weights together is at most 3/128 (bf16) or
- * 3/4096 (fp16) of the sum, over every 128 keys, of their largest product of a weight and its V row's largest
- * magnitude, however many keys there are, and as a rule far less. A row of q with an infinity or a NaN, and a row that sees a K or V row of scale 255 or
- * a NaN among K's values, is NaN; a NaN among V's values is seen in its column at least.
+ * 2^-8 (bf16) or 2^-11 + 2^-12 (fp16). What is lost besides of many small weights together is at most 3/128
+ * (bf16) or 3/4096 (fp16) of the sum, over every 128 keys, of their largest product of a weight and its V
+ * row's largest magnitude, however many keys there are, and as a rule far less. A row of q with an infinity
+ * or a NaN, and a row that sees a K or V row of scale 255 or a NaN among K's values, is NaN; a NaN among V's
+ * values is seen in its column at least.
  * Within these bounds the rounding of a row may depend on the other rows of the call that read the same KV head (behind a
  * prefix those of all sequences), not on what lies in rows past n_new[s]. */
 int dflash_cache_attend(dflash_cache* c, int32_t layer, const void* q, const int32_t* n_new, int32_t batch,
